@@ -374,6 +374,152 @@ kda_status kda_record_state_blocks(const kda_align *align,
                                    int32_t num_states,
                                    int32_t *error_word, void *stream);
 
+/*
+ * The full-attention layers and the acceptance of the same step
+ * --------------------------------------------------------------
+ * A hybrid model has softmax-attention layers between its KDA layers.  The
+ * calls below do their part of a speculative step on the same row metadata
+ * (cu_seqlens, and a kda_align with the block table, num_computed and
+ * request_indices of the attention layers' cache): kda_kv_append rotates the
+ * new tokens and writes their keys and values, kda_window_attention attends
+ * with them, and kda_token_logprobs reduces the target logits to what decides
+ * the accepted count that kda_commit takes.  A rejected token needs no
+ * rollback: its keys and values lie past the next step's num_computed and
+ * are overwritten by that step's append.
+ *
+ * Paged cache: key_cache and value_cache hold num_blocks blocks of
+ * align->block_size tokens, element (block, token, kv head, channel) at
+ * block*stride_block + token*stride_token + head*stride_head + channel
+ * elements (so both the token-major and the head-major layout fit); 16-byte
+ * aligned bases, strides multiples of 8.  Token t of row b (request r =
+ * request_indices[b], or b) has position p = num_computed[r] + t and lives in
+ * block block_table[r][p / block_size] at token p % block_size.  A table
+ * entry <= 0 is the null block: nothing is stored to it and its keys are
+ * masked (a cache that lets go of blocks behind a sliding window points their
+ * entries at it).  An entry >= num_blocks flags KDA_ROW_BAD_SLOT and is
+ * treated as the null block.  A row is skipped (its outputs and cache left
+ * alone) and flagged when its token count is negative, or above cfg->window
+ * in kda_window_attention (KDA_ROW_BAD_LENGTH), and when its request index is
+ * outside [0, num_requests), its num_computed negative or its last position
+ * past the table's last column (KDA_ROW_BAD_BLOCK).  Rows without tokens are
+ * skipped silently.
+ */
+#define KDA_DTYPE_BF16 0
+#define KDA_DTYPE_FP16 1
+#define KDA_DTYPE_FP32 2   /* kda_token_logprobs only */
+
+#define KDA_ROW_BAD_TOKEN 64  /* kda_token_logprobs: token >= vocab */
+
+#define KDA_MAX_QUERY_ROWS 128  /* window * q_heads / kv_heads in kda_window_attention */
+
+typedef struct kda_cache_config {
+    int32_t q_heads;          /* Hq >= 1, a multiple of kv_heads */
+    int32_t kv_heads;         /* Hkv >= 1 */
+    int32_t head_dim;         /* 64 or 128 */
+    int32_t dtype;            /* of q, k, v, the cache and out: KDA_DTYPE_BF16 or _FP16 */
+    int32_t num_blocks;       /* blocks of the cache (block 0 = null) */
+    int32_t window;           /* kda_window_attention: most new tokens of a row, 1..8 */
+    int32_t left_window;      /* kda_window_attention: keys a query sees, itself included; 0: all */
+    int32_t rotary_dim;       /* kda_kv_append: rotated channels, a multiple of 16, 0..head_dim */
+    int32_t interleaved;      /* kda_kv_append: pairs (2i, 2i+1) instead of (i, i + rotary_dim/2) */
+    float scale;              /* kda_window_attention: multiplies q.k */
+    int64_t stride_block;     /* cache strides in elements, multiples of 8 */
+    int64_t stride_token;
+    int64_t stride_head;
+    int64_t stride_q_t;       /* token strides of q, k, v: multiples of 8 */
+    int64_t stride_k_t;
+    int64_t stride_v_t;
+} kda_cache_config;
+
+/*
+ * kda_kv_append -- rotate the new tokens by position and write their keys
+ * and values to the paged cache.
+ *
+ * For token t of row b at position p, every query and key head is rotated:
+ * pair i of its first rotary_dim channels by the angle p * inv_freq[i],
+ * (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos), in fp32, rounded once to
+ * the storage type; channels from rotary_dim on are kept.  The angle is
+ * reduced exactly: the phase p * (inv_freq[i] / 2 pi) mod 1 is a 64-bit
+ * fixed-point product, so far positions are as accurate as near ones.
+ * Rotated keys and the values as they are go to the token's cache slot.
+ *
+ * q: [num_tokens][Hq][D] or NULL (keys and values only); k, v:
+ * [num_tokens][Hkv][D]; token strides in cfg, heads packed, 16-byte aligned.
+ * q_out: [num_tokens][Hq][D] contiguous, or q itself when its stride is
+ * Hq * D; not used when q is NULL.  inv_freq: fp64 [rotary_dim / 2], device,
+ * radians per position (unused when rotary_dim == 0).  Rows may have any
+ * number of tokens (prompts included); num_tokens bounds cu_seqlens, and
+ * tokens past it or outside every row are left alone.  B == 0 or num_tokens
+ * == 0: KDA_OK, nothing inspected.  Two tokens of one call must not share a
+ * cache slot.
+ */
+kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void *k, const void *v,
+                         void *q_out, void *key_cache, void *value_cache, const double *inv_freq,
+                         const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
+                         const kda_align *align, int32_t *error_word, void *stream);
+
+/* Bytes of the workspace kda_window_attention needs for B rows (0 for an
+ * invalid config).  It needs no initialisation and keeps nothing from call
+ * to call; calls that may overlap need one each. */
+size_t kda_attention_workspace_bytes(const kda_cache_config *cfg, int32_t B);
+
+/*
+ * kda_window_attention -- softmax attention of each row's new tokens over
+ * its paged keys and values, the new tokens' own included (kda_kv_append
+ * first).
+ *
+ * Query t of row b at position p = num_computed + t sees key j when
+ * j <= p, j > p - left_window (left_window > 0) and j's block is not the
+ * null block; query head h reads kv head h / (Hq / Hkv).
+ *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale q.k_j,
+ *   lse = ln sum_j e^(s_j)
+ * with products, sums and the softmax in fp32 and the weights rounded to the
+ * storage type for the product with v.  What a query does not see does not
+ * touch it, whatever it holds (NaN and infinities too).  A query that sees
+ * no key (or only scores of -inf) gets out = 0 and lse = -inf.
+ *
+ * q: [T][Hq][D], token stride in cfg; out: [T][Hq][D] contiguous; lse: fp32
+ * [T][Hq] or NULL.  workspace: workspace_bytes >=
+ * kda_attention_workspace_bytes, 16-byte aligned, not read before it is
+ * written.  The work is split over the rows' lengths, so few long rows fill
+ * the GPU as many short ones do; results do not depend on timing.  B == 0:
+ * KDA_OK, nothing inspected.  window * Hq / Hkv above KDA_MAX_QUERY_ROWS:
+ * KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_window_attention(const kda_cache_config *cfg, const void *q,
+                                const void *key_cache, const void *value_cache,
+                                const int32_t *cu_seqlens, int32_t B, const kda_align *align,
+                                void *workspace, size_t workspace_bytes, void *out, float *lse,
+                                int32_t *error_word, void *stream);
+
+/*
+ * kda_token_logprobs -- log probability of a given token, entropy and the
+ * top alternatives of each row of logits.
+ *
+ * Row i holds `vocab` logits x at logits + i * stride_row (element
+ * alignment is enough).  With lse = ln sum_j e^(x_j) in fp32:
+ *   logprob[i] = x[tokens[i]] - lse       (tokens[i] < 0: no token, 0)
+ *   entropy[i] = lse - sum_j p_j x_j,  p_j = e^(x_j - lse), masked (-inf)
+ *                logits weighing nothing
+ *   lse_out[i] = lse
+ *   top_logprob[i][0..num_top), top_index[i][0..num_top): the largest logits,
+ *                descending, equal ones by the lower index, as x - lse.
+ * A row of -inf only: lse and every log probability -inf, entropy 0.  A row
+ * with a NaN or +inf: lse, entropy and every log probability NaN; for the
+ * order of the alternatives a NaN counts as -inf.  tokens[i] >= vocab flags
+ * KDA_ROW_BAD_TOKEN and leaves the row's outputs alone.
+ *
+ * dtype: KDA_DTYPE_*.  num_top: 0..KDA_MAX_TOP, at most vocab; top_logprob
+ * and top_index: [rows][num_top] contiguous, unused when num_top == 0.
+ * lse_out and entropy may be NULL.  rows == 0: KDA_OK, nothing inspected.
+ */
+#define KDA_MAX_TOP 32
+kda_status kda_token_logprobs(const void *logits, int32_t dtype, int64_t stride_row, int32_t rows,
+                              int32_t vocab, const int32_t *tokens, int32_t num_top,
+                              float *logprob, float *entropy, float *lse_out,
+                              float *top_logprob, int32_t *top_index,
+                              int32_t *error_word, void *stream);
+
 /* Name of a status code (static string). */
 const char *kda_status_string(kda_status status);
 

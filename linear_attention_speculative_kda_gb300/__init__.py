@@ -10,7 +10,10 @@ from .api import (  # noqa: F401
     KDAError,
     kda_commit,
     kda_flush,
+    kda_kv_append,
     kda_records_bytes,
+    kda_token_logprobs,
     kda_verify,
+    kda_window_attention,
     library_path,
 )

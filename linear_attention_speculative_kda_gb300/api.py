@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -36,6 +37,11 @@ ROW_BAD_RECORD = 4
 ROW_BAD_PENDING = 8
 ERR_WAIT_TIMEOUT = 16
 ROW_BAD_BLOCK = 32
+ROW_BAD_TOKEN = 64
+
+MAX_QUERY_ROWS = 128         # window * q_heads / kv_heads of kda_window_attention
+MAX_TOP = 32                 # alternatives of kda_token_logprobs
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 EXPORTED = (
     "kda_records_bytes",
@@ -47,6 +53,10 @@ EXPORTED = (
     "kda_commit_align",
     "kda_conv_compact_align",
     "kda_record_state_blocks",
+    "kda_kv_append",
+    "kda_attention_workspace_bytes",
+    "kda_window_attention",
+    "kda_token_logprobs",
     "kda_status_string",
     "kda_abi_version",
 )
@@ -109,6 +119,28 @@ class KdaAlign(ctypes.Structure):
         ("request_indices", ctypes.c_void_p),
     ]
 
+
+class KdaCacheConfig(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("left_window", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("stride_block", ctypes.c_int64),
+        ("stride_token", ctypes.c_int64),
+        ("stride_head", ctypes.c_int64),
+        ("stride_q_t", ctypes.c_int64),
+        ("stride_k_t", ctypes.c_int64),
+        ("stride_v_t", ctypes.c_int64),
+    ]
+
+
 _lib_handle = None
 
 
@@ -156,6 +188,16 @@ def bind_library(path: str):
                                            [vp, alp, vp, vp])
     lib.kda_record_state_blocks.restype = ctypes.c_int
     lib.kda_record_state_blocks.argtypes = [alp, vp, vp, i32, vp, vp, i32, vp, vp]
+    ccp = ctypes.POINTER(KdaCacheConfig)
+    lib.kda_kv_append.restype = ctypes.c_int
+    lib.kda_kv_append.argtypes = [ccp] + [vp] * 8 + [i32, i32, alp, vp, vp]
+    lib.kda_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.kda_attention_workspace_bytes.argtypes = [ccp, i32]
+    lib.kda_window_attention.restype = ctypes.c_int
+    lib.kda_window_attention.argtypes = ([ccp] + [vp] * 4 + [i32, alp, vp, ctypes.c_size_t] +
+                                         [vp] * 4)
+    lib.kda_token_logprobs.restype = ctypes.c_int
+    lib.kda_token_logprobs.argtypes = [vp, i32, ctypes.c_int64, i32, i32, vp, i32] + [vp] * 7
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_abi_version.restype = i32
@@ -659,3 +701,250 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
                                      num_rows, _ptr(state_column), _ptr(num_accepted),
                                      state_column.shape[0], _ptr(error_word), _stream_ptr(dev))
     _check("kda_record_state_blocks", st)
+
+
+# ------------------------------------- full-attention layers and acceptance --
+
+@functools.lru_cache(maxsize=256)
+def _cache_config(q_heads, kv_heads, head_dim, dtype, num_blocks, window, left_window, rotary_dim,
+                  interleaved, scale, cache_strides, token_strides) -> KdaCacheConfig:
+    # read only by the library, so one object per distinct argument set
+    cfg = KdaCacheConfig()
+    cfg.q_heads, cfg.kv_heads, cfg.head_dim = q_heads, kv_heads, head_dim
+    cfg.dtype, cfg.num_blocks = dtype, num_blocks
+    cfg.window, cfg.left_window = window, left_window
+    cfg.rotary_dim, cfg.interleaved = rotary_dim, interleaved
+    cfg.scale = head_dim ** -0.5 if scale is None else float(scale)
+    cfg.stride_block, cfg.stride_token, cfg.stride_head = cache_strides
+    cfg.stride_q_t, cfg.stride_k_t, cfg.stride_v_t = token_strides
+    return cfg
+
+
+def _check_cache(key_cache, value_cache, dev):
+    """(num_blocks, block_size, kv_heads, head_dim) and the strides of a paged
+    cache viewed as [num_blocks, block_size, kv_heads, head_dim]."""
+    dtype = key_cache.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
+    _req(value_cache, dtype, "value_cache", dev)
+    shape, strides = tuple(key_cache.shape), key_cache.stride()
+    if len(shape) != 4 or strides[3] != 1:
+        raise ValueError("the caches must be [num_blocks, block_size, kv_heads, head_dim] views "
+                         "with contiguous channels")
+    if tuple(value_cache.shape) != shape or value_cache.stride() != strides:
+        raise ValueError("key_cache and value_cache must have the same shape and strides")
+    return shape, strides
+
+
+def _heads_tokens(t, name, heads, dim):
+    """Token count and token stride of a [T, heads, dim] activation with
+    heads and channels packed."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name} needs contiguous [H, D] inside a token")
+    return shape[0], stride[0] if shape[0] > 1 else heads * dim
+
+
+def _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev):
+    """Row count of a call on a paged key/value cache."""
+    i32 = torch.int32
+    _req(cu_seqlens, i32, "cu_seqlens", dev)
+    _opt(error_word, i32, "error_word", dev)
+    _check_align(block_table, num_computed, request_indices, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous with B + 1 entries")
+    B = cu_seqlens.shape[0] - 1
+    if request_indices is not None:
+        _at_least(request_indices, B, "request_indices")
+    elif B > block_table.shape[0]:
+        raise ValueError("more rows than requests without request_indices")
+    _at_least(error_word, 1, "error_word")
+    return B
+
+
+def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_computed, *,
+                  inv_freq=None, interleaved: bool = False, q_out=None, request_indices=None,
+                  error_word=None):
+    """``kda_kv_append``: rotate the new tokens' queries and keys by position
+    and write keys and values to the paged cache.
+
+    q: [T, Hq, D] or None; k, v: [T, Hkv, D] (token stride free, [H, D]
+    packed), bf16 or fp16; key_cache, value_cache: [num_blocks, block_size,
+    Hkv, D] views of the same strides; cu_seqlens int32 [B + 1]; block_table
+    int32 [num_requests, width] (entries <= 0: nothing is stored);
+    num_computed int32 [num_requests].  inv_freq: fp64 [rotary_dim / 2],
+    radians per position (None: no rotation).  Returns the rotated queries
+    (``q_out``, which may be ``q`` when it is contiguous; allocated when
+    None), or None without ``q``.
+    """
+    dev = key_cache.device
+    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache, dev)
+    dtype = key_cache.dtype
+    _req(k, dtype, "k", dev)
+    _req(v, dtype, "v", dev)
+    B = _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev)
+    T, stride_k = _heads_tokens(k, "k", kv_heads, dim)
+    Tv, stride_v = _heads_tokens(v, "v", kv_heads, dim)
+    if Tv != T:
+        raise ValueError("k and v have different token counts")
+    q_heads, stride_q = kv_heads, 8
+    if q is not None:
+        _req(q, dtype, "q", dev)
+        q_heads = q.shape[1] if q.dim() == 3 else 0
+        if q_heads < 1 or q_heads % kv_heads:
+            raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
+        Tq, stride_q = _heads_tokens(q, "q", q_heads, dim)
+        if Tq != T:
+            raise ValueError("q and k have different token counts")
+        if q_out is None:
+            q_out = torch.empty((T, q_heads, dim), dtype=dtype, device=dev)
+        else:
+            _req(q_out, dtype, "q_out", dev)
+            if tuple(q_out.shape) != (T, q_heads, dim) or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous and shaped like q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rotary_dim = 0
+    if inv_freq is not None:
+        _req(inv_freq, torch.float64, "inv_freq", dev)
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
+        rotary_dim = 2 * inv_freq.shape[0]
+    cfg = _cache_config(q_heads, kv_heads, dim, DTYPES[dtype], blocks, 1, 0, rotary_dim,
+                        1 if interleaved else 0, None, strides[:3], (stride_q, stride_k, stride_v))
+    al = make_align(block_table, num_computed, block_size, request_indices)
+    st = load_library().kda_kv_append(
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(key_cache),
+        _ptr(value_cache), _ptr(inv_freq) if rotary_dim else None, _ptr(cu_seqlens), B, T,
+        ctypes.byref(al), _ptr(error_word), _stream_ptr(dev))
+    _check("kda_kv_append", st)
+    return q_out
+
+
+@functools.lru_cache(maxsize=256)
+def kda_attention_workspace_bytes(num_rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                  window: int = MAX_WINDOW) -> int:
+    """Size in bytes of the workspace of ``kda_window_attention``
+    (``kda_attention_workspace_bytes``); 0 for sizes it does not support."""
+    cfg = _cache_config(q_heads, kv_heads, head_dim, 0, 1, window, 0, 0, 0, None, (8, 8, 8),
+                        (8, 8, 8))
+    return int(load_library().kda_attention_workspace_bytes(ctypes.byref(cfg), num_rows))
+
+
+def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, head_dim: int, device,
+                                 window: int | None = None) -> torch.Tensor:
+    """A workspace for ``kda_window_attention`` calls of up to ``num_rows``
+    rows and ``window`` tokens each (None: the largest window the head counts
+    allow).  It holds nothing between calls; calls that may overlap need one
+    each."""
+    if window is None:
+        group = q_heads // max(kv_heads, 1)
+        window = min(MAX_WINDOW, MAX_QUERY_ROWS // max(group, 1))
+    nbytes = kda_attention_workspace_bytes(num_rows, q_heads, kv_heads, head_dim, window)
+    if nbytes == 0:
+        raise ValueError("invalid attention sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num_computed,
+                         workspace, *, window: int = MAX_WINDOW, scale=None, left_window: int = 0,
+                         request_indices=None, out=None, lse=None, error_word=None):
+    """``kda_window_attention``: softmax attention of each row's new tokens
+    (at most ``window``) over its paged keys and values, the new ones included
+    (``kda_kv_append`` first).
+
+    q: [T, Hq, D] (token stride free), bf16 or fp16; caches, block_table and
+    num_computed as for ``kda_kv_append``; ``left_window``: keys a query sees,
+    itself included (0: all); ``scale``: D ** -0.5 when None; workspace from
+    ``allocate_attention_workspace``.  Returns ``(out, lse)``: out [T, Hq, D]
+    and the scores' log sum of exponentials, fp32 [T, Hq].  Rows that are
+    skipped leave theirs untouched."""
+    dev = key_cache.device
+    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache, dev)
+    dtype = key_cache.dtype
+    _req(q, dtype, "q", dev)
+    _req(workspace, torch.uint8, "workspace", dev)
+    B = _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev)
+    q_heads = q.shape[1] if q.dim() == 3 else 0
+    if q_heads < 1 or q_heads % kv_heads:
+        raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
+    T, stride_q = _heads_tokens(q, "q", q_heads, dim)
+    if out is None:
+        out = torch.empty((T, q_heads, dim), dtype=dtype, device=dev)
+    else:
+        _req(out, dtype, "out", dev)
+        if tuple(out.shape) != (T, q_heads, dim) or not out.is_contiguous():
+            raise ValueError("out must be contiguous and shaped like q")
+    if lse is None:
+        lse = torch.empty((T, q_heads), dtype=torch.float32, device=dev)
+    else:
+        _req(lse, torch.float32, "lse", dev)
+        if tuple(lse.shape) != (T, q_heads) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, Hq] tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if T == 0:  # an empty tensor has no address to pass on
+        return out, lse
+    cfg = _cache_config(q_heads, kv_heads, dim, DTYPES[dtype], blocks, window, left_window, 0, 0,
+                        scale, strides[:3], (stride_q, 8, 8))
+    al = make_align(block_table, num_computed, block_size, request_indices)
+    st = load_library().kda_window_attention(
+        ctypes.byref(cfg), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(cu_seqlens), B,
+        ctypes.byref(al), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
+        _ptr(error_word), _stream_ptr(dev))
+    _check("kda_window_attention", st)
+    return out, lse
+
+
+class TokenLogprobs(NamedTuple):
+    """Outputs of ``kda_token_logprobs``: fp32 [rows] each, the alternatives
+    fp32 and int32 [rows, num_top]."""
+
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: torch.Tensor
+    top_index: torch.Tensor
+
+
+def allocate_token_logprobs(rows: int, num_top: int, device) -> TokenLogprobs:
+    """Output buffers of ``kda_token_logprobs``."""
+    f32 = dict(dtype=torch.float32, device=device)
+    one = torch.empty((3, rows), **f32)
+    return TokenLogprobs(one[0], one[1], one[2], torch.empty((rows, num_top), **f32),
+                         torch.empty((rows, num_top), dtype=torch.int32, device=device))
+
+
+def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs | None = None,
+                       error_word=None) -> TokenLogprobs:
+    """``kda_token_logprobs``: log probability of ``tokens`` (int32 [rows];
+    negative: none, 0), entropy, log sum of exponentials and the ``num_top``
+    largest logits (ties: the lower index) of each row of ``logits`` [rows,
+    vocab], bf16, fp16 or fp32 with any row stride."""
+    dev = logits.device
+    if logits.dtype not in DTYPES:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [rows, vocab] with contiguous columns")
+    rows, vocab = logits.shape
+    _req(tokens, torch.int32, "tokens", dev)
+    _opt(error_word, torch.int32, "error_word", dev)
+    if tokens.dim() != 1 or tokens.shape[0] != rows or not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous with one entry per row")
+    _at_least(error_word, 1, "error_word")
+    if out is None:
+        out = allocate_token_logprobs(rows, num_top, dev)
+    else:
+        for name, t in zip(TokenLogprobs._fields, out):
+            _req(t, torch.int32 if name == "top_index" else torch.float32, name, dev)
+            want = (rows, num_top) if name.startswith("top_") else (rows,)
+            if tuple(t.shape) != want or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {want} tensor")
+    st = load_library().kda_token_logprobs(
+        _ptr(logits), DTYPES[logits.dtype], logits.stride(0), rows, vocab, _ptr(tokens), num_top,
+        _ptr(out.logprob), _ptr(out.entropy), _ptr(out.lse), _ptr(out.top_logprob),
+        _ptr(out.top_index), _ptr(error_word), _stream_ptr(dev))
+    _check("kda_token_logprobs", st)
+    return out

@@ -1,6 +1,6 @@
 """Compile the CUDA library ``libkda.so`` in-tree for sm_103a.
 
-Three translation units in one nvcc call, one ``-gencode`` (compute_103a /
+All translation units in one nvcc call (compiled side by side), one ``-gencode`` (compute_103a /
 sm_103a), the CUDA runtime linked statically so the library only needs the
 driver at run time.
 """
@@ -15,12 +15,15 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("kda_kernels.cu", "kda_conv.cu", "kda_blocks.cu")]
+SOURCES = [os.path.join(CSRC, f)
+           for f in ("kda_kernels.cu", "kda_conv.cu", "kda_blocks.cu", "kda_append.cu",
+                     "kda_attend.cu", "kda_logprobs.cu")]
 DEPENDS = SOURCES + [
     os.path.join(CSRC, "kda_device.cuh"),
     os.path.join(CSRC, "kda_async.cuh"),
     os.path.join(CSRC, "kda_align.cuh"),
     os.path.join(CSRC, "kda_tc.cuh"),
+    os.path.join(CSRC, "kda_cache.cuh"),
     os.path.join(ROOT, "include", "kda.h"),
 ]
 LIBRARY = os.path.join(PKG, "libkda.so")
@@ -49,6 +52,8 @@ def compile_command(output: str, extra=(), sources=None) -> list[str]:
         "-O3",
         "-lineinfo",
         "-std=c++17",
+        "--threads",
+        "0",
         "-shared",
         "-Xcompiler",
         "-fPIC",

@@ -1,0 +1,227 @@
+// kda_kv_append: rotate the new tokens' queries and keys by position and
+// write keys and values to the paged cache (sm_103a).  Contract in
+// include/kda.h.
+//
+// Mathematics.  Pair i of a head at position p turns by the angle p * f_i.
+// Only the angle modulo a full turn counts, so the phase is kept in turns:
+// u_i = (f_i / 2 pi mod 1) * 2^64 as a whole number, and p * u_i mod 2^64 is
+// the fraction of a turn exactly; the rounding of u_i (an fp64 value, 2^-53
+// of it) is all that grows with p, as it does for an angle formed in fp64.
+// Its top 32 bits, signed, give the angle in [-pi, pi) for sincospif.
+//
+// Every value is read and written once and the arithmetic is 3 flops per
+// rotated channel, so HBM bounds the large calls and latency the small ones.
+// A warp takes part of one token: a lane moves units of 16 channels of a
+// head (two 16-byte chunks: the two halves of its 8 pairs), and the sines and
+// cosines are made once per warp, in shared memory, for all heads it takes.
+#include "kda_cache.cuh"
+
+namespace {
+
+using kda_cache::Rows;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxPairs = 64;
+
+struct Params {
+    Rows rows;
+    const char *q, *k, *v;
+    char *q_out, *key_cache, *value_cache;
+    const double *inv_freq;
+    long long stride_q, stride_k, stride_v;              // elements
+    long long stride_block, stride_token, stride_head;   // elements
+    int q_heads, kv_heads, num_tokens;
+    int pairs;        // rotary_dim / 2
+    int interleaved;
+    int parts;        // warps that share a token
+    int rounds;       // rounds of 32 units each of them takes
+};
+
+__device__ __forceinline__ float2 to_float2(uint32_t u, __nv_bfloat16) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+__device__ __forceinline__ float2 to_float2(uint32_t u, __half) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+__device__ __forceinline__ uint32_t from_float2(float2 f, __nv_bfloat16) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(f);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t from_float2(float2 f, __half) {
+    const __half2 h = __float22half2_rn(f);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The row that owns token t (the last one that starts at or before t), found
+// by a warp in steps of 32; -1 when t lies before every row.
+__device__ __forceinline__ int find_row(const int *cu, int B, int t, int lane) {
+    int lo = 0, n = B;
+    for (;;) {
+        const int step = (n + 31) / 32;
+        const int i = lo + lane * step;
+        const bool starts = lane * step < n && cu[i] <= t;
+        const unsigned mask = __ballot_sync(kda_cache::kFull, starts);
+        if (mask == 0) return -1;
+        const int skip = (31 - __clz(mask)) * step;
+        lo += skip;
+        n = min(step, n - skip);
+        if (n <= 1) return lo;
+    }
+}
+
+// 8 pairs of one head: chunk a and chunk b hold them as halves (a[e], b[e])
+// or side by side (a[2e], a[2e+1], then b).
+template <typename T>
+__device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, bool interleaved) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 p = to_float2(x[i], T()), r = to_float2(y[i], T());
+        if (interleaved) {
+            const float2 s = turn[i], t = turn[4 + i];
+            p = make_float2(p.x * s.x - p.y * s.y, p.x * s.y + p.y * s.x);
+            r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
+        } else {
+            const float2 s = turn[2 * i], t = turn[2 * i + 1];
+            const float2 u = p;
+            p = make_float2(u.x * s.x - r.x * s.y, u.y * t.x - r.y * t.y);
+            r = make_float2(u.x * s.y + r.x * s.x, u.y * t.y + r.y * t.x);
+        }
+        x[i] = from_float2(p, T());
+        y[i] = from_float2(r, T());
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
+    constexpr int kUnits = kDim / 16;  // units of a head
+    __shared__ float2 turns[kWarps][kMaxPairs];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    kda_cache::grid_dependents_launch();
+    kda_cache::grid_dependency_wait();
+    const long long item = (long long)blockIdx.x * kWarps + warp;
+    const int t = (int)(item / p.parts), part = (int)(item % p.parts);
+    if (t >= p.num_tokens) return;
+    const int b = find_row(p.rows.cu_seqlens, p.rows.B, t, lane);
+    if (b < 0) return;
+    int bits = 0;
+    const kda_cache::Row row = kda_cache::read_row(p.rows, b, 0x7fffffff, bits);
+    if (bits != 0 && lane == 0) kda_cache::flag(p.rows.err, bits);
+    if (t - row.first >= row.tokens) return;  // between rows, or a row that is skipped
+    const int pos = row.computed + (t - row.first);
+    const int col = kda_cache::divide(pos, p.rows.by_block);
+    int block = p.rows.block_table[row.request * p.rows.bt_stride + col];
+    if (block >= p.rows.num_blocks) {
+        if (lane == 0) kda_cache::flag(p.rows.err, KDA_ROW_BAD_SLOT);
+        block = 0;
+    }
+    for (int i = lane; i < p.pairs; i += 32) {
+        const double turn = p.inv_freq[i] * 0.15915494309189533577;  // 1 / 2 pi
+        const unsigned long long u =
+            __double2ull_rz((turn - floor(turn)) * 18446744073709551616.0);
+        const int phase = (int)((u * (unsigned long long)pos) >> 32);
+        float2 cs;
+        sincospif((float)phase * 0x1p-31f, &cs.y, &cs.x);
+        turns[warp][i] = cs;
+    }
+    __syncwarp();
+    const long long slot = (long long)max(block, 0) * p.stride_block +
+                           (long long)(pos - col * p.rows.block_size) * p.stride_token;
+    const int first_k = p.q_heads, first_v = p.q_heads + p.kv_heads;
+    const int units = (first_v + p.kv_heads) * kUnits;
+    const int begin = part * p.rounds * 32, end = min(units, begin + p.rounds * 32);
+#pragma unroll 2
+    for (int u = begin + lane; u < end; u += 32) {
+        const int head = u / kUnits, j = u % kUnits;
+        const T *src;
+        T *dst;
+        if (head < first_k) {
+            src = reinterpret_cast<const T *>(p.q) + t * p.stride_q + head * kDim;
+            dst = reinterpret_cast<T *>(p.q_out) + ((long long)t * p.q_heads + head) * kDim;
+        } else if (head < first_v) {
+            src = reinterpret_cast<const T *>(p.k) + t * p.stride_k + (head - first_k) * kDim;
+            dst = reinterpret_cast<T *>(p.key_cache) + slot + (head - first_k) * p.stride_head;
+        } else {
+            src = reinterpret_cast<const T *>(p.v) + t * p.stride_v + (head - first_v) * kDim;
+            dst = reinterpret_cast<T *>(p.value_cache) + slot + (head - first_v) * p.stride_head;
+        }
+        const bool turned = head < first_v && j * 8 < p.pairs;
+        const int at = turned && !p.interleaved ? j * 8 : j * 16;
+        const int other = turned && !p.interleaved ? p.pairs + j * 8 : j * 16 + 8;
+        uint4 x = *reinterpret_cast<const uint4 *>(src + at);
+        uint4 y = *reinterpret_cast<const uint4 *>(src + other);
+        if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
+        if (head < first_k || block > 0) {
+            *reinterpret_cast<uint4 *>(dst + at) = x;
+            *reinterpret_cast<uint4 *>(dst + other) = y;
+        }
+    }
+}
+
+}  // namespace
+
+extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void *k,
+                                    const void *v, void *q_out, void *key_cache,
+                                    void *value_cache, const double *inv_freq,
+                                    const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
+                                    const kda_align *align, int32_t *error_word, void *stream) {
+    using kda_cache::aligned;
+    using kda_cache::stride_ok;
+    kda_status st = kda_cache::check_config(cfg);
+    if (st != KDA_OK) return st;
+    if (B < 0 || num_tokens < 0) return KDA_ERR_INVALID_ARG;
+    if (cfg->rotary_dim < 0 || cfg->rotary_dim > cfg->head_dim || (cfg->rotary_dim & 15) != 0 ||
+        (cfg->interleaved != 0 && cfg->interleaved != 1))
+        return KDA_ERR_INVALID_ARG;
+    if (B == 0 || num_tokens == 0) return KDA_OK;  // nothing to do; no pointer is inspected
+    Params p;
+    st = kda_cache::set_rows(cfg, align, cu_seqlens, B, error_word, p.rows);
+    if (st != KDA_OK) return st;
+    if (!k || !v || !key_cache || !value_cache || (q != nullptr && !q_out) ||
+        (cfg->rotary_dim > 0 && !inv_freq))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(key_cache, 16) ||
+        !aligned(value_cache, 16) || (q != nullptr && !aligned(q_out, 16)) ||
+        (cfg->rotary_dim > 0 && !aligned(inv_freq, 8)))
+        return KDA_ERR_INVALID_ARG;
+    if ((q != nullptr && !stride_ok(cfg->stride_q_t)) || !stride_ok(cfg->stride_k_t) ||
+        !stride_ok(cfg->stride_v_t))
+        return KDA_ERR_INVALID_ARG;
+    p.q = static_cast<const char *>(q);
+    p.k = static_cast<const char *>(k);
+    p.v = static_cast<const char *>(v);
+    p.q_out = static_cast<char *>(q_out);
+    p.key_cache = static_cast<char *>(key_cache);
+    p.value_cache = static_cast<char *>(value_cache);
+    p.inv_freq = inv_freq;
+    p.stride_q = cfg->stride_q_t;
+    p.stride_k = cfg->stride_k_t;
+    p.stride_v = cfg->stride_v_t;
+    p.stride_block = cfg->stride_block;
+    p.stride_token = cfg->stride_token;
+    p.stride_head = cfg->stride_head;
+    p.q_heads = q != nullptr ? cfg->q_heads : 0;
+    p.kv_heads = cfg->kv_heads;
+    p.num_tokens = num_tokens;
+    p.pairs = cfg->rotary_dim / 2;
+    p.interleaved = cfg->interleaved;
+    const int rounds =
+        ((p.q_heads + 2 * p.kv_heads) * (cfg->head_dim / 16) + 31) / 32;  // of a whole token
+    p.rounds = 1;
+    p.parts = (rounds + p.rounds - 1) / p.rounds;
+    const long long items = (long long)num_tokens * p.parts;
+    const long long grid = (items + kWarps - 1) / kWarps;
+    if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    void (*kernel)(const Params) =
+        cfg->dtype == KDA_DTYPE_BF16
+            ? (cfg->head_dim == 64 ? append_kernel<__nv_bfloat16, 64>
+                                   : append_kernel<__nv_bfloat16, 128>)
+            : (cfg->head_dim == 64 ? append_kernel<__half, 64> : append_kernel<__half, 128>);
+    return kda_cache::launch(kernel, dim3((unsigned)grid), dim3(kThreads), 0, 1, stream, p);
+}

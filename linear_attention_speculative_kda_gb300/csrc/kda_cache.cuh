@@ -1,0 +1,162 @@
+// Row metadata of the paged key/value cache, shared by the append and the
+// window attention, and small helpers of both (sm_103a).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+
+namespace kda_cache {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// Division of a position (0 <= n < 2^31) by the block size: with s =
+// ceil(log2 d) and m = ceil(2^(31 + s) / d), n * m >> (31 + s) is exact,
+// because m exceeds 2^(31 + s) / d by less than 1 and n / 2^(31 + s) < 1 / d.
+struct Divider {
+    uint32_t mul, shift;
+};
+
+inline Divider make_divider(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    const uint64_t m = ((1ull << (31 + s)) + d - 1) / d;
+    return Divider{(uint32_t)m, 31 + s};
+}
+
+__host__ __device__ __forceinline__ int divide(int n, const Divider &d) {
+    return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
+}
+
+// The rows' side of a call: where each row's tokens lie and which request's
+// table it reads.
+struct Rows {
+    const int *cu_seqlens;
+    const int *block_table, *num_computed, *request_indices;
+    long long bt_stride;
+    int B, bt_width, block_size, num_requests, num_blocks;
+    Divider by_block;
+    int *err;
+};
+
+struct Row {
+    int first, tokens;  // first token, token count (0: nothing to do)
+    int computed;       // position of the first token
+    int request;
+};
+
+__device__ __forceinline__ void flag(int *err, int bits) {
+    if (err != nullptr) atomicOr(err, bits);
+}
+
+// Row b, checked; `bits` collects what is wrong with it (the row is then
+// empty).  most: the largest token count allowed.
+__device__ __forceinline__ Row read_row(const Rows &r, int b, int most, int &bits) {
+    Row row{r.cu_seqlens[b], 0, 0, 0};
+    const long long n = (long long)r.cu_seqlens[b + 1] - row.first;
+    if (n == 0) return row;
+    if (n < 0 || n > most || row.first < 0) {
+        bits |= KDA_ROW_BAD_LENGTH;
+        return row;
+    }
+    row.request = r.request_indices != nullptr ? r.request_indices[b] : b;
+    if (row.request < 0 || row.request >= r.num_requests) {
+        bits |= KDA_ROW_BAD_BLOCK;
+        return row;
+    }
+    row.computed = r.num_computed[row.request];
+    const long long last = (long long)row.computed + n - 1;
+    if (row.computed < 0 || last > 0x7ffffff0LL || divide((int)last, r.by_block) >= r.bt_width) {
+        bits |= KDA_ROW_BAD_BLOCK;
+        return row;
+    }
+    row.tokens = (int)n;
+    return row;
+}
+
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_dependents_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------- host --
+
+inline bool aligned(const void *ptr, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
+}
+
+inline bool stride_ok(int64_t s) { return s >= 1 && (s & 7) == 0; }
+
+// Host checks of what the append and the attention share.
+inline kda_status check_config(const kda_cache_config *c) {
+    if (c == nullptr) return KDA_ERR_INVALID_ARG;
+    if (c->q_heads < 1 || c->kv_heads < 1 || c->q_heads % c->kv_heads != 0 || c->num_blocks < 1)
+        return KDA_ERR_INVALID_ARG;
+    if (c->dtype != KDA_DTYPE_BF16 && c->dtype != KDA_DTYPE_FP16) return KDA_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return KDA_ERR_UNSUPPORTED;
+    if (c->q_heads > KDA_MAX_HEADS) return KDA_ERR_UNSUPPORTED;
+    if (!stride_ok(c->stride_block) || !stride_ok(c->stride_token) || !stride_ok(c->stride_head))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+inline kda_status set_rows(const kda_cache_config *c, const kda_align *al, const int32_t *cu_seqlens,
+                           int32_t B, int32_t *error_word, Rows &r) {
+    if (al == nullptr || al->reserved != 0) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens || !al->block_table || !al->num_computed) return KDA_ERR_INVALID_ARG;
+    if (al->block_table_width < 1 || al->block_table_stride < al->block_table_width ||
+        al->num_requests < 1 || al->block_size < 1 || al->block_size > (1 << 30))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(al->block_table, 4) || !aligned(al->num_computed, 4) ||
+        (al->request_indices != nullptr && !aligned(al->request_indices, 4)) ||
+        (error_word != nullptr && !aligned(error_word, 4)))
+        return KDA_ERR_INVALID_ARG;
+    if (al->request_indices == nullptr && B > al->num_requests) return KDA_ERR_INVALID_ARG;
+    r.cu_seqlens = cu_seqlens;
+    r.block_table = al->block_table;
+    r.num_computed = al->num_computed;
+    r.request_indices = al->request_indices;
+    r.bt_stride = al->block_table_stride;
+    r.B = B;
+    r.bt_width = al->block_table_width;
+    r.block_size = al->block_size;
+    r.num_requests = al->num_requests;
+    r.num_blocks = c->num_blocks;
+    r.by_block = make_divider((uint32_t)al->block_size);
+    r.err = error_word;
+    return KDA_OK;
+}
+
+// Launch with programmatic dependent launch: the kernel may start its set-up
+// while the one before it in the stream drains; it waits for it
+// (grid_dependency_wait) before it touches memory.
+template <typename... P, typename... A>
+inline kda_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster,
+                         void *stream, A... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = smem;
+    lc.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        lc.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace kda_cache
