@@ -704,64 +704,84 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
 
 
 # ------------------------------------- full-attention layers and acceptance --
+#
+# These calls are short (a decode step's append takes 3 us on the device), so
+# their checks are written out inline: one comparison per fact, and the
+# message is worked out only once something is wrong.
 
-@functools.lru_cache(maxsize=256)
+def _raw_stream(dev):
+    # the handle torch.cuda.current_stream(dev).cuda_stream holds, without
+    # building the stream object
+    return torch._C._cuda_getCurrentRawStream(dev.index if dev.index is not None
+                                              else torch.cuda.current_device())
+
+
+def _mismatch(dev, **tensors):
+    """Raises for the first of name=(tensor, dtype) that is not on ``dev`` or
+    of its type (the callers found that one is not)."""
+    for name, (t, dtype) in tensors.items():
+        if t is not None:
+            _req(t, dtype, name, dev)
+
+
+@functools.lru_cache(maxsize=1024)
 def _cache_config(q_heads, kv_heads, head_dim, dtype, num_blocks, window, left_window, rotary_dim,
-                  interleaved, scale, cache_strides, token_strides) -> KdaCacheConfig:
-    # read only by the library, so one object per distinct argument set
-    cfg = KdaCacheConfig()
-    cfg.q_heads, cfg.kv_heads, cfg.head_dim = q_heads, kv_heads, head_dim
-    cfg.dtype, cfg.num_blocks = dtype, num_blocks
-    cfg.window, cfg.left_window = window, left_window
-    cfg.rotary_dim, cfg.interleaved = rotary_dim, interleaved
-    cfg.scale = head_dim ** -0.5 if scale is None else float(scale)
-    cfg.stride_block, cfg.stride_token, cfg.stride_head = cache_strides
-    cfg.stride_q_t, cfg.stride_k_t, cfg.stride_v_t = token_strides
-    return cfg
+                  interleaved, scale, stride_block, stride_token, stride_head, stride_q, stride_k,
+                  stride_v):
+    """A pointer to a ``kda_cache_config``, read only by the library: one
+    object per distinct argument set."""
+    cfg = KdaCacheConfig(
+        q_heads, kv_heads, head_dim, dtype, num_blocks, window, left_window, rotary_dim,
+        interleaved, head_dim ** -0.5 if scale is None else float(scale), stride_block,
+        stride_token, stride_head, stride_q, stride_k, stride_v)
+    return ctypes.pointer(cfg)
 
 
-def _check_cache(key_cache, value_cache, dev):
-    """(num_blocks, block_size, kv_heads, head_dim) and the strides of a paged
-    cache viewed as [num_blocks, block_size, kv_heads, head_dim]."""
-    dtype = key_cache.dtype
-    if dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
-    _req(value_cache, dtype, "value_cache", dev)
-    shape, strides = tuple(key_cache.shape), key_cache.stride()
+def _check_cache(key_cache, value_cache):
+    """Shape and strides of a paged cache viewed as [num_blocks, block_size,
+    kv_heads, head_dim], flat."""
+    shape, strides = key_cache.shape, key_cache.stride()
     if len(shape) != 4 or strides[3] != 1:
         raise ValueError("the caches must be [num_blocks, block_size, kv_heads, head_dim] views "
                          "with contiguous channels")
-    if tuple(value_cache.shape) != shape or value_cache.stride() != strides:
+    if value_cache.shape != shape or value_cache.stride() != strides:
         raise ValueError("key_cache and value_cache must have the same shape and strides")
-    return shape, strides
+    return *shape, strides[0], strides[1], strides[2]
 
 
-def _heads_tokens(t, name, heads, dim):
-    """Token count and token stride of a [T, heads, dim] activation with
-    heads and channels packed."""
+def _heads_tokens(t, name, dim):
+    """Token count, heads and token stride of a [T, heads, dim] activation
+    with heads and channels packed."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
-    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, H, {dim}], got {tuple(shape)}")
+    tokens, heads, _ = shape
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name} needs contiguous [H, D] inside a token")
-    return shape[0], stride[0] if shape[0] > 1 else heads * dim
+    return tokens, heads, stride[0] if tokens > 1 else heads * dim
 
 
-def _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev):
-    """Row count of a call on a paged key/value cache."""
-    i32 = torch.int32
-    _req(cu_seqlens, i32, "cu_seqlens", dev)
-    _opt(error_word, i32, "error_word", dev)
-    _check_align(block_table, num_computed, request_indices, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous with B + 1 entries")
+def _plan(cu_seqlens, block_table, num_computed, request_indices, block_size, error_word):
+    """Row count and ``kda_align`` of a call on a paged key/value cache."""
     B = cu_seqlens.shape[0] - 1
+    requests, width = block_table.shape
+    stride = block_table.stride()
+    if B < 0 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous with B + 1 entries")
+    if stride[1] != 1 and width > 1:
+        raise ValueError("block_table must be [num_requests, width] with contiguous columns")
+    if num_computed.shape[0] < requests or not num_computed.is_contiguous():
+        raise ValueError("num_computed must be contiguous with one entry per request")
     if request_indices is not None:
+        if not request_indices.is_contiguous():
+            raise ValueError("request_indices must be contiguous")
         _at_least(request_indices, B, "request_indices")
-    elif B > block_table.shape[0]:
+    elif B > requests:
         raise ValueError("more rows than requests without request_indices")
-    _at_least(error_word, 1, "error_word")
-    return B
+    if error_word is not None:
+        _at_least(error_word, 1, "error_word")
+    return B, KdaAlign(block_table.data_ptr(), stride[0] if requests > 1 else width, width,
+                       block_size, requests, 0, num_computed.data_ptr(), _ptr(request_indices))
 
 
 def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_computed, *,
@@ -779,47 +799,58 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
     (``q_out``, which may be ``q`` when it is contiguous; allocated when
     None), or None without ``q``.
     """
-    dev = key_cache.device
-    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache, dev)
-    dtype = key_cache.dtype
-    _req(k, dtype, "k", dev)
-    _req(v, dtype, "v", dev)
-    B = _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev)
-    T, stride_k = _heads_tokens(k, "k", kv_heads, dim)
-    Tv, stride_v = _heads_tokens(v, "v", kv_heads, dim)
-    if Tv != T:
-        raise ValueError("k and v have different token counts")
-    q_heads, stride_q = kv_heads, 8
+    dev, dtype, i32 = key_cache.device, key_cache.dtype, torch.int32
+    code = DTYPES.get(dtype, 2)
+    if code > 1:
+        raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
+    if (value_cache.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype
+            or cu_seqlens.dtype is not i32 or block_table.dtype is not i32
+            or num_computed.dtype is not i32 or value_cache.device != dev or k.device != dev
+            or v.device != dev or cu_seqlens.device != dev or block_table.device != dev
+            or num_computed.device != dev):
+        _mismatch(dev, value_cache=(value_cache, dtype), k=(k, dtype), v=(v, dtype),
+                  cu_seqlens=(cu_seqlens, i32), block_table=(block_table, i32),
+                  num_computed=(num_computed, i32))
+    _opt(request_indices, i32, "request_indices", dev)
+    _opt(error_word, i32, "error_word", dev)
+    blocks, block_size, kv_heads, dim, sb, st, sh = _check_cache(key_cache, value_cache)
+    B, align = _plan(cu_seqlens, block_table, num_computed, request_indices, block_size,
+                     error_word)
+    T, heads, stride_k = _heads_tokens(k, "k", dim)
+    Tv, heads_v, stride_v = _heads_tokens(v, "v", dim)
+    if heads != kv_heads or heads_v != kv_heads or Tv != T:
+        raise ValueError(f"k and v must be [T, {kv_heads}, {dim}] with the same T")
+    q_heads, stride_q, q_ptr, out_ptr = kv_heads, 8, None, None
     if q is not None:
         _req(q, dtype, "q", dev)
-        q_heads = q.shape[1] if q.dim() == 3 else 0
-        if q_heads < 1 or q_heads % kv_heads:
-            raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
-        Tq, stride_q = _heads_tokens(q, "q", q_heads, dim)
-        if Tq != T:
-            raise ValueError("q and k have different token counts")
+        Tq, q_heads, stride_q = _heads_tokens(q, "q", dim)
+        if Tq != T or q_heads < 1 or q_heads % kv_heads:
+            raise ValueError("q must be [T, Hq, D] with k's T and Hq a multiple of the cache's "
+                             "heads")
         if q_out is None:
-            q_out = torch.empty((T, q_heads, dim), dtype=dtype, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _req(q_out, dtype, "q_out", dev)
-            if tuple(q_out.shape) != (T, q_heads, dim) or not q_out.is_contiguous():
+            if q_out.shape != q.shape or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous and shaped like q")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rotary_dim = 0
+    rotary_dim, freq_ptr = 0, None
     if inv_freq is not None:
         _req(inv_freq, torch.float64, "inv_freq", dev)
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
         rotary_dim = 2 * inv_freq.shape[0]
-    cfg = _cache_config(q_heads, kv_heads, dim, DTYPES[dtype], blocks, 1, 0, rotary_dim,
-                        1 if interleaved else 0, None, strides[:3], (stride_q, stride_k, stride_v))
-    al = make_align(block_table, num_computed, block_size, request_indices)
-    st = load_library().kda_kv_append(
-        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(key_cache),
-        _ptr(value_cache), _ptr(inv_freq) if rotary_dim else None, _ptr(cu_seqlens), B, T,
-        ctypes.byref(al), _ptr(error_word), _stream_ptr(dev))
-    _check("kda_kv_append", st)
+        freq_ptr = inv_freq.data_ptr() if rotary_dim else None
+    cfg = _cache_config(q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim,
+                        1 if interleaved else 0, None, sb, st, sh, stride_q, stride_k, stride_v)
+    status = load_library().kda_kv_append(
+        cfg, q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, key_cache.data_ptr(),
+        value_cache.data_ptr(), freq_ptr, cu_seqlens.data_ptr(), B, T, ctypes.byref(align),
+        _ptr(error_word), _raw_stream(dev))
+    if status:
+        raise KDAError("kda_kv_append", status)
     return q_out
 
 
@@ -828,9 +859,8 @@ def kda_attention_workspace_bytes(num_rows: int, q_heads: int, kv_heads: int, he
                                   window: int = MAX_WINDOW) -> int:
     """Size in bytes of the workspace of ``kda_window_attention``
     (``kda_attention_workspace_bytes``); 0 for sizes it does not support."""
-    cfg = _cache_config(q_heads, kv_heads, head_dim, 0, 1, window, 0, 0, 0, None, (8, 8, 8),
-                        (8, 8, 8))
-    return int(load_library().kda_attention_workspace_bytes(ctypes.byref(cfg), num_rows))
+    cfg = _cache_config(q_heads, kv_heads, head_dim, 0, 1, window, 0, 0, 0, None, 8, 8, 8, 8, 8, 8)
+    return int(load_library().kda_attention_workspace_bytes(cfg, num_rows))
 
 
 def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, head_dim: int, device,
@@ -861,24 +891,35 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
     ``allocate_attention_workspace``.  Returns ``(out, lse)``: out [T, Hq, D]
     and the scores' log sum of exponentials, fp32 [T, Hq].  Rows that are
     skipped leave theirs untouched."""
-    dev = key_cache.device
-    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache, dev)
-    dtype = key_cache.dtype
-    _req(q, dtype, "q", dev)
-    _req(workspace, torch.uint8, "workspace", dev)
-    B = _check_plan(cu_seqlens, block_table, num_computed, request_indices, error_word, dev)
-    q_heads = q.shape[1] if q.dim() == 3 else 0
+    dev, dtype, i32 = key_cache.device, key_cache.dtype, torch.int32
+    code = DTYPES.get(dtype, 2)
+    if code > 1:
+        raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
+    if (value_cache.dtype is not dtype or q.dtype is not dtype
+            or workspace.dtype is not torch.uint8 or cu_seqlens.dtype is not i32
+            or block_table.dtype is not i32 or num_computed.dtype is not i32
+            or value_cache.device != dev or q.device != dev or workspace.device != dev
+            or cu_seqlens.device != dev or block_table.device != dev
+            or num_computed.device != dev):
+        _mismatch(dev, value_cache=(value_cache, dtype), q=(q, dtype),
+                  workspace=(workspace, torch.uint8), cu_seqlens=(cu_seqlens, i32),
+                  block_table=(block_table, i32), num_computed=(num_computed, i32))
+    _opt(request_indices, i32, "request_indices", dev)
+    _opt(error_word, i32, "error_word", dev)
+    blocks, block_size, kv_heads, dim, sb, st, sh = _check_cache(key_cache, value_cache)
+    B, align = _plan(cu_seqlens, block_table, num_computed, request_indices, block_size,
+                     error_word)
+    T, q_heads, stride_q = _heads_tokens(q, "q", dim)
     if q_heads < 1 or q_heads % kv_heads:
         raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
-    T, stride_q = _heads_tokens(q, "q", q_heads, dim)
     if out is None:
-        out = torch.empty((T, q_heads, dim), dtype=dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _req(out, dtype, "out", dev)
-        if tuple(out.shape) != (T, q_heads, dim) or not out.is_contiguous():
+        if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and shaped like q")
     if lse is None:
-        lse = torch.empty((T, q_heads), dtype=torch.float32, device=dev)
+        lse = q.new_empty((T, q_heads), dtype=torch.float32)
     else:
         _req(lse, torch.float32, "lse", dev)
         if tuple(lse.shape) != (T, q_heads) or not lse.is_contiguous():
@@ -887,14 +928,14 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
         raise ValueError("workspace must be contiguous")
     if T == 0:  # an empty tensor has no address to pass on
         return out, lse
-    cfg = _cache_config(q_heads, kv_heads, dim, DTYPES[dtype], blocks, window, left_window, 0, 0,
-                        scale, strides[:3], (stride_q, 8, 8))
-    al = make_align(block_table, num_computed, block_size, request_indices)
-    st = load_library().kda_window_attention(
-        ctypes.byref(cfg), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(cu_seqlens), B,
-        ctypes.byref(al), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
-        _ptr(error_word), _stream_ptr(dev))
-    _check("kda_window_attention", st)
+    cfg = _cache_config(q_heads, kv_heads, dim, code, blocks, window, left_window, 0, 0, scale,
+                        sb, st, sh, stride_q, 8, 8)
+    status = load_library().kda_window_attention(
+        cfg, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), cu_seqlens.data_ptr(), B,
+        ctypes.byref(align), workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+        lse.data_ptr(), _ptr(error_word), _raw_stream(dev))
+    if status:
+        raise KDAError("kda_window_attention", status)
     return out, lse
 
 
@@ -911,10 +952,10 @@ class TokenLogprobs(NamedTuple):
 
 def allocate_token_logprobs(rows: int, num_top: int, device) -> TokenLogprobs:
     """Output buffers of ``kda_token_logprobs``."""
-    f32 = dict(dtype=torch.float32, device=device)
-    one = torch.empty((3, rows), **f32)
-    return TokenLogprobs(one[0], one[1], one[2], torch.empty((rows, num_top), **f32),
-                         torch.empty((rows, num_top), dtype=torch.int32, device=device))
+    def one(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device=device)
+    return TokenLogprobs(one(rows), one(rows), one(rows), one(rows, num_top),
+                         one(rows, num_top, dtype=torch.int32))
 
 
 def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs | None = None,
@@ -923,28 +964,39 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
     negative: none, 0), entropy, log sum of exponentials and the ``num_top``
     largest logits (ties: the lower index) of each row of ``logits`` [rows,
     vocab], bf16, fp16 or fp32 with any row stride."""
-    dev = logits.device
-    if logits.dtype not in DTYPES:
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    code = DTYPES.get(logits.dtype)
+    if code is None:
         raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
-    if logits.dim() != 2 or logits.stride(1) != 1:
-        raise ValueError("logits must be [rows, vocab] with contiguous columns")
+    if tokens.dtype is not i32 or tokens.device != dev:
+        _mismatch(dev, tokens=(tokens, i32))
+    if error_word is not None:
+        _req(error_word, i32, "error_word", dev)
+        _at_least(error_word, 1, "error_word")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
     rows, vocab = logits.shape
-    _req(tokens, torch.int32, "tokens", dev)
-    _opt(error_word, torch.int32, "error_word", dev)
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits must have contiguous columns")
     if tokens.dim() != 1 or tokens.shape[0] != rows or not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous with one entry per row")
-    _at_least(error_word, 1, "error_word")
     if out is None:
-        out = allocate_token_logprobs(rows, num_top, dev)
+        out = TokenLogprobs(torch.empty_like(tokens, dtype=f32),
+                            torch.empty_like(tokens, dtype=f32),
+                            torch.empty_like(tokens, dtype=f32),
+                            tokens.new_empty((rows, num_top), dtype=f32),
+                            tokens.new_empty((rows, num_top)))
     else:
         for name, t in zip(TokenLogprobs._fields, out):
-            _req(t, torch.int32 if name == "top_index" else torch.float32, name, dev)
+            _req(t, i32 if name == "top_index" else f32, name, dev)
             want = (rows, num_top) if name.startswith("top_") else (rows,)
             if tuple(t.shape) != want or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {want} tensor")
-    st = load_library().kda_token_logprobs(
-        _ptr(logits), DTYPES[logits.dtype], logits.stride(0), rows, vocab, _ptr(tokens), num_top,
-        _ptr(out.logprob), _ptr(out.entropy), _ptr(out.lse), _ptr(out.top_logprob),
-        _ptr(out.top_index), _ptr(error_word), _stream_ptr(dev))
-    _check("kda_token_logprobs", st)
+    status = load_library().kda_token_logprobs(
+        logits.data_ptr(), code, stride, rows, vocab, tokens.data_ptr(), num_top,
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+        out[4].data_ptr(), _ptr(error_word), _raw_stream(dev))
+    if status:
+        raise KDAError("kda_token_logprobs", status)
     return out

@@ -5,15 +5,19 @@
 // Mathematics.  Pair i of a head at position p turns by the angle p * f_i.
 // Only the angle modulo a full turn counts, so the phase is kept in turns:
 // u_i = (f_i / 2 pi mod 1) * 2^64 as a whole number, and p * u_i mod 2^64 is
-// the fraction of a turn exactly; the rounding of u_i (an fp64 value, 2^-53
-// of it) is all that grows with p, as it does for an angle formed in fp64.
-// Its top 32 bits, signed, give the angle in [-pi, pi) for sincospif.
+// the fraction of a turn exactly; the rounding of u_i, 2^-63 of it, is all
+// that grows with p.  Its top 32 bits, signed, give the angle in [-pi, pi)
+// for sincospif.  u_i is made from f_i's bits in whole numbers too: with fp64
+// arithmetic, some 2 lanes a clock on an SM here, 256 tokens took 6.4 us and
+// not 4.8.
 //
 // Every value is read and written once and the arithmetic is 3 flops per
 // rotated channel, so HBM bounds the large calls and latency the small ones.
-// A warp takes part of one token: a lane moves units of 16 channels of a
-// head (two 16-byte chunks: the two halves of its 8 pairs), and the sines and
-// cosines are made once per warp, in shared memory, for all heads it takes.
+// A warp takes part of one token: a lane moves units of 16 channels of a head
+// (two 16-byte chunks: the two halves of its 8 pairs).  Where a unit lies
+// does not depend on the row, so a warp's first unit is loaded before the
+// row's metadata is read and the sines are made (once per warp, in shared
+// memory), and each later unit before the one ahead of it is written.
 #include "kda_cache.cuh"
 
 namespace {
@@ -23,6 +27,7 @@ using kda_cache::Rows;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 64;
+constexpr int kCtasPerSm = 5;   // 48 registers a thread
 
 struct Params {
     Rows rows;
@@ -35,7 +40,7 @@ struct Params {
     int pairs;        // rotary_dim / 2
     int interleaved;
     int parts;        // warps that share a token
-    int rounds;       // rounds of 32 units each of them takes
+    int rounds;       // rounds of 32 units (one a lane) each of them takes
 };
 
 __device__ __forceinline__ float2 to_float2(uint32_t u, __nv_bfloat16) {
@@ -73,6 +78,21 @@ __device__ __forceinline__ int find_row(const int *cu, int B, int t, int lane) {
     }
 }
 
+// f / 2 pi modulo 1 as a 64-bit fraction of a turn: with f = M 2^(e - 63),
+// 2^63 <= M < 2^64, and C = 2^66 / 2 pi, it is f / 2 pi 2^64 =
+// (M C / 2^64) 2^(e - 1).
+__device__ __forceinline__ unsigned long long turns_per_position(double f) {
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
+    const int e = (int)((bits >> 52) & 0x7ff) - 1023;
+    if (e == -1023) return 0;  // 0, or too small to turn anything
+    const unsigned long long m = (bits << 11) | 0x8000000000000000ull;
+    const unsigned long long h = __umul64hi(m, 0xa2f9836e4e44152aull);
+    const int right = 1 - e;
+    const unsigned long long u =
+        right >= 64 || right <= -64 ? 0 : right >= 0 ? h >> right : h << -right;
+    return (bits >> 63) != 0 ? 0 - u : u;
+}
+
 // 8 pairs of one head: chunk a and chunk b hold them as halves (a[e], b[e])
 // or side by side (a[2e], a[2e+1], then b).
 template <typename T>
@@ -98,8 +118,15 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, b
     b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+// Where the two chunks of a head's unit j start: the same pairs in both
+// halves, or 16 channels side by side.
+__device__ __forceinline__ int2 chunks_of(const Params &p, bool turned, int j) {
+    return turned && !p.interleaved ? make_int2(j * 8, p.pairs + j * 8)
+                                    : make_int2(j * 16, j * 16 + 8);
+}
+
 template <typename T, int kDim>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(const Params p) {
     constexpr int kUnits = kDim / 16;  // units of a head
     __shared__ float2 turns[kWarps][kMaxPairs];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -108,6 +135,27 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
     const long long item = (long long)blockIdx.x * kWarps + warp;
     const int t = (int)(item / p.parts), part = (int)(item % p.parts);
     if (t >= p.num_tokens) return;
+    const int first_k = p.q_heads, first_v = p.q_heads + p.kv_heads;
+    const int begin = part * p.rounds * 32;
+    const int end = min((first_v + p.kv_heads) * kUnits, begin + p.rounds * 32);
+
+    auto load = [&](int u, uint4 &x, uint4 &y) {
+        if (u >= end) return;
+        const int head = u / kUnits, j = u % kUnits;
+        const T *src;
+        if (head < first_k)
+            src = reinterpret_cast<const T *>(p.q) + t * p.stride_q + head * kDim;
+        else if (head < first_v)
+            src = reinterpret_cast<const T *>(p.k) + t * p.stride_k + (head - first_k) * kDim;
+        else
+            src = reinterpret_cast<const T *>(p.v) + t * p.stride_v + (head - first_v) * kDim;
+        const int2 at = chunks_of(p, head < first_v && j * 8 < p.pairs, j);
+        x = *reinterpret_cast<const uint4 *>(src + at.x);
+        y = *reinterpret_cast<const uint4 *>(src + at.y);
+    };
+    uint4 x[2], y[2];
+    load(begin + lane, x[0], y[0]);
+
     const int b = find_row(p.rows.cu_seqlens, p.rows.B, t, lane);
     if (b < 0) return;
     int bits = 0;
@@ -122,10 +170,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
         block = 0;
     }
     for (int i = lane; i < p.pairs; i += 32) {
-        const double turn = p.inv_freq[i] * 0.15915494309189533577;  // 1 / 2 pi
-        const unsigned long long u =
-            __double2ull_rz((turn - floor(turn)) * 18446744073709551616.0);
-        const int phase = (int)((u * (unsigned long long)pos) >> 32);
+        const int phase =
+            (int)((turns_per_position(p.inv_freq[i]) * (unsigned long long)pos) >> 32);
         float2 cs;
         sincospif((float)phase * 0x1p-31f, &cs.y, &cs.x);
         turns[warp][i] = cs;
@@ -133,34 +179,30 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params p) {
     __syncwarp();
     const long long slot = (long long)max(block, 0) * p.stride_block +
                            (long long)(pos - col * p.rows.block_size) * p.stride_token;
-    const int first_k = p.q_heads, first_v = p.q_heads + p.kv_heads;
-    const int units = (first_v + p.kv_heads) * kUnits;
-    const int begin = part * p.rounds * 32, end = min(units, begin + p.rounds * 32);
-#pragma unroll 2
-    for (int u = begin + lane; u < end; u += 32) {
+
+    auto store = [&](int u, uint4 &x, uint4 &y) {
+        if (u >= end) return;
         const int head = u / kUnits, j = u % kUnits;
-        const T *src;
         T *dst;
-        if (head < first_k) {
-            src = reinterpret_cast<const T *>(p.q) + t * p.stride_q + head * kDim;
+        if (head < first_k)
             dst = reinterpret_cast<T *>(p.q_out) + ((long long)t * p.q_heads + head) * kDim;
-        } else if (head < first_v) {
-            src = reinterpret_cast<const T *>(p.k) + t * p.stride_k + (head - first_k) * kDim;
+        else if (head < first_v)
             dst = reinterpret_cast<T *>(p.key_cache) + slot + (head - first_k) * p.stride_head;
-        } else {
-            src = reinterpret_cast<const T *>(p.v) + t * p.stride_v + (head - first_v) * kDim;
+        else
             dst = reinterpret_cast<T *>(p.value_cache) + slot + (head - first_v) * p.stride_head;
-        }
         const bool turned = head < first_v && j * 8 < p.pairs;
-        const int at = turned && !p.interleaved ? j * 8 : j * 16;
-        const int other = turned && !p.interleaved ? p.pairs + j * 8 : j * 16 + 8;
-        uint4 x = *reinterpret_cast<const uint4 *>(src + at);
-        uint4 y = *reinterpret_cast<const uint4 *>(src + other);
+        const int2 at = chunks_of(p, turned, j);
         if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
         if (head < first_k || block > 0) {
-            *reinterpret_cast<uint4 *>(dst + at) = x;
-            *reinterpret_cast<uint4 *>(dst + other) = y;
+            *reinterpret_cast<uint4 *>(dst + at.x) = x;
+            *reinterpret_cast<uint4 *>(dst + at.y) = y;
         }
+    };
+    for (int u = begin + lane; u < end; u += 64) {
+        load(u + 32, x[1], y[1]);
+        store(u, x[0], y[0]);
+        load(u + 64, x[0], y[0]);
+        store(u + 32, x[1], y[1]);
     }
 }
 
@@ -213,7 +255,15 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     p.interleaved = cfg->interleaved;
     const int rounds =
         ((p.q_heads + 2 * p.kv_heads) * (cfg->head_dim / 16) + 31) / 32;  // of a whole token
-    p.rounds = 1;
+    // A warp that takes a whole token makes its sines once and keeps its loads
+    // ahead of its stores, one that takes a round of it leaves more warps for
+    // few tokens.  Measured (us, a round | a token of 10 or 12): 256 tokens
+    // 4.9 | 7.2, 16k tokens 77 | 54.  So rounds grow once two full sets of
+    // resident warps have one each.
+    const long long most = (long long)kda_cache::sm_count() * kCtasPerSm * kWarps * 2;
+    if (most <= 0) return KDA_ERR_CUDA;
+    const long long wanted = (long long)num_tokens * rounds / most;
+    p.rounds = wanted < 1 ? 1 : wanted > rounds ? rounds : (int)wanted;
     p.parts = (rounds + p.rounds - 1) / p.rounds;
     const long long items = (long long)num_tokens * p.parts;
     const long long grid = (items + kWarps - 1) / kWarps;

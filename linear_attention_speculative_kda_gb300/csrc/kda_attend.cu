@@ -822,17 +822,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
 
 // ------------------------------------------------------------------- host --
 
-int sm_count() {
-    static int cache[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) cache[dev] = n;
-    return n;
-}
-
 template <typename T, int kDim, int kMT, int kMW>
 kda_status launch_attend(const Params &p, int grid, void *stream) {
     using L = Layout<kDim, kMT, kMW>;
@@ -897,7 +886,7 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
         return KDA_ERR_INVALID_ARG;
     if (!(cfg->scale == cfg->scale) || cfg->scale - cfg->scale != 0.0f) return KDA_ERR_INVALID_ARG;
     if (workspace_bytes < kda_attention_workspace_bytes(cfg, B)) return KDA_ERR_INVALID_ARG;
-    const int sms = sm_count();
+    const int sms = kda_cache::sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     p.q = static_cast<const char *>(q);
     p.key_cache = static_cast<const char *>(key_cache);

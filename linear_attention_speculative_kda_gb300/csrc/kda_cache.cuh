@@ -133,6 +133,17 @@ inline kda_status set_rows(const kda_cache_config *c, const kda_align *al, const
     return KDA_OK;
 }
 
+inline int sm_count() {
+    static int cache[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) cache[dev] = n;
+    return n;
+}
+
 // Launch with programmatic dependent launch: the kernel may start its set-up
 // while the one before it in the stream drains; it waits for it
 // (grid_dependency_wait) before it touches memory.
