@@ -10,19 +10,31 @@
 // result, only how often O is rescaled.
 //
 // Work split.  The unit is a tile of 64 keys of one (row, kv head); all tiles
-// of the call, in row, head, key order, are cut into equal runs, one per CTA,
-// two CTAs per SM.  Each CTA finds its run from the rows' lengths by itself.
-// A run may cut a (row, head) segment: the pieces leave (m, l, O) in fp32 in
-// the workspace, and a second, short kernel joins them in a fixed order.
+// of the call, in row, head, key order, are cut into equal runs, one per CTA
+// of the two or three that fit an SM.  Each CTA finds its run from the rows'
+// lengths by itself.  A run may cut a (row, head) segment: the pieces leave
+// (m, l, O) in fp32 in the workspace, and a second, short kernel joins them in
+// a fixed order.
 //
-// A CTA has 4 warps in groups of kMW.  A group's warps hold different query
-// rows (16 * kMT each) of the same keys; the 4 / kMW groups take different
-// keys of each tile.  Keys and values arrive by 16-byte cp.async in a ring of
-// tiles, each warp loading its own 16 keys, so with kMW = 1 no warp waits for
-// another inside a segment.  The products are mma.sync m16n8k16 on fragments
-// that ldmatrix reads from XOR-swizzled rows.
+// Two forms.  HBM bounds both where there are keys to read (each once: 256
+// bytes of 64 channels' K and V a key and head, 512 of 128).
+//
+// - attend_kernel, for up to 32 query rows (64 at 64 channels): 4 warps in
+//   groups of kMW.  A group's warps hold different query rows (16 * kMT each)
+//   of the same keys; the 4 / kMW groups take different keys of each tile.
+//   Keys and values arrive by 16-byte cp.async in a ring of tiles, each warp
+//   loading its own 16 keys, so with kMW = 1 no warp waits for another inside
+//   a segment.  The products are mma.sync m16n8k16 on fragments that ldmatrix
+//   reads from XOR-swizzled rows.  64 requests of 4 tokens over up to 8192
+//   keys, 16 rows: 192 us, 92% of the measured HBM rate.
+// - tc::attend_tc_kernel, for more: tcgen05.mma with S and O in tensor memory
+//   and tensor-map TMA loads (below).  128 requests of 8 tokens over up to
+//   12000 keys, 64 rows: 595 us, 89% (762 with the first form).
+#include <cuda.h>
+
 #include "kda_async.cuh"
 #include "kda_cache.cuh"
+#include "kda_tc.cuh"
 
 namespace {
 
@@ -33,7 +45,6 @@ using kda_cache::Rows;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 64;             // keys of a tile
-constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 512;         // bound of the grid, for the workspace
 constexpr float kLazy = 8.0f;         // log2 of the growth a stale maximum may have
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -51,11 +62,15 @@ struct Params {
     const char *q, *key_cache, *value_cache;
     char *out;
     float *lse;
-    float *partials;         // [2 * grid][R_max * (D + 2)]
+    float *partials;         // [2 * grid][slot_size]
     Cut *cuts;               // [grid]
     long long stride_q, stride_block, stride_token, stride_head;  // elements
     int q_heads, kv_heads, group, window, left_window, most_rows;
-    float scale_log2;
+    int by_group;            // 2^16 / group, rounded up
+    int box;                 // tokens of a tensor-map box
+    long long slot_size;     // floats of a partial slot: O, the maxima, the sums
+    float scale_log2;        // |scale| log2 e
+    uint32_t flip;           // sign bits of a pair of queries when scale < 0
 };
 
 // ------------------------------------------------------------ instructions --
@@ -151,9 +166,10 @@ __device__ __forceinline__ void group_sync(int group) {
 
 // The tiles a row's keys span: [first, end).
 __device__ __forceinline__ void row_tiles(const Params &p, const Row &row, int &first, int &end) {
-    const int lo = p.left_window > 0 ? max(0, row.computed + 1 - p.left_window) : 0;
-    first = lo / kTile;
-    end = row.tokens > 0 ? (row.computed + row.tokens - 1) / kTile + 1 : first;
+    first = end = 0;
+    if (row.tokens == 0) return;
+    first = p.left_window > 0 ? max(0, row.computed + 1 - p.left_window) / kTile : 0;
+    end = (row.computed + row.tokens - 1) / kTile + 1;
 }
 
 __device__ __forceinline__ int tile_count(const Params &p, int b, int &bits) {
@@ -206,12 +222,17 @@ __device__ __forceinline__ int cta_of(long long units, int ctas, long long u) {
 // Every CTA adds up the rows' tiles itself: thread i takes a run of rows, a
 // scan over the threads gives the units before it, and the thread whose rows
 // hold the CTA's first unit finds the row.
-__device__ __forceinline__ Run plan(const Params &p) {
-    __shared__ long long sums[kWarps];
-    __shared__ long long found_before;
-    __shared__ int found_row;
+struct PlanScratch {
+    long long sums[8];
+    long long before;
+    int row;
+};
+
+template <int kWarpCount>
+__device__ __forceinline__ Run plan(const Params &p, PlanScratch &sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.rows.B + kThreads - 1) / kThreads;
+    constexpr int kCount = 32 * kWarpCount;
+    const int per = (p.rows.B + kCount - 1) / kCount;
     const int b0 = min(p.rows.B, tid * per), b1 = min(p.rows.B, b0 + per);
     long long mine = 0;
     int bits = 0;
@@ -223,13 +244,13 @@ __device__ __forceinline__ Run plan(const Params &p) {
         const long long other = __shfl_up_sync(kFull, upto, o);
         if (lane >= o) upto += other;
     }
-    if (lane == 31) sums[warp] = upto;
+    if (lane == 31) sc.sums[warp] = upto;
     __syncthreads();
     long long before = upto - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
+    for (int w = 0; w < kWarpCount; ++w) {
+        if (w < warp) before += sc.sums[w];
+        total += sc.sums[w];
     }
     Run run;
     run.units = total * p.kv_heads;
@@ -246,18 +267,53 @@ __device__ __forceinline__ Run plan(const Params &p) {
             if (at < before + n) break;
             before += n;
         }
-        found_row = b;
-        found_before = before * p.kv_heads;
+        sc.row = b;
+        sc.before = before * p.kv_heads;
     }
     __syncthreads();
-    run.row = found_row;
-    run.before_row = found_before;
+    run.row = sc.row;
+    run.before_row = sc.before;
     return run;
 }
 
+// Where the CTA's run begins.
+__device__ __forceinline__ Cursor run_start(const Params &p, const Run &run) {
+    Cursor at;
+    at.head = 0;
+    at.set_row(p, run.row);
+    const long long in_row = run.begin - run.before_row;
+    const int n = at.end - at.first;
+    at.head = (int)(in_row / n);
+    at.tile = at.first + (int)(in_row % n);
+    return at;
+}
+
+// The join's work item of a CTA whose run starts at `at`: the segment that is
+// first cut there, if there is one.
+__device__ __forceinline__ Cut first_cut(const Run &run, const Cursor &at, int cta) {
+    Cut cut = {};
+    const int n = at.end - at.first;
+    const long long s = run.before_row + (long long)at.head * n;
+    if (s < run.begin) {
+        const int i0 = cta_of(run.units, run.ctas, s);
+        if (i0 == cta - 1) {
+            cut.pieces = cta_of(run.units, run.ctas, s + n - 1) - i0 + 1;
+            cut.first_slot = 2 * i0 + (run_begin(run.units, run.ctas, i0) < s ? 1 : 0);
+            cut.first_token = at.row.first;
+            cut.tokens = at.row.tokens;
+            cut.head = at.head;
+        }
+    }
+    return cut;
+}
+
+// Row r of a segment's queries is query head r % group of token r / group
+// (r < 128, group <= 128: the product with 2^16 / group, rounded up, is exact).
+__device__ __forceinline__ int token_of(const Params &p, int r) { return (r * p.by_group) >> 16; }
+
 // ---------------------------------------------------------------- layout --
 
-template <int kDim, int kMT, int kMW>
+template <int kDim, int kMT, int kMW, int kCtas>
 struct Layout {
     static constexpr int kRows = 16 * kMT * kMW;       // query rows, padded
     static constexpr int kGroups = kWarps / kMW;
@@ -272,7 +328,8 @@ struct Layout {
     static constexpr int kShared = kQuery > kSum ? kQuery : kSum;
     static constexpr int kStats = kGroups * kRows * 8;
     static constexpr int kFixed = kShared + kStats;
-    static constexpr int kBudget = 114000;             // two CTAs per SM
+    // the SM's 228 KB, less 1 KB a CTA that the system takes and the static part
+    static constexpr int kBudget = 233472 / kCtas - 1024 - 1280;
     static constexpr int kStages = (kBudget - kFixed) / kStage < 6 ? (kBudget - kFixed) / kStage : 6;
     static constexpr int kBytes = kFixed + kStages * kStage;
     static_assert(kStages >= 2, "the ring needs two tiles");
@@ -286,9 +343,9 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
 
 // ---------------------------------------------------------------- kernel --
 
-template <typename T, int kDim, int kMT, int kMW>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Params p) {
-    using L = Layout<kDim, kMT, kMW>;
+template <typename T, int kDim, int kMT, int kMW, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p) {
+    using L = Layout<kDim, kMT, kMW, kCtas>;
     constexpr int kNB = L::kKeys / 16;      // blocks of 16 keys in a group's step
     constexpr int kDT = kDim / 8;           // 8-channel tiles of O
     constexpr int kChunks = kDim / 8;       // 16-byte chunks of a cache row
@@ -306,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
 
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
-    const Run run = plan(p);
+    __shared__ PlanScratch plan_scratch;
+    const Run run = plan<kWarps>(p, plan_scratch);
     const int cta = blockIdx.x;
     if (cta >= run.ctas) {
         if (tid == 0) p.cuts[cta].pieces = 0;
@@ -314,35 +372,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
     }
 
     // cursor of the tile to compute and of the tile to load
-    Cursor at;
-    at.head = 0;
-    at.set_row(p, run.row);
-    {
-        const long long in_row = run.begin - run.before_row;
-        const int n = at.end - at.first;
-        at.head = (int)(in_row / n);
-        at.tile = at.first + (int)(in_row % n);
-    }
+    Cursor at = run_start(p, run);
     Cursor ld = at;
     long long left = run.end - run.begin;       // tiles to compute
     long long to_load = left;
 
-    if (tid == 0) {  // the join's work item: a segment first cut where this run begins
-        Cut cut = {};
-        const int n = at.end - at.first;
-        const long long s = run.before_row + (long long)at.head * n;
-        if (s < run.begin) {
-            const int i0 = cta_of(run.units, run.ctas, s);
-            if (i0 == cta - 1) {
-                cut.pieces = cta_of(run.units, run.ctas, s + n - 1) - i0 + 1;
-                cut.first_slot = 2 * i0 + (run_begin(run.units, run.ctas, i0) < s ? 1 : 0);
-                cut.first_token = at.row.first;
-                cut.tokens = at.row.tokens;
-                cut.head = at.head;
-            }
-        }
-        p.cuts[cta] = cut;
-    }
+    if (tid == 0) p.cuts[cta] = first_cut(run, at, cta);
 
     // Load one tile into ring slot `slot`: this warp's 16 keys and values.
     // Lane l looks up key l mod 16; the address goes to the loading lanes by
@@ -392,17 +427,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
         const bool whole = at.tile == at.first && tiles == at.end - at.first;
         const int partial_slot = 2 * cta + (piece_first ? 0 : 1);
         const int rows = at.row.tokens * p.group;
+        const bool busy = mwarp * 16 * kMT < rows;  // whether this warp has query rows
         // queries to shared memory (rows past the last one: zeros)
-        for (int i = tid; i < L::kRows * kChunks; i += kThreads) {
-            const int r = i / kChunks, c = i % kChunks;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int t = r / p.group, h = at.head * p.group + r % p.group;
-                x = *reinterpret_cast<const uint4 *>(
-                    reinterpret_cast<const T *>(p.q) + (at.row.first + t) * p.stride_q +
-                    (long long)h * kDim + c * 8);
+        // (a batch's loads are in flight together: one after the other they
+        // took most of the 10 us that 64 rows cost beside their tiles)
+        constexpr int kEach = L::kRows * kChunks / kThreads, kBatch = kEach < 8 ? kEach : 8;
+#pragma unroll 1
+        for (int n0 = 0; n0 < kEach; n0 += kBatch) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                const int i = (n0 + n) * kThreads + tid, r = i / kChunks;
+                x[n] = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int t = token_of(p, r), h = at.head * p.group + r - t * p.group;
+                    x[n] = __ldg(reinterpret_cast<const uint4 *>(
+                        reinterpret_cast<const T *>(p.q) + (at.row.first + t) * p.stride_q +
+                        (long long)h * kDim + i % kChunks * 8));
+                }
             }
-            *reinterpret_cast<uint4 *>(shared_area + swizzled<kDim>(r, c)) = x;
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                const int i = (n0 + n) * kThreads + tid;
+                *reinterpret_cast<uint4 *>(shared_area + swizzled<kDim>(i / kChunks, i % kChunks)) =
+                    make_uint4(x[n].x ^ p.flip, x[n].y ^ p.flip, x[n].z ^ p.flip, x[n].w ^ p.flip);
+            }
         }
         __syncthreads();
         const uint32_t q_addr = kda::smem_u32(shared_area);
@@ -422,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = (mwarp * kMT + a) * 16 + qr + 8 * h;
-                hi[a][h] = at.row.computed + min(r / p.group, at.row.tokens - 1);
+                hi[a][h] = at.row.computed + min(token_of(p, r), at.row.tokens - 1);
                 lo[a][h] = p.left_window > 0 ? hi[a][h] - p.left_window : -1;
                 m[a][h] = -INFINITY;
                 l[a][h] = 0.0f;
@@ -447,6 +496,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
             for (int w = 0; w < kMW; ++w)
                 seen |= (unsigned long long)there[slot][group * kMW + w] << (16 * w);
 
+            // a step that some row does not see whole: at the window's own
+            // keys, at a sliding window's start, at null blocks
+            constexpr unsigned long long kAll = kNB == 4 ? ~0ull : (1ull << (16 * kNB % 64)) - 1;
+            const bool edge =
+                key0 + L::kKeys - 1 > at.row.computed || seen != kAll ||
+                (p.left_window > 0 && key0 <= at.row.computed + at.row.tokens - 1 - p.left_window);
             float s[kMT][2 * kNB][4];
 #pragma unroll
             for (int a = 0; a < kMT; ++a)
@@ -454,118 +509,124 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
                 for (int n = 0; n < 2 * kNB; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[a][n][e] = 0.0f;
+            if (busy) {
 #pragma unroll
-            for (int k = 0; k < kDim / 16; ++k) {
-                uint32_t af[kMT][4];
-#pragma unroll
-                for (int a = 0; a < kMT; ++a) {
-                    if constexpr (kMT == 1) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) af[a][e] = qf[k][e];
-                    } else {
-                        ldmatrix4(af[a], q_addr + swizzled<kDim>(q_row + 16 * a,
-                                                                 2 * k + (lane >> 4)));
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < kNB; ++n) {
-                    uint32_t bf[4];
-                    ldmatrix4(bf, k_addr + swizzled<kDim>(16 * n + ((lane >> 4) << 3) + (lane & 7),
-                                                          2 * k + ((lane >> 3) & 1)));
+                for (int k = 0; k < kDim / 16; ++k) {
+                    uint32_t af[kMT][4];
 #pragma unroll
                     for (int a = 0; a < kMT; ++a) {
-                        mma(s[a][2 * n], af[a], bf[0], bf[1], T());
-                        mma(s[a][2 * n + 1], af[a], bf[2], bf[3], T());
+                        if constexpr (kMT == 1) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) af[a][e] = qf[k][e];
+                        } else {
+                            ldmatrix4(af[a], q_addr + swizzled<kDim>(q_row + 16 * a,
+                                                                     2 * k + (lane >> 4)));
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < kNB; ++n) {
+                        uint32_t bf[4];
+                        ldmatrix4(bf, k_addr + swizzled<kDim>(16 * n + ((lane >> 4) << 3) + (lane & 7),
+                                                              2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int a = 0; a < kMT; ++a) {
+                            mma(s[a][2 * n], af[a], bf[0], bf[1], T());
+                            mma(s[a][2 * n + 1], af[a], bf[2], bf[3], T());
+                        }
                     }
                 }
-            }
-#pragma unroll
-            for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                for (int n = 0; n < 2 * kNB; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[a][n][e] *= p.scale_log2;
-
-            // a step that some row does not see whole: at the window's own
-            // keys, at a sliding window's start, at null blocks
-            constexpr unsigned long long kAll = kNB == 4 ? ~0ull : (1ull << (16 * kNB % 64)) - 1;
-            const bool edge =
-                key0 + L::kKeys - 1 > at.row.computed || seen != kAll ||
-                (p.left_window > 0 && key0 <= at.row.computed + at.row.tokens - 1 - p.left_window);
-            if (edge) {
 #pragma unroll
                 for (int a = 0; a < kMT; ++a)
 #pragma unroll
                     for (int n = 0; n < 2 * kNB; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 8 * n + 2 * qc + (e & 1);
-                            const int pos = key0 + j;
-                            if (!((seen >> j) & 1ull) || pos > hi[a][e >> 1] ||
-                                pos <= lo[a][e >> 1])
-                                s[a][n][e] = -INFINITY;
-                        }
-            }
+                        for (int e = 0; e < 4; ++e) s[a][n][e] *= p.scale_log2;
 
-            // running maximum; O is rescaled only when it grew past the slack
-            float top[kMT][2];
-            bool grew = false;
+                if (edge) {
 #pragma unroll
-            for (int a = 0; a < kMT; ++a)
+                    for (int a = 0; a < kMT; ++a)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x = -INFINITY;
+                        for (int n = 0; n < 2 * kNB; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2 * kNB; ++n)
-                        x = fmaxf(x, fmaxf(s[a][n][2 * h], s[a][n][2 * h + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
-                    top[a][h] = x;
-                    grew |= x > m[a][h] + kLazy;
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = 8 * n + 2 * qc + (e & 1);
+                                const int pos = key0 + j;
+                                if (!((seen >> j) & 1ull) || pos > hi[a][e >> 1] ||
+                                    pos <= lo[a][e >> 1])
+                                    s[a][n][e] = -INFINITY;
+                            }
                 }
-            if (__any_sync(kFull, grew)) {
+
+                // running maximum; O is rescaled only when it grew past the slack
+                float top[kMT][2];
+                bool grew = false;
 #pragma unroll
                 for (int a = 0; a < kMT; ++a)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float now = fmaxf(m[a][h], top[a][h]);
-                        const float f = now == -INFINITY ? 1.0f : exp2_fast(m[a][h] - now);
-                        m[a][h] = now;
-                        l[a][h] *= f;
+                        float x = -INFINITY;
 #pragma unroll
-                        for (int d = 0; d < kDT; ++d) {
-                            o[a][d][2 * h] *= f;
-                            o[a][d][2 * h + 1] *= f;
+                        for (int n = 0; n < 2 * kNB; ++n)
+                            x = fmaxf(x, fmaxf(s[a][n][2 * h], s[a][n][2 * h + 1]));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+                        top[a][h] = x;
+                        grew |= x > m[a][h] + kLazy;
+                    }
+                if (__any_sync(kFull, grew)) {
+#pragma unroll
+                    for (int a = 0; a < kMT; ++a)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float now = fmaxf(m[a][h], top[a][h]);
+                            const float f = now == -INFINITY ? 1.0f : exp2_fast(m[a][h] - now);
+                            m[a][h] = now;
+                            l[a][h] *= f;
+#pragma unroll
+                            for (int d = 0; d < kDT; ++d) {
+                                o[a][d][2 * h] *= f;
+                                o[a][d][2 * h + 1] *= f;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int a = 0; a < kMT; ++a)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float base = m[a][h] == -INFINITY ? 0.0f : m[a][h];
+#pragma unroll
+                        for (int n = 0; n < 2 * kNB; ++n) {
+                            s[a][n][2 * h] = exp2_fast(s[a][n][2 * h] - base);
+                            s[a][n][2 * h + 1] = exp2_fast(s[a][n][2 * h + 1] - base);
+                            l[a][h] += s[a][n][2 * h] + s[a][n][2 * h + 1];
                         }
                     }
+
             }
-#pragma unroll
-            for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float base = m[a][h] == -INFINITY ? 0.0f : m[a][h];
-#pragma unroll
-                    for (int n = 0; n < 2 * kNB; ++n) {
-                        s[a][n][2 * h] = exp2_fast(s[a][n][2 * h] - base);
-                        s[a][n][2 * h + 1] = exp2_fast(s[a][n][2 * h + 1] - base);
-                        l[a][h] += s[a][n][2 * h] + s[a][n][2 * h + 1];
-                    }
-                }
 
             // A value that is not finite must not reach the rows that do not
             // see its key (0 * inf is NaN in the product): where rows see
             // different keys, such values are added by hand to the rows that
             // do and zeroed for the product.
-            if (edge) {
+            // (That can only be the window's own keys but the first, and as
+            // many at a sliding window's start.)
+            if (edge && at.row.tokens > 1) {
+                const int own = at.row.tokens - 1;
                 unsigned long long odd = 0;
-                for (int i = lane; i < L::kKeys * kChunks; i += 32) {
+                for (int i = lane; i < (p.left_window > 0 ? 2 : 1) * own * kChunks; i += 32) {
+                    const int k = i / kChunks;
+                    const int key = (k < own ? at.row.computed + 1 + k
+                                             : at.row.computed + 1 - p.left_window + k - own) -
+                                    key0;
+                    if (key < 0 || key >= L::kKeys) continue;
                     uint4 x;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                 : "r"(v_addr + swizzled<kDim>(i / kChunks, i % kChunks)));
+                                 : "r"(v_addr + swizzled<kDim>(key, i % kChunks))
+                                 : "memory");
                     if (not_finite(x.x, T()) || not_finite(x.y, T()) || not_finite(x.z, T()) ||
                         not_finite(x.w, T()))
-                        odd |= 1ull << (i / kChunks);
+                        odd |= 1ull << key;
                 }
                 odd = (unsigned long long)__reduce_or_sync(kFull, (uint32_t)odd) |
                       (unsigned long long)__reduce_or_sync(kFull, (uint32_t)(odd >> 32)) << 32;
@@ -594,11 +655,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
                                                  : "r"(v_addr + swizzled<kDim>(8 * n + j, d) +
                                                        4 * qc));
                                     const float2 x = unpack(u, T());
-                                    if (see0) {
+                                    if (busy && see0) {
                                         o[a][d][0] = fmaf(p0, x.x, o[a][d][0]);
                                         o[a][d][1] = fmaf(p0, x.y, o[a][d][1]);
                                     }
-                                    if (see1) {
+                                    if (busy && see1) {
                                         o[a][d][2] = fmaf(p1, x.x, o[a][d][2]);
                                         o[a][d][3] = fmaf(p1, x.y, o[a][d][3]);
                                     }
@@ -617,25 +678,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
                 }
             }
 
+            if (busy) {
 #pragma unroll
-            for (int n = 0; n < kNB; ++n) {
-                uint32_t pf[kMT][4];
-#pragma unroll
-                for (int a = 0; a < kMT; ++a) {
-                    pf[a][0] = pack(s[a][2 * n][0], s[a][2 * n][1], T());
-                    pf[a][1] = pack(s[a][2 * n][2], s[a][2 * n][3], T());
-                    pf[a][2] = pack(s[a][2 * n + 1][0], s[a][2 * n + 1][1], T());
-                    pf[a][3] = pack(s[a][2 * n + 1][2], s[a][2 * n + 1][3], T());
-                }
-#pragma unroll
-                for (int d = 0; d < kDim / 16; ++d) {
-                    uint32_t bf[4];
-                    ldmatrix4_trans(bf, v_addr + swizzled<kDim>(16 * n + (lane & 15),
-                                                                2 * d + (lane >> 4)));
+                for (int n = 0; n < kNB; ++n) {
+                    uint32_t pf[kMT][4];
 #pragma unroll
                     for (int a = 0; a < kMT; ++a) {
-                        mma(o[a][2 * d], pf[a], bf[0], bf[1], T());
-                        mma(o[a][2 * d + 1], pf[a], bf[2], bf[3], T());
+                        pf[a][0] = pack(s[a][2 * n][0], s[a][2 * n][1], T());
+                        pf[a][1] = pack(s[a][2 * n][2], s[a][2 * n][3], T());
+                        pf[a][2] = pack(s[a][2 * n + 1][0], s[a][2 * n + 1][1], T());
+                        pf[a][3] = pack(s[a][2 * n + 1][2], s[a][2 * n + 1][3], T());
+                    }
+#pragma unroll
+                    for (int d = 0; d < kDim / 16; ++d) {
+                        uint32_t bf[4];
+                        ldmatrix4_trans(bf, v_addr + swizzled<kDim>(16 * n + (lane & 15),
+                                                                    2 * d + (lane >> 4)));
+#pragma unroll
+                        for (int a = 0; a < kMT; ++a) {
+                            mma(o[a][2 * d], pf[a], bf[0], bf[1], T());
+                            mma(o[a][2 * d + 1], pf[a], bf[2], bf[3], T());
+                        }
                     }
                 }
             }
@@ -726,8 +789,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
                     const int r = (mwarp * kMT + a) * 16 + qr + 8 * h;
                     if (r >= rows) continue;
                     if (whole) {
-                        const long long row = (long long)(at.row.first + r / p.group) * p.q_heads +
-                                              at.head * p.group + r % p.group;
+                        const int t = token_of(p, r);
+                        const long long row = (long long)(at.row.first + t) * p.q_heads +
+                                              at.head * p.group + r - t * p.group;
                         const float f = l[a][h] == 0.0f ? 0.0f : 1.0f / l[a][h];
                         uint32_t *dst = reinterpret_cast<uint32_t *>(p.out) + row * (kDim / 2) + qc;
 #pragma unroll
@@ -736,8 +800,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
                         if (p.lse != nullptr && qc == 0)
                             p.lse[row] = (m[a][h] + log2f(l[a][h])) * kLn2;
                     } else {
-                        float *part =
-                            p.partials + (long long)partial_slot * p.most_rows * (kDim + 2);
+                        float *part = p.partials + partial_slot * p.slot_size;
                         float2 *dst = reinterpret_cast<float2 *>(part + r * kDim) + qc;
 #pragma unroll
                         for (int d = 0; d < kDT; ++d)
@@ -756,92 +819,935 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Para
     cp_async_wait<0>();
 }
 
+
+// ------------------------------------------------------- tensor-core form --
+//
+// For more query rows: S = Q K^T and O += P V on the 5th-generation tensor
+// cores, with 128 query rows (unused ones zero), S and O in tensor memory and
+// P written over its S as the second product's A operand.  Two warps load
+// keys and values (ring stages of 64 rows, keys and values in turn), a thread
+// of one warp issues the products S and a thread of another O (one thread for
+// both spent 1500 of a tile's 1950 clocks on issuing at 64 channels), four
+// warps do the softmax, a thread or two per query row.  S of the next tile is
+// made while the softmax of this one runs; two CTAs on an SM fill each
+// other's gaps.
+//
+// Shared memory: rows of 128 bytes (64 channels) with the 128-byte swizzle,
+// channel block after channel block.  The same rows are a K-major operand
+// for S (queries and keys) and an MN-major one for O (values).
+namespace tc {
+
+constexpr int kSoftmaxWarps = 4;
+constexpr int kLoadWarp = kSoftmaxWarps, kScoreWarp = kLoadWarp + 1;
+constexpr int kOutWarp = kScoreWarp + 1, kQueryWarp = kOutWarp + 1;
+constexpr int kWarpCount = kQueryWarp + 1;
+constexpr int kThreadCount = 32 * kWarpCount;
+constexpr int kRows = 128;
+constexpr int kCtasPerSm = 2;
+constexpr int kTmemColumns = 256;                 // two CTAs per SM share 512
+constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
+
+template <int kDim, int kQRows>
+struct Form {
+    static constexpr int kBlocks = kDim / 64;                 // channel blocks of 128 bytes
+    static constexpr int kQuery = kBlocks * kQRows * 128;
+    static constexpr int kStage = kBlocks * kTile * 128;      // 64 keys, or their values
+    static constexpr int kStages = kDim == 64 ? 10 : kQRows == 64 ? 6 : 5;
+    static constexpr int kControl = 512;
+    static constexpr int kBytes = kQuery + kStages * kStage + kControl;
+    static constexpr int kS = 128;                            // column of the first S; O at 0
+    // Stage 0 lies before the queries, the others behind them: with 64 query
+    // rows the products read the 8 KB to either side of a block of them.
+    __device__ static __forceinline__ uint32_t stage(uint32_t smem, int i) {
+        return smem + i * kStage + (i > 0 ? kQuery : 0);
+    }
+    __device__ static __forceinline__ uint32_t query(uint32_t smem) { return smem + kStage; }
+};
+
+// The query rows' first lane.  Up to 64 rows take the softmax warps 0 and 1,
+// or 2 and 3 in the second half of the grid, so that the two CTAs of an SM,
+// which come from the two halves, share out its four schedulers and their
+// exponentials (4 lanes a clock each): 1.48 us a tile and SM, not 1.54.  The
+// products take what lies there for the other 64 rows; nothing reads what
+// they make of it.
+template <int kQRows>
+__device__ __forceinline__ int first_lane() {
+    return kQRows == 64 && blockIdx.x >= gridDim.x / 2 ? 64 : 0;
+}
+
+struct Control {
+    PlanScratch plan;
+    uint64_t full[10], empty[10];   // ring stages
+    uint64_t s_full[2], p_full[2];  // S in tensor memory, P over it
+    uint64_t o_done[2];             // the product of P with V is complete
+    uint64_t q_full, q_empty;       // a segment's queries are in shared memory, are done with
+    uint64_t meet;                  // the softmax warps' own barrier
+    uint64_t drained[2];
+    uint32_t there[8][2];           // keys of a tile that are in the cache
+    int keep[2];                    // O was started by hand: add to it
+    int abort;
+    uint32_t tmem;
+};
+
+// Bounded wait: gives up after the budget, or when another warp has.
+__device__ __forceinline__ bool wait(Control &c, uint64_t *bar, uint32_t parity, int *err) {
+    if (kda::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!kda::mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile int *>(&c.abort) != 0) return false;
+        if (clock64() - t0 > kWaitBudget) {
+            *reinterpret_cast<volatile int *>(&c.abort) = 1;
+            kda_cache::flag(err, KDA_ERR_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for a whole warp: every lane gets the same answer, converged.
+__device__ __forceinline__ bool warp_wait(Control &c, uint64_t *bar, uint32_t parity, int *err) {
+    return __all_sync(kFull, wait(c, bar, parity, err));
+}
+
+// 4-D tensor-map load of one box: 64 channels, some tokens, one head, one block.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap *map, int channel,
+                                             int token, int head, int block, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(channel), "r"(token), "r"(head), "r"(block),
+        "r"(kda::smem_u32(bar))
+        : "memory");
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulation, A and B of type T,
+// A K-major, B K-major or MN-major.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc(int m, int n, bool b_mn) {
+    const uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u;
+    return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// MN-major operand with the 128-byte swizzle: 64-element blocks along MN
+// `block` bytes apart, 8-row groups along K 1024 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(block >> 4) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(add)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(add)
+        : "memory");
+}
+
+// The registers of a tensor-memory load are there only after its wait; this
+// keeps the compiler from using them before it (a wait names no register).
+__device__ __forceinline__ void landed(uint32_t (&u)[16]) {
+    asm volatile(""
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
+                   "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]),
+                   "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&u)[16]) {
+    kda::tmem_ld16(addr, u);
+    kda::tmem_wait_ld();
+    landed(u);
+}
+
+__device__ __forceinline__ uint32_t tmem_load1(uint32_t addr) {
+    uint32_t u;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                 : "=r"(u)
+                 : "r"(addr)
+                 : "memory");
+    kda::tmem_wait_ld();
+    asm volatile("" : "+r"(u) : : "memory");
+    return u;
+}
+
+__device__ __forceinline__ void store16(uint32_t addr, uint4 x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y),
+                 "r"(x.z), "r"(x.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 load16(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+
+// Byte offset of 16-byte chunk c (of a row's kDim / 8) of row r, with `rows`
+// rows in a channel block.
+__device__ __forceinline__ uint32_t place(int r, int c, int rows) {
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Multiplies the warp's rows of O (kDim columns at `o`) by each thread's f.
+template <int kDim>
+__device__ __forceinline__ void scale_o(uint32_t o, float f) {
+#pragma unroll
+    for (int c = 0; c < kDim; c += 16) {
+        uint32_t u[16];
+        tmem_load16(o + c, u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+        kda::tmem_st16(o + c, u);
+    }
+    kda::tmem_wait_st();
+}
+
+// ---- the loading warp -----------------------------------------------------
+//
+// A box is p.box keys, the greatest common divisor of the block size and the
+// tile, so a tile is kTile / p.box boxes of each channel block, each inside
+// one block of the cache.  A lane fetches the table entry of a box's block a
+// tile ahead and asks for the box.  The null block and boxes past the row's
+// end are boxes past the tensor's last block, which arrive as zeros.
+
+template <typename T, int kDim, int kQRows>
+__device__ __forceinline__ void run_loader(const Params &p, const Run &run, Control &c,
+                                           uint32_t smem, int lane, const CUtensorMap *k_map,
+                                           const CUtensorMap *v_map) {
+    using F = Form<kDim, kQRows>;
+    Cursor at = run_start(p, run);
+    const long long tiles = run.end - run.begin;
+    const int boxes = kTile / p.box, mine = lane % boxes;
+    const int channel_block = lane / boxes;
+    int pos = 0, block = 0;
+    auto look_up = [&]() {
+        pos = at.tile * kTile + mine * p.box;
+        block = 0;
+        if (pos < at.row.computed + at.row.tokens)
+            block = p.rows.block_table[at.row.request * p.rows.bt_stride +
+                                       kda_cache::divide(pos, p.rows.by_block)];
+    };
+    look_up();
+    int stage = 0;
+    uint32_t phase = 1;  // of the stage's empty barrier; the first use waits for nothing
+    long long loaded = 0;
+    bool ok = true;
+    for (long long g = 0; ok && g < tiles; ++g) {
+        if (block >= p.rows.num_blocks) {
+            kda_cache::flag(p.rows.err, KDA_ROW_BAD_SLOT);
+            block = 0;
+        }
+        const int token = pos - kda_cache::divide(pos, p.rows.by_block) * p.rows.block_size;
+        const int from = block > 0 ? block : p.rows.num_blocks;
+        const int head = at.head;
+        const unsigned there = __ballot_sync(kFull, block > 0);
+        if (lane == 0) {
+            unsigned long long keys = 0;
+            for (int i = 0; i < boxes; ++i)
+                if ((there >> i) & 1u)
+                    keys |= (p.box == 64 ? ~0ull : (1ull << p.box) - 1) << (i * p.box);
+            c.there[g & 7][0] = (uint32_t)keys;
+            c.there[g & 7][1] = (uint32_t)(keys >> 32);
+        }
+        if (g + 1 < tiles) {
+            if (++at.tile == at.end) at.next_segment(p);
+            look_up();
+        }
+        for (int half = 0; half < 2; ++half) {
+            ok = warp_wait(c, &c.empty[stage], phase, p.rows.err);
+            if (!ok) break;
+            if (lane == 0) kda::mbar_arrive_expect_tx(&c.full[stage], F::kStage);
+            __syncwarp();
+            if (channel_block < F::kBlocks)
+                tma_load_box(F::stage(smem, stage) + channel_block * kTile * 128 +
+                                 mine * p.box * 128,
+                             half == 0 ? k_map : v_map, channel_block * 64, token, head, from,
+                             &c.full[stage]);
+            ++loaded;
+            if (++stage == F::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (!ok) {  // another wait ran out: no copy may outlive the CTA
+        for (long long j = loaded > F::kStages ? loaded - F::kStages : 0; j < loaded; ++j)
+            kda::mbar_wait_bounded(&c.full[j % F::kStages], (uint32_t)((j / F::kStages) & 1),
+                                   kWaitBudget);
+        __syncwarp();
+    }
+}
+
+// ---- the query warp -------------------------------------------------------
+//
+// Copies each segment's queries to shared memory as soon as the segment
+// before has its last S.
+
+template <typename T, int kDim, int kQRows>
+__device__ __forceinline__ void run_queries(const Params &p, const Run &run, Control &c,
+                                            uint32_t smem, int lane) {
+    constexpr int kChunks = kDim / 8;
+    const uint32_t query = Form<kDim, kQRows>::query(smem);
+    Cursor at = run_start(p, run);
+    long long left = run.end - run.begin;
+    for (uint32_t segment = 0;; ++segment) {
+        if (!warp_wait(c, &c.q_empty, (segment & 1u) ^ 1u, p.rows.err)) break;
+        const int rows = at.row.tokens * p.group;
+        // the rows that make up whole warps of the softmax: zeros past the last
+        for (int i = lane; i < (rows + 31) / 32 * 32 * kChunks; i += 32) {
+            const int r = i / kChunks, ch = i % kChunks;
+            const int t = token_of(p, r), h = at.head * p.group + r - t * p.group;
+            const T *src = reinterpret_cast<const T *>(p.q);
+            if (r < rows) src += (at.row.first + t) * p.stride_q + (long long)h * kDim + ch * 8;
+            cp_async16_or_zero(query + place(r, ch, kQRows), src, r < rows);
+        }
+        kda::cp_async_commit();
+        cp_async_wait<0>();
+        kda::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) kda::mbar_arrive(&c.q_full);
+        left -= min(left, (long long)(at.end - at.tile));
+        if (left == 0) break;
+        at.next_segment(p);
+    }
+}
+
+// ---- the issuing threads --------------------------------------------------
+//
+// Neither relies on the order in which the tensor cores take up products of
+// different shape: each waits until what it overwrites has been read.
+
+// Nothing a thread issued may outlive the CTA's shared and tensor memory.
+__device__ __forceinline__ void drain(uint64_t *bar) {
+    kda::umma_commit(bar);
+    kda::mbar_wait_bounded(bar, 0, kWaitBudget);
+}
+
+// S = Q K^T of every tile.
+template <typename T, int kDim, int kQRows>
+__device__ __forceinline__ void run_scores(const Params &p, const Run &run, Control &c,
+                                           uint32_t smem, uint32_t tmem) {
+    using F = Form<kDim, kQRows>;
+    constexpr uint32_t kId = idesc<T>(kRows, kTile, false);
+    Cursor at = run_start(p, run);
+    const long long tiles = run.end - run.begin;
+    const uint64_t q_desc = kda::sw128_desc(F::query(smem) - first_lane<kQRows>() * 128);
+    uint32_t phase = 0;
+    int stage = 0;
+    uint32_t segment = 0;
+    for (long long g = 0; g < tiles; ++g) {
+        if (g == 0 || at.tile == at.first) {
+            if (!wait(c, &c.q_full, segment & 1u, p.rows.err)) break;
+            ++segment;
+        }
+        // it goes where P(g - 2) was: that product has to be complete
+        if (g >= 2 && !wait(c, &c.o_done[g & 1], (uint32_t)((g / 2 - 1) & 1), p.rows.err)) break;
+        if (!wait(c, &c.full[stage], phase, p.rows.err)) break;
+        kda::tc_fence_after();
+        const uint64_t k_desc = kda::sw128_desc(F::stage(smem, stage));
+        const uint32_t s = tmem + F::kS + (uint32_t)(g & 1) * kTile;
+#pragma unroll
+        for (int k = 0; k < kDim / 16; ++k)
+            mma_ss(s, q_desc + (((k >> 2) * kQRows * 128 + (k & 3) * 32) >> 4),
+                   k_desc + (((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4), kId, k > 0);
+        kda::umma_commit(&c.s_full[g & 1]);
+        kda::umma_commit(&c.empty[stage]);
+        if (g + 1 == tiles || at.tile + 1 == at.end) kda::umma_commit(&c.q_empty);
+        stage += 2;
+        if (stage >= F::kStages) {
+            stage -= F::kStages;
+            phase ^= 1u;
+        }
+        if (g + 1 < tiles && ++at.tile == at.end) at.next_segment(p);
+    }
+    drain(&c.drained[0]);
+}
+
+// O += P V of every tile.
+template <typename T, int kDim, int kQRows>
+__device__ __forceinline__ void run_outputs(const Params &p, const Run &run, Control &c,
+                                            uint32_t smem, uint32_t tmem) {
+    using F = Form<kDim, kQRows>;
+    constexpr uint32_t kId = idesc<T>(kRows, kDim, true);
+    Cursor at = run_start(p, run);
+    p.cuts[blockIdx.x] = first_cut(run, at, blockIdx.x);
+    const long long tiles = run.end - run.begin;
+    uint32_t phase = 0;
+    int stage = 1;
+    bool first = true;   // the segment's first tile
+    for (long long g = 0; g < tiles; ++g) {
+        const int b = (int)(g & 1);
+        if (!wait(c, &c.p_full[b], (uint32_t)((g >> 1) & 1), p.rows.err)) break;
+        if (!wait(c, &c.full[stage], phase, p.rows.err)) break;
+        kda::tc_fence_after();
+        uint32_t add = first ? 0u : 1u;
+        volatile int *keep = &c.keep[b];
+        if (*keep != 0) {
+            add = 1;
+            *keep = 0;
+        }
+        const uint64_t v_desc = mn_desc(F::stage(smem, stage), kTile * 128);
+        const uint32_t pp = tmem + F::kS + (uint32_t)b * kTile;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tmem, pp + 8 * k, v_desc + (k * 2048 >> 4), kId, k > 0 ? 1u : add);
+        kda::umma_commit(&c.o_done[b]);
+        kda::umma_commit(&c.empty[stage]);
+        stage += 2;
+        if (stage >= F::kStages) {
+            stage -= F::kStages;
+            phase ^= 1u;
+        }
+        first = false;
+        if (g + 1 < tiles && ++at.tile == at.end) {
+            at.next_segment(p);
+            first = true;
+        }
+    }
+    drain(&c.drained[1]);
+}
+
+// ---- the softmax warps ----------------------------------------------------
+
+template <typename T, int kDim, int kQRows>
+__device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Control &c,
+                                            uint32_t smem, uint32_t tmem_all, int cta, int warp,
+                                            int lane) {
+    using F = Form<kDim, kQRows>;
+    constexpr int kChunks = kDim / 8;
+    const int tid = warp * 32 + lane;
+    const int row = tid - first_lane<kQRows>();                           // query row of this thread
+    const uint32_t tmem = tmem_all + ((uint32_t)(warp * 32) << 16);  // the warp's lanes
+    const float scale = p.flip != 0 ? -p.scale_log2 : p.scale_log2;
+    Cursor at = run_start(p, run);
+    long long left = run.end - run.begin, g = 0;
+    bool run_first = true;
+    uint32_t meetings = 0;
+    auto meet = [&]() -> bool {  // a barrier of the four warps
+        __syncwarp();
+        if (lane == 0) kda::mbar_arrive(&c.meet);
+        return warp_wait(c, &c.meet, meetings++ & 1u, p.rows.err);
+    };
+    auto product_done = [&]() -> bool {  // of the tile before tile g
+        return warp_wait(c, &c.o_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1), p.rows.err);
+    };
+    while (left > 0) {
+        const int tiles = (int)min(left, (long long)(at.end - at.tile));
+        const bool whole = at.tile == at.first && tiles == at.end - at.first;
+        const int rows = at.row.tokens * p.group;
+        const bool active = row - lane >= 0 && row - lane < rows;
+        const bool mine = row >= 0 && row < rows;
+        const int token = token_of(p, max(row, 0));
+        const int hi = at.row.computed + min(token, at.row.tokens - 1);
+        const int lo = p.left_window > 0 ? hi - p.left_window : -1;
+        float m = -INFINITY, l = 0.0f;
+        for (int done = 0; done < tiles; ++done, ++g) {
+            const int b = (int)(g & 1);
+            const uint32_t s_col = tmem + F::kS + b * kTile;
+            if (!warp_wait(c, &c.s_full[b], (uint32_t)((g >> 1) & 1), p.rows.err)) return;
+            kda::tc_fence_after();
+            const int key0 = (at.tile + done) * kTile;
+            const unsigned long long seen =
+                (unsigned long long)*reinterpret_cast<volatile uint32_t *>(&c.there[g & 7][0]) |
+                (unsigned long long)*reinterpret_cast<volatile uint32_t *>(&c.there[g & 7][1]) << 32;
+            // a tile that some row does not see whole
+            const bool edge =
+                key0 + kTile - 1 > at.row.computed || seen != ~0ull ||
+                (p.left_window > 0 &&
+                 key0 <= at.row.computed + at.row.tokens - 1 - p.left_window);
+            if (active) {
+                float s[kTile];
+                {
+                    uint32_t u[kTile / 16][16];
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i) kda::tmem_ld16(s_col + 16 * i, u[i]);
+                    kda::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i) {
+                        landed(u[i]);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[16 * i + e] = __uint_as_float(u[i][e]);
+                    }
+                }
+                // scores as they are times mul: where all of a tile counts and
+                // the scale is positive, the factor is part of the exponent
+                float mul = scale;
+                if (edge || p.flip != 0) {
+                    mul = 1.0f;
+                    // the row's keys of the tile: up to hi, past lo, in the cache
+                    const int upto = hi - key0 + 1, from = lo - key0 + 1;
+                    unsigned long long own = upto >= 64  ? ~0ull
+                                             : upto > 0 ? (1ull << upto) - 1
+                                                        : 0ull;
+                    own &= from >= 64 ? 0ull : from > 0 ? ~0ull << from : ~0ull;
+                    own &= seen;
+                    const uint32_t half[2] = {(uint32_t)own, (uint32_t)(own >> 32)};
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i)
+                        s[i] = (half[i / 32] >> (i % 32)) & 1u ? s[i] * scale : -INFINITY;
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
+                if (__any_sync(kFull, most > m + kLazy)) {
+                    const float now = fmaxf(m, most);
+                    const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
+                    if (done > 0) {
+                        if (!product_done()) return;
+                        kda::tc_fence_after();
+                        scale_o<kDim>(tmem, f);
+                    }
+                    m = now;
+                    l *= f;
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x = exp2_fast(fmaf(s[i + e], mul, -base));
+                        const float y = exp2_fast(fmaf(s[i + e + 1], mul, -base));
+                        sum[e & 2] += x;
+                        sum[(e & 2) + 1] += y;
+                        u[e / 2] = pack(x, y, T());
+                    }
+                    kda::tmem_st16(s_col + i / 2, u);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                kda::tmem_wait_st();
+            }
+            // A value that is not finite must not reach the rows that do not
+            // see its key (0 * inf is NaN in the product).  What lies past the
+            // row's end is zeroed; of the row's own keys only those matter that
+            // some rows see and others do not: the window's own but the first,
+            // and as many at a sliding window's start.
+            const int tail = at.row.computed + at.row.tokens - key0;  // first key past the row
+            if (edge && (at.row.tokens > 1 || tail < kTile)) {
+                const int j = (int)((2 * g + 1) % F::kStages);
+                if (!warp_wait(c, &c.full[j], (uint32_t)(((2 * g + 1) / F::kStages) & 1),
+                               p.rows.err))
+                    return;
+                const uint32_t values = F::stage(smem, j);
+                for (int i = max(tail, 0) * kChunks + tid; i < kTile * kChunks;
+                     i += 32 * kSoftmaxWarps)
+                    store16(values + place(i / kChunks, i % kChunks, kTile), make_uint4(0, 0, 0, 0));
+                kda::fence_proxy_async_smem();
+                const int own = at.row.tokens - 1;
+                unsigned long long odd = 0;
+                for (int i = lane; i < (p.left_window > 0 ? 2 : 1) * own * kChunks; i += 32) {
+                    const int k = i / kChunks;
+                    const int key = (k < own ? at.row.computed + 1 + k
+                                             : at.row.computed + 1 - p.left_window + k - own) -
+                                    key0;
+                    if (key < 0 || key >= kTile) continue;
+                    const uint4 x = load16(values + place(key, i % kChunks, kTile));
+                    if (not_finite(x.x, T()) || not_finite(x.y, T()) || not_finite(x.z, T()) ||
+                        not_finite(x.w, T()))
+                        odd |= 1ull << key;
+                }
+                odd = (unsigned long long)__reduce_or_sync(kFull, (uint32_t)odd) |
+                      (unsigned long long)__reduce_or_sync(kFull, (uint32_t)(odd >> 32)) << 32;
+                if (odd != 0) {  // the same for the four warps
+                    if (active) {
+                        // such values are added by hand to the rows that do
+                        // see them, and zeroed for the product
+                        if (done > 0) {
+                            if (!product_done()) return;
+                            kda::tc_fence_after();
+                        } else {
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) zero[e] = 0;
+#pragma unroll
+                            for (int d = 0; d < kDim; d += 16) kda::tmem_st16(tmem + d, zero);
+                            kda::tmem_wait_st();
+                            *reinterpret_cast<volatile int *>(&c.keep[b]) = 1;
+                        }
+                        for (unsigned long long bits = odd; bits != 0; bits &= bits - 1) {
+                            const int key = __ffsll((long long)bits) - 1;
+                            const float2 both = unpack(tmem_load1(s_col + key / 2), T());
+                            const float weight = (key & 1) ? both.y : both.x;
+                            const bool sees = key0 + key <= hi && key0 + key > lo;
+#pragma unroll 1
+                            for (int d = 0; d < kDim; d += 16) {
+                                uint32_t u[16];
+                                tmem_load16(tmem + d, u);
+#pragma unroll
+                                for (int e = 0; e < 16; e += 8) {
+                                    const uint4 x =
+                                        load16(values + place(key, (d + e) / 8, kTile));
+                                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                    for (int n = 0; n < 4; ++n) {
+                                        const float2 v = unpack(w[n], T());
+                                        float *a = reinterpret_cast<float *>(&u[e + 2 * n]);
+                                        if (sees) {
+                                            a[0] = fmaf(weight, v.x, a[0]);
+                                            a[1] = fmaf(weight, v.y, a[1]);
+                                        }
+                                    }
+                                }
+                                __syncwarp();
+                                kda::tmem_st16(tmem + d, u);
+                                kda::tmem_wait_st();
+                            }
+                        }
+                    }
+                    if (!meet()) return;  // every warp has read them
+                    for (int i = tid; i < kTile * kChunks; i += 32 * kSoftmaxWarps)
+                        if ((odd >> (i / kChunks)) & 1ull)
+                            store16(values + place(i / kChunks, i % kChunks, kTile),
+                                    make_uint4(0, 0, 0, 0));
+                    kda::fence_proxy_async_smem();
+                }
+            }
+            // A warp sees every product's phase, one after the other: had it
+            // skipped one, a later wait could take the parity of the phase
+            // before for its own.  (The next product cannot start before this
+            // one is complete, so nothing is lost here.)
+            if (g > 0 && !product_done()) return;
+            kda::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) kda::mbar_arrive(&c.p_full[b]);
+        }
+
+        // the segment's place in the results, then on to the next one while
+        // this one's last product is made
+        const long long out_row = (long long)(at.row.first + token) * p.q_heads +
+                                  at.head * p.group + row - token * p.group;
+        float *piece = p.partials + (2ll * cta + (run_first ? 0 : 1)) * p.slot_size;
+        left -= tiles;
+        run_first = false;
+        if (left > 0) at.next_segment(p);
+        if (!product_done()) return;
+        kda::tc_fence_after();
+        if (active) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int d0 = 0; d0 < kDim; d0 += 32) {
+                uint32_t u[2][16];
+                kda::tmem_ld16(tmem + d0, u[0]);
+                kda::tmem_ld16(tmem + d0 + 16, u[1]);
+                kda::tmem_wait_ld();
+                landed(u[0]);
+                landed(u[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int d = d0 + 16 * i;
+                    if (mine && whole) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack(__uint_as_float(u[i][2 * e]) * inv,
+                                        __uint_as_float(u[i][2 * e + 1]) * inv, T());
+                        uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.out) +
+                                                               out_row * kDim + d);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (mine) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(piece + row * kDim + d);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            dst[e / 4] = make_uint4(u[i][e], u[i][e + 1], u[i][e + 2], u[i][e + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (mine) {
+            if (!whole) {
+                piece[p.most_rows * kDim + row] = m;
+                piece[p.most_rows * (kDim + 1) + row] = l;
+            } else if (p.lse != nullptr) {
+                p.lse[out_row] = (m + log2f(l)) * kLn2;
+            }
+        }
+        kda::tc_fence_before();
+    }
+}
+
+template <typename T, int kDim, int kQRows>
+__global__ void __launch_bounds__(kThreadCount, kCtasPerSm)
+    attend_tc_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+    using F = Form<kDim, kQRows>;
+    extern __shared__ __align__(1024) unsigned char smem_tc[];
+    Control &c = *reinterpret_cast<Control *>(smem_tc + F::kQuery + F::kStages * F::kStage);
+    static_assert(sizeof(Control) <= F::kControl, "control area");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t smem = kda::smem_u32(smem_tc);
+    kda_cache::grid_dependents_launch();
+    if (tid == 0) {
+        for (int i = 0; i < F::kStages; ++i) {
+            kda::mbar_init(&c.full[i], 1);
+            kda::mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            kda::mbar_init(&c.s_full[i], 1);
+            kda::mbar_init(&c.p_full[i], kSoftmaxWarps);
+            kda::mbar_init(&c.o_done[i], 1);
+            c.keep[i] = 0;
+        }
+        kda::mbar_init(&c.q_full, 1);
+        kda::mbar_init(&c.q_empty, 1);
+        kda::mbar_init(&c.meet, kSoftmaxWarps);
+        kda::mbar_init(&c.drained[0], 1);
+        kda::mbar_init(&c.drained[1], 1);
+        c.abort = 0;
+        kda::fence_mbar_init();
+    }
+    if (warp == kScoreWarp) kda::tmem_alloc(&c.tmem, kTmemColumns);
+    kda_cache::grid_dependency_wait();
+    const Run run = plan<kWarpCount>(p, c.plan);
+    const int cta = blockIdx.x;
+    const bool busy = cta < run.ctas;
+    if (!busy && tid == 0) p.cuts[cta].pieces = 0;
+    kda::tc_fence_before();
+    __syncthreads();
+    kda::tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    if (busy) {
+        if (warp < kSoftmaxWarps) {
+            run_softmax<T, kDim, kQRows>(p, run, c, smem, tmem, cta, warp, lane);
+        } else if (warp == kLoadWarp) {
+            run_loader<T, kDim, kQRows>(p, run, c, smem, lane, &k_map, &v_map);
+        } else if (warp == kQueryWarp) {
+            run_queries<T, kDim, kQRows>(p, run, c, smem, lane);
+        } else if (lane == 0) {
+            if (warp == kScoreWarp)
+                run_scores<T, kDim, kQRows>(p, run, c, smem, tmem);
+            else
+                run_outputs<T, kDim, kQRows>(p, run, c, smem, tmem);
+        }
+        __syncwarp();
+    }
+    kda::tc_fence_before();
+    __syncthreads();
+    kda::tc_fence_after();
+    if (warp == kScoreWarp) kda::tmem_dealloc(tmem, kTmemColumns);
+}
+
+}  // namespace tc
+
 // Joins the pieces of the segments that runs cut: block (i, y) takes the
-// segment first cut at the start of CTA i's run and its query rows y, y +
-// gridDim.y, ...; a warp adds every fourth piece, then the warps' sums are
-// added in order.
+// segment first cut at the start of CTA i + 1's run, a warp its query rows
+// 4 y + warp, then 4 gridDim.y on.  The pieces' maxima and sums are read one a
+// lane, their O in batches of kBatch loads, the first batch in flight with
+// them.
+constexpr int kJoinRows = 8;   // blocks a cut, at most
+
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
-    constexpr int kVec = kDim / 32;
-    __shared__ float sum[kWarps][kDim];
-    __shared__ float sum_l[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kLanes = kDim / 4;           // lanes that hold a row
+    constexpr int kSide = 32 / kLanes;         // pieces a warp reads side by side
+    constexpr int kBatch = 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
     const int cta = blockIdx.x + 1;
-    const Cut cut = p.cuts[cta];
-    if (cut.pieces == 0) return;
-    const int rows = cut.tokens * p.group;
-    const long long slot_size = (long long)p.most_rows * (kDim + 2);
-    const float *first = p.partials + cut.first_slot * slot_size;
-    const float *others = p.partials + 2 * (cta - 1) * slot_size;  // piece i > 0 at 2 i slots on
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        float m = -INFINITY;
-        for (int i = lane; i < cut.pieces; i += 32) {
-            const float *part = i == 0 ? first : others + 2 * i * slot_size;
-            m = fmaxf(m, __ldcg(part + p.most_rows * kDim + r));
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-        const float base = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, o[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
-#pragma unroll 4
-        for (int i = warp; i < cut.pieces; i += kWarps) {
-            const float *part = i == 0 ? first : others + 2 * i * slot_size;
-            const float f = exp2_fast(__ldcg(part + p.most_rows * kDim + r) - base);
-            l = fmaf(f, __ldcg(part + p.most_rows * (kDim + 1) + r), l);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                o[e] = fmaf(f, __ldcg(part + r * kDim + lane * kVec + e), o[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum[warp][lane * kVec + e] = o[e];
-        if (lane == 0) sum_l[warp] = l;
-        __syncthreads();
-        float total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) total += sum_l[w];
-        const float f = total == 0.0f ? 0.0f : 1.0f / total;
-        const long long row = (long long)(cut.first_token + r / p.group) * p.q_heads +
-                              cut.head * p.group + r % p.group;
-        if (tid < kDim / 2) {
-            float x = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                x += sum[w][2 * tid];
-                y += sum[w][2 * tid + 1];
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(&p.cuts[cta]));
+    const int kv_head = __ldcg(&p.cuts[cta].head);
+    const int pieces = head.x, tokens = head.w;
+    if (pieces == 0) return;
+    const float *first = p.partials + head.y * p.slot_size;
+    const float *others = p.partials + 2 * (cta - 1) * p.slot_size;  // piece i > 0: 2 i slots on
+    auto piece = [&](int i) { return i == 0 ? first : others + 2 * i * p.slot_size; };
+    for (int r = blockIdx.y * kWarps + warp; r < tokens * p.group; r += gridDim.y * kWarps) {
+        float m = -INFINITY, l = 0.0f;  // of the pieces so far, in every lane and per lane
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            const int here = min(32, pieces - i0);
+            float own_m = -INFINITY, own_l = 0.0f;
+            if (lane < here) {
+                const float *part = piece(i0 + lane);
+                own_m = __ldcg(part + p.most_rows * kDim + r);
+                own_l = __ldcg(part + p.most_rows * (kDim + 1) + r);
             }
-            reinterpret_cast<uint32_t *>(p.out)[row * (kDim / 2) + tid] = pack(x * f, y * f, T());
+            float weight = 0.0f;
+            for (int k = 0; k < here; k += kBatch * kSide) {
+                float4 x[kBatch];
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) {
+                    const int i = k + n * kSide + lane / kLanes;
+                    x[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < here)
+                        x[n] = __ldcg(reinterpret_cast<const float4 *>(
+                            piece(i0 + i) + r * kDim + lane % kLanes * 4));
+                }
+                if (k == 0) {  // the weights of these 32 pieces
+                    float top = own_m;
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+                    top = fmaxf(top, m);
+                    const float base = top == -INFINITY ? 0.0f : top;
+                    const float f = exp2_fast(m - base);
+                    l *= f;
+                    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                    weight = exp2_fast(own_m - base);
+                    l = fmaf(weight, own_l, l);
+                    m = top;
+                }
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) {
+                    const float w =
+                        __shfl_sync(kFull, weight, min(31, k + n * kSide + lane / kLanes));
+                    o.x = fmaf(w, x[n].x, o.x);
+                    o.y = fmaf(w, x[n].y, o.y);
+                    o.z = fmaf(w, x[n].z, o.z);
+                    o.w = fmaf(w, x[n].w, o.w);
+                }
+            }
         }
-        if (tid == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(total)) * kLn2;
-        __syncthreads();
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(kFull, l, s);
+        if constexpr (kSide == 2) {
+            o.x += __shfl_xor_sync(kFull, o.x, 16);
+            o.y += __shfl_xor_sync(kFull, o.y, 16);
+            o.z += __shfl_xor_sync(kFull, o.z, 16);
+            o.w += __shfl_xor_sync(kFull, o.w, 16);
+        }
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        const int t = token_of(p, r);
+        const long long row =
+            (long long)(head.z + t) * p.q_heads + kv_head * p.group + r - t * p.group;
+        if (lane < kLanes)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(p.out) + row * kDim + lane * 4) =
+                make_uint2(pack(o.x * f, o.y * f, T()), pack(o.z * f, o.w * f, T()));
+        if (lane == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(l)) * kLn2;
     }
+}
+
+template <typename T, int kDim>
+kda_status launch_join(const Params &p, int grid, void *stream) {
+    void (*join)(const Params) = join_kernel<T, kDim>;
+    const int blocks = min(kJoinRows, (p.most_rows + kWarps - 1) / kWarps);
+    return kda_cache::launch(join, dim3(grid - 1, blocks), dim3(kThreads), 0, 1, stream, p);
 }
 
 // ------------------------------------------------------------------- host --
 
-template <typename T, int kDim, int kMT, int kMW>
-kda_status launch_attend(const Params &p, int grid, void *stream) {
-    using L = Layout<kDim, kMT, kMW>;
-    void (*kernel)(const Params) = attend_kernel<T, kDim, kMT, kMW>;
+template <typename T, int kDim, int kMT, int kMW, int kCtas>
+kda_status launch_attend(const Params &p, int sms, void *stream) {
+    using L = Layout<kDim, kMT, kMW, kCtas>;
+    const int grid = min(kCtas * sms, kMaxCtas);
+    void (*kernel)(const Params) = attend_kernel<T, kDim, kMT, kMW, kCtas>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
         cudaSuccess)
         return KDA_ERR_CUDA;
     kda_status st = kda_cache::launch(kernel, dim3(grid), dim3(kThreads), L::kBytes, 1, stream, p);
     if (st != KDA_OK || grid == 1) return st;
-    void (*join)(const Params) = join_kernel<T, kDim>;
-    return kda_cache::launch(join, dim3(grid - 1, min(p.most_rows, 16)), dim3(kThreads), 0, 1,
-                             stream, p);
+    return launch_join<T, kDim>(p, grid, stream);
+}
+
+// The driver's tensor-map encoder, looked up once through the runtime (the
+// library links no driver library).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+
+// A cache as [block][head][token][channel], read in boxes of 64 channels of
+// p.box tokens with the 128-byte swizzle.  False when it cannot be described.
+template <typename T, int kDim>
+bool cache_map(const Params &p, const char *base, CUtensorMap *map) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)kDim, (cuuint64_t)p.rows.block_size,
+                                (cuuint64_t)p.kv_heads, (cuuint64_t)p.rows.num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.stride_token * 2, (cuuint64_t)p.stride_head * 2,
+                                   (cuuint64_t)p.stride_block * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map,
+                  sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, const_cast<char *>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  kDim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                              : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int kDim, int kQRows>
+kda_status launch_tc(const Params &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int sms,
+                     void *stream) {
+    const int grid = min(tc::kCtasPerSm * sms, kMaxCtas);
+    using F = tc::Form<kDim, kQRows>;
+    void (*kernel)(const Params, const CUtensorMap, const CUtensorMap) =
+        tc::attend_tc_kernel<T, kDim, kQRows>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes) !=
+        cudaSuccess)
+        return KDA_ERR_CUDA;
+    kda_status st = kda_cache::launch(kernel, dim3(grid), dim3(tc::kThreadCount), F::kBytes, 1,
+                                      stream, p, k_map, v_map);
+    if (st != KDA_OK || grid == 1) return st;
+    return launch_join<T, kDim>(p, grid, stream);
 }
 
 template <typename T, int kDim>
-kda_status launch_rows(const Params &p, int grid, void *stream) {
-    if (p.most_rows <= 16) return launch_attend<T, kDim, 1, 1>(p, grid, stream);
-    if (p.most_rows <= 32) return launch_attend<T, kDim, 2, 1>(p, grid, stream);
-    if (p.most_rows <= 64) return launch_attend<T, kDim, 2, 2>(p, grid, stream);
-    return launch_attend<T, kDim, 2, 4>(p, grid, stream);
+kda_status launch_rows(Params &p, int sms, void *stream) {
+    // Which kernel: measured on 96 rows of up to 2000 keys | 16 rows of up to
+    // 30000 (us), 4 kv heads.
+    //   channels  query rows   16 rows a warp      tensor-core form
+    //   128       16           51 | 95             63 | 100
+    //   128       32           57 | 100            66 | 103
+    //   128       40           69 | 123            70 | 105
+    //   128       64           78 | 130            77 | 110
+    //   64        32           39 | 60             46 | 69
+    //   64        64           52 | 83             54 | 79
+    //   64        96           78 | 128            64 | 84
+    // The tensor-core form reads the cache in boxes of p.box keys and 64
+    // channels, which have to be swizzled atoms of 8 rows; with 64 channels
+    // boxes of 8 keys were slower (197 us against 181 in boxes of 16).
+    p.box = kTile;
+    while (p.rows.block_size % p.box != 0) p.box /= 2;
+    if (p.most_rows > (kDim == 128 ? 32 : 64) && p.box * kDim >= 1024) {
+        CUtensorMap k_map, v_map;
+        if (!cache_map<T, kDim>(p, p.key_cache, &k_map) ||
+            !cache_map<T, kDim>(p, p.value_cache, &v_map))
+            return KDA_ERR_CUDA;
+        return p.most_rows <= 64 ? launch_tc<T, kDim, 64>(p, k_map, v_map, sms, stream)
+                                 : launch_tc<T, kDim, 128>(p, k_map, v_map, sms, stream);
+    }
+    // With 64 channels and 32 or 64 rows three CTAs fit an SM, which measured
+    // 43 and 58 us with two (39 and 52 with three); with 16 rows two measured
+    // better (33 | 57 us against 38 | 66 at 8 rows).
+    constexpr int kWide = kDim == 64 ? 3 : 2;
+    if (p.most_rows <= 16) return launch_attend<T, kDim, 1, 1, 2>(p, sms, stream);
+    if (p.most_rows <= 32) return launch_attend<T, kDim, 1, 2, kWide>(p, sms, stream);
+    if (p.most_rows <= 64) return launch_attend<T, kDim, 1, 4, kWide>(p, sms, stream);
+    return launch_attend<T, kDim, 2, 4, 2>(p, sms, stream);
 }
 
 kda_status check_attention(const kda_cache_config *c) {
@@ -853,9 +1759,10 @@ kda_status check_attention(const kda_cache_config *c) {
     return KDA_OK;
 }
 
-size_t partial_bytes(const kda_cache_config *c) {
-    return (size_t)2 * kMaxCtas * (size_t)(c->window * (c->q_heads / c->kv_heads)) *
-           (size_t)(c->head_dim + 2) * 4u;
+// Floats of a partial slot, a multiple of 16 bytes.
+long long slot_floats(const kda_cache_config *c) {
+    const long long rows = c->window * (c->q_heads / c->kv_heads);
+    return (rows * (c->head_dim + 2) + 3) / 4 * 4;
 }
 
 }  // namespace
@@ -864,7 +1771,7 @@ extern "C" {
 
 size_t kda_attention_workspace_bytes(const kda_cache_config *cfg, int32_t B) {
     if (check_attention(cfg) != KDA_OK || B < 0) return 0;
-    return kMaxCtas * sizeof(Cut) + partial_bytes(cfg);
+    return kMaxCtas * (sizeof(Cut) + 2 * (size_t)slot_floats(cfg) * sizeof(float));
 }
 
 kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, const void *key_cache,
@@ -902,16 +1809,18 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
     p.q_heads = cfg->q_heads;
     p.kv_heads = cfg->kv_heads;
     p.group = cfg->q_heads / cfg->kv_heads;
+    p.by_group = (65536 + p.group - 1) / p.group;
     p.window = cfg->window;
     p.left_window = cfg->left_window;
     p.most_rows = cfg->window * p.group;
-    p.scale_log2 = cfg->scale * kLog2e;
-    const int grid = kCtasPerSm * sms < kMaxCtas ? kCtasPerSm * sms : kMaxCtas;
+    p.slot_size = slot_floats(cfg);
+    p.scale_log2 = fabsf(cfg->scale) * kLog2e;
+    p.flip = cfg->scale < 0.0f ? 0x80008000u : 0u;
     if (cfg->dtype == KDA_DTYPE_BF16)
-        return cfg->head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, grid, stream)
-                                   : launch_rows<__nv_bfloat16, 128>(p, grid, stream);
-    return cfg->head_dim == 64 ? launch_rows<__half, 64>(p, grid, stream)
-                               : launch_rows<__half, 128>(p, grid, stream);
+        return cfg->head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, sms, stream)
+                                   : launch_rows<__nv_bfloat16, 128>(p, sms, stream);
+    return cfg->head_dim == 64 ? launch_rows<__half, 64>(p, sms, stream)
+                               : launch_rows<__half, 128>(p, sms, stream);
 }
 
 }  // extern "C"

@@ -53,27 +53,23 @@ __device__ __forceinline__ void flag(int *err, int bits) {
 }
 
 // Row b, checked; `bits` collects what is wrong with it (the row is then
-// empty).  most: the largest token count allowed.
+// empty).  most: the largest token count allowed.  Every load is issued before
+// any is looked at: one way to memory, two with request_indices.
 __device__ __forceinline__ Row read_row(const Rows &r, int b, int most, int &bits) {
-    Row row{r.cu_seqlens[b], 0, 0, 0};
-    const long long n = (long long)r.cu_seqlens[b + 1] - row.first;
+    const int first = r.cu_seqlens[b], end = r.cu_seqlens[b + 1];
+    const int request = r.request_indices != nullptr ? r.request_indices[b] : b;
+    const bool known = request >= 0 && request < r.num_requests;
+    const int computed = r.num_computed[known ? request : 0];
+    Row row{first, 0, computed, request};
+    const long long n = (long long)end - first, last = (long long)computed + n - 1;
     if (n == 0) return row;
-    if (n < 0 || n > most || row.first < 0) {
+    if (n < 0 || n > most || first < 0)
         bits |= KDA_ROW_BAD_LENGTH;
-        return row;
-    }
-    row.request = r.request_indices != nullptr ? r.request_indices[b] : b;
-    if (row.request < 0 || row.request >= r.num_requests) {
+    else if (!known || computed < 0 || last > 0x7ffffff0LL ||
+             divide((int)last, r.by_block) >= r.bt_width)
         bits |= KDA_ROW_BAD_BLOCK;
-        return row;
-    }
-    row.computed = r.num_computed[row.request];
-    const long long last = (long long)row.computed + n - 1;
-    if (row.computed < 0 || last > 0x7ffffff0LL || divide((int)last, r.by_block) >= r.bt_width) {
-        bits |= KDA_ROW_BAD_BLOCK;
-        return row;
-    }
-    row.tokens = (int)n;
+    else
+        row.tokens = (int)n;
     return row;
 }
 

@@ -262,3 +262,27 @@ def test_capture_and_replay_with_changed_lengths():
         replayed, replayed_lse = out.clone(), lse.clone()
         want, want_lse = _run(c, 4)
         assert torch.equal(replayed, want) and torch.equal(replayed_lse, want_lse)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,window", [(1, 3), (6, 4), (8, 8), (16, 8)])
+def test_growing_maxima_and_scales(dim, group, window):
+    # maxima that keep growing along the keys, then shrinking ones
+    c = Case([window, 1], [1500, 300], group, 1, dim, 16, seed=20)
+    for b in range(2):
+        for p in range(int(c.computed[b]) + 1):
+            c.keys[int(c.table[b, p // 16]), p % 16, 0] += 0.02 * p
+    c.q[...] = c.q.abs()
+    for scale in (None, -0.05, 0.0, 1.0):
+        _check(c, window, scale=scale)
+
+
+@pytest.mark.parametrize("group,window", [(1, 1), (4, 4), (8, 8), (16, 8)])
+def test_many_segments_of_every_length(group, window):
+    # a CTA's run spans several rows and heads, short and long in turn
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, window + 1, size=90).tolist()
+    computed = [int(x) for x in np.exp(rng.uniform(0, np.log(700), size=90))]
+    c = Case(lens, computed, 3 * group, 3, 64, 16, seed=21)
+    _check(c, window)
+    _check(c, window, left_window=37)
