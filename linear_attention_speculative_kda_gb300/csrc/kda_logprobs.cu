@@ -9,17 +9,24 @@
 // lowest value, and the difference of near values is exact.
 //
 // Alternatives without a second pass: each thread's running maximum is kept
-// anyway.  The k-th largest of them is a lower bound of the k-th largest
-// logit, so only threads whose maximum reaches it can hold one of the top k:
-// about k of 512.  Their elements are read once more (from L2), and warps
-// insert what qualifies into a list sorted across the lanes.  Rows of equal
-// values, where every thread qualifies, cost one more pass and no more.
+// anyway, and those of 16 stretches of its elements beside it.  The k-th
+// largest of the best maxima of each warp is a lower bound of the k-th largest
+// logit, so only stretches whose maximum reaches it can hold one of the top k:
+// little more than k of them.  Their elements are read once more (from L2),
+// what reaches the bound becomes a candidate, and a candidate's place is the
+// number of candidates before it.  (Reading all elements of the threads that
+// reach it again took as long as the row itself for 20 alternatives.)  Where
+// that leaves too many (rows of equal or masked values), warps insert what
+// qualifies into lists sorted across the lanes: one more pass over the row and
+// no more.
 //
 // HBM bounds the large calls: each logit is read once, by 16-byte loads (a
 // row that does not start on 16 bytes has a few elements before and after
-// them).  A CTA takes a row; where there are fewer rows than CTAs fill the
-// GPU, a cluster of 2 to 8 CTAs shares a row and joins over distributed
-// shared memory, in rank order.
+// them).  A row is taken by a cluster of 1 to 8 CTAs, joined over distributed
+// shared memory in rank order: CTAs of 128 threads, up to 8 on an SM with 8
+// loads a thread in flight, so that rows of any length and number fill the GPU
+// evenly, and of 512 for the few rows that latency counts for.  4096 rows of
+// 131072 in bf16: 157 us, the measured copy rate (184 with a CTA of 512 a row).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,10 +37,9 @@ namespace {
 
 using kda_cache::kFull;
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kUnroll = 4;        // 16-byte loads in flight per thread
-constexpr int kTopOfWarp = 4;     // thread maxima of a warp that the bound looks at
+constexpr int kCandidates = 512;
+constexpr int kStretches = 16;    // parts of a thread's elements whose maxima are kept
+constexpr int kListed = 128;      // (thread, stretch) pairs that are read again
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNever = -140.0f; // a distance whose weight e^d is 0 in fp32
@@ -77,6 +83,24 @@ __device__ __forceinline__ void unpack(uint4 u, float (&x)[4], float) {
     x[1] = __uint_as_float(u.y);
     x[2] = __uint_as_float(u.z);
     x[3] = __uint_as_float(u.w);
+}
+
+// The largest element of a vector; NaNs are passed over.
+__device__ __forceinline__ float largest(uint4 u, __nv_bfloat16) {
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(pair(u.x), pair(u.y)), __hmax2(pair(u.z), pair(u.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+__device__ __forceinline__ float largest(uint4 u, __half) {
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
+    const __half2 m = __hmax2(__hmax2(pair(u.x), pair(u.y)), __hmax2(pair(u.z), pair(u.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+__device__ __forceinline__ float largest(uint4 u, float) {
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                 fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -126,82 +150,95 @@ __device__ __forceinline__ Stats join(Stats a, Stats b) {
     return Stats{m, a.s + b.s, a.w + b.w};
 }
 
-__device__ __forceinline__ Stats shuffle_xor(Stats a, int o) {
-    return Stats{__shfl_xor_sync(kFull, a.m, o), __shfl_xor_sync(kFull, a.s, o),
-                 __shfl_xor_sync(kFull, a.w, o)};
-}
-
-// Whether (v, i) comes before (u, j): larger, or equal at the lower index.
-__device__ __forceinline__ bool before(float v, int i, float u, int j) {
-    return v > u || (v == u && i < j);
-}
-
-// A list of up to 32 (value, index) pairs, the best in lane 0.
-struct TopList {
-    float v;
-    int i;
-    __device__ __forceinline__ void clear() {
-        v = -INFINITY;
-        i = 0x7fffffff;
+// The statistics of a warp's 32 lanes together, in every lane.
+__device__ __forceinline__ Stats warp_join(Stats a) {
+    float m = a.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (a.m != m) rescale(a, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(kFull, a.s, o);
+        a.w += __shfl_xor_sync(kFull, a.w, o);
     }
-    // Offer each lane's (x, at) where `offered`; only the first k places count.
-    __device__ __forceinline__ void offer(float x, int at, bool offered, int k, int lane) {
-        float kv = __shfl_sync(kFull, v, k - 1);
-        int ki = __shfl_sync(kFull, i, k - 1);
-        unsigned todo = __ballot_sync(kFull, offered && before(x, at, kv, ki));
+    return Stats{m, a.s, a.w};
+}
+
+// Sorted across the lanes, the largest in lane 0 (a bitonic network).
+__device__ __forceinline__ float warp_sort(float v, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(kFull, v, o);
+            const bool larger = ((lane & size) == 0) == ((lane & o) == 0);
+            v = larger ? fmaxf(v, u) : fminf(v, u);
+        }
+    return v;
+}
+
+// A logit and its index as one number that orders by value, then by the lower
+// index; a NaN counts as -inf, and 0 comes after every logit.
+__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+    const uint32_t b = __float_as_uint((v == v ? v : -INFINITY) + 0.0f);
+    const uint32_t order = (b >> 31) != 0 ? ~b : b | 0x80000000u;
+    return (unsigned long long)order << 32 | (uint32_t)~i;
+}
+
+__device__ __forceinline__ float value_of(unsigned long long key) {
+    const uint32_t order = (uint32_t)(key >> 32);
+    return __uint_as_float((order >> 31) != 0 ? order & 0x7fffffffu : ~order);
+}
+
+__device__ __forceinline__ int index_of(unsigned long long key) { return (int)~(uint32_t)key; }
+
+// A list of up to 32 keys, the best in lane 0.
+struct TopList {
+    unsigned long long key;
+    // Offer each lane's key (0: none); only the first k places count.
+    __device__ __forceinline__ void offer(unsigned long long offered, int k, int lane) {
+        const unsigned long long last = __shfl_sync(kFull, key, k - 1);
+        unsigned todo = __ballot_sync(kFull, offered > last);
         while (todo != 0) {
             const int src = __ffs(todo) - 1;
             todo &= todo - 1;
-            const float nv = __shfl_sync(kFull, x, src);
-            const int ni = __shfl_sync(kFull, at, src);
-            const int place = __popc(__ballot_sync(kFull, before(v, i, nv, ni)));
-            const float uv = __shfl_up_sync(kFull, v, 1);
-            const int ui = __shfl_up_sync(kFull, i, 1);
-            if (lane == place) {
-                v = nv;
-                i = ni;
-            } else if (lane > place) {
-                v = uv;
-                i = ui;
-            }
+            const unsigned long long in = __shfl_sync(kFull, offered, src);
+            const int place = __popc(__ballot_sync(kFull, key > in));
+            const unsigned long long up = __shfl_up_sync(kFull, key, 1);
+            if (lane == place)
+                key = in;
+            else if (lane > place)
+                key = up;
         }
     }
 };
 
+template <int kWarps, bool kTop>
 struct Shared {
     Stats stats[kWarps];
     Stats row;                        // this CTA's, for the cluster
-    float maxima[kWarps * kTopOfWarp];
-    float bound;
-    int threads;                      // threads that reach the bound
+    float maxima[32];
+    int listed;                       // pairs that reach the bound
     int candidates;
-    int list[kThreads];
-    float cand_v[kThreads];
-    int cand_i[kThreads];
-    float top_v[KDA_MAX_TOP];         // this CTA's top k
-    int top_i[KDA_MAX_TOP];
+    int list[kListed];                // thread * kStretches + stretch
+    unsigned long long candidate[kCandidates];
+    unsigned long long top[KDA_MAX_TOP];  // this CTA's top k
+    float stretch[kTop ? kStretches : 1][32 * kWarps];  // each thread's maxima
 };
 
 // The top k of the n candidates in shared memory, each placed by the number
 // of candidates before it.
-__device__ __forceinline__ void place(Shared &sh, int n, int k) {
+template <int kWarps>
+__device__ __forceinline__ void place(Shared<kWarps, true> &sh, int n, int k) {
     const int tid = threadIdx.x;
-    if (tid < k) {
-        sh.top_v[tid] = -INFINITY;
-        sh.top_i[tid] = 0x7fffffff;
-    }
-    float v = 0.0f;
-    int i = 0, rank = k;
-    if (tid < n) {
-        v = sh.cand_v[tid];
-        i = sh.cand_i[tid];
-        rank = 0;
-        for (int c = 0; c < n; ++c) rank += before(sh.cand_v[c], sh.cand_i[c], v, i) ? 1 : 0;
-    }
+    if (tid < k) sh.top[tid] = 0;
     __syncthreads();
-    if (rank < k) {
-        sh.top_v[rank] = v;
-        sh.top_i[rank] = i;
+    for (int i = tid; i < n; i += 32 * kWarps) {
+        const unsigned long long key = sh.candidate[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) rank += sh.candidate[c] > key ? 1 : 0;
+        if (rank < k) sh.top[rank] = key;
     }
     __syncthreads();
 }
@@ -226,19 +263,22 @@ __device__ __forceinline__ float remote_f32(const float *ptr, int rank) {
     return x;
 }
 
-__device__ __forceinline__ int remote_s32(const int *ptr, int rank) {
-    int x;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(remote(ptr, rank)) : "memory");
+__device__ __forceinline__ unsigned long long remote_u64(const unsigned long long *ptr, int rank) {
+    unsigned long long x;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(remote(ptr, rank)) : "memory");
     return x;
 }
 
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
-    constexpr int kN = 16 / (int)sizeof(T);
-    __shared__ Shared sh;
+template <typename T, int kWarps, bool kTop>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
+    logprobs_kernel(const Params p) {
+    constexpr int kN = 16 / (int)sizeof(T), kThreads = 32 * kWarps;
+    constexpr int kUnroll = kWarps == 4 ? 8 : 4;  // 16-byte loads in flight per thread
+    __shared__ Shared<kWarps, kTop> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / p.ctas, rank = blockIdx.x % p.ctas;
     kda_cache::grid_dependents_launch();
+    if (tid == 0) sh.listed = sh.candidates = 0;
     kda_cache::grid_dependency_wait();
     const int token = p.tokens[row];
     if (token >= p.vocab) {  // uniform over the cluster
@@ -246,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
         return;
     }
     const T *x = reinterpret_cast<const T *>(p.logits) + row * p.stride;
+    float x_token = 0.0f;
+    if (tid == 0 && token >= 0) x_token = to_float(x[token]);
     // head elements up to a 16-byte boundary, whole vectors, tail elements
     const int head = min(p.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) /
                                       (int)sizeof(T));
@@ -254,15 +296,16 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
     const uint4 *body = reinterpret_cast<const uint4 *>(x + head);
     const int begin = (int)((long long)vectors * rank / p.ctas);
     const int end = (int)((long long)vectors * (rank + 1) / p.ctas);
-    // the single element before or after the vectors that this thread adds
-    int extra = -1;
-    if (rank == 0) {
-        if (tid < head) extra = tid;
-        else if (tid - head < tail) extra = head + vectors * kN + (tid - head);
-    }
+    // the single element before or after the vectors that a thread adds
+    auto extra_of = [&](int thread) {
+        if (rank != 0) return -1;
+        if (thread < head) return thread;
+        return thread - head < tail ? vectors * kN + thread : -1;
+    };
 
     Stats st{-INFINITY, 0.0f, 0.0f};
     float base = 0.0f;  // st.m, the thread's largest logit, or 0 while that is -inf
+    const int extra = extra_of(tid);
     if (extra >= 0) {
         const float v = to_float(x[extra]);
         st.m = fmaxf(v, -INFINITY);
@@ -271,19 +314,27 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
         st.s = exp2_fast(d * kLog2e);
         st.w = st.s * fmaxf(d, kNever);
     }
+    // rounds of kUnroll vectors a thread, and rounds of a stretch
+    const int rounds = (end - begin + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+    const int stretch = (rounds + kStretches - 1) / kStretches;
+    float stretch_most = -INFINITY;
+    int stretch_left = stretch, stretch_at = 0;
     for (int j = begin + tid; j < end; j += kUnroll * kThreads) {
         uint4 u[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
             u[i] = j + i * kThreads < end ? load_once(body + j + i * kThreads)
                                           : minus_infinity<T>();
-        float f[kUnroll][kN];
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            unpack(u[i], f[i], T());
-#pragma unroll
-            for (int e = 0; e < kN; ++e) top = fmaxf(top, f[i][e]);
+        for (int i = 0; i < kUnroll; ++i) top = fmaxf(top, largest(u[i], T()));
+        if constexpr (kTop) {
+            stretch_most = fmaxf(stretch_most, top);
+            if (--stretch_left == 0) {
+                sh.stretch[stretch_at++][tid] = stretch_most;
+                stretch_most = -INFINITY;
+                stretch_left = stretch;
+            }
         }
         if (top > st.m) {
             rescale(st, top);
@@ -291,105 +342,95 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
         }
         float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+        for (int i = 0; i < kUnroll; ++i) {
+            float f[kN];
+            unpack(u[i], f, T());
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
-                const float d = f[i][e] - base;
+                const float d = f[e] - base;
                 const float z = exp2_fast(d * kLog2e);
                 s[e & 1] += z;
                 w[e & 1] = fmaf(z, fmaxf(d, kNever), w[e & 1]);
             }
+        }
         st.s += s[0] + s[1];
         st.w += w[0] + w[1];
     }
 
-    Stats all = st;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all = join(all, shuffle_xor(all, o));
-    if (lane == 0) sh.stats[warp] = all;
+    const Stats of_warp = warp_join(st);
+    if (lane == 0) sh.stats[warp] = of_warp;
     if constexpr (kTop) {
-        // the warp's thread maxima in descending order (a bitonic network)
-        float v = st.m;
-#pragma unroll
-        for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-            for (int o = size >> 1; o > 0; o >>= 1) {
-                const float u = __shfl_xor_sync(kFull, v, o);
-                const bool larger = ((lane & size) == 0) == ((lane & o) == 0);
-                v = larger ? fmaxf(v, u) : fminf(v, u);
-            }
-        if (lane < kTopOfWarp) sh.maxima[warp * kTopOfWarp + lane] = v;
-        if (tid == 0) sh.threads = sh.candidates = 0;
+        constexpr int kKept = 32 / kWarps;  // maxima of each warp that the bound looks at
+        const float v = warp_sort(st.m, lane);
+        if (lane < kKept) sh.maxima[warp * kKept + lane] = v;
     }
     __syncthreads();
     if (warp == 0) {
-        Stats a = lane < kWarps ? sh.stats[lane] : Stats{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = join(a, shuffle_xor(a, o));
+        const Stats a =
+            warp_join(lane < kWarps ? sh.stats[lane] : Stats{-INFINITY, 0.0f, 0.0f});
         if (lane == 0) sh.row = a;
     }
     if constexpr (kTop) {
-        constexpr int kMaxima = kWarps * kTopOfWarp;
-        if (warp == 1) {  // the k-th largest of the maxima kept
-            float bound = -INFINITY;
-            for (int c = lane; c < kMaxima; c += 32) {
-                const float v = sh.maxima[c];
-                int ge = 0;
-                for (int d = 0; d < kMaxima; ++d) ge += sh.maxima[d] >= v ? 1 : 0;
-                if (ge >= p.top) bound = fmaxf(bound, v);
+        const float bound = __shfl_sync(kFull, warp_sort(sh.maxima[lane], lane), p.top - 1);
+        auto push = [&](float v, int i) {
+            if (!(v < bound)) {  // (a NaN counts as -inf, which may be the bound)
+                if (v != v && bound != -INFINITY) return;
+                const int c = atomicAdd(&sh.candidates, 1);
+                if (c < kCandidates) sh.candidate[c] = key_of(v, i);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, o));
-            if (lane == 0) sh.bound = bound;
-        }
-        __syncthreads();
-        const float bound = sh.bound;
-        if (st.m >= bound) sh.list[atomicAdd(&sh.threads, 1)] = tid;
-        __syncthreads();
-        // read those threads' elements again
-        TopList best;
-        best.clear();
-        for (int c = warp; c < sh.threads; c += kWarps) {
-            const int who = sh.list[c];
-            int who_extra = -1;
-            if (rank == 0) {
-                if (who < head) who_extra = who;
-                else if (who - head < tail) who_extra = head + vectors * kN + (who - head);
-            }
-            if (who_extra >= 0) {
-                float v = to_float(x[who_extra]);
-                v = v == v ? v : -INFINITY;
-                best.offer(v, who_extra, lane == 0 && v >= bound, p.top, lane);
-            }
-            for (int j0 = begin + who; j0 < end; j0 += 32 * kThreads) {
-                const int j = j0 + lane * kThreads;
-                const bool in = j < end;
-                float f[kN];
-                unpack(in ? body[j] : minus_infinity<T>(), f, T());
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    const float v = f[e] == f[e] ? f[e] : -INFINITY;
-                    best.offer(v, head + j * kN + e, in && v >= bound, p.top, lane);
+        };
+        // which stretches reach it
+        if (st.m >= bound) {
+            if (extra >= 0) push(to_float(x[extra]), extra);
+            for (int i = 0; i <= stretch_at; ++i) {
+                const float v = i < stretch_at ? sh.stretch[i][tid] : stretch_most;
+                if (v >= bound && i * stretch < rounds) {
+                    const int c = atomicAdd(&sh.listed, 1);
+                    if (c < kListed) sh.list[c] = tid * kStretches + i;
                 }
             }
         }
-        if (lane < p.top && best.i != 0x7fffffff) {
-            const int c = atomicAdd(&sh.candidates, 1);
-            sh.cand_v[c] = best.v;
-            sh.cand_i[c] = best.i;
+        __syncthreads();
+        // their elements again, as candidates
+        const int listed = sh.listed, each = stretch * kUnroll;
+        if (listed <= kListed) {
+#pragma unroll 2
+            for (int i = tid; i < listed * each; i += kThreads) {
+                const int who = sh.list[i / each], n = who % kStretches * each + i % each;
+                const int j = begin + who / kStretches + n * kThreads;
+                if (j >= end) continue;
+                float f[kN];
+                unpack(body[j], f, T());
+#pragma unroll
+                for (int e = 0; e < kN; ++e) push(f[e], head + j * kN + e);
+            }
         }
         __syncthreads();
+        if (listed > kListed || sh.candidates > kCandidates) {  // uniform over the CTA
+            TopList best{0};
+            best.offer(extra >= 0 ? key_of(to_float(x[extra]), extra) : 0, p.top, lane);
+            for (int j0 = begin + warp * 32; j0 < end; j0 += kThreads) {
+                const int j = j0 + lane;
+                float f[kN];
+                unpack(j < end ? body[j] : minus_infinity<T>(), f, T());
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    best.offer(j < end ? key_of(f[e], head + j * kN + e) : 0, p.top, lane);
+            }
+            __syncthreads();
+            if (tid == 0) sh.candidates = 32 * kWarps;
+            sh.candidate[tid] = lane < p.top ? best.key : 0;
+            __syncthreads();
+        }
         place(sh, sh.candidates, p.top);
     }
 
     if (p.ctas > 1) {
         cluster_sync();
         if (rank == 0) {
-            if (kTop && tid < p.ctas * p.top) {  // at most 8 * 32
-                sh.cand_v[tid] = remote_f32(&sh.top_v[tid % p.top], tid / p.top);
-                sh.cand_i[tid] = remote_s32(&sh.top_i[tid % p.top], tid / p.top);
-            }
+            if (kTop)
+                for (int i = tid; i < p.ctas * p.top; i += kThreads)  // at most 8 * 32
+                    sh.candidate[i] = remote_u64(&sh.top[i % p.top], i / p.top);
             if (tid == 0) {
                 Stats a = sh.row;
                 for (int c = 1; c < p.ctas; ++c)
@@ -401,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
         cluster_sync();
         if (rank != 0) return;
         if constexpr (kTop) place(sh, p.ctas * p.top, p.top);
-    } else {
+    } else if (!kTop) {
         __syncthreads();
     }
 
@@ -409,24 +450,38 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
     const float log_s = kLn2 * log2f(a.s);
     const float lse = a.s == 0.0f ? -INFINITY : a.m + log_s;
     if (tid == 0) {
-        p.logprob[row] = token < 0 ? 0.0f
-                                   : (lse == -INFINITY ? lse : to_float(x[token]) - lse);
-        if (p.entropy != nullptr)
-            p.entropy[row] = a.s == 0.0f ? 0.0f : log_s - a.w / a.s;
+        p.logprob[row] = token < 0 ? 0.0f : (lse == -INFINITY ? lse : x_token - lse);
+        if (p.entropy != nullptr) p.entropy[row] = a.s == 0.0f ? 0.0f : log_s - a.w / a.s;
         if (p.lse != nullptr) p.lse[row] = lse;
     }
     if (kTop && tid < p.top) {
         const long long at = (long long)row * p.top + tid;
-        p.top_logprob[at] = lse == -INFINITY ? lse : to_float(x[sh.top_i[tid]]) - lse;
-        p.top_index[at] = sh.top_i[tid];
+        const unsigned long long key = sh.top[tid];
+        p.top_logprob[at] = lse == -INFINITY ? lse : value_of(key) - lse;
+        p.top_index[at] = index_of(key);
     }
 }
 
-template <typename T>
+template <typename T, int kWarps>
 kda_status launch_logprobs(const Params &p, int rows, void *stream) {
-    void (*kernel)(const Params) = p.top > 0 ? logprobs_kernel<T, true> : logprobs_kernel<T, false>;
-    return kda_cache::launch(kernel, dim3((unsigned)rows * (unsigned)p.ctas), dim3(kThreads), 0,
+    void (*kernel)(const Params) =
+        p.top > 0 ? logprobs_kernel<T, kWarps, true> : logprobs_kernel<T, kWarps, false>;
+    return kda_cache::launch(kernel, dim3((unsigned)rows * (unsigned)p.ctas), dim3(32 * kWarps), 0,
                              p.ctas, stream, p);
+}
+
+template <typename T>
+kda_status launch_rows(Params &p, int rows, void *stream) {
+    // CTAs of 512 threads for few rows: one of 131072 8.1 us (9.9 with 128
+    // threads), 40 of 115069 39 us (19).  More CTAs a row up to some four an
+    // SM, each with enough elements to be worth its part of the join: 256 rows
+    // of 131072 with 2, 4 or 8 CTAs 28, 21 and 27 us, 517 of 100003 in fp32
+    // with 1, 2 or 4 44, 39 and 47 us.
+    const bool wide = rows * 8ll <= 304;
+    p.ctas = 1;
+    while (p.ctas < 8 && (long long)rows * p.ctas < 600 && p.vocab / (2 * p.ctas) >= 16384)
+        p.ctas *= 2;
+    return wide ? launch_logprobs<T, 16>(p, rows, stream) : launch_logprobs<T, 4>(p, rows, stream);
 }
 
 }  // namespace
@@ -462,11 +517,7 @@ extern "C" kda_status kda_token_logprobs(const void *logits, int32_t dtype, int6
     p.stride = stride_row;
     p.vocab = vocab;
     p.top = num_top;
-    // CTAs of a row: enough to fill the SMs, each with two rounds of loads
-    p.ctas = 1;
-    while (p.ctas < 8 && (long long)rows * p.ctas * 2 <= 304 && vocab / (p.ctas * 2) >= 8192)
-        p.ctas *= 2;
-    if (dtype == KDA_DTYPE_BF16) return launch_logprobs<__nv_bfloat16>(p, rows, stream);
-    if (dtype == KDA_DTYPE_FP16) return launch_logprobs<__half>(p, rows, stream);
-    return launch_logprobs<float>(p, rows, stream);
+    if (dtype == KDA_DTYPE_BF16) return launch_rows<__nv_bfloat16>(p, rows, stream);
+    if (dtype == KDA_DTYPE_FP16) return launch_rows<__half>(p, rows, stream);
+    return launch_rows<float>(p, rows, stream);
 }
