@@ -520,6 +520,52 @@ kda_status kda_token_logprobs(const void *logits, int32_t dtype, int64_t stride_
                               float *top_logprob, int32_t *top_index,
                               int32_t *error_word, void *stream);
 
+/*
+ * The three calls above with their arguments in one structure, for bindings
+ * in which every argument costs (ctypes: some 4 us a call on a GB300 host).
+ * The fields are those arguments, in natural alignment without padding.
+ */
+typedef struct kda_append_args {
+    kda_cache_config config;
+    kda_align align;
+    const void *q, *k, *v;
+    void *q_out, *key_cache, *value_cache;
+    const double *inv_freq;
+    const int32_t *cu_seqlens;
+    int32_t B, num_tokens;
+    int32_t *error_word;
+    void *stream;
+} kda_append_args;
+
+typedef struct kda_attention_args {
+    kda_cache_config config;
+    kda_align align;
+    const void *q, *key_cache, *value_cache;
+    const int32_t *cu_seqlens;
+    int64_t B;
+    void *workspace;
+    uint64_t workspace_bytes;
+    void *out;
+    float *lse;
+    int32_t *error_word;
+    void *stream;
+} kda_attention_args;
+
+typedef struct kda_logprobs_args {
+    const void *logits;
+    int64_t stride_row;
+    int32_t dtype, rows, vocab, num_top;
+    const int32_t *tokens;
+    float *logprob, *entropy, *lse_out, *top_logprob;
+    int32_t *top_index;
+    int32_t *error_word;
+    void *stream;
+} kda_logprobs_args;
+
+kda_status kda_kv_append_packed(const kda_append_args *args);
+kda_status kda_window_attention_packed(const kda_attention_args *args);
+kda_status kda_token_logprobs_packed(const kda_logprobs_args *args);
+
 /* Name of a status code (static string). */
 const char *kda_status_string(kda_status status);
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -57,6 +58,9 @@ EXPORTED = (
     "kda_attention_workspace_bytes",
     "kda_window_attention",
     "kda_token_logprobs",
+    "kda_kv_append_packed",
+    "kda_window_attention_packed",
+    "kda_token_logprobs_packed",
     "kda_status_string",
     "kda_abi_version",
 )
@@ -198,6 +202,10 @@ def bind_library(path: str):
                                          [vp] * 4)
     lib.kda_token_logprobs.restype = ctypes.c_int
     lib.kda_token_logprobs.argtypes = [vp, i32, ctypes.c_int64, i32, i32, vp, i32] + [vp] * 7
+    for fn in (lib.kda_kv_append_packed, lib.kda_window_attention_packed,
+               lib.kda_token_logprobs_packed):
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.c_char_p]   # the bytes of the argument structure
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_abi_version.restype = i32
@@ -706,47 +714,44 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
 # ------------------------------------- full-attention layers and acceptance --
 #
 # These calls are short (a decode step's append takes 3 us on the device), so
-# their checks are written out inline: one comparison per fact, and the
-# message is worked out only once something is wrong.
+# their checks are written out inline, one comparison per fact, with the
+# message worked out only once something is wrong, and their arguments go to
+# the library as the bytes of one structure.
 
-def _raw_stream(dev):
-    # the handle torch.cuda.current_stream(dev).cuda_stream holds, without
+_CACHE_FORMAT = "9if6qQqiiiiQQ"     # kda_cache_config, kda_align
+_APPEND_ARGS = struct.Struct("=" + _CACHE_FORMAT + "8Q2i2Q").pack
+_ATTENTION_ARGS = struct.Struct("=" + _CACHE_FORMAT + "4Qq6Q").pack
+_LOGPROBS_ARGS = struct.Struct("=Qq4i8Q").pack
+
+
+def _raw_stream(device: int):
+    # the handle torch.cuda.current_stream(device).cuda_stream holds, without
     # building the stream object
-    return torch._C._cuda_getCurrentRawStream(dev.index if dev.index is not None
-                                              else torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _mismatch(dev, **tensors):
-    """Raises for the first of name=(tensor, dtype) that is not on ``dev`` or
-    of its type (the callers found that one is not)."""
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _mismatch(device, **tensors):
+    """Raises for the first of name=(tensor, dtype) that is not on the device
+    or of its type (the callers found that one is not)."""
     for name, (t, dtype) in tensors.items():
         if t is not None:
-            _req(t, dtype, name, dev)
-
-
-@functools.lru_cache(maxsize=1024)
-def _cache_config(q_heads, kv_heads, head_dim, dtype, num_blocks, window, left_window, rotary_dim,
-                  interleaved, scale, stride_block, stride_token, stride_head, stride_q, stride_k,
-                  stride_v):
-    """A pointer to a ``kda_cache_config``, read only by the library: one
-    object per distinct argument set."""
-    cfg = KdaCacheConfig(
-        q_heads, kv_heads, head_dim, dtype, num_blocks, window, left_window, rotary_dim,
-        interleaved, head_dim ** -0.5 if scale is None else float(scale), stride_block,
-        stride_token, stride_head, stride_q, stride_k, stride_v)
-    return ctypes.pointer(cfg)
+            _req(t, dtype, name, device)
 
 
 def _check_cache(key_cache, value_cache):
     """Shape and strides of a paged cache viewed as [num_blocks, block_size,
-    kv_heads, head_dim], flat."""
+    kv_heads, head_dim]."""
     shape, strides = key_cache.shape, key_cache.stride()
     if len(shape) != 4 or strides[3] != 1:
         raise ValueError("the caches must be [num_blocks, block_size, kv_heads, head_dim] views "
                          "with contiguous channels")
-    if value_cache.shape != shape or value_cache.stride() != strides:
+    if value_cache.stride() != strides or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must have the same shape and strides")
-    return *shape, strides[0], strides[1], strides[2]
+    return shape, strides
 
 
 def _heads_tokens(t, name, dim):
@@ -761,16 +766,17 @@ def _heads_tokens(t, name, dim):
     return tokens, heads, stride[0] if tokens > 1 else heads * dim
 
 
-def _plan(cu_seqlens, block_table, num_computed, request_indices, block_size, error_word):
-    """Row count and ``kda_align`` of a call on a paged key/value cache."""
-    B = cu_seqlens.shape[0] - 1
+def _plan(cu_seqlens, block_table, num_computed, request_indices, error_word):
+    """Row count, and the table's requests, width and row stride, of a call on
+    a paged key/value cache."""
+    B = cu_seqlens.numel() - 1
     requests, width = block_table.shape
-    stride = block_table.stride()
-    if B < 0 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+    stride, one = block_table.stride()
+    if B < 0 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous with B + 1 entries")
-    if stride[1] != 1 and width > 1:
+    if one != 1 and width > 1:
         raise ValueError("block_table must be [num_requests, width] with contiguous columns")
-    if num_computed.shape[0] < requests or not num_computed.is_contiguous():
+    if num_computed.numel() < requests or not num_computed.is_contiguous():
         raise ValueError("num_computed must be contiguous with one entry per request")
     if request_indices is not None:
         if not request_indices.is_contiguous():
@@ -780,8 +786,7 @@ def _plan(cu_seqlens, block_table, num_computed, request_indices, block_size, er
         raise ValueError("more rows than requests without request_indices")
     if error_word is not None:
         _at_least(error_word, 1, "error_word")
-    return B, KdaAlign(block_table.data_ptr(), stride[0] if requests > 1 else width, width,
-                       block_size, requests, 0, num_computed.data_ptr(), _ptr(request_indices))
+    return B, requests, width, stride if requests > 1 else width
 
 
 def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_computed, *,
@@ -799,30 +804,32 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
     (``q_out``, which may be ``q`` when it is contiguous; allocated when
     None), or None without ``q``.
     """
-    dev, dtype, i32 = key_cache.device, key_cache.dtype, torch.int32
+    dev, dtype, i32 = key_cache.get_device(), key_cache.dtype, torch.int32
     code = DTYPES.get(dtype, 2)
     if code > 1:
         raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
     if (value_cache.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype
             or cu_seqlens.dtype is not i32 or block_table.dtype is not i32
-            or num_computed.dtype is not i32 or value_cache.device != dev or k.device != dev
-            or v.device != dev or cu_seqlens.device != dev or block_table.device != dev
-            or num_computed.device != dev):
-        _mismatch(dev, value_cache=(value_cache, dtype), k=(k, dtype), v=(v, dtype),
+            or num_computed.dtype is not i32 or value_cache.get_device() != dev
+            or k.get_device() != dev or v.get_device() != dev or cu_seqlens.get_device() != dev
+            or block_table.get_device() != dev or num_computed.get_device() != dev):
+        _mismatch(key_cache.device, value_cache=(value_cache, dtype), k=(k, dtype), v=(v, dtype),
                   cu_seqlens=(cu_seqlens, i32), block_table=(block_table, i32),
                   num_computed=(num_computed, i32))
-    _opt(request_indices, i32, "request_indices", dev)
-    _opt(error_word, i32, "error_word", dev)
-    blocks, block_size, kv_heads, dim, sb, st, sh = _check_cache(key_cache, value_cache)
-    B, align = _plan(cu_seqlens, block_table, num_computed, request_indices, block_size,
-                     error_word)
+    if request_indices is not None or error_word is not None:
+        _mismatch(key_cache.device, request_indices=(request_indices, i32),
+                  error_word=(error_word, i32))
+    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache)
+    B, requests, width, table_stride = _plan(cu_seqlens, block_table, num_computed,
+                                             request_indices, error_word)
     T, heads, stride_k = _heads_tokens(k, "k", dim)
     Tv, heads_v, stride_v = _heads_tokens(v, "v", dim)
     if heads != kv_heads or heads_v != kv_heads or Tv != T:
         raise ValueError(f"k and v must be [T, {kv_heads}, {dim}] with the same T")
-    q_heads, stride_q, q_ptr, out_ptr = kv_heads, 8, None, None
+    q_heads, stride_q, q_ptr, out_ptr = kv_heads, 8, 0, 0
     if q is not None:
-        _req(q, dtype, "q", dev)
+        if q.dtype is not dtype or q.get_device() != dev:
+            _mismatch(key_cache.device, q=(q, dtype))
         Tq, q_heads, stride_q = _heads_tokens(q, "q", dim)
         if Tq != T or q_heads < 1 or q_heads % kv_heads:
             raise ValueError("q must be [T, Hq, D] with k's T and Hq a multiple of the cache's "
@@ -830,25 +837,26 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _req(q_out, dtype, "q_out", dev)
+            _req(q_out, dtype, "q_out", key_cache.device)
             if q_out.shape != q.shape or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous and shaped like q")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rotary_dim, freq_ptr = 0, None
+    rotary_dim = freq_ptr = 0
     if inv_freq is not None:
-        _req(inv_freq, torch.float64, "inv_freq", dev)
+        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev:
+            _mismatch(key_cache.device, inv_freq=(inv_freq, torch.float64))
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
-        rotary_dim = 2 * inv_freq.shape[0]
-        freq_ptr = inv_freq.data_ptr() if rotary_dim else None
-    cfg = _cache_config(q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim,
-                        1 if interleaved else 0, None, sb, st, sh, stride_q, stride_k, stride_v)
-    status = load_library().kda_kv_append(
-        cfg, q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, key_cache.data_ptr(),
-        value_cache.data_ptr(), freq_ptr, cu_seqlens.data_ptr(), B, T, ctypes.byref(align),
-        _ptr(error_word), _raw_stream(dev))
+        rotary_dim, freq_ptr = 2 * inv_freq.numel(), inv_freq.data_ptr()
+    status = load_library().kda_kv_append_packed(_APPEND_ARGS(
+        q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim, 1 if interleaved else 0, 1.0,
+        strides[0], strides[1], strides[2], stride_q, stride_k, stride_v, block_table.data_ptr(),
+        table_stride, width, block_size, requests, 0, num_computed.data_ptr(),
+        _address(request_indices), q_ptr, k.data_ptr(), v.data_ptr(), out_ptr,
+        key_cache.data_ptr(), value_cache.data_ptr(), freq_ptr, cu_seqlens.data_ptr(), B, T,
+        _address(error_word), _raw_stream(dev)))
     if status:
         raise KDAError("kda_kv_append", status)
     return q_out
@@ -859,8 +867,8 @@ def kda_attention_workspace_bytes(num_rows: int, q_heads: int, kv_heads: int, he
                                   window: int = MAX_WINDOW) -> int:
     """Size in bytes of the workspace of ``kda_window_attention``
     (``kda_attention_workspace_bytes``); 0 for sizes it does not support."""
-    cfg = _cache_config(q_heads, kv_heads, head_dim, 0, 1, window, 0, 0, 0, None, 8, 8, 8, 8, 8, 8)
-    return int(load_library().kda_attention_workspace_bytes(cfg, num_rows))
+    cfg = KdaCacheConfig(q_heads, kv_heads, head_dim, 0, 1, window, 0, 0, 0, 1.0, 8, 8, 8, 8, 8, 8)
+    return int(load_library().kda_attention_workspace_bytes(ctypes.byref(cfg), num_rows))
 
 
 def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, head_dim: int, device,
@@ -891,49 +899,51 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
     ``allocate_attention_workspace``.  Returns ``(out, lse)``: out [T, Hq, D]
     and the scores' log sum of exponentials, fp32 [T, Hq].  Rows that are
     skipped leave theirs untouched."""
-    dev, dtype, i32 = key_cache.device, key_cache.dtype, torch.int32
+    dev, dtype, i32 = key_cache.get_device(), key_cache.dtype, torch.int32
     code = DTYPES.get(dtype, 2)
     if code > 1:
         raise TypeError(f"key_cache must be bfloat16 or float16, got {dtype}")
     if (value_cache.dtype is not dtype or q.dtype is not dtype
             or workspace.dtype is not torch.uint8 or cu_seqlens.dtype is not i32
             or block_table.dtype is not i32 or num_computed.dtype is not i32
-            or value_cache.device != dev or q.device != dev or workspace.device != dev
-            or cu_seqlens.device != dev or block_table.device != dev
-            or num_computed.device != dev):
-        _mismatch(dev, value_cache=(value_cache, dtype), q=(q, dtype),
+            or value_cache.get_device() != dev or q.get_device() != dev
+            or workspace.get_device() != dev or cu_seqlens.get_device() != dev
+            or block_table.get_device() != dev or num_computed.get_device() != dev):
+        _mismatch(key_cache.device, value_cache=(value_cache, dtype), q=(q, dtype),
                   workspace=(workspace, torch.uint8), cu_seqlens=(cu_seqlens, i32),
                   block_table=(block_table, i32), num_computed=(num_computed, i32))
-    _opt(request_indices, i32, "request_indices", dev)
-    _opt(error_word, i32, "error_word", dev)
-    blocks, block_size, kv_heads, dim, sb, st, sh = _check_cache(key_cache, value_cache)
-    B, align = _plan(cu_seqlens, block_table, num_computed, request_indices, block_size,
-                     error_word)
+    if request_indices is not None or error_word is not None:
+        _mismatch(key_cache.device, request_indices=(request_indices, i32),
+                  error_word=(error_word, i32))
+    (blocks, block_size, kv_heads, dim), strides = _check_cache(key_cache, value_cache)
+    B, requests, width, table_stride = _plan(cu_seqlens, block_table, num_computed,
+                                             request_indices, error_word)
     T, q_heads, stride_q = _heads_tokens(q, "q", dim)
     if q_heads < 1 or q_heads % kv_heads:
         raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _req(out, dtype, "out", dev)
+        _req(out, dtype, "out", key_cache.device)
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and shaped like q")
     if lse is None:
         lse = q.new_empty((T, q_heads), dtype=torch.float32)
     else:
-        _req(lse, torch.float32, "lse", dev)
+        _req(lse, torch.float32, "lse", key_cache.device)
         if tuple(lse.shape) != (T, q_heads) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, Hq] tensor")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if T == 0:  # an empty tensor has no address to pass on
         return out, lse
-    cfg = _cache_config(q_heads, kv_heads, dim, code, blocks, window, left_window, 0, 0, scale,
-                        sb, st, sh, stride_q, 8, 8)
-    status = load_library().kda_window_attention(
-        cfg, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), cu_seqlens.data_ptr(), B,
-        ctypes.byref(align), workspace.data_ptr(), workspace.numel(), out.data_ptr(),
-        lse.data_ptr(), _ptr(error_word), _raw_stream(dev))
+    status = load_library().kda_window_attention_packed(_ATTENTION_ARGS(
+        q_heads, kv_heads, dim, code, blocks, window, left_window, 0, 0,
+        dim ** -0.5 if scale is None else scale, strides[0], strides[1], strides[2], stride_q, 8,
+        8, block_table.data_ptr(), table_stride, width, block_size, requests, 0,
+        num_computed.data_ptr(), _address(request_indices), q.data_ptr(), key_cache.data_ptr(),
+        value_cache.data_ptr(), cu_seqlens.data_ptr(), B, workspace.data_ptr(), workspace.numel(),
+        out.data_ptr(), lse.data_ptr(), _address(error_word), _raw_stream(dev)))
     if status:
         raise KDAError("kda_window_attention", status)
     return out, lse
@@ -964,22 +974,22 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
     negative: none, 0), entropy, log sum of exponentials and the ``num_top``
     largest logits (ties: the lower index) of each row of ``logits`` [rows,
     vocab], bf16, fp16 or fp32 with any row stride."""
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
     code = DTYPES.get(logits.dtype)
     if code is None:
         raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
-    if tokens.dtype is not i32 or tokens.device != dev:
-        _mismatch(dev, tokens=(tokens, i32))
+    if tokens.dtype is not i32 or tokens.get_device() != dev:
+        _mismatch(logits.device, tokens=(tokens, i32))
     if error_word is not None:
-        _req(error_word, i32, "error_word", dev)
+        _req(error_word, i32, "error_word", logits.device)
         _at_least(error_word, 1, "error_word")
-    if logits.dim() != 2:
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) != 2:
         raise ValueError("logits must be [rows, vocab]")
-    rows, vocab = logits.shape
-    stride, one = logits.stride()
-    if one != 1 and vocab > 1:
+    rows, vocab = shape
+    if strides[1] != 1 and vocab > 1:
         raise ValueError("logits must have contiguous columns")
-    if tokens.dim() != 1 or tokens.shape[0] != rows or not tokens.is_contiguous():
+    if tokens.dim() != 1 or tokens.numel() != rows or not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous with one entry per row")
     if out is None:
         out = TokenLogprobs(torch.empty_like(tokens, dtype=f32),
@@ -989,14 +999,15 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
                             tokens.new_empty((rows, num_top)))
     else:
         for name, t in zip(TokenLogprobs._fields, out):
-            _req(t, i32 if name == "top_index" else f32, name, dev)
+            _req(t, i32 if name == "top_index" else f32, name, logits.device)
             want = (rows, num_top) if name.startswith("top_") else (rows,)
             if tuple(t.shape) != want or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {want} tensor")
-    status = load_library().kda_token_logprobs(
-        logits.data_ptr(), code, stride, rows, vocab, tokens.data_ptr(), num_top,
-        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-        out[4].data_ptr(), _ptr(error_word), _raw_stream(dev))
+    logprob, entropy, lse, top_logprob, top_index = out
+    status = load_library().kda_token_logprobs_packed(_LOGPROBS_ARGS(
+        logits.data_ptr(), strides[0], code, rows, vocab, num_top, tokens.data_ptr(),
+        logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr(),
+        top_index.data_ptr(), _address(error_word), _raw_stream(dev)))
     if status:
         raise KDAError("kda_token_logprobs", status)
     return out

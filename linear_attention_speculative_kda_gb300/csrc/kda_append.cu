@@ -275,3 +275,10 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
             : (cfg->head_dim == 64 ? append_kernel<__half, 64> : append_kernel<__half, 128>);
     return kda_cache::launch(kernel, dim3((unsigned)grid), dim3(kThreads), 0, 1, stream, p);
 }
+
+extern "C" kda_status kda_kv_append_packed(const kda_append_args *a) {
+    if (a == nullptr) return KDA_ERR_INVALID_ARG;
+    return kda_kv_append(&a->config, a->q, a->k, a->v, a->q_out, a->key_cache, a->value_cache,
+                         a->inv_freq, a->cu_seqlens, a->B, a->num_tokens, &a->align, a->error_word,
+                         a->stream);
+}

@@ -1645,13 +1645,25 @@ kda_status launch_join(const Params &p, int grid, void *stream) {
 
 // ------------------------------------------------------------------- host --
 
+// Allows a kernel its shared memory, once per device (`done` is the kernel's).
+bool allow_shared(const void *kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && done[dev]) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return false;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return true;
+}
+
 template <typename T, int kDim, int kMT, int kMW, int kCtas>
 kda_status launch_attend(const Params &p, int sms, void *stream) {
     using L = Layout<kDim, kMT, kMW, kCtas>;
     const int grid = min(kCtas * sms, kMaxCtas);
     void (*kernel)(const Params) = attend_kernel<T, kDim, kMT, kMW, kCtas>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
-        cudaSuccess)
+    static bool allowed[64];
+    if (!allow_shared(reinterpret_cast<const void *>(kernel), L::kBytes, allowed))
         return KDA_ERR_CUDA;
     kda_status st = kda_cache::launch(kernel, dim3(grid), dim3(kThreads), L::kBytes, 1, stream, p);
     if (st != KDA_OK || grid == 1) return st;
@@ -1706,8 +1718,8 @@ kda_status launch_tc(const Params &p, const CUtensorMap &k_map, const CUtensorMa
     using F = tc::Form<kDim, kQRows>;
     void (*kernel)(const Params, const CUtensorMap, const CUtensorMap) =
         tc::attend_tc_kernel<T, kDim, kQRows>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kBytes) !=
-        cudaSuccess)
+    static bool allowed[64];
+    if (!allow_shared(reinterpret_cast<const void *>(kernel), F::kBytes, allowed))
         return KDA_ERR_CUDA;
     kda_status st = kda_cache::launch(kernel, dim3(grid), dim3(tc::kThreadCount), F::kBytes, 1,
                                       stream, p, k_map, v_map);
@@ -1821,6 +1833,13 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
                                    : launch_rows<__nv_bfloat16, 128>(p, sms, stream);
     return cfg->head_dim == 64 ? launch_rows<__half, 64>(p, sms, stream)
                                : launch_rows<__half, 128>(p, sms, stream);
+}
+
+kda_status kda_window_attention_packed(const kda_attention_args *a) {
+    if (a == nullptr || a->B < INT32_MIN || a->B > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    return kda_window_attention(&a->config, a->q, a->key_cache, a->value_cache, a->cu_seqlens,
+                                (int32_t)a->B, &a->align, a->workspace, a->workspace_bytes, a->out,
+                                a->lse, a->error_word, a->stream);
 }
 
 }  // extern "C"

@@ -521,3 +521,10 @@ extern "C" kda_status kda_token_logprobs(const void *logits, int32_t dtype, int6
     if (dtype == KDA_DTYPE_FP16) return launch_rows<__half>(p, rows, stream);
     return launch_rows<float>(p, rows, stream);
 }
+
+extern "C" kda_status kda_token_logprobs_packed(const kda_logprobs_args *a) {
+    if (a == nullptr) return KDA_ERR_INVALID_ARG;
+    return kda_token_logprobs(a->logits, a->dtype, a->stride_row, a->rows, a->vocab, a->tokens,
+                              a->num_top, a->logprob, a->entropy, a->lse_out, a->top_logprob,
+                              a->top_index, a->error_word, a->stream);
+}

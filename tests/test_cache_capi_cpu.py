@@ -218,3 +218,61 @@ def test_binding_refuses_bad_logprob_arguments(lib):
         api.kda_token_logprobs(x.t(), torch.zeros(50, dtype=torch.int32))
     with pytest.raises(ValueError):
         api.kda_token_logprobs(x, tokens, num_top=2, out=api.allocate_token_logprobs(3, 1, "cpu"))
+
+
+def test_packed_calls_read_their_fields(lib):
+    # each field where it belongs: breaking one gives the status that the call
+    # with separate arguments gives, and only then
+    def append(**change):
+        f = dict(q_heads=8, kv_heads=2, head_dim=128, dtype=0, num_blocks=9, window=1,
+                 left_window=0, rotary_dim=64, interleaved=0, scale=1.0, stride_block=4096,
+                 stride_token=256, stride_head=128, stride_q=1536, stride_k=1536, stride_v=1536,
+                 table=FAKE, table_stride=8, width=8, block_size=16, requests=4, reserved=0,
+                 computed=FAKE, request_indices=0, q=FAKE, k=FAKE, v=FAKE, q_out=FAKE, keys=FAKE,
+                 values=FAKE, freq=FAKE, cu=FAKE, B=3, T=5, err=0, stream=0)
+        f.update(change)
+        return lib.kda_kv_append_packed(api._APPEND_ARGS(*f.values()))
+
+    def attend(**change):
+        f = dict(q_heads=8, kv_heads=2, head_dim=128, dtype=0, num_blocks=9, window=4,
+                 left_window=0, rotary_dim=0, interleaved=0, scale=0.1, stride_block=4096,
+                 stride_token=256, stride_head=128, stride_q=1536, stride_k=8, stride_v=8,
+                 table=FAKE, table_stride=8, width=8, block_size=16, requests=4, reserved=0,
+                 computed=FAKE, request_indices=0, q=FAKE, keys=FAKE, values=FAKE, cu=FAKE, B=3,
+                 work=FAKE, size=1 << 40, out=FAKE, lse=0, err=0, stream=0)
+        f.update(change)
+        return lib.kda_window_attention_packed(api._ATTENTION_ARGS(*f.values()))
+
+    def logprobs(**change):
+        f = dict(logits=FAKE, stride=100, dtype=0, rows=3, vocab=100, top=4, tokens=FAKE, lp=FAKE,
+                 ent=FAKE, lse=FAKE, tv=FAKE, ti=FAKE, err=0, stream=0)
+        f.update(change)
+        return lib.kda_token_logprobs_packed(api._LOGPROBS_ARGS(*f.values()))
+
+    assert append(B=0) == OK and append(T=0) == OK
+    assert attend(B=0) == OK and logprobs(rows=0) == OK
+    common = [dict(q_heads=7), dict(kv_heads=0), dict(dtype=3), dict(num_blocks=0),
+              dict(stride_block=4), dict(stride_token=0), dict(stride_head=129), dict(stride_q=4),
+              dict(table=0), dict(table_stride=7), dict(width=0), dict(block_size=0),
+              dict(requests=0), dict(reserved=1), dict(computed=FAKE + 1),
+              dict(request_indices=FAKE + 2), dict(q=FAKE + 8), dict(keys=0), dict(values=FAKE + 8),
+              dict(cu=FAKE + 2), dict(B=-1), dict(err=FAKE + 1)]
+    for change in common:
+        assert append(**change) == BAD, change
+        assert attend(**change) == BAD, change
+    assert append(head_dim=96) == UNSUPPORTED and attend(head_dim=96) == UNSUPPORTED
+    for change in (dict(rotary_dim=24), dict(interleaved=2), dict(stride_k=0), dict(stride_v=4),
+                   dict(k=0), dict(v=FAKE + 8), dict(q_out=0), dict(freq=FAKE + 4), dict(T=-1)):
+        assert append(**change) == BAD, change
+    for change in (dict(window=0), dict(left_window=-1), dict(scale=float("nan")), dict(work=0),
+                   dict(size=64), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(B=1 << 40)):
+        assert attend(**change) == BAD, change
+    assert attend(window=9) == UNSUPPORTED
+    for change in (dict(logits=0), dict(stride=-1), dict(dtype=3), dict(rows=-1), dict(vocab=0),
+                   dict(top=101), dict(tokens=FAKE + 1), dict(lp=0), dict(ent=FAKE + 1),
+                   dict(lse=FAKE + 1), dict(tv=0), dict(ti=FAKE + 2), dict(err=FAKE + 2)):
+        assert logprobs(**change) == BAD, change
+    assert logprobs(top=33) == UNSUPPORTED
+    assert lib.kda_kv_append_packed(None) == BAD
+    assert lib.kda_window_attention_packed(None) == BAD
+    assert lib.kda_token_logprobs_packed(None) == BAD
