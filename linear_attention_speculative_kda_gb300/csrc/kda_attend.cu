@@ -419,6 +419,36 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
 
     for (int i = 0; i < kStages - 1; ++i) load_tile(i);
 
+    // A segment's queries (rows past the last one: zeros), a batch of loads in
+    // flight together: one after the other they took most of the 10 us that 64
+    // rows cost beside their tiles.
+    constexpr int kEach = L::kRows * kChunks / kThreads, kBatch = kEach < 8 ? kEach : 8;
+    constexpr int kBatches = kEach / kBatch;
+    constexpr bool kAhead = kEach <= 4;
+    uint4 queries[kBatch];
+    auto fetch_queries = [&](const Cursor &c, int batch) {
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int i = (batch * kBatch + n) * kThreads + tid, r = i / kChunks;
+            queries[n] = make_uint4(0, 0, 0, 0);
+            if (r < c.row.tokens * p.group) {
+                const int t = token_of(p, r), h = c.head * p.group + r - t * p.group;
+                queries[n] = __ldg(reinterpret_cast<const uint4 *>(
+                    reinterpret_cast<const T *>(p.q) + (c.row.first + t) * p.stride_q +
+                    (long long)h * kDim + i % kChunks * 8));
+            }
+        }
+    };
+    auto store_queries = [&](int batch) {
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int i = (batch * kBatch + n) * kThreads + tid;
+            const uint4 x = queries[n];
+            *reinterpret_cast<uint4 *>(shared_area + swizzled<kDim>(i / kChunks, i % kChunks)) =
+                make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip);
+        }
+    };
+
     int slot = 0;            // ring slot of the tile to compute
     int piece_first = 1;     // whether the segment is this run's first
     while (left > 0) {
@@ -428,30 +458,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         const int partial_slot = 2 * cta + (piece_first ? 0 : 1);
         const int rows = at.row.tokens * p.group;
         const bool busy = mwarp * 16 * kMT < rows;  // whether this warp has query rows
-        // queries to shared memory (rows past the last one: zeros)
-        // (a batch's loads are in flight together: one after the other they
-        // took most of the 10 us that 64 rows cost beside their tiles)
-        constexpr int kEach = L::kRows * kChunks / kThreads, kBatch = kEach < 8 ? kEach : 8;
+        // queries to shared memory; few enough are here already, fetched while
+        // the segment before was joined
+        if (!kAhead || piece_first) fetch_queries(at, 0);
+        store_queries(0);
 #pragma unroll 1
-        for (int n0 = 0; n0 < kEach; n0 += kBatch) {
-            uint4 x[kBatch];
-#pragma unroll
-            for (int n = 0; n < kBatch; ++n) {
-                const int i = (n0 + n) * kThreads + tid, r = i / kChunks;
-                x[n] = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int t = token_of(p, r), h = at.head * p.group + r - t * p.group;
-                    x[n] = __ldg(reinterpret_cast<const uint4 *>(
-                        reinterpret_cast<const T *>(p.q) + (at.row.first + t) * p.stride_q +
-                        (long long)h * kDim + i % kChunks * 8));
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < kBatch; ++n) {
-                const int i = (n0 + n) * kThreads + tid;
-                *reinterpret_cast<uint4 *>(shared_area + swizzled<kDim>(i / kChunks, i % kChunks)) =
-                    make_uint4(x[n].x ^ p.flip, x[n].y ^ p.flip, x[n].z ^ p.flip, x[n].w ^ p.flip);
-            }
+        for (int batch = 1; batch < kBatches; ++batch) {
+            fetch_queries(at, batch);
+            store_queries(batch);
         }
         __syncthreads();
         const uint32_t q_addr = kda::smem_u32(shared_area);
@@ -706,6 +720,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
             slot = slot + 1 == kStages ? 0 : slot + 1;
         }
 
+        // the next segment, and its queries on their way
+        Cursor next = at;
+        if (left > tiles) {
+            next.next_segment(p);
+            if (kAhead) fetch_queries(next, 0);
+        }
+
         // ------------------------------------------- the groups' sums joined
 #pragma unroll
         for (int a = 0; a < kMT; ++a)
@@ -814,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         }
         left -= tiles;
         piece_first = 0;
-        if (left > 0) at.next_segment(p);
+        at = next;
     }
     cp_async_wait<0>();
 }
