@@ -398,11 +398,12 @@ kda_status kda_record_state_blocks(const kda_align *align,
  * masked (a cache that lets go of blocks behind a sliding window points their
  * entries at it).  An entry >= num_blocks flags KDA_ROW_BAD_SLOT and is
  * treated as the null block.  A row is skipped (its outputs and cache left
- * alone) and flagged when its token count is negative, or above cfg->window
- * in kda_window_attention (KDA_ROW_BAD_LENGTH), and when its request index is
- * outside [0, num_requests), its num_computed negative or its last position
- * past the table's last column (KDA_ROW_BAD_BLOCK).  Rows without tokens are
- * skipped silently.
+ * alone) and flagged when its token count is negative, above cfg->window in
+ * kda_window_attention, or its tokens reach past num_tokens, the tokens that
+ * q, k and v have (KDA_ROW_BAD_LENGTH), and when its request index is outside
+ * [0, num_requests), its num_computed negative or its last position past the
+ * table's last column (KDA_ROW_BAD_BLOCK).  Rows without tokens are skipped
+ * silently.
  */
 #define KDA_DTYPE_BF16 0
 #define KDA_DTYPE_FP16 1
@@ -448,8 +449,8 @@ typedef struct kda_cache_config {
  * q_out: [num_tokens][Hq][D] contiguous, or q itself when its stride is
  * Hq * D; not used when q is NULL.  inv_freq: fp64 [rotary_dim / 2], device,
  * radians per position (unused when rotary_dim == 0).  Rows may have any
- * number of tokens (prompts included); num_tokens bounds cu_seqlens, and
- * tokens past it or outside every row are left alone.  B == 0 or num_tokens
+ * number of tokens (prompts included); tokens outside every row are left
+ * alone.  B == 0 or num_tokens
  * == 0: KDA_OK, nothing inspected.  Two tokens of one call must not share a
  * cache slot.
  */
@@ -482,15 +483,16 @@ size_t kda_attention_workspace_bytes(const kda_cache_config *cfg, int32_t B);
  * [T][Hq] or NULL.  workspace: workspace_bytes >=
  * kda_attention_workspace_bytes, 16-byte aligned, not read before it is
  * written.  The work is split over the rows' lengths, so few long rows fill
- * the GPU as many short ones do; results do not depend on timing.  B == 0:
- * KDA_OK, nothing inspected.  window * Hq / Hkv above KDA_MAX_QUERY_ROWS:
+ * the GPU as many short ones do; results do not depend on timing.  B == 0 or
+ * num_tokens == 0: KDA_OK, nothing inspected.  A wait of the tensor-core form
+ * that runs out (about 2 s) flags KDA_ERR_WAIT_TIMEOUT.  window * Hq / Hkv above KDA_MAX_QUERY_ROWS:
  * KDA_ERR_UNSUPPORTED.
  */
 kda_status kda_window_attention(const kda_cache_config *cfg, const void *q,
                                 const void *key_cache, const void *value_cache,
-                                const int32_t *cu_seqlens, int32_t B, const kda_align *align,
-                                void *workspace, size_t workspace_bytes, void *out, float *lse,
-                                int32_t *error_word, void *stream);
+                                const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
+                                const kda_align *align, void *workspace, size_t workspace_bytes,
+                                void *out, float *lse, int32_t *error_word, void *stream);
 
 /*
  * kda_token_logprobs -- log probability of a given token, entropy and the
@@ -542,7 +544,7 @@ typedef struct kda_attention_args {
     kda_align align;
     const void *q, *key_cache, *value_cache;
     const int32_t *cu_seqlens;
-    int64_t B;
+    int32_t B, num_tokens;
     void *workspace;
     uint64_t workspace_bytes;
     void *out;

@@ -198,7 +198,7 @@ def bind_library(path: str):
     lib.kda_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_attention_workspace_bytes.argtypes = [ccp, i32]
     lib.kda_window_attention.restype = ctypes.c_int
-    lib.kda_window_attention.argtypes = ([ccp] + [vp] * 4 + [i32, alp, vp, ctypes.c_size_t] +
+    lib.kda_window_attention.argtypes = ([ccp] + [vp] * 4 + [i32, i32, alp, vp, ctypes.c_size_t] +
                                          [vp] * 4)
     lib.kda_token_logprobs.restype = ctypes.c_int
     lib.kda_token_logprobs.argtypes = [vp, i32, ctypes.c_int64, i32, i32, vp, i32] + [vp] * 7
@@ -720,7 +720,7 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
 
 _CACHE_FORMAT = "9if6qQqiiiiQQ"     # kda_cache_config, kda_align
 _APPEND_ARGS = struct.Struct("=" + _CACHE_FORMAT + "8Q2i2Q").pack
-_ATTENTION_ARGS = struct.Struct("=" + _CACHE_FORMAT + "4Qq6Q").pack
+_ATTENTION_ARGS = struct.Struct("=" + _CACHE_FORMAT + "4Q2i6Q").pack
 _LOGPROBS_ARGS = struct.Struct("=Qq4i8Q").pack
 
 
@@ -942,7 +942,8 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
         dim ** -0.5 if scale is None else scale, strides[0], strides[1], strides[2], stride_q, 8,
         8, block_table.data_ptr(), table_stride, width, block_size, requests, 0,
         num_computed.data_ptr(), _address(request_indices), q.data_ptr(), key_cache.data_ptr(),
-        value_cache.data_ptr(), cu_seqlens.data_ptr(), B, workspace.data_ptr(), workspace.numel(),
+        value_cache.data_ptr(), cu_seqlens.data_ptr(), B, T, workspace.data_ptr(),
+        workspace.numel(),
         out.data_ptr(), lse.data_ptr(), _address(error_word), _raw_stream(dev)))
     if status:
         raise KDAError("kda_window_attention", status)

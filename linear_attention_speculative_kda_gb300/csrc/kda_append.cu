@@ -223,7 +223,7 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
         return KDA_ERR_INVALID_ARG;
     if (B == 0 || num_tokens == 0) return KDA_OK;  // nothing to do; no pointer is inspected
     Params p;
-    st = kda_cache::set_rows(cfg, align, cu_seqlens, B, error_word, p.rows);
+    st = kda_cache::set_rows(cfg, align, cu_seqlens, B, num_tokens, error_word, p.rows);
     if (st != KDA_OK) return st;
     if (!k || !v || !key_cache || !value_cache || (q != nullptr && !q_out) ||
         (cfg->rotary_dim > 0 && !inv_freq))

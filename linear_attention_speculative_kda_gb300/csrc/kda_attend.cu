@@ -236,7 +236,8 @@ __device__ __forceinline__ Run plan(const Params &p, PlanScratch &sc) {
     const int b0 = min(p.rows.B, tid * per), b1 = min(p.rows.B, b0 + per);
     long long mine = 0;
     int bits = 0;
-    for (int b = b0; b < b1; ++b) mine += tile_count(p, b, bits);
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += tile_count(p, b, bits);  // the loads overlap
     if (bits != 0 && blockIdx.x == 0) kda_cache::flag(p.rows.err, bits);
     long long upto = mine;
 #pragma unroll
@@ -866,7 +867,11 @@ constexpr int kThreadCount = 32 * kWarpCount;
 constexpr int kRows = 128;
 constexpr int kCtasPerSm = 2;
 constexpr int kTmemColumns = 256;                 // two CTAs per SM share 512
+#ifdef KDA_TEST_ATTENTION_WAIT_BUDGET  // a test build: a wait that runs out, soon
+constexpr long long kWaitBudget = KDA_TEST_ATTENTION_WAIT_BUDGET;
+#else
 constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
+#endif
 
 template <int kDim, int kQRows>
 struct Form {
@@ -1106,12 +1111,11 @@ __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Cont
             }
         }
     }
-    if (!ok) {  // another wait ran out: no copy may outlive the CTA
-        for (long long j = loaded > F::kStages ? loaded - F::kStages : 0; j < loaded; ++j)
-            kda::mbar_wait_bounded(&c.full[j % F::kStages], (uint32_t)((j / F::kStages) & 1),
-                                   kWaitBudget);
-        __syncwarp();
-    }
+    // no copy may outlive the CTA, whatever became of its users
+    for (long long j = loaded > F::kStages ? loaded - F::kStages : 0; j < loaded; ++j)
+        kda::mbar_wait_bounded(&c.full[j % F::kStages], (uint32_t)((j / F::kStages) & 1),
+                               kWaitBudget);
+    __syncwarp();
 }
 
 // ---- the query warp -------------------------------------------------------
@@ -1141,6 +1145,9 @@ __device__ __forceinline__ void run_queries(const Params &p, const Run &run, Con
         cp_async_wait<0>();
         kda::fence_proxy_async_smem();
         __syncwarp();
+#ifdef KDA_TEST_ATTENTION_WAIT_BUDGET
+        if (blockIdx.x == 0) break;  // CTA 0's queries are never handed over
+#endif
         if (lane == 0) kda::mbar_arrive(&c.q_full);
         left -= min(left, (long long)(at.end - at.tile));
         if (left == 0) break;
@@ -1766,12 +1773,11 @@ kda_status launch_rows(Params &p, int sms, void *stream) {
     p.box = kTile;
     while (p.rows.block_size % p.box != 0) p.box /= 2;
     if (p.most_rows > (kDim == 128 ? 32 : 64) && p.box * kDim >= 1024) {
-        CUtensorMap k_map, v_map;
-        if (!cache_map<T, kDim>(p, p.key_cache, &k_map) ||
-            !cache_map<T, kDim>(p, p.value_cache, &v_map))
-            return KDA_ERR_CUDA;
-        return p.most_rows <= 64 ? launch_tc<T, kDim, 64>(p, k_map, v_map, sms, stream)
-                                 : launch_tc<T, kDim, 128>(p, k_map, v_map, sms, stream);
+        CUtensorMap k_map, v_map;  // (a cache they cannot describe goes the other way)
+        if (cache_map<T, kDim>(p, p.key_cache, &k_map) &&
+            cache_map<T, kDim>(p, p.value_cache, &v_map))
+            return p.most_rows <= 64 ? launch_tc<T, kDim, 64>(p, k_map, v_map, sms, stream)
+                                     : launch_tc<T, kDim, 128>(p, k_map, v_map, sms, stream);
     }
     // With 64 channels and 32 or 64 rows three CTAs fit an SM, which measured
     // 43 and 58 us with two (39 and 52 with three); with 16 rows two measured
@@ -1809,15 +1815,16 @@ size_t kda_attention_workspace_bytes(const kda_cache_config *cfg, int32_t B) {
 
 kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, const void *key_cache,
                                 const void *value_cache, const int32_t *cu_seqlens, int32_t B,
-                                const kda_align *align, void *workspace, size_t workspace_bytes,
-                                void *out, float *lse, int32_t *error_word, void *stream) {
+                                int32_t num_tokens, const kda_align *align, void *workspace,
+                                size_t workspace_bytes, void *out, float *lse,
+                                int32_t *error_word, void *stream) {
     using kda_cache::aligned;
     kda_status st = check_attention(cfg);
     if (st != KDA_OK) return st;
-    if (B < 0) return KDA_ERR_INVALID_ARG;
-    if (B == 0) return KDA_OK;  // nothing to do; no pointer is inspected
+    if (B < 0 || num_tokens < 0) return KDA_ERR_INVALID_ARG;
+    if (B == 0 || num_tokens == 0) return KDA_OK;  // nothing to do; no pointer is inspected
     Params p;
-    st = kda_cache::set_rows(cfg, align, cu_seqlens, B, error_word, p.rows);
+    st = kda_cache::set_rows(cfg, align, cu_seqlens, B, num_tokens, error_word, p.rows);
     if (st != KDA_OK) return st;
     if (!q || !key_cache || !value_cache || !out || !workspace) return KDA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
@@ -1857,9 +1864,9 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
 }
 
 kda_status kda_window_attention_packed(const kda_attention_args *a) {
-    if (a == nullptr || a->B < INT32_MIN || a->B > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if (a == nullptr) return KDA_ERR_INVALID_ARG;
     return kda_window_attention(&a->config, a->q, a->key_cache, a->value_cache, a->cu_seqlens,
-                                (int32_t)a->B, &a->align, a->workspace, a->workspace_bytes, a->out,
+                                a->B, a->num_tokens, &a->align, a->workspace, a->workspace_bytes, a->out,
                                 a->lse, a->error_word, a->stream);
 }
 

@@ -37,7 +37,7 @@ struct Rows {
     const int *cu_seqlens;
     const int *block_table, *num_computed, *request_indices;
     long long bt_stride;
-    int B, bt_width, block_size, num_requests, num_blocks;
+    int B, num_tokens, bt_width, block_size, num_requests, num_blocks;
     Divider by_block;
     int *err;
 };
@@ -63,7 +63,7 @@ __device__ __forceinline__ Row read_row(const Rows &r, int b, int most, int &bit
     Row row{first, 0, computed, request};
     const long long n = (long long)end - first, last = (long long)computed + n - 1;
     if (n == 0) return row;
-    if (n < 0 || n > most || first < 0)
+    if (n < 0 || n > most || first < 0 || end > r.num_tokens)
         bits |= KDA_ROW_BAD_LENGTH;
     else if (!known || computed < 0 || last > 0x7ffffff0LL ||
              divide((int)last, r.by_block) >= r.bt_width)
@@ -103,7 +103,7 @@ inline kda_status check_config(const kda_cache_config *c) {
 }
 
 inline kda_status set_rows(const kda_cache_config *c, const kda_align *al, const int32_t *cu_seqlens,
-                           int32_t B, int32_t *error_word, Rows &r) {
+                           int32_t B, int32_t num_tokens, int32_t *error_word, Rows &r) {
     if (al == nullptr || al->reserved != 0) return KDA_ERR_INVALID_ARG;
     if (!cu_seqlens || !al->block_table || !al->num_computed) return KDA_ERR_INVALID_ARG;
     if (al->block_table_width < 1 || al->block_table_stride < al->block_table_width ||
@@ -120,6 +120,7 @@ inline kda_status set_rows(const kda_cache_config *c, const kda_align *al, const
     r.request_indices = al->request_indices;
     r.bt_stride = al->block_table_stride;
     r.B = B;
+    r.num_tokens = num_tokens;
     r.bt_width = al->block_table_width;
     r.block_size = al->block_size;
     r.num_requests = al->num_requests;

@@ -9,13 +9,15 @@ from __future__ import annotations
 import numpy as np
 
 
-def plan_row(cu, b, computed, width, block_size, num_requests, requests=None, window=None):
+def plan_row(cu, b, computed, width, block_size, num_requests, requests=None, window=None,
+             num_tokens=None):
     """(first token, token count, position of the first, request) of row b, or
     the name of what is wrong with it ("" for an empty row)."""
     first, n = int(cu[b]), int(cu[b + 1]) - int(cu[b])
     if n == 0:
         return ""
-    if n < 0 or first < 0 or (window is not None and n > window):
+    if (n < 0 or first < 0 or (window is not None and n > window)
+            or (num_tokens is not None and first + n > num_tokens)):
         return "length"
     q = b if requests is None else int(requests[b])
     if not 0 <= q < num_requests:
@@ -49,7 +51,8 @@ def append(q, k, v, keys, values, cu, table, computed, inv_freq=(), interleaved=
     touched = np.zeros((blocks, bs), dtype=bool)
     issues = []
     for b in range(len(cu) - 1):
-        row = plan_row(cu, b, computed, table.shape[1], bs, table.shape[0], requests)
+        row = plan_row(cu, b, computed, table.shape[1], bs, table.shape[0], requests,
+                       num_tokens=len(k))
         if isinstance(row, str):
             if row:
                 issues.append((b, row))
@@ -84,7 +87,8 @@ def attend(q, keys, values, cu, table, computed, scale, window=8, left_window=0,
     spread = np.zeros(q.shape[:2])
     issues = []
     for b in range(len(cu) - 1):
-        row = plan_row(cu, b, computed, table.shape[1], bs, table.shape[0], requests, window)
+        row = plan_row(cu, b, computed, table.shape[1], bs, table.shape[0], requests, window,
+                       len(q))
         if isinstance(row, str):
             if row:
                 issues.append((b, row))

@@ -47,7 +47,7 @@ def _append(lib, cfg=None, al=None, B=3, T=5, **ptrs):
                              alp, p["err"], None)
 
 
-def _attend(lib, cfg=None, al=None, B=3, size=None, **ptrs):
+def _attend(lib, cfg=None, al=None, B=3, T=5, size=None, **ptrs):
     p = dict(q=FAKE, keys=FAKE, values=FAKE, cu=FAKE, work=FAKE, out=FAKE, lse=None, err=None)
     p.update(ptrs)
     cfg = _cfg() if cfg is None else cfg
@@ -55,7 +55,7 @@ def _attend(lib, cfg=None, al=None, B=3, size=None, **ptrs):
     alp = ctypes.byref(_align() if al is None else al) if al is not False else None
     if size is None:
         size = 1 << 40
-    return lib.kda_window_attention(cfgp, p["q"], p["keys"], p["values"], p["cu"], B, alp,
+    return lib.kda_window_attention(cfgp, p["q"], p["keys"], p["values"], p["cu"], B, T, alp,
                                     p["work"], size, p["out"], p["lse"], p["err"], None)
 
 
@@ -116,7 +116,8 @@ def test_attention_refusals(lib):
     assert _attend(lib, _cfg(window=8, q_heads=34)) == UNSUPPORTED     # 8 * 17 query rows
     need = lib.kda_attention_workspace_bytes(ctypes.byref(_cfg()), 3)
     assert need > 0 and _attend(lib, size=need - 1) == BAD
-    assert _attend(lib, B=-1) == BAD
+    assert _attend(lib, B=-1) == BAD and _attend(lib, T=-1) == BAD
+    assert _attend(lib, T=0, al=False, q=None, work=None, size=0) == OK
     assert _attend(lib, B=0, al=False, q=None, work=None, size=0) == OK
     assert lib.kda_attention_workspace_bytes(ctypes.byref(_cfg(window=9)), 3) == 0
     assert lib.kda_attention_workspace_bytes(None, 3) == 0
@@ -239,7 +240,7 @@ def test_packed_calls_read_their_fields(lib):
                  stride_token=256, stride_head=128, stride_q=1536, stride_k=8, stride_v=8,
                  table=FAKE, table_stride=8, width=8, block_size=16, requests=4, reserved=0,
                  computed=FAKE, request_indices=0, q=FAKE, keys=FAKE, values=FAKE, cu=FAKE, B=3,
-                 work=FAKE, size=1 << 40, out=FAKE, lse=0, err=0, stream=0)
+                 T=5, work=FAKE, size=1 << 40, out=FAKE, lse=0, err=0, stream=0)
         f.update(change)
         return lib.kda_window_attention_packed(api._ATTENTION_ARGS(*f.values()))
 
@@ -250,7 +251,7 @@ def test_packed_calls_read_their_fields(lib):
         return lib.kda_token_logprobs_packed(api._LOGPROBS_ARGS(*f.values()))
 
     assert append(B=0) == OK and append(T=0) == OK
-    assert attend(B=0) == OK and logprobs(rows=0) == OK
+    assert attend(B=0) == OK and attend(T=0) == OK and logprobs(rows=0) == OK
     common = [dict(q_heads=7), dict(kv_heads=0), dict(dtype=3), dict(num_blocks=0),
               dict(stride_block=4), dict(stride_token=0), dict(stride_head=129), dict(stride_q=4),
               dict(table=0), dict(table_stride=7), dict(width=0), dict(block_size=0),
@@ -265,7 +266,7 @@ def test_packed_calls_read_their_fields(lib):
                    dict(k=0), dict(v=FAKE + 8), dict(q_out=0), dict(freq=FAKE + 4), dict(T=-1)):
         assert append(**change) == BAD, change
     for change in (dict(window=0), dict(left_window=-1), dict(scale=float("nan")), dict(work=0),
-                   dict(size=64), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(B=1 << 40)):
+                   dict(size=64), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(T=-1)):
         assert attend(**change) == BAD, change
     assert attend(window=9) == UNSUPPORTED
     for change in (dict(logits=0), dict(stride=-1), dict(dtype=3), dict(rows=-1), dict(vocab=0),

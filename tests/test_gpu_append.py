@@ -128,3 +128,9 @@ def test_empty_calls():
     api.kda_kv_append(c.q, c.k, c.v, c.keys, c.values, none, c.table, c.computed)
     torch.cuda.synchronize()
     assert torch.equal(before, c.keys)
+
+
+def test_rows_that_reach_past_the_tokens():
+    c = Case([3, 2, 4], [0, 1, 7], 4, 2, 64, 8, seed=8)
+    c.q, c.k, c.v = c.q[:8], c.k[:8], c.v[:8]     # the last row's last token is not there
+    _check(c, 64, True, want_err=api.ROW_BAD_LENGTH)

@@ -286,3 +286,23 @@ def test_many_segments_of_every_length(group, window):
     c = Case(lens, computed, 3 * group, 3, 64, 16, seed=21)
     _check(c, window)
     _check(c, window, left_window=37)
+
+
+@pytest.mark.parametrize("group,window", [(1, 4), (12, 4)])
+def test_rows_that_reach_past_the_tokens(group, window):
+    c = Case([window, 2, 3], [20, 5, 70], 2 * group, 2, 128, 16, seed=22)
+    total = c.q.shape[0]
+    c.q = c.q[:total - 1]          # the last row's last token is not there
+    _check(c, window, want_err=api.ROW_BAD_LENGTH)
+    c = Case([window, 2, 3], [20, 5, 70], 2 * group, 2, 128, 16, seed=22)
+    c.cu[0] = -1                   # a row that starts before the first token
+    _check(c, window, want_err=api.ROW_BAD_LENGTH)
+
+
+@pytest.mark.parametrize("group,window", [(1, 1), (16, 4)])
+def test_thousands_of_rows(group, window):
+    rng = np.random.default_rng(9)
+    lens = rng.integers(0, window + 1, size=3000).tolist()
+    computed = rng.integers(0, 20, size=3000).tolist()
+    c = Case(lens, computed, group, 1, 64, 16, seed=23)
+    _check(c, window)
