@@ -726,7 +726,10 @@ _LOGPROBS_ARGS = struct.Struct("=Qq4i8Q").pack
 
 def _raw_stream(device: int):
     # the handle torch.cuda.current_stream(device).cuda_stream holds, without
-    # building the stream object
+    # building the stream object; -1 is a host tensor's device, whose addresses
+    # no kernel may be given
+    if device < 0:
+        raise ValueError("the tensors must be on a GPU")
     return torch._C._cuda_getCurrentRawStream(device)
 
 
@@ -928,7 +931,7 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and shaped like q")
     if lse is None:
-        lse = q.new_empty((T, q_heads), dtype=torch.float32)
+        lse = torch.empty((T, q_heads), dtype=torch.float32, device=q.device)
     else:
         _req(lse, torch.float32, "lse", key_cache.device)
         if tuple(lse.shape) != (T, q_heads) or not lse.is_contiguous():
@@ -996,8 +999,8 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
         out = TokenLogprobs(torch.empty_like(tokens, dtype=f32),
                             torch.empty_like(tokens, dtype=f32),
                             torch.empty_like(tokens, dtype=f32),
-                            tokens.new_empty((rows, num_top), dtype=f32),
-                            tokens.new_empty((rows, num_top)))
+                            torch.empty((rows, num_top), dtype=f32, device=tokens.device),
+                            torch.empty((rows, num_top), dtype=i32, device=tokens.device))
     else:
         for name, t in zip(TokenLogprobs._fields, out):
             _req(t, i32 if name == "top_index" else f32, name, logits.device)
