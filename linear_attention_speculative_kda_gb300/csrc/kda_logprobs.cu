@@ -10,11 +10,13 @@
 //
 // Alternatives without a second pass: each thread's running maximum is kept
 // anyway, and those of 16 stretches of its elements beside it.  The k-th
-// largest of the best maxima of each warp is a lower bound of the k-th largest
-// logit, so only stretches whose maximum reaches it can hold one of the top k:
-// little more than k of them.  Their elements are read once more (from L2),
-// what reaches the bound becomes a candidate, and a candidate's place is the
-// number of candidates before it.  (Reading all elements of the threads that
+// largest of the maxima of 64 groups of threads is a lower bound of the k-th
+// largest logit, so only stretches whose maximum reaches it can hold one of
+// the top k: little more than k of them.  (Of 32 groups the 32nd is too weak a
+// bound, and the lists overflow: 32 alternatives of 131072 in 256 rows 78 us,
+// not 24.)  Their elements are read once more (from L2), what reaches the
+// bound becomes a candidate, and a candidate's place is the number of
+// candidates before it.  (Reading all elements of the threads that
 // reach it again took as long as the row itself for 20 alternatives.)  Where
 // that leaves too many (rows of equal or masked values), warps insert what
 // qualifies into lists sorted across the lanes: one more pass over the row and
@@ -39,6 +41,8 @@ using kda_cache::kFull;
 
 constexpr int kCandidates = 512;
 constexpr int kStretches = 16;    // parts of a thread's elements whose maxima are kept
+constexpr int kMaxima = 64;       // groups of threads whose maxima give the bound
+constexpr int kFew = 64;          // keys of a cluster that are compared with each other
 constexpr int kListed = 128;      // (thread, stretch) pairs that are read again
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
@@ -248,30 +252,23 @@ __device__ __forceinline__ Stats warp_join(Stats a) {
     return Stats{m, a.s, a.w};
 }
 
-// Sorted across the lanes, the largest in lane 0 (a bitonic network).
-__device__ __forceinline__ float warp_sort(float v, int lane) {
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int o = size >> 1; o > 0; o >>= 1) {
-            const float u = __shfl_xor_sync(kFull, v, o);
-            const bool larger = ((lane & size) == 0) == ((lane & o) == 0);
-            v = larger ? fmaxf(v, u) : fminf(v, u);
-        }
-    return v;
-}
-
 // A logit and its index as one number that orders by value, then by the lower
 // index; a NaN counts as -inf, and 0 comes after every logit.
-__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+__device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t b = __float_as_uint((v == v ? v : -INFINITY) + 0.0f);
-    const uint32_t order = (b >> 31) != 0 ? ~b : b | 0x80000000u;
-    return (unsigned long long)order << 32 | (uint32_t)~i;
+    return (b >> 31) != 0 ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of_order(uint32_t order) {
+    return __uint_as_float((order >> 31) != 0 ? order & 0x7fffffffu : ~order);
+}
+
+__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+    return (unsigned long long)order_of(v) << 32 | (uint32_t)~i;
 }
 
 __device__ __forceinline__ float value_of(unsigned long long key) {
-    const uint32_t order = (uint32_t)(key >> 32);
-    return __uint_as_float((order >> 31) != 0 ? order & 0x7fffffffu : ~order);
+    return value_of_order((uint32_t)(key >> 32));
 }
 
 __device__ __forceinline__ int index_of(unsigned long long key) { return (int)~(uint32_t)key; }
@@ -301,7 +298,8 @@ template <int kWarps, bool kTop>
 struct Shared {
     Stats stats[kWarps];
     Stats row;                        // this CTA's, for the cluster
-    float maxima[32];
+    alignas(16) uint32_t maxima[kMaxima];
+    float bound;                      // a lower bound of the k-th largest logit
     int listed;                       // pairs that reach the bound
     int candidates;
     int list[kListed];                // thread * kStretches + stretch
@@ -326,6 +324,35 @@ __device__ __forceinline__ void place(Shared<kWarps, true> &sh, int n, int k) {
             rank += (two.x > key ? 1 : 0) + (two.y > key ? 1 : 0);
         }
         if (n % 2 != 0) rank += sh.candidate[n - 1] > key ? 1 : 0;
+        if (rank < k) sh.top[rank] = key;
+    }
+    __syncthreads();
+}
+
+// The top k of the lists of `ctas` CTAs, k sorted keys each (0: none), in
+// shared memory: a key's place is its own and those of the keys before it in
+// the other lists, found by bisection: 8 lists of 32 take 0.5 to 2 us less than
+// by comparing it with each, as `place` does, which takes 0.8 us less for 8
+// lists of 8.
+template <int kWarps>
+__device__ __forceinline__ void merge(Shared<kWarps, true> &sh, int ctas, int k) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    for (int i = tid; i < ctas * k; i += 32 * kWarps) {
+        const unsigned long long key = sh.candidate[i];
+        if (key == 0) continue;
+        int at[8] = {};
+#pragma unroll
+        for (int step = KDA_MAX_TOP; step > 0; step >>= 1)
+            if (step <= k)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < ctas && at[c] + step <= k &&
+                        sh.candidate[c * k + at[c] + step - 1] > key)
+                        at[c] += step;
+        int rank = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) rank += at[c];  // of its own list: its place there
         if (rank < k) sh.top[rank] = key;
     }
     __syncthreads();
@@ -445,9 +472,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
     const Stats of_warp = warp_join(st);
     if (lane == 0) sh.stats[warp] = of_warp;
     if constexpr (kTop) {
-        constexpr int kKept = 32 / kWarps;  // maxima of each warp that the bound looks at
-        const float v = warp_sort(st.m, lane);
-        if (lane < kKept) sh.maxima[warp * kKept + lane] = v;
+        constexpr int kEach = kThreads / kMaxima;  // threads of a group
+        float v = st.m;
+#pragma unroll
+        for (int o = 1; o < kEach; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+        // the group's number in the last bits makes them differ; what they
+        // held only lowers the bound
+        if (lane % kEach == 0)
+            sh.maxima[tid / kEach] = (order_of(v) & ~(uint32_t)(kMaxima - 1)) | (tid / kEach);
     }
     __syncthreads();
     if (warp == 0) {
@@ -456,7 +488,24 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
         if (lane == 0) sh.row = a;
     }
     if constexpr (kTop) {
-        const float bound = __shfl_sync(kFull, warp_sort(sh.maxima[lane], lane), p.top - 1);
+        if (warp >= kWarps - kMaxima / 32) {  // the k-th largest of the maxima
+            const uint32_t mine = sh.maxima[tid - (kThreads - kMaxima)];
+            int rank[4] = {};
+#pragma unroll
+            for (int c = 0; c < kMaxima; c += 4) {
+                const uint4 four = *reinterpret_cast<const uint4 *>(&sh.maxima[c]);
+                rank[0] += four.x > mine ? 1 : 0;
+                rank[1] += four.y > mine ? 1 : 0;
+                rank[2] += four.z > mine ? 1 : 0;
+                rank[3] += four.w > mine ? 1 : 0;
+            }
+            if (rank[0] + rank[1] + rank[2] + rank[3] == p.top - 1) {
+                const uint32_t order = mine & ~(uint32_t)(kMaxima - 1);
+                sh.bound = order <= order_of(-INFINITY) ? -INFINITY : value_of_order(order);
+            }
+        }
+        __syncthreads();
+        const float bound = sh.bound;
         auto push = [&](float v, int i) {
             if (!(v < bound)) {  // (a NaN counts as -inf, which may be the bound)
                 if (v != v && bound != -INFINITY) return;
@@ -479,15 +528,28 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
         // their elements again, as candidates
         const int listed = sh.listed, each = stretch * kUnroll;
         if (listed <= kListed) {
-#pragma unroll 2
-            for (int i = tid; i < listed * each; i += kThreads) {
-                const int who = sh.list[i / each], n = who % kStretches * each + i % each;
-                const int j = begin + who / kStretches + n * kThreads;
-                if (j >= end) continue;
-                float f[kN];
-                unpack(body[j], f, T());
+            constexpr int kBatch = 2;  // loads in flight together
+            for (int i0 = tid; i0 < listed * each; i0 += kBatch * kThreads) {
+                uint4 u[kBatch];
+                int j[kBatch];
 #pragma unroll
-                for (int e = 0; e < kN; ++e) push(f[e], head + j * kN + e);
+                for (int b = 0; b < kBatch; ++b) {
+                    const int i = i0 + b * kThreads;
+                    j[b] = end;
+                    if (i < listed * each) {
+                        const int who = sh.list[i / each], n = who % kStretches * each + i % each;
+                        j[b] = begin + who / kStretches + n * kThreads;
+                    }
+                    if (j[b] < end) u[b] = body[j[b]];
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (j[b] >= end) continue;
+                    float f[kN];
+                    unpack(u[b], f, T());
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) push(f[e], head + j[b] * kN + e);
+                }
             }
         }
         __syncthreads();
@@ -526,7 +588,12 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
         }
         cluster_sync();
         if (rank != 0) return;
-        if constexpr (kTop) place(sh, p.ctas * p.top, p.top);
+        if constexpr (kTop) {
+            if (p.ctas * p.top <= kFew)
+                place(sh, p.ctas * p.top, p.top);
+            else
+                merge(sh, p.ctas, p.top);
+        }
     } else if (!kTop) {
         __syncthreads();
     }
