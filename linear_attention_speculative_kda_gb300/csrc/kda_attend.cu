@@ -81,6 +81,25 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2 ulp, 0 at -in
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -499,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                 for (int e = 0; e < 4; ++e) o[a][d][e] = 0.0f;
 
         for (int done = 0; done < tiles; ++done) {
+            cp_async_wait<kStages - 2>();
+            group_sync<kMW>(group);  // the tile is here, and the one before is done with
             load_tile(slot == 0 ? kStages - 1 : slot - 1);
-            cp_async_wait<kStages - 1>();
-            group_sync<kMW>(group);
             const uint32_t k_addr = kda::smem_u32(ring + slot * L::kStage) +
                                     group * L::kKeys * L::kRowBytes;
             const uint32_t v_addr = k_addr + L::kHalfTile;
@@ -550,12 +569,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                         }
                     }
                 }
-#pragma unroll
-                for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                    for (int n = 0; n < 2 * kNB; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[a][n][e] *= p.scale_log2;
 
                 if (edge) {
 #pragma unroll
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                         for (int n = 0; n < 2 * kNB; ++n)
                             x = fmaxf(x, fmaxf(s[a][n][2 * h], s[a][n][2 * h + 1]));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 2)) * p.scale_log2;
                         top[a][h] = x;
                         grew |= x > m[a][h] + kLazy;
                     }
@@ -608,13 +621,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                 for (int a = 0; a < kMT; ++a)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float base = m[a][h] == -INFINITY ? 0.0f : m[a][h];
+                        const float base = m[a][h] == -INFINITY ? 0.0f : -m[a][h];
+                        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                         for (int n = 0; n < 2 * kNB; ++n) {
-                            s[a][n][2 * h] = exp2_fast(s[a][n][2 * h] - base);
-                            s[a][n][2 * h + 1] = exp2_fast(s[a][n][2 * h + 1] - base);
-                            l[a][h] += s[a][n][2 * h] + s[a][n][2 * h + 1];
+                            const float2 x =
+                                fma2(make_float2(s[a][n][2 * h], s[a][n][2 * h + 1]),
+                                     make_float2(p.scale_log2, p.scale_log2),
+                                     make_float2(base, base));
+                            s[a][n][2 * h] = exp2_fast(x.x);
+                            s[a][n][2 * h + 1] = exp2_fast(x.y);
+                            sum = add2(sum, make_float2(s[a][n][2 * h], s[a][n][2 * h + 1]));
                         }
+                        l[a][h] += sum.x + sum.y;
                     }
 
             }
@@ -717,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                     }
                 }
             }
-            group_sync<kMW>(group);  // the slot may be loaded again
             slot = slot + 1 == kStages ? 0 : slot + 1;
         }
 
@@ -1855,6 +1873,7 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
     p.most_rows = cfg->window * p.group;
     p.slot_size = slot_floats(cfg);
     p.scale_log2 = fabsf(cfg->scale) * kLog2e;
+    if (p.scale_log2 == 0.0f) p.scale_log2 = 1.4e-45f;  // 0 times a masked -inf is NaN
     p.flip = cfg->scale < 0.0f ? 0x80008000u : 0u;
     if (cfg->dtype == KDA_DTYPE_BF16)
         return cfg->head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, sms, stream)
