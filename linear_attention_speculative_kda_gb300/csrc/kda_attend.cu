@@ -191,34 +191,27 @@ __device__ __forceinline__ void row_tiles(const Params &p, const Row &row, int &
     end = (row.computed + row.tokens - 1) / kTile + 1;
 }
 
-__device__ __forceinline__ int tile_count(const Params &p, int b, int &bits) {
-    int first, end;
-    const Row row = kda_cache::read_row(p.rows, b, p.window, bits);
-    row_tiles(p, row, first, end);
-    return end - first;
-}
-
 // Where a CTA's run stands: tile `tile` of kv head `head` of row `b`.
 struct Cursor {
     Row row;
     int b, head, tile, first, end;
 
-    __device__ __forceinline__ void set_row(const Params &p, int row_index) {
+    __device__ __forceinline__ void set_row(const Params &p, int row_index, int &bits) {
         b = row_index;
-        int bits = 0;
         row = kda_cache::read_row(p.rows, b, p.window, bits);
         row_tiles(p, row, first, end);
         tile = first;
+        head = 0;
     }
     __device__ __forceinline__ void next_segment(const Params &p) {
         if (++head < p.kv_heads) {
             tile = first;
             return;
         }
-        head = 0;
+        int bits = 0;
         do {
             if (b + 1 >= p.rows.B) return;  // past the last unit; never read
-            set_row(p, b + 1);
+            set_row(p, b + 1, bits);
         } while (end == first);
     }
 };
@@ -226,16 +219,21 @@ struct Cursor {
 struct Run {
     long long units, begin, end;  // of the call; this CTA's [begin, end)
     long long before_row;         // units before the starting row
-    int row, ctas;                // CTAs with work
+    int ctas;                     // CTAs with work
 };
+
+// a / b of whole numbers >= 0: nearly always in 32 bits, in a third of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // First unit of CTA i's run, and the CTA whose run holds unit u.
 __device__ __forceinline__ long long run_begin(long long units, int ctas, int i) {
-    return units * i / ctas;
+    return quotient(units * i, ctas);
 }
 
 __device__ __forceinline__ int cta_of(long long units, int ctas, long long u) {
-    return (int)(((u + 1) * ctas - 1) / units);
+    return (int)quotient((u + 1) * ctas - 1, units);
 }
 
 // Every CTA adds up the rows' tiles itself: thread i takes a run of rows, a
@@ -244,7 +242,7 @@ __device__ __forceinline__ int cta_of(long long units, int ctas, long long u) {
 struct PlanScratch {
     long long sums[8];
     long long before;
-    int row;
+    Cursor row;
 };
 
 template <int kWarpCount>
@@ -255,8 +253,14 @@ __device__ __forceinline__ Run plan(const Params &p, PlanScratch &sc) {
     const int b0 = min(p.rows.B, tid * per), b1 = min(p.rows.B, b0 + per);
     long long mine = 0;
     int bits = 0;
+    Cursor own = {};  // the thread's first row
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) mine += tile_count(p, b, bits);  // the loads overlap
+    for (int b = b0; b < b1; ++b) {  // the loads overlap
+        Cursor c;
+        c.set_row(p, b, bits);
+        mine += c.end - c.first;
+        if (b == b0) own = c;
+    }
     if (bits != 0 && blockIdx.x == 0) kda_cache::flag(p.rows.err, bits);
     long long upto = mine;
 #pragma unroll
@@ -279,32 +283,27 @@ __device__ __forceinline__ Run plan(const Params &p, PlanScratch &sc) {
     if ((int)blockIdx.x >= run.ctas) return run;  // uniform over the CTA
     run.begin = run_begin(run.units, run.ctas, blockIdx.x);
     run.end = run_begin(run.units, run.ctas, blockIdx.x + 1);
-    const long long at = run.begin / p.kv_heads;  // the first tile, counted over rows
+    const long long at = quotient(run.begin, p.kv_heads);  // the first tile, counted over rows
     if (at >= before && at < before + mine) {
-        int b = b0;
-        for (;; ++b) {
-            const int n = tile_count(p, b, bits);
-            if (at < before + n) break;
-            before += n;
+        while (at >= before + own.end - own.first) {
+            before += own.end - own.first;
+            own.set_row(p, own.b + 1, bits);
         }
-        sc.row = b;
+        sc.row = own;
         sc.before = before * p.kv_heads;
     }
     __syncthreads();
-    run.row = sc.row;
     run.before_row = sc.before;
     return run;
 }
 
 // Where the CTA's run begins.
-__device__ __forceinline__ Cursor run_start(const Params &p, const Run &run) {
-    Cursor at;
-    at.head = 0;
-    at.set_row(p, run.row);
+__device__ __forceinline__ Cursor run_start(const Run &run, const PlanScratch &sc) {
+    Cursor at = sc.row;
     const long long in_row = run.begin - run.before_row;
     const int n = at.end - at.first;
-    at.head = (int)(in_row / n);
-    at.tile = at.first + (int)(in_row % n);
+    at.head = (int)quotient(in_row, n);
+    at.tile += (int)(in_row - (long long)at.head * n);
     return at;
 }
 
@@ -341,10 +340,10 @@ struct Layout {
     static constexpr int kRowBytes = kDim * 2;
     static constexpr int kHalfTile = kTile * kRowBytes;
     static constexpr int kStage = 2 * kHalfTile;       // keys, then values
-    // the queries and, between segments, half of the channels of the sum
-    // over the groups share one area
+    // the queries and, between segments, 64 channels of the sum over the
+    // groups (what the others add to a group's share of them) share one area
     static constexpr int kQuery = kRows * kRowBytes;
-    static constexpr int kSum = kGroups > 1 ? kRows * kDim / 2 * 4 : 0;
+    static constexpr int kSum = (kGroups - 1) * kRows * 64 * 4;
     static constexpr int kShared = kQuery > kSum ? kQuery : kSum;
     static constexpr int kStats = kGroups * kRows * 8;
     static constexpr int kFixed = kShared + kStats;
@@ -368,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
     using L = Layout<kDim, kMT, kMW, kCtas>;
     constexpr int kNB = L::kKeys / 16;      // blocks of 16 keys in a group's step
     constexpr int kDT = kDim / 8;           // 8-channel tiles of O
+    constexpr int kOwn = 8 / L::kGroups;    // of each 8 of them, a group's share of the sum
     constexpr int kChunks = kDim / 8;       // 16-byte chunks of a cache row
     constexpr int kPerInstr = 32 / kChunks; // cache rows one cp.async of a warp covers
     constexpr int kStages = L::kStages;
@@ -392,12 +392,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
     }
 
     // cursor of the tile to compute and of the tile to load
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, plan_scratch);
     Cursor ld = at;
     long long left = run.end - run.begin;       // tiles to compute
     long long to_load = left;
-
-    if (tid == 0) p.cuts[cta] = first_cut(run, at, cta);
 
     // Load one tile into ring slot `slot`: this warp's 16 keys and values.
     // Lane l looks up key l mod 16; the address goes to the loading lanes by
@@ -437,8 +435,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         kda::cp_async_commit();
     };
 
-    for (int i = 0; i < kStages - 1; ++i) load_tile(i);
-
     // A segment's queries (rows past the last one: zeros), a batch of loads in
     // flight together: one after the other they took most of the 10 us that 64
     // rows cost beside their tiles.
@@ -469,6 +465,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         }
     };
 
+    if (kAhead) fetch_queries(at, 0);
+    for (int i = 0; i < kStages - 1; ++i) load_tile(i);
+    if (tid == 0) p.cuts[cta] = first_cut(run, at, cta);
+
     int slot = 0;            // ring slot of the tile to compute
     int piece_first = 1;     // whether the segment is this run's first
     while (left > 0) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         const bool busy = mwarp * 16 * kMT < rows;  // whether this warp has query rows
         // queries to shared memory; few enough are here already, fetched while
         // the segment before was joined
-        if (!kAhead || piece_first) fetch_queries(at, 0);
+        if (!kAhead) fetch_queries(at, 0);
         store_queries(0);
 #pragma unroll 1
         for (int batch = 1; batch < kBatches; ++batch) {
@@ -788,40 +788,46 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                         o[a][d][2 * h + 1] *= f;
                     }
                 }
-            // group after group adds its half of the channels; the last
-            // group keeps the sum
+            // 64 channels at a time: a group sums and writes its share of
+            // them, the others hand it theirs through shared memory
             float2 *sum = reinterpret_cast<float2 *>(shared_area);
+            auto place = [&](int a, int t, int from, int h) {
+                return sum + ((((mwarp * kMT + a) * 8 + t) * (L::kGroups - 1) + from) * 2 + h) * 32 +
+                       lane;
+            };
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int d0 = 0; d0 < kDT; d0 += 8) {
+                if (d0 > 0) __syncthreads();
 #pragma unroll
-                for (int g = 0; g < L::kGroups; ++g) {
-                    if (group == g) {
+                for (int t = 0; t < 8; ++t)
+                    if (t / kOwn != group)
 #pragma unroll
                         for (int a = 0; a < kMT; ++a)
 #pragma unroll
-                            for (int d = 0; d < kDT / 2; ++d)
+                            for (int h = 0; h < 2; ++h)
+                                *place(a, t, (group - t / kOwn - 1) & (L::kGroups - 1), h) =
+                                    make_float2(o[a][d0 + t][2 * h], o[a][d0 + t][2 * h + 1]);
+                __syncthreads();
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    float *x = &o[a][half * (kDT / 2) + d][2 * h];
-                                    float2 *y = sum + ((((mwarp * kMT + a) * (kDT / 2) + d) * 2 + h) *
-                                                           32 +
-                                                       lane);
-                                    if (g > 0) {
-                                        const float2 z = *y;
-                                        x[0] += z.x;
-                                        x[1] += z.y;
-                                    }
-                                    if (g + 1 < L::kGroups) *y = make_float2(x[0], x[1]);
+                for (int t = 0; t < 8; ++t)
+                    if (t / kOwn == group)
+#pragma unroll
+                        for (int a = 0; a < kMT; ++a)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int g = 0; g + 1 < L::kGroups; ++g) {
+                                    const float2 x = *place(a, t, g, h);
+                                    o[a][d0 + t][2 * h] += x.x;
+                                    o[a][d0 + t][2 * h + 1] += x.y;
                                 }
-                    }
-                    __syncthreads();
-                }
+            }
+            __syncthreads();
         } else {
             __syncthreads();  // every warp is done with the queries
         }
 
         // ---------------------------------------------------------- results
-        if (group == L::kGroups - 1) {
 #pragma unroll
             for (int a = 0; a < kMT; ++a)
 #pragma unroll
@@ -836,22 +842,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                         uint32_t *dst = reinterpret_cast<uint32_t *>(p.out) + row * (kDim / 2) + qc;
 #pragma unroll
                         for (int d = 0; d < kDT; ++d)
-                            dst[4 * d] = pack(o[a][d][2 * h] * f, o[a][d][2 * h + 1] * f, T());
-                        if (p.lse != nullptr && qc == 0)
+                            if (d % 8 / kOwn == group)
+                                dst[4 * d] = pack(o[a][d][2 * h] * f, o[a][d][2 * h + 1] * f, T());
+                        if (p.lse != nullptr && qc == 0 && group == 0)
                             p.lse[row] = (m[a][h] + log2f(l[a][h])) * kLn2;
                     } else {
                         float *part = p.partials + partial_slot * p.slot_size;
                         float2 *dst = reinterpret_cast<float2 *>(part + r * kDim) + qc;
 #pragma unroll
                         for (int d = 0; d < kDT; ++d)
-                            dst[4 * d] = make_float2(o[a][d][2 * h], o[a][d][2 * h + 1]);
-                        if (qc == 0) {
+                            if (d % 8 / kOwn == group)
+                                dst[4 * d] = make_float2(o[a][d][2 * h], o[a][d][2 * h + 1]);
+                        if (qc == 0 && group == 0) {
                             part[p.most_rows * kDim + r] = m[a][h];
                             part[p.most_rows * (kDim + 1) + r] = l[a][h];
                         }
                     }
                 }
-        }
         left -= tiles;
         piece_first = 0;
         at = next;
@@ -1074,7 +1081,7 @@ __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Cont
                                            uint32_t smem, int lane, const CUtensorMap *k_map,
                                            const CUtensorMap *v_map) {
     using F = Form<kDim, kQRows>;
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, c.plan);
     const long long tiles = run.end - run.begin;
     const int boxes = kTile / p.box, mine = lane % boxes;
     const int channel_block = lane / boxes;
@@ -1146,7 +1153,7 @@ __device__ __forceinline__ void run_queries(const Params &p, const Run &run, Con
                                             uint32_t smem, int lane) {
     constexpr int kChunks = kDim / 8;
     const uint32_t query = Form<kDim, kQRows>::query(smem);
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, c.plan);
     long long left = run.end - run.begin;
     for (uint32_t segment = 0;; ++segment) {
         if (!warp_wait(c, &c.q_empty, (segment & 1u) ^ 1u, p.rows.err)) break;
@@ -1190,7 +1197,7 @@ __device__ __forceinline__ void run_scores(const Params &p, const Run &run, Cont
                                            uint32_t smem, uint32_t tmem) {
     using F = Form<kDim, kQRows>;
     constexpr uint32_t kId = idesc<T>(kRows, kTile, false);
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, c.plan);
     const long long tiles = run.end - run.begin;
     const uint64_t q_desc = kda::sw128_desc(F::query(smem) - first_lane<kQRows>() * 128);
     uint32_t phase = 0;
@@ -1230,7 +1237,7 @@ __device__ __forceinline__ void run_outputs(const Params &p, const Run &run, Con
                                             uint32_t smem, uint32_t tmem) {
     using F = Form<kDim, kQRows>;
     constexpr uint32_t kId = idesc<T>(kRows, kDim, true);
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, c.plan);
     p.cuts[blockIdx.x] = first_cut(run, at, blockIdx.x);
     const long long tiles = run.end - run.begin;
     uint32_t phase = 0;
@@ -1280,7 +1287,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
     const int row = tid - first_lane<kQRows>();                           // query row of this thread
     const uint32_t tmem = tmem_all + ((uint32_t)(warp * 32) << 16);  // the warp's lanes
     const float scale = p.flip != 0 ? -p.scale_log2 : p.scale_log2;
-    Cursor at = run_start(p, run);
+    Cursor at = run_start(run, c.plan);
     long long left = run.end - run.begin, g = 0;
     bool run_first = true;
     uint32_t meetings = 0;
