@@ -67,6 +67,7 @@ struct Params {
     long long stride_q, stride_block, stride_token, stride_head;  // elements
     int q_heads, kv_heads, group, window, left_window, most_rows;
     int by_group;            // 2^16 / group, rounded up
+    kda_cache::Divider by_heads, by_grid;
     int box;                 // tokens of a tensor-map box
     long long slot_size;     // floats of a partial slot: O, the maxima, the sums
     float scale_log2;        // |scale| log2 e
@@ -219,7 +220,8 @@ struct Cursor {
 struct Run {
     long long units, begin, end;  // of the call; this CTA's [begin, end)
     long long before_row;         // units before the starting row
-    int ctas;                     // CTAs with work
+    long long each;               // units of a run; the first `more` runs have one more
+    int more, ctas;               // CTAs with work
 };
 
 // a / b of whole numbers >= 0: nearly always in 32 bits, in a third of the time.
@@ -227,13 +229,19 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// First unit of CTA i's run, and the CTA whose run holds unit u.
-__device__ __forceinline__ long long run_begin(long long units, int ctas, int i) {
-    return quotient(units * i, ctas);
+__device__ __forceinline__ long long quotient(long long a, int b, const kda_cache::Divider &by) {
+    return (a >> 31) == 0 ? kda_cache::divide((int)a, by) : a / b;
 }
 
-__device__ __forceinline__ int cta_of(long long units, int ctas, long long u) {
-    return (int)quotient((u + 1) * ctas - 1, units);
+// First unit of CTA i's run, and the CTA whose run holds unit u.
+__device__ __forceinline__ long long run_begin(const Run &run, int i) {
+    return i * run.each + min(i, run.more);
+}
+
+__device__ __forceinline__ int cta_of(const Run &run, long long u) {
+    const long long split = run.more * (run.each + 1);
+    return u < split ? (int)quotient(u, run.each + 1)
+                     : run.more + (int)quotient(u - split, run.each);
 }
 
 // Every CTA adds up the rows' tiles itself: thread i takes a run of rows, a
@@ -279,11 +287,13 @@ __device__ __forceinline__ Run plan(const Params &p, PlanScratch &sc) {
     Run run;
     run.units = total * p.kv_heads;
     run.ctas = (int)min((long long)gridDim.x, run.units);
+    run.each = quotient(run.units, gridDim.x, p.by_grid);
+    run.more = (int)(run.units - run.each * gridDim.x);
     run.begin = run.end = 0;
     if ((int)blockIdx.x >= run.ctas) return run;  // uniform over the CTA
-    run.begin = run_begin(run.units, run.ctas, blockIdx.x);
-    run.end = run_begin(run.units, run.ctas, blockIdx.x + 1);
-    const long long at = quotient(run.begin, p.kv_heads);  // the first tile, counted over rows
+    run.begin = run_begin(run, blockIdx.x);
+    run.end = run_begin(run, blockIdx.x + 1);
+    const long long at = quotient(run.begin, p.kv_heads, p.by_heads);  // the first tile, counted over rows
     if (at >= before && at < before + mine) {
         while (at >= before + own.end - own.first) {
             before += own.end - own.first;
@@ -314,10 +324,10 @@ __device__ __forceinline__ Cut first_cut(const Run &run, const Cursor &at, int c
     const int n = at.end - at.first;
     const long long s = run.before_row + (long long)at.head * n;
     if (s < run.begin) {
-        const int i0 = cta_of(run.units, run.ctas, s);
-        if (i0 == cta - 1) {
-            cut.pieces = cta_of(run.units, run.ctas, s + n - 1) - i0 + 1;
-            cut.first_slot = 2 * i0 + (run_begin(run.units, run.ctas, i0) < s ? 1 : 0);
+        const long long before = run_begin(run, cta - 1);
+        if (s >= before) {
+            cut.pieces = cta_of(run, s + n - 1) - cta + 2;
+            cut.first_slot = 2 * (cta - 1) + (before < s ? 1 : 0);
             cut.first_token = at.row.first;
             cut.tokens = at.row.tokens;
             cut.head = at.head;
@@ -340,17 +350,14 @@ struct Layout {
     static constexpr int kRowBytes = kDim * 2;
     static constexpr int kHalfTile = kTile * kRowBytes;
     static constexpr int kStage = 2 * kHalfTile;       // keys, then values
-    // the queries and, between segments, 64 channels of the sum over the
-    // groups (what the others add to a group's share of them) share one area
     static constexpr int kQuery = kRows * kRowBytes;
-    static constexpr int kSum = (kGroups - 1) * kRows * 64 * 4;
-    static constexpr int kShared = kQuery > kSum ? kQuery : kSum;
     static constexpr int kStats = kGroups * kRows * 8;
-    static constexpr int kFixed = kShared + kStats;
+    static constexpr int kFixed = kQuery + kStats;
     // the SM's 228 KB, less 1 KB a CTA that the system takes and the static part
     static constexpr int kBudget = 233472 / kCtas - 1024 - 1280;
     static constexpr int kStages = (kBudget - kFixed) / kStage < 6 ? (kBudget - kFixed) / kStage : 6;
     static constexpr int kBytes = kFixed + kStages * kStage;
+    static_assert(kGroups == 1 || kMT == 1, "a group hands over one tile of rows a warp");
     static_assert(kStages >= 2, "the ring needs two tiles");
 };
 
@@ -374,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint32_t there[kStages][kWarps];  // keys of each warp's 16 that are in the cache
     unsigned char *ring = smem;
-    unsigned char *shared_area = smem + kStages * L::kStage;
-    float *stat_m = reinterpret_cast<float *>(shared_area + L::kShared);
+    unsigned char *query_area = smem + kStages * L::kStage;
+    float *stat_m = reinterpret_cast<float *>(query_area + L::kQuery);
     float *stat_l = stat_m + L::kGroups * L::kRows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = warp / kMW, mwarp = warp % kMW;
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
         for (int n = 0; n < kBatch; ++n) {
             const int i = (batch * kBatch + n) * kThreads + tid;
             const uint4 x = queries[n];
-            *reinterpret_cast<uint4 *>(shared_area + swizzled<kDim>(i / kChunks, i % kChunks)) =
+            *reinterpret_cast<uint4 *>(query_area + swizzled<kDim>(i / kChunks, i % kChunks)) =
                 make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip);
         }
     };
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
             store_queries(batch);
         }
         __syncthreads();
-        const uint32_t q_addr = kda::smem_u32(shared_area);
+        const uint32_t q_addr = kda::smem_u32(query_area);
         const int q_row = mwarp * 16 * kMT + (lane & 15);
         uint32_t qf[kMT == 1 ? kDim / 16 : 1][4];
         if constexpr (kMT == 1) {
@@ -764,65 +771,64 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                         stat_m[group * L::kRows + r] = m[a][h];
                         stat_l[group * L::kRows + r] = l[a][h];
                     }
-            __syncthreads();
-#pragma unroll
-            for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = (mwarp * kMT + a) * 16 + qr + 8 * h;
-                    float all = -INFINITY, sum = 0.0f;
-#pragma unroll
-                    for (int g = 0; g < L::kGroups; ++g)
-                        all = fmaxf(all, stat_m[g * L::kRows + r]);
-                    const float base = all == -INFINITY ? 0.0f : all;
-#pragma unroll
-                    for (int g = 0; g < L::kGroups; ++g)
-                        sum += stat_l[g * L::kRows + r] *
-                               exp2_fast(stat_m[g * L::kRows + r] - base);
-                    const float f = exp2_fast(m[a][h] - base);
-                    m[a][h] = all;
-                    l[a][h] = sum;
-#pragma unroll
-                    for (int d = 0; d < kDT; ++d) {
-                        o[a][d][2 * h] *= f;
-                        o[a][d][2 * h + 1] *= f;
-                    }
-                }
-            // 64 channels at a time: a group sums and writes its share of
-            // them, the others hand it theirs through shared memory
-            float2 *sum = reinterpret_cast<float2 *>(shared_area);
-            auto place = [&](int a, int t, int from, int h) {
-                return sum + ((((mwarp * kMT + a) * 8 + t) * (L::kGroups - 1) + from) * 2 + h) * 32 +
-                       lane;
+            // Each group sums and writes its share of the channels.  The others
+            // hand it theirs through the group's part of the ring slot of the
+            // last tile, which is not loaded again before the next segment's
+            // first barrier.
+            const uint32_t area = kda::smem_u32(ring + (slot == 0 ? kStages - 1 : slot - 1) *
+                                                           L::kStage) +
+                                  8 * lane;
+            auto place = [&](int g, int d, int h) {  // 256 bytes of a warp of group g
+                constexpr int kHalf = kMW == 1 ? kDT : 2 * kDT;  // of keys, of values
+                const int c = 2 * d + h, half = kMW == 1 ? c / kHalf : mwarp;
+                return area + g * L::kKeys * L::kRowBytes + half * L::kHalfTile + c % kHalf * 256;
             };
+            group_sync<kMW>(group);
 #pragma unroll
-            for (int d0 = 0; d0 < kDT; d0 += 8) {
-                if (d0 > 0) __syncthreads();
+            for (int d = 0; d < kDT; ++d)
+                if (d % 8 / kOwn != group)
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t / kOwn != group)
-#pragma unroll
-                        for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                *place(a, t, (group - t / kOwn - 1) & (L::kGroups - 1), h) =
-                                    make_float2(o[a][d0 + t][2 * h], o[a][d0 + t][2 * h + 1]);
-                __syncthreads();
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t / kOwn == group)
-#pragma unroll
-                        for (int a = 0; a < kMT; ++a)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int g = 0; g + 1 < L::kGroups; ++g) {
-                                    const float2 x = *place(a, t, g, h);
-                                    o[a][d0 + t][2 * h] += x.x;
-                                    o[a][d0 + t][2 * h + 1] += x.y;
-                                }
-            }
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(place(group, d, h)),
+                                     "f"(o[0][d][2 * h]), "f"(o[0][d][2 * h + 1])
+                                     : "memory");
             __syncthreads();
+            float f[2][L::kGroups];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = mwarp * 16 + qr + 8 * h;
+                float all = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int g = 0; g < L::kGroups; ++g) all = fmaxf(all, stat_m[g * L::kRows + r]);
+                const float base = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+                for (int g = 0; g < L::kGroups; ++g) {
+                    f[h][g] = exp2_fast(stat_m[g * L::kRows + r] - base);
+                    sum += stat_l[g * L::kRows + r] * f[h][g];
+                }
+                m[0][h] = all;
+                l[0][h] = sum;
+            }
+#pragma unroll
+            for (int d = 0; d < kDT; ++d)
+                if (d % 8 / kOwn == group)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2 all = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int g = 0; g < L::kGroups; ++g) {
+                            float2 x = make_float2(o[0][d][2 * h], o[0][d][2 * h + 1]);
+                            if (g != group)
+                                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                             : "=f"(x.x), "=f"(x.y)
+                                             : "r"(place(g, d, h))
+                                             : "memory");
+                            all.x = fmaf(x.x, f[h][g], all.x);
+                            all.y = fmaf(x.y, f[h][g], all.y);
+                        }
+                        o[0][d][2 * h] = all.x;
+                        o[0][d][2 * h + 1] = all.y;
+                    }
         } else {
             __syncthreads();  // every warp is done with the queries
         }
@@ -1711,9 +1717,10 @@ bool allow_shared(const void *kernel, int bytes, bool (&done)[64]) {
 }
 
 template <typename T, int kDim, int kMT, int kMW, int kCtas>
-kda_status launch_attend(const Params &p, int sms, void *stream) {
+kda_status launch_attend(Params &p, int sms, void *stream) {
     using L = Layout<kDim, kMT, kMW, kCtas>;
     const int grid = min(kCtas * sms, kMaxCtas);
+    p.by_grid = kda_cache::make_divider(grid);
     void (*kernel)(const Params) = attend_kernel<T, kDim, kMT, kMW, kCtas>;
     static bool allowed[64];
     if (!allow_shared(reinterpret_cast<const void *>(kernel), L::kBytes, allowed))
@@ -1765,9 +1772,10 @@ bool cache_map(const Params &p, const char *base, CUtensorMap *map) {
 }
 
 template <typename T, int kDim, int kQRows>
-kda_status launch_tc(const Params &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int sms,
+kda_status launch_tc(Params &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int sms,
                      void *stream) {
     const int grid = min(tc::kCtasPerSm * sms, kMaxCtas);
+    p.by_grid = kda_cache::make_divider(grid);
     using F = tc::Form<kDim, kQRows>;
     void (*kernel)(const Params, const CUtensorMap, const CUtensorMap) =
         tc::attend_tc_kernel<T, kDim, kQRows>;
@@ -1875,6 +1883,7 @@ kda_status kda_window_attention(const kda_cache_config *cfg, const void *q, cons
     p.kv_heads = cfg->kv_heads;
     p.group = cfg->q_heads / cfg->kv_heads;
     p.by_group = (65536 + p.group - 1) / p.group;
+    p.by_heads = kda_cache::make_divider(p.kv_heads);
     p.window = cfg->window;
     p.left_window = cfg->left_window;
     p.most_rows = cfg->window * p.group;
