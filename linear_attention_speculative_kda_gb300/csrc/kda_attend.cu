@@ -1611,7 +1611,7 @@ __global__ void __launch_bounds__(kThreadCount, kCtasPerSm)
 // 4 y + warp, then 4 gridDim.y on.  The pieces' maxima and sums are read one a
 // lane, their O in batches of kBatch loads, the first batch in flight with
 // them.
-constexpr int kJoinRows = 8;   // blocks a cut, at most
+constexpr int kJoinRows = 16;   // blocks a cut, at most
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
