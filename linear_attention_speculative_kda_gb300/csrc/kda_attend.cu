@@ -26,10 +26,10 @@
 //   loading its own 16 keys, so with kMW = 1 no warp waits for another inside
 //   a segment.  The products are mma.sync m16n8k16 on fragments that ldmatrix
 //   reads from XOR-swizzled rows.  64 requests of 4 tokens over up to 8192
-//   keys, 16 rows: 192 us, 92% of the measured HBM rate.
+//   keys, 16 rows: 188 us, 95% of the measured HBM rate.
 // - tc::attend_tc_kernel, for more: tcgen05.mma with S and O in tensor memory
 //   and tensor-map TMA loads (below).  128 requests of 8 tokens over up to
-//   12000 keys, 64 rows: 595 us, 89% (762 with the first form).
+//   12000 keys, 64 rows: 573 us, 92% (698 with the first form).
 #include <cuda.h>
 
 #include "kda_async.cuh"
@@ -1791,30 +1791,32 @@ kda_status launch_tc(Params &p, const CUtensorMap &k_map, const CUtensorMap &v_m
 template <typename T, int kDim>
 kda_status launch_rows(Params &p, int sms, void *stream) {
     // Which kernel: measured on 96 rows of up to 2000 keys | 16 rows of up to
-    // 30000 (us), 4 kv heads.
+    // 30000 | 300 ragged rows of up to 1000 (us), 4 kv heads.
     //   channels  query rows   16 rows a warp      tensor-core form
-    //   128       16           51 | 95             63 | 100
-    //   128       32           57 | 100            66 | 103
-    //   128       40           69 | 123            70 | 105
-    //   128       64           78 | 130            77 | 110
-    //   64        32           39 | 60             46 | 69
-    //   64        64           52 | 83             54 | 79
-    //   64        96           78 | 128            64 | 84
-    // The tensor-core form reads the cache in boxes of p.box keys and 64
-    // channels, which have to be swizzled atoms of 8 rows; with 64 channels
-    // boxes of 8 keys were slower (197 us against 181 in boxes of 16).
+    //   128       16           47 |  90 |  66      61 |  96 | 102
+    //   128       32           55 |  95 |  73      64 |  98 | 106
+    //   128       40           69 | 117 |  92      68 | 100 | 108
+    //   128       64           78 | 124 | 100      75 | 105 | 114
+    //   128       128         169 | 283 | 227     102 | 120 | 133
+    //   64        32           35 |  56 |  49      51 |  70 |  85
+    //   64        64           49 |  80 |  66      58 |  77 |  91
+    //   64        96           76 | 121 | 102      65 |  84 |  98
+    // (The lengths are on the device, so they are no part of the rule.)  The
+    // tensor-core form reads the cache in boxes of p.box keys and 64 channels,
+    // which have to be swizzled atoms of 8 rows; with 96 rows of 64 channels
+    // 66 us in boxes of 8 keys, 65 of 16, and 76 for the other form.
     p.box = kTile;
     while (p.rows.block_size % p.box != 0) p.box /= 2;
-    if (p.most_rows > (kDim == 128 ? 32 : 64) && p.box * kDim >= 1024) {
+    if (p.most_rows > (kDim == 128 ? 32 : 64) && p.box >= 8) {
         CUtensorMap k_map, v_map;  // (a cache they cannot describe goes the other way)
         if (cache_map<T, kDim>(p, p.key_cache, &k_map) &&
             cache_map<T, kDim>(p, p.value_cache, &v_map))
             return p.most_rows <= 64 ? launch_tc<T, kDim, 64>(p, k_map, v_map, sms, stream)
                                      : launch_tc<T, kDim, 128>(p, k_map, v_map, sms, stream);
     }
-    // With 64 channels and 32 or 64 rows three CTAs fit an SM, which measured
-    // 43 and 58 us with two (39 and 52 with three); with 16 rows two measured
-    // better (33 | 57 us against 38 | 66 at 8 rows).
+    // With 64 channels and 32 or 64 rows three CTAs fit an SM: 35 and 49 us,
+    // with two 40 and 54; with up to 16 rows two measured better (31 | 55 | 45
+    // us against 34 | 64 | 52 at 8 rows).
     constexpr int kWide = kDim == 64 ? 3 : 2;
     if (p.most_rows <= 16) return launch_attend<T, kDim, 1, 1, 2>(p, sms, stream);
     if (p.most_rows <= 32) return launch_attend<T, kDim, 1, 2, kWide>(p, sms, stream);
