@@ -145,6 +145,7 @@ class KdaCacheConfig(ctypes.Structure):
     ]
 
 
+_quick = None        # the compiled part of the binding of the short calls
 _lib_handle = None
 
 
@@ -162,7 +163,18 @@ def load_library():
             f"libkda.so not found at {_LIBRARY}; build it first "
             "(python -c 'import __graft_entry__ as g; g.build()')")
     _lib_handle = bind_library(_LIBRARY)
+    _load_quick()
     return _lib_handle
+
+
+def _load_quick():
+    """The compiled part of the binding of the short calls, where it was built."""
+    global _quick
+    try:
+        from . import _binding
+        _quick = _binding
+    except ImportError:
+        _quick = None
 
 
 def bind_library(path: str):
@@ -210,6 +222,11 @@ def bind_library(path: str):
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_abi_version.restype = i32
     lib.kda_abi_version.argtypes = []
+    # for the compiled part of the binding, which calls the library it is given
+    lib.append_address, lib.attend_address, lib.logprobs_address = (
+        ctypes.cast(fn, vp).value for fn in (lib.kda_kv_append_packed,
+                                             lib.kda_window_attention_packed,
+                                             lib.kda_token_logprobs_packed))
     return lib
 
 
@@ -713,15 +730,21 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
 
 # ------------------------------------- full-attention layers and acceptance --
 #
-# These calls are short (a decode step's append takes 3 us on the device), so
-# their checks are written out inline, one comparison per fact, with the
-# message worked out only once something is wrong, and their arguments go to
-# the library as the bytes of one structure.
+# These calls are short (a decode step's append takes 3 us on the device).  So
+# the compiled part of the binding, _quick, checks and marshals what is plainly
+# right; where it finds something else (None), or was not built, the functions
+# here do.  Their checks too are written out inline, one comparison per fact,
+# with the message worked out only once something is wrong, and their arguments
+# go to the library as the bytes of one structure.
 
 _CACHE_FORMAT = "9if6qQqiiiiQQ"     # kda_cache_config, kda_align
 _APPEND_ARGS = struct.Struct("=" + _CACHE_FORMAT + "8Q2i2Q").pack
 _ATTENTION_ARGS = struct.Struct("=" + _CACHE_FORMAT + "4Q2i6Q").pack
 _LOGPROBS_ARGS = struct.Struct("=Qq4i8Q").pack
+
+
+def _failed(fn: str, status: int):
+    raise KDAError(fn, status)
 
 
 def _raw_stream(device: int):
@@ -807,6 +830,13 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
     (``q_out``, which may be ``q`` when it is contiguous; allocated when
     None), or None without ``q``.
     """
+    lib = load_library()
+    if _quick is not None:
+        done = _quick.append(lib.append_address, q, k, v, key_cache, value_cache, cu_seqlens,
+                             block_table, num_computed, inv_freq, interleaved, q_out,
+                             request_indices, error_word)
+        if done is not None:
+            return done[0] if done.__class__ is tuple else _failed("kda_kv_append", done)
     dev, dtype, i32 = key_cache.get_device(), key_cache.dtype, torch.int32
     code = DTYPES.get(dtype, 2)
     if code > 1:
@@ -853,7 +883,7 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
         rotary_dim, freq_ptr = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    status = load_library().kda_kv_append_packed(_APPEND_ARGS(
+    status = lib.kda_kv_append_packed(_APPEND_ARGS(
         q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim, 1 if interleaved else 0, 1.0,
         strides[0], strides[1], strides[2], stride_q, stride_k, stride_v, block_table.data_ptr(),
         table_stride, width, block_size, requests, 0, num_computed.data_ptr(),
@@ -902,6 +932,13 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
     ``allocate_attention_workspace``.  Returns ``(out, lse)``: out [T, Hq, D]
     and the scores' log sum of exponentials, fp32 [T, Hq].  Rows that are
     skipped leave theirs untouched."""
+    lib = load_library()
+    if _quick is not None:
+        done = _quick.attend(lib.attend_address, q, key_cache, value_cache, cu_seqlens,
+                             block_table, num_computed, workspace, window, scale, left_window,
+                             request_indices, out, lse, error_word)
+        if done is not None:
+            return done if done.__class__ is tuple else _failed("kda_window_attention", done)
     dev, dtype, i32 = key_cache.get_device(), key_cache.dtype, torch.int32
     code = DTYPES.get(dtype, 2)
     if code > 1:
@@ -940,7 +977,7 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
         raise ValueError("workspace must be contiguous")
     if T == 0:  # an empty tensor has no address to pass on
         return out, lse
-    status = load_library().kda_window_attention_packed(_ATTENTION_ARGS(
+    status = lib.kda_window_attention_packed(_ATTENTION_ARGS(
         q_heads, kv_heads, dim, code, blocks, window, left_window, 0, 0,
         dim ** -0.5 if scale is None else scale, strides[0], strides[1], strides[2], stride_q, 8,
         8, block_table.data_ptr(), table_stride, width, block_size, requests, 0,
@@ -978,6 +1015,12 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
     negative: none, 0), entropy, log sum of exponentials and the ``num_top``
     largest logits (ties: the lower index) of each row of ``logits`` [rows,
     vocab], bf16, fp16 or fp32 with any row stride."""
+    lib = load_library()
+    if _quick is not None and out is None:
+        done = _quick.logprobs(lib.logprobs_address, logits, tokens, num_top, error_word)
+        if done is not None:
+            return (TokenLogprobs._make(done) if done.__class__ is tuple
+                    else _failed("kda_token_logprobs", done))
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
     code = DTYPES.get(logits.dtype)
     if code is None:
@@ -1008,7 +1051,7 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
             if tuple(t.shape) != want or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {want} tensor")
     logprob, entropy, lse, top_logprob, top_index = out
-    status = load_library().kda_token_logprobs_packed(_LOGPROBS_ARGS(
+    status = lib.kda_token_logprobs_packed(_LOGPROBS_ARGS(
         logits.data_ptr(), strides[0], code, rows, vocab, num_top, tokens.data_ptr(),
         logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr(),
         top_index.data_ptr(), _address(error_word), _raw_stream(dev)))

@@ -1,8 +1,10 @@
-"""Compile the CUDA library ``libkda.so`` in-tree for sm_103a.
+"""Compile the CUDA library ``libkda.so`` in-tree for sm_103a, and the compiled
+part of the Python binding, ``_binding.so``.
 
 All translation units in one nvcc call (compiled side by side), one ``-gencode`` (compute_103a /
 sm_103a), the CUDA runtime linked statically so the library only needs the
-driver at run time.
+driver at run time.  The binding's part is host code against PyTorch's headers;
+where they or Python's are not installed, ``api.py`` does its work.
 """
 
 from __future__ import annotations
@@ -11,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +31,8 @@ DEPENDS = SOURCES + [
     os.path.join(ROOT, "include", "kda.h"),
 ]
 LIBRARY = os.path.join(PKG, "libkda.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,11 +44,15 @@ def nvcc_path() -> str:
     return os.path.join(cuda_home, "bin", "nvcc")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIBRARY):
+def _older(output: str, sources) -> bool:
+    if not os.path.exists(output):
         return True
-    built = os.path.getmtime(LIBRARY)
-    return any(os.path.getmtime(src) > built for src in DEPENDS)
+    built = os.path.getmtime(output)
+    return any(os.path.getmtime(src) > built for src in sources)
+
+
+def _stale() -> bool:
+    return _older(LIBRARY, DEPENDS)
 
 
 def compile_command(output: str, extra=(), sources=None) -> list[str]:
@@ -68,14 +78,54 @@ def compile_command(output: str, extra=(), sources=None) -> list[str]:
     ]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Build ``libkda.so`` if any source is newer than it; return its path."""
-    if not force and not _stale():
-        return LIBRARY
+def binding_command(output: str) -> list[str]:
+    import torch
+
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    home = os.path.dirname(torch.__file__)
+    headers = os.path.join(home, "include")
+    return [
+        "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", os.path.join(ROOT, "include"),
+        "-I", sysconfig.get_paths()["include"],
+        "-I", headers,
+        "-I", os.path.join(headers, "torch", "csrc", "api", "include"),
+        "-I", os.path.join(cuda, "include"),
+        "-o", output, BINDING_SOURCE,
+        "-L", os.path.join(home, "lib"),
+        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+    ]
+
+
+def _build_library(verbose: bool) -> None:
     tmp = LIBRARY + f".tmp{os.getpid()}"
     extra = ["-Xptxas", "-v"] if verbose else []
     subprocess.run(compile_command(tmp, extra), check=True)
     os.replace(tmp, LIBRARY)
+
+
+def _build_binding() -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    done = subprocess.run(binding_command(tmp), capture_output=True, text=True)
+    if done.returncode == 0:
+        os.replace(tmp, BINDING)
+    else:
+        print("the compiled part of the binding was not built; api.py does its work:\n"
+              + done.stderr[:2000], file=sys.stderr)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build ``libkda.so`` and ``_binding.so``, side by side, where a source is
+    newer; return the library's path."""
+    with ThreadPoolExecutor(2) as pool:
+        jobs = []
+        if force or _older(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "kda.h")]):
+            jobs.append(pool.submit(_build_binding))
+        if force or _stale():
+            jobs.append(pool.submit(_build_library, verbose))
+        for job in jobs:
+            job.result()
     return LIBRARY
 
 
