@@ -992,7 +992,8 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
 
 class TokenLogprobs(NamedTuple):
     """Outputs of ``kda_token_logprobs``: fp32 [rows] each, the alternatives
-    fp32 and int32 [rows, num_top]."""
+    fp32 and int32 [rows, num_top].  Those that a call allocates may lie in one
+    allocation."""
 
     logprob: torch.Tensor
     entropy: torch.Tensor
