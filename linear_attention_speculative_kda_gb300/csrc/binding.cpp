@@ -111,9 +111,21 @@ int32_t *error_address(PyObject *o, c10::Device device) {
     return e.data_ptr<int32_t>();
 }
 
+// Other threads run Python meanwhile: an allocation or a launch may wait for
+// the GPU, and what runs there may wait for a host function in Python.
+struct Unlocked {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+Tensor allocate(at::IntArrayRef shape, at::ScalarType type, c10::Device device) {
+    const Unlocked unlocked;
+    return at::empty(shape, at::dtype(type).device(device));
+}
+
 // The output that was given, checked, or a new one.
 Tensor output(PyObject *given, at::IntArrayRef shape, at::ScalarType type, c10::Device device) {
-    if (given == Py_None) return at::empty(shape, at::dtype(type).device(device));
+    if (given == Py_None) return allocate(shape, type, device);
     const Tensor &t = tensor(given, type, device);
     need(t.sizes() == shape && t.is_contiguous());
     return t;
@@ -131,7 +143,9 @@ Tensor part(const Tensor &all, int64_t at, at::IntArrayRef shape, at::ScalarType
 
 template <typename Args>
 int call(PyObject *address, const Args &args) {
-    return reinterpret_cast<int (*)(const Args *)>(PyLong_AsVoidPtr(address))(&args);
+    const auto function = reinterpret_cast<int (*)(const Args *)>(PyLong_AsVoidPtr(address));
+    const Unlocked unlocked;
+    return function(&args);
 }
 
 template <typename Body>
@@ -276,7 +290,7 @@ PyObject *logprobs(PyObject *, PyObject *const *o, Py_ssize_t n) {
         a.num_top = integer(o[3]);
         need(a.num_top >= 0 && a.num_top <= KDA_MAX_TOP);
         const int64_t rows = a.rows, top = a.num_top;
-        const Tensor all = at::empty({rows * (3 + 2 * top)}, at::dtype(at::kFloat).device(device));
+        const Tensor all = allocate({rows * (3 + 2 * top)}, at::kFloat, device);
         const Tensor outputs[5] = {part(all, 0, {rows}, at::kFloat),
                                    part(all, rows, {rows}, at::kFloat),
                                    part(all, 2 * rows, {rows}, at::kFloat),

@@ -115,3 +115,24 @@ def test_refusals_are_the_same():
     for i, call in enumerate(calls):
         quick, plain = _both_ways(lambda: kind(call))
         assert quick == plain, (i, quick, plain)
+
+
+def test_threads_on_their_own_streams():
+    # the calls let other threads run while they allocate and launch
+    from concurrent.futures import ThreadPoolExecutor
+    x = torch.randn((4, 6, 30000), device="cuda").bfloat16()
+    tokens = torch.arange(6, dtype=torch.int32, device="cuda")
+    want = [api.kda_token_logprobs(x[i], tokens, num_top=5) for i in range(4)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [api.kda_token_logprobs(x[i], tokens, num_top=5) for _ in range(50)]
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as pool:
+        for i, got in enumerate(pool.map(work, range(4))):
+            for g in got:
+                assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
