@@ -9,7 +9,7 @@
 // that grows with p.  Its top 32 bits, signed, give the angle in [-pi, pi)
 // for sincospif.  u_i is made from f_i's bits in whole numbers too: with fp64
 // arithmetic, some 2 lanes a clock on an SM here, 256 tokens took 6.4 us and
-// not 4.8.
+// not 4.2.
 //
 // Every value is read and written once and the arithmetic is 3 flops per
 // rotated channel, so HBM bounds the large calls and latency the small ones.
@@ -27,7 +27,12 @@ using kda_cache::Rows;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 64;
-constexpr int kCtasPerSm = 5;   // 48 registers a thread
+
+// With 64 registers a thread for heads of 128 channels and 48 for 64.  Measured
+// (us, 4 | 5 CTAs an SM): 256 tokens 4.2 | 4.9 and 13.7k tokens 45 | 48 with
+// 128 channels (16k interleaved ones 53 | 51), 10k tokens 7.4 | 6.8 and 56k
+// tokens 22 | 20 with 64.
+constexpr int ctas_per_sm(int dim) { return dim == 128 ? 4 : 5; }
 
 struct Params {
     Rows rows;
@@ -126,7 +131,7 @@ __device__ __forceinline__ int2 chunks_of(const Params &p, bool turned, int j) {
 }
 
 template <typename T, int kDim>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(const Params p) {
     constexpr int kUnits = kDim / 16;  // units of a head
     __shared__ float2 turns[kWarps][kMaxPairs];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -150,8 +155,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(const Para
         else
             src = reinterpret_cast<const T *>(p.v) + t * p.stride_v + (head - first_v) * kDim;
         const int2 at = chunks_of(p, head < first_v && j * 8 < p.pairs, j);
-        x = *reinterpret_cast<const uint4 *>(src + at.x);
-        y = *reinterpret_cast<const uint4 *>(src + at.y);
+        // read and written once here: marked to leave the caches first, which
+        // takes 2 of 53 us off 16k tokens
+        x = __ldcs(reinterpret_cast<const uint4 *>(src + at.x));
+        y = __ldcs(reinterpret_cast<const uint4 *>(src + at.y));
     };
     uint4 x[2], y[2];
     load(begin + lane, x[0], y[0]);
@@ -194,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(const Para
         const int2 at = chunks_of(p, turned, j);
         if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
         if (head < first_k || block > 0) {
-            *reinterpret_cast<uint4 *>(dst + at.x) = x;
-            *reinterpret_cast<uint4 *>(dst + at.y) = y;
+            __stcs(reinterpret_cast<uint4 *>(dst + at.x), x);
+            __stcs(reinterpret_cast<uint4 *>(dst + at.y), y);
         }
     };
     for (int u = begin + lane; u < end; u += 64) {
@@ -258,9 +265,10 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     // A warp that takes a whole token makes its sines once and keeps its loads
     // ahead of its stores, one that takes a round of it leaves more warps for
     // few tokens.  Measured (us, a round | a token of 10 or 12): 256 tokens
-    // 4.9 | 7.2, 16k tokens 77 | 54.  So rounds grow once two full sets of
+    // 4.2 | 7.1, 16k tokens 75 | 53.  So rounds grow once two full sets of
     // resident warps have one each.
-    const long long most = (long long)kda_cache::sm_count() * kCtasPerSm * kWarps * 2;
+    const long long most =
+        (long long)kda_cache::sm_count() * ctas_per_sm(cfg->head_dim) * kWarps * 2;
     if (most <= 0) return KDA_ERR_CUDA;
     const long long wanted = (long long)num_tokens * rounds / most;
     p.rounds = wanted < 1 ? 1 : wanted > rounds ? rounds : (int)wanted;
