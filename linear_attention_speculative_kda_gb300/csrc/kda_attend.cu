@@ -184,11 +184,17 @@ __device__ __forceinline__ void group_sync(int group) {
 
 // ------------------------------------------------------------------- plan --
 
+// The first key that a query of the row sees.  What lies before it in its tile
+// is never read, or zeroed: its weights are 0, but 0 times a NaN is one.
+__device__ __forceinline__ int first_key(const Params &p, const Row &row) {
+    return p.left_window > 0 ? max(0, row.computed + 1 - p.left_window) : 0;
+}
+
 // The tiles a row's keys span: [first, end).
 __device__ __forceinline__ void row_tiles(const Params &p, const Row &row, int &first, int &end) {
     first = end = 0;
     if (row.tokens == 0) return;
-    first = p.left_window > 0 ? max(0, row.computed + 1 - p.left_window) / kTile : 0;
+    first = first_key(p, row) / kTile;
     end = (row.computed + row.tokens - 1) / kTile + 1;
 }
 
@@ -406,13 +412,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
 
     // Load one tile into ring slot `slot`: this warp's 16 keys and values.
     // Lane l looks up key l mod 16; the address goes to the loading lanes by
-    // shuffle.  Keys past the row's end and in null blocks become zeros.
+    // shuffle.  Keys behind a sliding window, past the row's end and in null
+    // blocks become zeros.
     auto load_tile = [&](int slot) {
         if (to_load > 0) {
             const int pos = ld.tile * kTile + 16 * warp + (lane & 15);
             int block = 0;
             long long off = 0;
-            if (pos < ld.row.computed + ld.row.tokens) {
+            if (pos >= first_key(p, ld.row) && pos < ld.row.computed + ld.row.tokens) {
                 const int col = kda_cache::divide(pos, p.rows.by_block);
                 block = p.rows.block_table[ld.row.request * p.rows.bt_stride + col];
                 if (block >= p.rows.num_blocks) {
@@ -1079,8 +1086,9 @@ __device__ __forceinline__ void scale_o(uint32_t o, float f) {
 // A box is p.box keys, the greatest common divisor of the block size and the
 // tile, so a tile is kTile / p.box boxes of each channel block, each inside
 // one block of the cache.  A lane fetches the table entry of a box's block a
-// tile ahead and asks for the box.  The null block and boxes past the row's
-// end are boxes past the tensor's last block, which arrive as zeros.
+// tile ahead and asks for the box.  The null block, boxes past the row's end
+// and boxes behind a sliding window are boxes past the tensor's last block,
+// which arrive as zeros.
 
 template <typename T, int kDim, int kQRows>
 __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Control &c,
@@ -1095,7 +1103,7 @@ __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Cont
     auto look_up = [&]() {
         pos = at.tile * kTile + mine * p.box;
         block = 0;
-        if (pos < at.row.computed + at.row.tokens)
+        if (first_key(p, at.row) - pos < p.box && pos < at.row.computed + at.row.tokens)
             block = p.rows.block_table[at.row.request * p.rows.bt_stride +
                                        kda_cache::divide(pos, p.rows.by_block)];
     };
@@ -1395,19 +1403,22 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
             }
             // A value that is not finite must not reach the rows that do not
             // see its key (0 * inf is NaN in the product).  What lies past the
-            // row's end is zeroed; of the row's own keys only those matter that
-            // some rows see and others do not: the window's own but the first,
-            // and as many at a sliding window's start.
+            // row's end or behind a sliding window is zeroed; of the other keys
+            // only those matter that some rows see and others do not: the
+            // window's own but the first, and as many at a sliding window's
+            // start.
             const int tail = at.row.computed + at.row.tokens - key0;  // first key past the row
-            if (edge && (at.row.tokens > 1 || tail < kTile)) {
+            if (edge && (at.row.tokens > 1 || tail < kTile || p.left_window > 0)) {
                 const int j = (int)((2 * g + 1) % F::kStages);
                 if (!warp_wait(c, &c.full[j], (uint32_t)(((2 * g + 1) / F::kStages) & 1),
                                p.rows.err))
                     return;
                 const uint32_t values = F::stage(smem, j);
-                for (int i = max(tail, 0) * kChunks + tid; i < kTile * kChunks;
-                     i += 32 * kSoftmaxWarps)
-                    store16(values + place(i / kChunks, i % kChunks, kTile), make_uint4(0, 0, 0, 0));
+                const int front = first_key(p, at.row) - key0;  // first key that is seen
+                for (int i = tid; i < kTile * kChunks; i += 32 * kSoftmaxWarps)
+                    if (i / kChunks < front || i / kChunks >= tail)
+                        store16(values + place(i / kChunks, i % kChunks, kTile),
+                                make_uint4(0, 0, 0, 0));
                 kda::fence_proxy_async_smem();
                 const int own = at.row.tokens - 1;
                 unsigned long long odd = 0;
