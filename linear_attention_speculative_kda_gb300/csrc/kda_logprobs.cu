@@ -200,11 +200,21 @@ __device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, uns
     return d;
 }
 
+// Whether the lowest value of a 16-bit type has the weight 0 at this base (a
+// row that is masked by that value may have no larger one), and no distance
+// from base overflows.
+template <typename T>
+__device__ __forceinline__ bool far_from_lowest(float base) {
+    constexpr float kAbove = sizeof(T) == 2 && __is_same(T, __half) ? -65504.0f + 200.0f : -1e30f;
+    return base > kAbove && base < 1e30f;
+}
+
 // Adds a vector's elements to s and w (even and odd elements apart), as
 // distances from base.  A masked element (-inf) has the weight 0 but an
 // infinite distance, whose product is no number: kClamp bounds the distance;
-// without it (16-bit types, |base| far from overflow) the element is the
-// type's lowest value instead, one instruction for two elements.  The pairs
+// without it the element is the type's lowest value instead, one instruction
+// for two elements, which weighs nothing either where base is far above it
+// (`far_from_lowest`).  The pairs
 // and that took 12 instructions an element to 8, where some 11 keep up with
 // HBM: 256 x 131072 with 8 alternatives 21.2 -> 19.6 us.
 template <typename T, bool kClamp>
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 8 : 3)
             base = top;
         }
         unsigned long long s = 0, w = 0;  // pairs of 0
-        if (sizeof(T) == 2 && base < 1e30f) {
+        if (sizeof(T) == 2 && far_from_lowest<T>(base)) {
             if constexpr (sizeof(T) == 2)
 #pragma unroll
                 for (int i = 0; i < kUnroll; ++i) accumulate<T, false>(u[i], base, s, w);
