@@ -475,7 +475,8 @@ size_t kda_attention_workspace_bytes(const kda_cache_config *cfg, int32_t B);
  *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale q.k_j,
  *   lse = ln sum_j e^(s_j)
  * with products, sums and the softmax in fp32 and the weights rounded to the
- * storage type for the product with v.  What a query does not see does not
+ * storage type for the product with v (fp16: relative to 2^-7 of the largest,
+ * so that those of many keys far below a leading one are not lost).  What a query does not see does not
  * touch it, whatever it holds (NaN and infinities too).  A query that sees
  * no key (or only scores of -inf) gets out = 0 and lse = -inf.
  *

@@ -9,6 +9,16 @@
 // one; smaller growth stays in m's old units (P <= 2^8), which changes no
 // result, only how often O is rescaled.
 //
+// S, m, l and O are fp32.  P is rounded to the storage type for P V, because the
+// matrix instructions take both operands in one type: half a step of it a
+// weight, relative, where a second product with what the rounding left would
+// cost as much as the first, and give NaN for a weight without a rest times an
+// infinite value.  l adds the weights as they were.  In fp16 P and l are held
+// times 2^7: weights would be subnormal from 2^-14 of the largest one on, and
+// vanish below 2^-25, where half of the sum can lie if one key leads the others
+// far enough; so they keep their bits down to 2^-21, and the largest, 2^15 with
+// the slack, stays below 65504.
+//
 // Work split.  The unit is a tile of 64 keys of one (row, kv head); all tiles
 // of the call, in row, head, key order, are cut into equal runs, one per CTA
 // of the two or three that fit an SM.  Each CTA finds its run from the rows'
@@ -47,6 +57,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 64;             // keys of a tile
 constexpr int kMaxCtas = 512;         // bound of the grid, for the workspace
 constexpr float kLazy = 8.0f;         // log2 of the growth a stale maximum may have
+template <typename T>                 // log2 of the factor that P and l are held times
+constexpr float kLift = __is_same(T, __half) ? 7.0f : 0.0f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
                 for (int a = 0; a < kMT; ++a)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float base = m[a][h] == -INFINITY ? 0.0f : -m[a][h];
+                        const float base = m[a][h] == -INFINITY ? 0.0f : kLift<T> - m[a][h];
                         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                         for (int n = 0; n < 2 * kNB; ++n) {
@@ -767,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
             for (int h = 0; h < 2; ++h) {
                 l[a][h] += __shfl_xor_sync(kFull, l[a][h], 1);
                 l[a][h] += __shfl_xor_sync(kFull, l[a][h], 2);
+                m[a][h] -= kLift<T>;  // what l and O are relative to
             }
         if constexpr (L::kGroups > 1) {
 #pragma unroll
@@ -1383,7 +1396,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
                     m = now;
                     l *= f;
                 }
-                const float base = m == -INFINITY ? 0.0f : m;
+                const float base = m == -INFINITY ? 0.0f : m - kLift<T>;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < kTile; i += 32) {
@@ -1509,6 +1522,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
         if (left > 0) at.next_segment(p);
         if (!product_done()) return;
         kda::tc_fence_after();
+        m -= kLift<T>;  // what l and O are relative to
         if (active) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
