@@ -403,7 +403,9 @@ kda_status kda_record_state_blocks(const kda_align *align,
  * q, k and v have (KDA_ROW_BAD_LENGTH), and when its request index is outside
  * [0, num_requests), its num_computed negative or its last position past the
  * table's last column (KDA_ROW_BAD_BLOCK).  Rows without tokens are skipped
- * silently.
+ * silently.  Around a negative count cu_seqlens is out of order, and rows may
+ * overlap: a token that lies in several, or behind the start of a later one
+ * that ends before it, is taken for one of them or left alone.
  */
 #define KDA_DTYPE_BF16 0
 #define KDA_DTYPE_FP16 1

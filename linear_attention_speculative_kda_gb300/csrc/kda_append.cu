@@ -46,6 +46,7 @@ struct Params {
     int interleaved;
     int parts;        // warps that share a token
     int rounds;       // rounds of 32 units (one a lane) each of them takes
+    int token_blocks; // CTAs that take tokens; those behind them check the rows
 };
 
 __device__ __forceinline__ float2 to_float2(uint32_t u, __nv_bfloat16) {
@@ -137,6 +138,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
+    if ((int)blockIdx.x >= p.token_blocks) {  // these check the rows
+        const long long r = ((long long)blockIdx.x - p.token_blocks) * kThreads + threadIdx.x;
+        int bits = 0;
+        if (r < p.rows.B) kda_cache::read_row(p.rows, (int)r, 0x7fffffff, bits);
+        if (bits != 0) kda_cache::flag(p.rows.err, bits);
+        return;
+    }
     const long long item = (long long)blockIdx.x * kWarps + warp;
     const int t = (int)(item / p.parts), part = (int)(item % p.parts);
     if (t >= p.num_tokens) return;
@@ -165,9 +173,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
 
     const int b = find_row(p.rows.cu_seqlens, p.rows.B, t, lane);
     if (b < 0) return;
-    int bits = 0;
+    int bits = 0;  // flagged where the rows are checked
     const kda_cache::Row row = kda_cache::read_row(p.rows, b, 0x7fffffff, bits);
-    if (bits != 0 && lane == 0) kda_cache::flag(p.rows.err, bits);
     if (t - row.first >= row.tokens) return;  // between rows, or a row that is skipped
     const int pos = row.computed + (t - row.first);
     const int col = kda_cache::divide(pos, p.rows.by_block);
@@ -274,8 +281,14 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     p.rounds = wanted < 1 ? 1 : wanted > rounds ? rounds : (int)wanted;
     p.parts = (rounds + p.rounds - 1) / p.rounds;
     const long long items = (long long)num_tokens * p.parts;
-    const long long grid = (items + kWarps - 1) / kWarps;
+    const long long token_blocks = (items + kWarps - 1) / kWarps;
+    // CTAs of their own check the rows, each once, a thread a row: a row that is
+    // wrong may have no token that leads to it, and where it has, every warp of
+    // its tokens would report it.
+    const long long grid =
+        token_blocks + (error_word != nullptr ? ((long long)B + kThreads - 1) / kThreads : 0);
     if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    p.token_blocks = (int)token_blocks;
     void (*kernel)(const Params) =
         cfg->dtype == KDA_DTYPE_BF16
             ? (cfg->head_dim == 64 ? append_kernel<__nv_bfloat16, 64>
