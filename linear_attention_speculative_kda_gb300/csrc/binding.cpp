@@ -203,7 +203,9 @@ PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
             c.rotary_dim = narrow(2 * f.numel());
             a.inv_freq = f.const_data_ptr<double>();
         }
-        c.interleaved = PyObject_IsTrue(o[10]) == 1 ? 1 : 0;
+        const int interleaved = PyObject_IsTrue(o[10]);
+        need(interleaved >= 0);  // no truth value: it raises again in api.py
+        c.interleaved = interleaved;
         a.k = k.const_data_ptr();
         a.v = v.const_data_ptr();
         a.key_cache = keys.data_ptr();
