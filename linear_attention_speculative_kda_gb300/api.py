@@ -770,12 +770,16 @@ def _mismatch(device, **tensors):
 
 def _check_cache(key_cache, value_cache):
     """Shape and strides of a paged cache viewed as [num_blocks, block_size,
-    kv_heads, head_dim]."""
-    shape, strides = key_cache.shape, key_cache.stride()
+    kv_heads, head_dim].  The stride of a dimension of one element says nothing
+    and may be anything; a head's channels stand for it."""
+    shape, strides, others = key_cache.shape, key_cache.stride(), value_cache.stride()
     if len(shape) != 4 or strides[3] != 1:
         raise ValueError("the caches must be [num_blocks, block_size, kv_heads, head_dim] views "
                          "with contiguous channels")
-    if value_cache.stride() != strides or value_cache.shape != shape:
+    if 1 in shape:
+        strides = tuple(shape[3] if n == 1 else s for n, s in zip(shape, strides))
+        others = tuple(shape[3] if n == 1 else s for n, s in zip(value_cache.shape, others))
+    if others != strides or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must have the same shape and strides")
     return shape, strides
 

@@ -60,18 +60,25 @@ int32_t dtype_code(at::ScalarType t) {
     return t == at::kBFloat16 ? KDA_DTYPE_BF16 : t == at::kHalf ? KDA_DTYPE_FP16 : KDA_DTYPE_FP32;
 }
 
-// Both caches: their type, shape and strides.
+// Both caches: their type, shape and strides.  The stride of a dimension of one
+// element says nothing and may be anything; a head's channels stand for it.
 void set_cache(kda_cache_config &c, int32_t &block_size, const Tensor &keys, const Tensor &values) {
-    need(keys.dim() == 4 && keys.stride(3) == 1 && values.sizes() == keys.sizes() &&
-         values.strides() == keys.strides() && keys.scalar_type() != at::kFloat);
+    need(keys.dim() == 4 && keys.stride(3) == 1 && values.dim() == 4 && values.stride(3) == 1 &&
+         values.sizes() == keys.sizes() && keys.scalar_type() != at::kFloat);
+    int64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        const bool one = keys.size(i) == 1;
+        need(one || values.stride(i) == keys.stride(i));
+        strides[i] = one ? keys.size(3) : keys.stride(i);
+    }
     c.dtype = dtype_code(keys.scalar_type());
     c.num_blocks = narrow(keys.size(0));
     block_size = narrow(keys.size(1));
     c.kv_heads = narrow(keys.size(2));
     c.head_dim = narrow(keys.size(3));
-    c.stride_block = keys.stride(0);
-    c.stride_token = keys.stride(1);
-    c.stride_head = keys.stride(2);
+    c.stride_block = strides[0];
+    c.stride_token = strides[1];
+    c.stride_head = strides[2];
 }
 
 // A [T, heads, dim] activation, heads and channels packed: its token stride.
