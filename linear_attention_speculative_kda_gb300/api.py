@@ -908,6 +908,11 @@ def kda_attention_workspace_bytes(num_rows: int, q_heads: int, kv_heads: int, he
     return int(load_library().kda_attention_workspace_bytes(ctypes.byref(cfg), num_rows))
 
 
+def _largest_window(q_heads: int, kv_heads: int) -> int:
+    group = q_heads // max(kv_heads, 1)
+    return min(MAX_WINDOW, max(1, MAX_QUERY_ROWS // max(group, 1)))
+
+
 def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, head_dim: int, device,
                                  window: int | None = None) -> torch.Tensor:
     """A workspace for ``kda_window_attention`` calls of up to ``num_rows``
@@ -915,8 +920,7 @@ def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, hea
     allow).  It holds nothing between calls; calls that may overlap need one
     each."""
     if window is None:
-        group = q_heads // max(kv_heads, 1)
-        window = min(MAX_WINDOW, MAX_QUERY_ROWS // max(group, 1))
+        window = _largest_window(q_heads, kv_heads)
     nbytes = kda_attention_workspace_bytes(num_rows, q_heads, kv_heads, head_dim, window)
     if nbytes == 0:
         raise ValueError("invalid attention sizes")
@@ -924,11 +928,11 @@ def allocate_attention_workspace(num_rows: int, q_heads: int, kv_heads: int, hea
 
 
 def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num_computed,
-                         workspace, *, window: int = MAX_WINDOW, scale=None, left_window: int = 0,
+                         workspace, *, window: int | None = None, scale=None, left_window: int = 0,
                          request_indices=None, out=None, lse=None, error_word=None):
     """``kda_window_attention``: softmax attention of each row's new tokens
-    (at most ``window``) over its paged keys and values, the new ones included
-    (``kda_kv_append`` first).
+    (at most ``window``; None: the largest window the head counts allow) over
+    its paged keys and values, the new ones included (``kda_kv_append`` first).
 
     q: [T, Hq, D] (token stride free), bf16 or fp16; caches, block_table and
     num_computed as for ``kda_kv_append``; ``left_window``: keys a query sees,
@@ -965,6 +969,8 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
     T, q_heads, stride_q = _heads_tokens(q, "q", dim)
     if q_heads < 1 or q_heads % kv_heads:
         raise ValueError("q must be [T, Hq, D] with Hq a multiple of the cache's heads")
+    if window is None:
+        window = _largest_window(q_heads, kv_heads)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:

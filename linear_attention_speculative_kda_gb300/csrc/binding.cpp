@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -256,7 +257,10 @@ PyObject *attend(PyObject *, PyObject *const *o, Py_ssize_t n) {
         need(c.kv_heads > 0 && c.q_heads > 0 && c.q_heads % c.kv_heads == 0 && q.size(0) > 0 &&
              work.is_contiguous());
         a.num_tokens = narrow(q.size(0));
-        c.window = integer(o[8]);
+        c.window = o[8] != Py_None
+                       ? integer(o[8])
+                       : std::min(KDA_MAX_WINDOW,
+                                  std::max(1, KDA_MAX_QUERY_ROWS / (c.q_heads / c.kv_heads)));
         c.left_window = integer(o[10]);
         need(o[9] == Py_None || PyFloat_CheckExact(o[9]));
         c.scale = (float)(o[9] == Py_None ? 1.0 / std::sqrt((double)c.head_dim)

@@ -1,6 +1,6 @@
 """GPU: arguments of the attention layers' calls that both parts of the binding
-have to take alike: a truth value that raises, strides of dimensions of one
-element, which mean nothing."""
+have to take alike: a window that is left to the call, a truth value that
+raises, strides of dimensions of one element, which mean nothing."""
 
 import pytest
 import torch
@@ -21,6 +21,30 @@ def part(request):
         pytest.skip("the compiled part was not built")
     yield request.param
     api._quick = saved
+
+
+@pytest.mark.parametrize("group,most", [(2, 8), (16, 8), (20, 6), (64, 2), (128, 1)])
+def test_the_window_that_the_head_counts_allow(group, most):
+    c = Case([most, 1], [30, 5], group, 1, 64, 16, seed=group)
+    work = api.allocate_attention_workspace(2, group, 1, 64, "cuda")
+    out, lse = api.kda_window_attention(c.q, c.keys, c.values, c.cu, c.table, c.computed, work,
+                                        error_word=c.err)
+    given, given_lse = api.kda_window_attention(c.q, c.keys, c.values, c.cu, c.table, c.computed,
+                                                work, window=most, error_word=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    assert torch.equal(out, given) and torch.equal(lse, given_lse)
+    if most < 8:
+        with pytest.raises(api.KDAError, match="UNSUPPORTED"):
+            api.kda_window_attention(c.q, c.keys, c.values, c.cu, c.table, c.computed, work,
+                                     window=most + 1)
+
+
+def test_too_many_heads_are_unsupported():
+    c = Case([1], [5], 129, 1, 64, 16, seed=1)
+    work = api.allocate_attention_workspace(1, 128, 1, 64, "cuda")
+    with pytest.raises(api.KDAError, match="UNSUPPORTED"):
+        api.kda_window_attention(c.q, c.keys, c.values, c.cu, c.table, c.computed, work)
 
 
 def test_a_truth_value_that_raises_launches_nothing():
