@@ -251,6 +251,15 @@ def _stream_ptr(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _on(index: int, fn, *args):
+    """fn(*args) with the tensors' GPU as the current one: the library launches
+    on the current device, and a stream handle may not say which it belongs to."""
+    if index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
 def _token_stride(t: torch.Tensor) -> int:
     # [T, H, D] (or [1, T, H, D]) activation with heads and channels packed
     if t.dim() == 4:
@@ -460,11 +469,10 @@ def kda_verify(q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens,
                   record_format)
     _check_records(records, H, window, record_slots, record_format)
     lib = load_library()
-    st = lib.kda_verify(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw),
-                        _ptr(beta_raw), _ptr(A_log), _ptr(g_bias), _ptr(state_pool),
-                        _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(record_rows),
-                        _ptr(pending), _ptr(records), _ptr(out), _ptr(trajectory_out),
-                        _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_verify, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw),
+             _ptr(beta_raw), _ptr(A_log), _ptr(g_bias), _ptr(state_pool), _ptr(cu_seqlens),
+             _ptr(state_indices), B, _ptr(record_rows), _ptr(pending), _ptr(records), _ptr(out),
+             _ptr(trajectory_out), _ptr(error_word), _stream_ptr(dev))
     _check("kda_verify", st)
     return out
 
@@ -500,10 +508,10 @@ def kda_commit(A_log, g_bias, state_pool, cu_seqlens, state_indices, num_accepte
                   record_format)
     _check_records(records, H, window, record_slots, record_format)
     lib = load_library()
-    st = lib.kda_commit(ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias), _ptr(state_pool),
-                        _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(num_accepted),
-                        _ptr(record_rows), _ptr(records), _ptr(pending), _ptr(eager),
-                        _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_commit, ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias),
+             _ptr(state_pool), _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(num_accepted),
+             _ptr(record_rows), _ptr(records), _ptr(pending), _ptr(eager), _ptr(error_word),
+             _stream_ptr(dev))
     _check("kda_commit", st)
 
 
@@ -531,9 +539,9 @@ def kda_flush(A_log, g_bias, state_pool, state_indices, records, pending, *, win
                   record_format)
     _check_records(records, H, window, record_slots, record_format)
     lib = load_library()
-    st = lib.kda_flush(ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias), _ptr(state_pool),
-                       _ptr(state_indices), B, _ptr(record_rows), _ptr(records), _ptr(pending),
-                       _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_flush, ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias),
+             _ptr(state_pool), _ptr(state_indices), B, _ptr(record_rows), _ptr(records),
+             _ptr(pending), _ptr(error_word), _stream_ptr(dev))
     _check("kda_flush", st)
 
 
@@ -573,9 +581,8 @@ def kda_conv_compact(conv_state, cu_seqlens, state_indices, num_accepted, *, win
         raise ValueError("metadata sizes do not match the batch")
     cc = make_conv_config(conv_state, window)
     lib = load_library()
-    st = lib.kda_conv_compact(ctypes.byref(cc), _ptr(conv_state), _ptr(cu_seqlens),
-                              _ptr(state_indices), B, _ptr(num_accepted), _ptr(error_word),
-                              _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_conv_compact, ctypes.byref(cc), _ptr(conv_state), _ptr(cu_seqlens),
+             _ptr(state_indices), B, _ptr(num_accepted), _ptr(error_word), _stream_ptr(dev))
     _check("kda_conv_compact", st)
 
 
@@ -647,10 +654,10 @@ def kda_commit_align(A_log, g_bias, state_pool, cu_seqlens, state_indices, num_a
     _check_records(records, H, window, record_slots, record_format)
     al = make_align(block_table, num_computed, block_size, request_indices)
     lib = load_library()
-    st = lib.kda_commit_align(ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias), _ptr(state_pool),
-                              _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(num_accepted),
-                              _ptr(record_rows), _ptr(records), ctypes.byref(al),
-                              _ptr(pending), _ptr(eager), _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_commit_align, ctypes.byref(cfg), _ptr(A_log), _ptr(g_bias),
+             _ptr(state_pool), _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(num_accepted),
+             _ptr(record_rows), _ptr(records), ctypes.byref(al), _ptr(pending), _ptr(eager),
+             _ptr(error_word), _stream_ptr(dev))
     _check("kda_commit_align", st)
 
 
@@ -674,9 +681,9 @@ def kda_conv_compact_align(conv_state, cu_seqlens, state_indices, num_accepted, 
     cc = make_conv_config(conv_state, window)
     al = make_align(block_table, num_computed, block_size, request_indices)
     lib = load_library()
-    st = lib.kda_conv_compact_align(ctypes.byref(cc), _ptr(conv_state), _ptr(cu_seqlens),
-                                    _ptr(state_indices), B, _ptr(num_accepted),
-                                    ctypes.byref(al), _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_conv_compact_align, ctypes.byref(cc), _ptr(conv_state),
+             _ptr(cu_seqlens), _ptr(state_indices), B, _ptr(num_accepted), ctypes.byref(al),
+             _ptr(error_word), _stream_ptr(dev))
     _check("kda_conv_compact_align", st)
 
 
@@ -722,9 +729,9 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
     al.num_computed = num_computed.data_ptr()
     al.request_indices = None if request_indices is None else request_indices.data_ptr()
     lib = load_library()
-    st = lib.kda_record_state_blocks(ctypes.byref(al), _ptr(idx_mapping), _ptr(num_sampled),
-                                     num_rows, _ptr(state_column), _ptr(num_accepted),
-                                     state_column.shape[0], _ptr(error_word), _stream_ptr(dev))
+    st = _on(dev.index, lib.kda_record_state_blocks, ctypes.byref(al), _ptr(idx_mapping),
+             _ptr(num_sampled), num_rows, _ptr(state_column), _ptr(num_accepted),
+             state_column.shape[0], _ptr(error_word), _stream_ptr(dev))
     _check("kda_record_state_blocks", st)
 
 
@@ -887,7 +894,7 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
         rotary_dim, freq_ptr = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    status = lib.kda_kv_append_packed(_APPEND_ARGS(
+    status = _on(dev, lib.kda_kv_append_packed, _APPEND_ARGS(
         q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim, 1 if interleaved else 0, 1.0,
         strides[0], strides[1], strides[2], stride_q, stride_k, stride_v, block_table.data_ptr(),
         table_stride, width, block_size, requests, 0, num_computed.data_ptr(),
@@ -987,7 +994,7 @@ def kda_window_attention(q, key_cache, value_cache, cu_seqlens, block_table, num
         raise ValueError("workspace must be contiguous")
     if T == 0:  # an empty tensor has no address to pass on
         return out, lse
-    status = lib.kda_window_attention_packed(_ATTENTION_ARGS(
+    status = _on(dev, lib.kda_window_attention_packed, _ATTENTION_ARGS(
         q_heads, kv_heads, dim, code, blocks, window, left_window, 0, 0,
         dim ** -0.5 if scale is None else scale, strides[0], strides[1], strides[2], stride_q, 8,
         8, block_table.data_ptr(), table_stride, width, block_size, requests, 0,
@@ -1062,7 +1069,7 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
             if tuple(t.shape) != want or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {want} tensor")
     logprob, entropy, lse, top_logprob, top_index = out
-    status = lib.kda_token_logprobs_packed(_LOGPROBS_ARGS(
+    status = _on(dev, lib.kda_token_logprobs_packed, _LOGPROBS_ARGS(
         logits.data_ptr(), strides[0], code, rows, vocab, num_top, tokens.data_ptr(),
         logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr(),
         top_index.data_ptr(), _address(error_word), _raw_stream(dev)))

@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -29,6 +30,12 @@ struct NotPlain {};  // thrown where api.py has to look
 
 void need(bool ok) {
     if (!ok) throw NotPlain{};
+}
+
+// The library launches on the current device; where the tensors are on another
+// GPU, api.py switches to it.
+void need_current(c10::Device device) {
+    need(device.is_cuda() && device.index() == c10::cuda::current_device());
 }
 
 const Tensor &tensor(PyObject *o) {
@@ -173,7 +180,7 @@ PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
         need(n == 14);
         const Tensor &keys = tensor(o[4]);
         const c10::Device device = keys.device();
-        need(device.is_cuda());
+        need_current(device);
         const at::ScalarType type = keys.scalar_type();
         const Tensor &k = tensor(o[2], type, device), &v = tensor(o[3], type, device);
         const Tensor &values = tensor(o[5], type, device);
@@ -240,7 +247,7 @@ PyObject *attend(PyObject *, PyObject *const *o, Py_ssize_t n) {
         need(n == 15);
         const Tensor &keys = tensor(o[2]);
         const c10::Device device = keys.device();
-        need(device.is_cuda());
+        need_current(device);
         const at::ScalarType type = keys.scalar_type();
         const Tensor &q = tensor(o[1], type, device), &values = tensor(o[3], type, device);
         const Tensor &cu = tensor(o[4], at::kInt, device), &table = tensor(o[5], at::kInt, device);
@@ -292,7 +299,8 @@ PyObject *logprobs(PyObject *, PyObject *const *o, Py_ssize_t n) {
         need(n == 5);
         const Tensor &x = tensor(o[1]);
         const c10::Device device = x.device();
-        need(device.is_cuda() && x.dim() == 2 && (x.stride(1) == 1 || x.size(1) <= 1) &&
+        need_current(device);
+        need(x.dim() == 2 && (x.stride(1) == 1 || x.size(1) <= 1) &&
              x.layout() == at::kStrided);
         const Tensor &tokens = tensor(o[2], at::kInt, device);
         need(tokens.dim() == 1 && tokens.numel() == x.size(0) && tokens.is_contiguous());
