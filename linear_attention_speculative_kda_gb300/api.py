@@ -168,13 +168,16 @@ def load_library():
 
 
 def _load_quick():
-    """The compiled part of the binding of the short calls, where it was built."""
+    """The compiled part of the binding of the short calls, where it was built
+    for these argument structures and this PyTorch."""
     global _quick
     try:
         from . import _binding
-        _quick = _binding
     except ImportError:
-        _quick = None
+        _binding = None
+    fits = (getattr(_binding, "torch_version", None) == torch.__version__
+            and _binding.argument_sizes == _ARGUMENT_SIZES)
+    _quick = _binding if fits else None
 
 
 def bind_library(path: str):
@@ -745,9 +748,10 @@ def kda_record_state_blocks(idx_mapping, num_sampled, num_computed, state_column
 # go to the library as the bytes of one structure.
 
 _CACHE_FORMAT = "9if6qQqiiiiQQ"     # kda_cache_config, kda_align
-_APPEND_ARGS = struct.Struct("=" + _CACHE_FORMAT + "8Q2i2Q").pack
-_ATTENTION_ARGS = struct.Struct("=" + _CACHE_FORMAT + "4Q2i6Q").pack
-_LOGPROBS_ARGS = struct.Struct("=Qq4i8Q").pack
+_FORMATS = [struct.Struct(f) for f in ("=" + _CACHE_FORMAT + "8Q2i2Q",
+                                       "=" + _CACHE_FORMAT + "4Q2i6Q", "=Qq4i8Q")]
+_APPEND_ARGS, _ATTENTION_ARGS, _LOGPROBS_ARGS = (f.pack for f in _FORMATS)
+_ARGUMENT_SIZES = tuple(f.size for f in _FORMATS)
 
 
 def _failed(fn: str, status: int):

@@ -3,13 +3,15 @@ part of the Python binding, ``_binding.so``.
 
 All translation units in one nvcc call (compiled side by side), one ``-gencode`` (compute_103a /
 sm_103a), the CUDA runtime linked statically so the library only needs the
-driver at run time.  The binding's part is host code against PyTorch's headers;
-where they or Python's are not installed, ``api.py`` does its work.
+driver at run time.  The binding's part is host code against PyTorch's headers,
+for one version of PyTorch and Python, which is noted beside it; where it cannot
+be built, none is left behind and ``api.py`` does its work.
 """
 
 from __future__ import annotations
 
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -78,6 +80,25 @@ def compile_command(output: str, extra=(), sources=None) -> list[str]:
     ]
 
 
+def _built_for() -> str:
+    """What a build of the binding's part is for ("" where PyTorch is missing)."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return f"PyTorch {torch.__version__}, Python {platform.python_version()}"
+
+
+def _binding_stale() -> bool:
+    if _older(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "kda.h")]):
+        return True
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read() != _built_for()
+    except OSError:
+        return True
+
+
 def binding_command(output: str) -> list[str]:
     import torch
 
@@ -87,6 +108,7 @@ def binding_command(output: str) -> list[str]:
     return [
         "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        f'-DKDA_TORCH_VERSION="{torch.__version__}"',
         "-I", os.path.join(ROOT, "include"),
         "-I", sysconfig.get_paths()["include"],
         "-I", headers,
@@ -107,20 +129,27 @@ def _build_library(verbose: bool) -> None:
 
 def _build_binding() -> None:
     tmp = BINDING + f".tmp{os.getpid()}"
-    done = subprocess.run(binding_command(tmp), capture_output=True, text=True)
-    if done.returncode == 0:
-        os.replace(tmp, BINDING)
-    else:
+    try:
+        subprocess.run(binding_command(tmp), check=True, capture_output=True, text=True)
+    except (ImportError, OSError, subprocess.SubprocessError) as error:
+        # an old one would be given the argument structures of another kda.h
+        for path in (BINDING, BINDING + ".for", tmp):
+            if os.path.exists(path):
+                os.remove(path)
         print("the compiled part of the binding was not built; api.py does its work:\n"
-              + done.stderr[:2000], file=sys.stderr)
+              f"{error}\n{(getattr(error, 'stderr', None) or '')[:2000]}", file=sys.stderr)
+        return
+    os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(_built_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build ``libkda.so`` and ``_binding.so``, side by side, where a source is
-    newer; return the library's path."""
+    newer (for the binding: or PyTorch another); return the library's path."""
     with ThreadPoolExecutor(2) as pool:
         jobs = []
-        if force or _older(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "kda.h")]):
+        if force or _binding_stale():
             jobs.append(pool.submit(_build_binding))
         if force or _stale():
             jobs.append(pool.submit(_build_library, verbose))

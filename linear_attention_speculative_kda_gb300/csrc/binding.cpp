@@ -349,4 +349,18 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// What this was built for: api.py uses it only where its own structures have the
+// same sizes and PyTorch, whose tensors are laid out in here, is the same.
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m == nullptr) return nullptr;
+    PyObject *sizes = Py_BuildValue("(nnn)", (Py_ssize_t)sizeof(kda_append_args),
+                                    (Py_ssize_t)sizeof(kda_attention_args),
+                                    (Py_ssize_t)sizeof(kda_logprobs_args));
+    if (sizes == nullptr || PyModule_AddObject(m, "argument_sizes", sizes) != 0 ||
+        PyModule_AddStringConstant(m, "torch_version", KDA_TORCH_VERSION) != 0) {
+        Py_XDECREF(m);
+        return nullptr;
+    }
+    return m;
+}
