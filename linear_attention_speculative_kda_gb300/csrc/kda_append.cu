@@ -184,10 +184,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
         block = 0;
     }
     for (int i = lane; i < p.pairs; i += 32) {
-        const int phase =
-            (int)((turns_per_position(p.inv_freq[i]) * (unsigned long long)pos) >> 32);
+        const double f = p.inv_freq[i];
+        const int phase = (int)((turns_per_position(f) * (unsigned long long)pos) >> 32);
         float2 cs;
         sincospif((float)phase * 0x1p-31f, &cs.y, &cs.x);
+        if ((__double2hiint(f) & 0x7ff00000) == 0x7ff00000)  // infinite or a NaN: no angle
+            cs = make_float2(NAN, NAN);
         turns[warp][i] = cs;
     }
     __syncwarp();

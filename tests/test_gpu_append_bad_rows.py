@@ -98,3 +98,22 @@ def test_a_request_that_is_not_there_in_a_row_of_its_own():
     assert int(c.err.item()) == api.ROW_BAD_BLOCK
     assert torch.equal(q_out[:2], c.q[:2]) and torch.equal(q_out[5:], c.q[5:])
     assert bool((q_out[2:5] == 7.0).all())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_frequency_that_is_no_number(bad, interleaved):
+    # its pair's channels are no numbers either, the others are as they were
+    c = Case([2, 1], [0, 9], 4, 2, 64, 8, "fp16", seed=6)
+    freq = frequencies(32)
+    want = _append(c, 3, inv_freq=freq, interleaved=interleaved)
+    keys = c.keys.clone()
+    freq[5] = bad
+    q_out = _append(c, 3, inv_freq=freq, interleaved=interleaved)
+    pair = [10, 11] if interleaved else [5, 21]
+    rest = [i for i in range(64) if i not in pair]
+    assert torch.isnan(q_out[..., pair]).all() and torch.equal(q_out[..., rest], want[..., rest])
+    for row, p in ((0, 0), (0, 1), (1, 9)):
+        at = int(c.table[row, p // 8]), p % 8
+        assert torch.isnan(c.keys[at][..., pair]).all()
+        assert torch.equal(c.keys[at][..., rest], keys[at][..., rest])
