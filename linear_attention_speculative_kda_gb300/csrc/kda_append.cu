@@ -22,7 +22,9 @@
 
 namespace {
 
+using kda_cache::pack;
 using kda_cache::Rows;
+using kda_cache::unpack;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -48,24 +50,6 @@ struct Params {
     int rounds;       // rounds of 32 units (one a lane) each of them takes
     int token_blocks; // CTAs that take tokens; those behind them check the rows
 };
-
-__device__ __forceinline__ float2 to_float2(uint32_t u, __nv_bfloat16) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
-__device__ __forceinline__ float2 to_float2(uint32_t u, __half) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-
-__device__ __forceinline__ uint32_t from_float2(float2 f, __nv_bfloat16) {
-    const __nv_bfloat162 h = __float22bfloat162_rn(f);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint32_t from_float2(float2 f, __half) {
-    const __half2 h = __float22half2_rn(f);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 
 // The row that owns token t (the last one that starts at or before t), found
 // by a warp in steps of 32; -1 when t lies before every row.
@@ -106,7 +90,7 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, b
     uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 p = to_float2(x[i], T()), r = to_float2(y[i], T());
+        float2 p = unpack(x[i], T()), r = unpack(y[i], T());
         if (interleaved) {
             const float2 s = turn[i], t = turn[4 + i];
             p = make_float2(p.x * s.x - p.y * s.y, p.x * s.y + p.y * s.x);
@@ -117,8 +101,8 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, b
             p = make_float2(u.x * s.x - r.x * s.y, u.y * t.x - r.y * t.y);
             r = make_float2(u.x * s.y + r.x * s.x, u.y * t.y + r.y * t.x);
         }
-        x[i] = from_float2(p, T());
-        y[i] = from_float2(r, T());
+        x[i] = pack(p.x, p.y, T());
+        y[i] = pack(r.x, r.y, T());
     }
     a = make_uint4(x[0], x[1], x[2], x[3]);
     b = make_uint4(y[0], y[1], y[2], y[3]);

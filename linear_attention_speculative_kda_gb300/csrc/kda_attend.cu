@@ -48,9 +48,12 @@
 
 namespace {
 
+using kda_cache::exp2_fast;
 using kda_cache::kFull;
+using kda_cache::pack;
 using kda_cache::Row;
 using kda_cache::Rows;
+using kda_cache::unpack;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -88,31 +91,6 @@ struct Params {
 
 // ------------------------------------------------------------ instructions --
 
-__device__ __forceinline__ float exp2_fast(float x) {  // within 2 ulp, 0 at -inf
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -143,24 +121,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float2 unpack(uint32_t u, __nv_bfloat16) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
-__device__ __forceinline__ float2 unpack(uint32_t u, __half) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
 // Whether either half of u is a NaN or an infinity.
@@ -648,18 +608,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_kernel(const Params p)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float base = m[a][h] == -INFINITY ? 0.0f : kLift<T> - m[a][h];
-                        float2 sum = make_float2(0.0f, 0.0f);
+                        unsigned long long sum = 0;  // a pair of 0
 #pragma unroll
                         for (int n = 0; n < 2 * kNB; ++n) {
-                            const float2 x =
-                                fma2(make_float2(s[a][n][2 * h], s[a][n][2 * h + 1]),
-                                     make_float2(p.scale_log2, p.scale_log2),
-                                     make_float2(base, base));
+                            const float2 x = kda_cache::both(kda_cache::fma_pair(
+                                kda_cache::pair(s[a][n][2 * h], s[a][n][2 * h + 1]),
+                                kda_cache::pair(p.scale_log2, p.scale_log2),
+                                kda_cache::pair(base, base)));
                             s[a][n][2 * h] = exp2_fast(x.x);
                             s[a][n][2 * h + 1] = exp2_fast(x.y);
-                            sum = add2(sum, make_float2(s[a][n][2 * h], s[a][n][2 * h + 1]));
+                            sum = kda_cache::add_pair(
+                                sum, kda_cache::pair(s[a][n][2 * h], s[a][n][2 * h + 1]));
                         }
-                        l[a][h] += sum.x + sum.y;
+                        const float2 two = kda_cache::both(sum);
+                        l[a][h] += two.x + two.y;
                     }
 
             }

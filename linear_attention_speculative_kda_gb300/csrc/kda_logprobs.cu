@@ -37,7 +37,13 @@
 
 namespace {
 
+using kda_cache::add_pair;
+using kda_cache::both;
+using kda_cache::exp2_fast;
+using kda_cache::fma_pair;
 using kda_cache::kFull;
+using kda_cache::mul_pair;
+using kda_cache::pair;
 
 constexpr int kCandidates = 512;
 constexpr int kStretches = 16;    // parts of a thread's elements whose maxima are kept
@@ -57,26 +63,12 @@ struct Params {
     int vocab, top, ctas;         // ctas: of a row's cluster
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {  // within 2 ulp, 0 at -inf
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void unpack(uint4 u, float (&x)[8], __nv_bfloat16) {
+template <typename T>  // of 16 bits
+__device__ __forceinline__ void unpack(uint4 u, float (&x)[8], T) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ void unpack(uint4 u, float (&x)[8], __half) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        const float2 f = kda_cache::unpack(w[i], T());
         x[2 * i] = f.x;
         x[2 * i + 1] = f.y;
     }
@@ -166,38 +158,6 @@ __device__ __forceinline__ void rescale(Stats &a, float m) {  // m >= a.m
         a.s *= f;
     }
     a.m = m;
-}
-
-// Pairs of fp32 operations in one instruction, each as its scalar form rounds.
-__device__ __forceinline__ unsigned long long pair(float x, float y) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-
-__device__ __forceinline__ float2 both(unsigned long long v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-
-__device__ __forceinline__ unsigned long long add_pair(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ unsigned long long mul_pair(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b,
-                                                       unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 
 // Whether the lowest value of a 16-bit type has the weight 0 at this base (a
