@@ -1065,7 +1065,7 @@ __device__ __forceinline__ void scale_o(uint32_t o, float f) {
 // and boxes behind a sliding window are boxes past the tensor's last block,
 // which arrive as zeros.
 
-template <typename T, int kDim, int kQRows>
+template <typename T, int kDim, int kQRows, bool kSliding>
 __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Control &c,
                                            uint32_t smem, int lane, const CUtensorMap *k_map,
                                            const CUtensorMap *v_map) {
@@ -1078,7 +1078,8 @@ __device__ __forceinline__ void run_loader(const Params &p, const Run &run, Cont
     auto look_up = [&]() {
         pos = at.tile * kTile + mine * p.box;
         block = 0;
-        if (first_key(p, at.row) - pos < p.box && pos < at.row.computed + at.row.tokens)
+        if ((!kSliding || first_key(p, at.row) - pos < p.box) &&
+            pos < at.row.computed + at.row.tokens)
             block = p.rows.block_table[at.row.request * p.rows.bt_stride +
                                        kda_cache::divide(pos, p.rows.by_block)];
     };
@@ -1266,7 +1267,7 @@ __device__ __forceinline__ void run_outputs(const Params &p, const Run &run, Con
 
 // ---- the softmax warps ----------------------------------------------------
 
-template <typename T, int kDim, int kQRows>
+template <typename T, int kDim, int kQRows, bool kSliding>
 __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Control &c,
                                             uint32_t smem, uint32_t tmem_all, int cta, int warp,
                                             int lane) {
@@ -1296,7 +1297,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
         const bool mine = row >= 0 && row < rows;
         const int token = token_of(p, max(row, 0));
         const int hi = at.row.computed + min(token, at.row.tokens - 1);
-        const int lo = p.left_window > 0 ? hi - p.left_window : -1;
+        const int lo = kSliding ? hi - p.left_window : -1;
         float m = -INFINITY, l = 0.0f;
         for (int done = 0; done < tiles; ++done, ++g) {
             const int b = (int)(g & 1);
@@ -1310,8 +1311,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
             // a tile that some row does not see whole
             const bool edge =
                 key0 + kTile - 1 > at.row.computed || seen != ~0ull ||
-                (p.left_window > 0 &&
-                 key0 <= at.row.computed + at.row.tokens - 1 - p.left_window);
+                (kSliding && key0 <= at.row.computed + at.row.tokens - 1 - p.left_window);
             if (active) {
                 float s[kTile];
                 {
@@ -1383,21 +1383,22 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
             // window's own but the first, and as many at a sliding window's
             // start.
             const int tail = at.row.computed + at.row.tokens - key0;  // first key past the row
-            if (edge && (at.row.tokens > 1 || tail < kTile || p.left_window > 0)) {
+            if (edge && (at.row.tokens > 1 || kSliding || tail < kTile)) {
                 const int j = (int)((2 * g + 1) % F::kStages);
                 if (!warp_wait(c, &c.full[j], (uint32_t)(((2 * g + 1) / F::kStages) & 1),
                                p.rows.err))
                     return;
                 const uint32_t values = F::stage(smem, j);
-                const int front = first_key(p, at.row) - key0;  // first key that is seen
-                for (int i = tid; i < kTile * kChunks; i += 32 * kSoftmaxWarps)
+                const int front = kSliding ? first_key(p, at.row) - key0 : 0;  // first key seen
+                for (int i = (front > 0 ? 0 : max(tail, 0) * kChunks) + tid; i < kTile * kChunks;
+                     i += 32 * kSoftmaxWarps)
                     if (i / kChunks < front || i / kChunks >= tail)
                         store16(values + place(i / kChunks, i % kChunks, kTile),
                                 make_uint4(0, 0, 0, 0));
                 kda::fence_proxy_async_smem();
                 const int own = at.row.tokens - 1;
                 unsigned long long odd = 0;
-                for (int i = lane; i < (p.left_window > 0 ? 2 : 1) * own * kChunks; i += 32) {
+                for (int i = lane; i < (kSliding ? 2 : 1) * own * kChunks; i += 32) {
                     const int k = i / kChunks;
                     const int key = (k < own ? at.row.computed + 1 + k
                                              : at.row.computed + 1 - p.left_window + k - own) -
@@ -1530,7 +1531,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, const Run &run, Con
     }
 }
 
-template <typename T, int kDim, int kQRows>
+template <typename T, int kDim, int kQRows, bool kSliding>
 __global__ void __launch_bounds__(kThreadCount, kCtasPerSm)
     attend_tc_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
@@ -1572,9 +1573,9 @@ __global__ void __launch_bounds__(kThreadCount, kCtasPerSm)
     const uint32_t tmem = c.tmem;
     if (busy) {
         if (warp < kSoftmaxWarps) {
-            run_softmax<T, kDim, kQRows>(p, run, c, smem, tmem, cta, warp, lane);
+            run_softmax<T, kDim, kQRows, kSliding>(p, run, c, smem, tmem, cta, warp, lane);
         } else if (warp == kLoadWarp) {
-            run_loader<T, kDim, kQRows>(p, run, c, smem, lane, &k_map, &v_map);
+            run_loader<T, kDim, kQRows, kSliding>(p, run, c, smem, lane, &k_map, &v_map);
         } else if (warp == kQueryWarp) {
             run_queries<T, kDim, kQRows>(p, run, c, smem, lane);
         } else if (lane == 0) {
@@ -1758,14 +1759,14 @@ bool cache_map(const Params &p, const char *base, CUtensorMap *map) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int kDim, int kQRows>
+template <typename T, int kDim, int kQRows, bool kSliding>
 kda_status launch_tc(Params &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int sms,
                      void *stream) {
     const int grid = min(tc::kCtasPerSm * sms, kMaxCtas);
     p.by_grid = kda_cache::make_divider(grid);
     using F = tc::Form<kDim, kQRows>;
     void (*kernel)(const Params, const CUtensorMap, const CUtensorMap) =
-        tc::attend_tc_kernel<T, kDim, kQRows>;
+        tc::attend_tc_kernel<T, kDim, kQRows, kSliding>;
     static bool allowed[64];
     if (!allow_shared(reinterpret_cast<const void *>(kernel), F::kBytes, allowed))
         return KDA_ERR_CUDA;
@@ -1796,10 +1797,19 @@ kda_status launch_rows(Params &p, int sms, void *stream) {
     while (p.rows.block_size % p.box != 0) p.box /= 2;
     if (p.most_rows > (kDim == 128 ? 32 : 64) && p.box >= 8) {
         CUtensorMap k_map, v_map;  // (a cache they cannot describe goes the other way)
+        // A sliding window is a kernel of its own: where one served both, what it
+        // has to leave out cost calls without one too, 118 us for 300 rows of up
+        // to 1000 keys and 64 query rows, 109 so, and 95 over the last 300 keys of
+        // them, 92 so.
         if (cache_map<T, kDim>(p, p.key_cache, &k_map) &&
             cache_map<T, kDim>(p, p.value_cache, &v_map))
-            return p.most_rows <= 64 ? launch_tc<T, kDim, 64>(p, k_map, v_map, sms, stream)
-                                     : launch_tc<T, kDim, 128>(p, k_map, v_map, sms, stream);
+            return p.most_rows <= 64
+                       ? (p.left_window > 0
+                              ? launch_tc<T, kDim, 64, true>(p, k_map, v_map, sms, stream)
+                              : launch_tc<T, kDim, 64, false>(p, k_map, v_map, sms, stream))
+                       : (p.left_window > 0
+                              ? launch_tc<T, kDim, 128, true>(p, k_map, v_map, sms, stream)
+                              : launch_tc<T, kDim, 128, false>(p, k_map, v_map, sms, stream));
     }
     // With 64 channels and 32 or 64 rows three CTAs fit an SM: 35 and 49 us,
     // with two 40 and 54; with up to 16 rows two measured better (31 | 55 | 45
