@@ -36,10 +36,13 @@
 //   loading its own 16 keys, so with kMW = 1 no warp waits for another inside
 //   a segment.  The products are mma.sync m16n8k16 on fragments that ldmatrix
 //   reads from XOR-swizzled rows.  64 requests of 4 tokens over up to 8192
-//   keys, 16 rows: 188 us, 95% of the measured HBM rate.
+//   keys, 16 rows: 188 to 192 us, 93% to 95% of the measured HBM rate.
 // - tc::attend_tc_kernel, for more: tcgen05.mma with S and O in tensor memory
 //   and tensor-map TMA loads (below).  128 requests of 8 tokens over up to
-//   12000 keys, 64 rows: 573 us, 92% (698 with the first form).
+//   12000 keys, 64 rows: 573 to 578 us, 91% (698 with the first form).  A
+//   sliding window is a template parameter of it (launch_rows says why).  Its
+//   128 registers a thread, for two CTAs on an SM, leave 56 to 72 bytes of
+//   spills, of values that a segment uses once.
 #include <cuda.h>
 
 #include "kda_async.cuh"
@@ -1779,16 +1782,17 @@ kda_status launch_tc(Params &p, const CUtensorMap &k_map, const CUtensorMap &v_m
 template <typename T, int kDim>
 kda_status launch_rows(Params &p, int sms, void *stream) {
     // Which kernel: measured on 96 rows of up to 2000 keys | 16 rows of up to
-    // 30000 | 300 ragged rows of up to 1000 (us), 4 kv heads.
-    //   channels  query rows   16 rows a warp      tensor-core form
-    //   128       16           47 |  90 |  66      61 |  96 | 102
-    //   128       32           55 |  95 |  73      64 |  98 | 106
-    //   128       40           69 | 117 |  92      68 | 100 | 108
-    //   128       64           78 | 124 | 100      75 | 105 | 114
-    //   128       128         169 | 283 | 227     102 | 120 | 133
-    //   64        32           35 |  56 |  49      51 |  70 |  85
-    //   64        64           49 |  80 |  66      58 |  77 |  91
-    //   64        96           76 | 121 | 102      65 |  84 |  98
+    // 30000 | 300 ragged rows of up to 1000 (us), 4 kv heads, the rows' lengths
+    // spread evenly over an eighth of the longest to the longest.
+    //   channels  query rows   16 rows a warp      tensor-core form     floor
+    //   128       16           49 |  93 |  68      59 |  98 |  99       33 | 83 | 52
+    //   128       32           56 |  98 |  74      63 | 100 | 102       34 | 83 | 53
+    //   128       40           71 | 118 |  95      66 | 103 | 105       34 | 83 | 53
+    //   128       64           79 | 125 | 100      74 | 106 | 109       35 | 83 | 55
+    //   128       128         168 | 281 | 227     100 | 120 | 129       37 | 83 | 58
+    //   64        32           35 |  57 |  49      53 |  70 |  89       17 | 41 | 27
+    //   64        64           49 |  80 |  66      60 |  77 |  95       17 | 41 | 27
+    //   64        96           77 | 121 | 102      65 |  84 |  99       18 | 42 | 28
     // (The lengths are on the device, so they are no part of the rule.)  The
     // tensor-core form reads the cache in boxes of p.box keys and 64 channels,
     // which have to be swizzled atoms of 8 rows; with 96 rows of 64 channels
