@@ -375,6 +375,54 @@ kda_status kda_record_state_blocks(const kda_align *align,
                                    int32_t *error_word, void *stream);
 
 /*
+ * Prompts and plain decoding
+ * --------------------------
+ * kda_verify and kda_commit take windows of up to 8 drafted tokens.  The two
+ * calls below take tokens that are not drafts: whole prompts (or pieces of
+ * them), and one token a row.  Both run each row from one state of the pool
+ * and write its outputs and the state behind its last token:
+ *   from = initial_indices[b] (NULL: state_indices[b]); from <= 0: zeros,
+ *   to   = state_indices[b]; to <= 0: padding, the row is skipped.
+ * So a row may go on in its slot, start from nothing, or start from a cached
+ * block and leave it as it is (several rows may start from one block).  A slot
+ * that one row writes must not be one that another reads or writes.
+ *
+ * Per token and head the recurrence is kda_verify's (same norms, gates and
+ * scale).  Rows without tokens are skipped and write nothing.  Outputs of
+ * tokens in no row, or in skipped rows, are left as they are.
+ *
+ * cfg: num_heads, head_dim, num_slots, the gate, scale and strides as for
+ * kda_verify; window, record_slots and record_format are not looked at.
+ * q, k, v, g_raw: bf16 [num_tokens][H][128], 8-byte aligned, token strides
+ * multiples of 4; beta_raw: bf16 [num_tokens][H]; out: bf16
+ * [num_tokens][H][128] contiguous, 16-byte aligned; A_log, g_bias, state_pool
+ * as for kda_verify.  Rows with a slot >= num_slots (KDA_ROW_BAD_SLOT), a
+ * negative token count or tokens outside [0, num_tokens) (KDA_ROW_BAD_LENGTH)
+ * are skipped and flagged.  B == 0 or num_tokens == 0: KDA_OK, nothing
+ * inspected.
+ */
+
+/* kda_prefill -- the gated delta rule over rows of any length: row b has the
+ * tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 (rows must not overlap). */
+kda_status kda_prefill(const kda_config *cfg,
+                       const void *q, const void *k, const void *v,
+                       const void *g_raw, const void *beta_raw,
+                       const float *A_log, const float *g_bias,
+                       float *state_pool,
+                       const int32_t *cu_seqlens, const int32_t *state_indices,
+                       const int32_t *initial_indices, int32_t B, int32_t num_tokens,
+                       void *out, int32_t *error_word, void *stream);
+
+/* kda_decode -- the same for one token a row: token b is row b's. */
+kda_status kda_decode(const kda_config *cfg,
+                      const void *q, const void *k, const void *v,
+                      const void *g_raw, const void *beta_raw,
+                      const float *A_log, const float *g_bias,
+                      float *state_pool,
+                      const int32_t *state_indices, const int32_t *initial_indices,
+                      int32_t B, void *out, int32_t *error_word, void *stream);
+
+/*
  * The full-attention layers and the acceptance of the same step
  * --------------------------------------------------------------
  * A hybrid model has softmax-attention layers between its KDA layers.  The
@@ -461,6 +509,23 @@ kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void 
                          const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
                          const kda_align *align, int32_t *error_word, void *stream);
 
+/*
+ * kda_kv_norm_append -- kda_kv_append of a layer that norms its queries and
+ * keys: every query and key head x of D channels becomes
+ *   y = x * weight / sqrt(sum x^2 / D + eps)
+ * in fp32 before its rotation, and is rounded once, behind it.  q_weight and
+ * k_weight: [D] of the cache's type or fp32 (weight_dtype), or NULL (ones);
+ * eps >= 0.  A model that stores weight - 1 adds the 1 before the call.  The
+ * sum of squares is fp32: it overflows for elements above some 1e18, whose
+ * head is then 0.  All else as for kda_kv_append.
+ */
+kda_status kda_kv_norm_append(const kda_cache_config *cfg, const void *q, const void *k,
+                              const void *v, const void *q_weight, const void *k_weight,
+                              int32_t weight_dtype, float eps, void *q_out, void *key_cache,
+                              void *value_cache, const double *inv_freq,
+                              const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
+                              const kda_align *align, int32_t *error_word, void *stream);
+
 /* Bytes of the workspace kda_window_attention needs for B rows (0 for an
  * invalid config).  It needs no initialisation and keeps nothing from call
  * to call; calls that may overlap need one each. */
@@ -526,7 +591,7 @@ kda_status kda_token_logprobs(const void *logits, int32_t dtype, int64_t stride_
                               int32_t *error_word, void *stream);
 
 /*
- * The three calls above with their arguments in one structure, for bindings
+ * The short calls above with their arguments in one structure, for bindings
  * in which every argument costs (ctypes: some 4 us a call on a GB300 host).
  * The fields are those arguments, in natural alignment without padding.
  */
@@ -567,7 +632,30 @@ typedef struct kda_logprobs_args {
     void *stream;
 } kda_logprobs_args;
 
+typedef struct kda_norm_append_args {
+    kda_append_args append;
+    const void *q_weight, *k_weight;
+    int32_t weight_dtype;
+    float eps;
+} kda_norm_append_args;
+
+typedef struct kda_delta_args {   /* kda_prefill, kda_decode (without the last line's) */
+    kda_config config;
+    const void *q, *k, *v, *g_raw, *beta_raw;
+    const float *A_log, *g_bias;
+    float *state_pool;
+    const int32_t *state_indices, *initial_indices;
+    void *out;
+    int32_t *error_word;
+    void *stream;
+    int32_t B, num_tokens;
+    const int32_t *cu_seqlens;
+} kda_delta_args;
+
 kda_status kda_kv_append_packed(const kda_append_args *args);
+kda_status kda_kv_norm_append_packed(const kda_norm_append_args *args);
+kda_status kda_prefill_packed(const kda_delta_args *args);
+kda_status kda_decode_packed(const kda_delta_args *args);
 kda_status kda_window_attention_packed(const kda_attention_args *args);
 kda_status kda_token_logprobs_packed(const kda_logprobs_args *args);
 

@@ -58,7 +58,13 @@ EXPORTED = (
     "kda_attention_workspace_bytes",
     "kda_window_attention",
     "kda_token_logprobs",
+    "kda_prefill",
+    "kda_decode",
+    "kda_kv_norm_append",
     "kda_kv_append_packed",
+    "kda_kv_norm_append_packed",
+    "kda_prefill_packed",
+    "kda_decode_packed",
     "kda_window_attention_packed",
     "kda_token_logprobs_packed",
     "kda_status_string",
@@ -146,6 +152,7 @@ class KdaCacheConfig(ctypes.Structure):
 
 
 _quick = None        # the compiled part of the binding of the short calls
+_quick_more = None   # the same, for those whose argument structures it records apart
 _lib_handle = None
 
 
@@ -170,7 +177,7 @@ def load_library():
 def _load_quick():
     """The compiled part of the binding of the short calls, where it was built
     for these argument structures and this PyTorch."""
-    global _quick
+    global _quick, _quick_more
     try:
         from . import _binding
     except ImportError:
@@ -178,6 +185,8 @@ def _load_quick():
     fits = (getattr(_binding, "torch_version", None) == torch.__version__
             and _binding.argument_sizes == _ARGUMENT_SIZES)
     _quick = _binding if fits else None
+    _quick_more = (_quick if getattr(_quick, "more_argument_sizes", None) == _MORE_ARGUMENT_SIZES
+                   else None)
 
 
 def bind_library(path: str):
@@ -217,8 +226,17 @@ def bind_library(path: str):
                                          [vp] * 4)
     lib.kda_token_logprobs.restype = ctypes.c_int
     lib.kda_token_logprobs.argtypes = [vp, i32, ctypes.c_int64, i32, i32, vp, i32] + [vp] * 7
+    delta = [cfgp] + [vp] * 8
+    lib.kda_prefill.restype = ctypes.c_int
+    lib.kda_prefill.argtypes = delta + [vp, vp, vp, i32, i32, vp, vp, vp]
+    lib.kda_decode.restype = ctypes.c_int
+    lib.kda_decode.argtypes = delta + [vp, vp, i32, vp, vp, vp]
+    lib.kda_kv_norm_append.restype = ctypes.c_int
+    lib.kda_kv_norm_append.argtypes = ([ccp] + [vp] * 5 + [i32, ctypes.c_float] + [vp] * 5 +
+                                       [i32, i32, alp, vp, vp])
     for fn in (lib.kda_kv_append_packed, lib.kda_window_attention_packed,
-               lib.kda_token_logprobs_packed):
+               lib.kda_token_logprobs_packed, lib.kda_kv_norm_append_packed,
+               lib.kda_prefill_packed, lib.kda_decode_packed):
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.c_char_p]   # the bytes of the argument structure
     lib.kda_status_string.restype = ctypes.c_char_p
@@ -226,10 +244,13 @@ def bind_library(path: str):
     lib.kda_abi_version.restype = i32
     lib.kda_abi_version.argtypes = []
     # for the compiled part of the binding, which calls the library it is given
-    lib.append_address, lib.attend_address, lib.logprobs_address = (
+    (lib.append_address, lib.attend_address, lib.logprobs_address, lib.norm_append_address,
+     lib.prefill_address, lib.decode_address) = (
         ctypes.cast(fn, vp).value for fn in (lib.kda_kv_append_packed,
                                              lib.kda_window_attention_packed,
-                                             lib.kda_token_logprobs_packed))
+                                             lib.kda_token_logprobs_packed,
+                                             lib.kda_kv_norm_append_packed,
+                                             lib.kda_prefill_packed, lib.kda_decode_packed))
     return lib
 
 
@@ -752,6 +773,9 @@ _FORMATS = [struct.Struct(f) for f in ("=" + _CACHE_FORMAT + "8Q2i2Q",
                                        "=" + _CACHE_FORMAT + "4Q2i6Q", "=Qq4i8Q")]
 _APPEND_ARGS, _ATTENTION_ARGS, _LOGPROBS_ARGS = (f.pack for f in _FORMATS)
 _ARGUMENT_SIZES = tuple(f.size for f in _FORMATS)
+_MORE_FORMATS = [struct.Struct(f) for f in ("=2Qif", "=6i2f5q2i13Q2iQ")]
+_NORM_ARGS, _DELTA_ARGS = (f.pack for f in _MORE_FORMATS)   # the norm's: behind the append's
+_MORE_ARGUMENT_SIZES = (_FORMATS[0].size + _MORE_FORMATS[0].size, _MORE_FORMATS[1].size)
 
 
 def _failed(fn: str, status: int):
@@ -852,6 +876,56 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
                              request_indices, error_word)
         if done is not None:
             return done[0] if done.__class__ is tuple else _failed("kda_kv_append", done)
+    dev, q_out, args = _append_arguments(q, k, v, key_cache, value_cache, cu_seqlens, block_table,
+                                         num_computed, inv_freq, interleaved, q_out,
+                                         request_indices, error_word)
+    status = _on(dev, lib.kda_kv_append_packed, args)
+    if status:
+        raise KDAError("kda_kv_append", status)
+    return q_out
+
+
+def kda_kv_norm_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_computed, *,
+                       q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                       interleaved: bool = False, q_out=None, request_indices=None,
+                       error_word=None):
+    """``kda_kv_norm_append``: ``kda_kv_append`` of a layer that norms each
+    head's queries and keys before their rotation, ``y = x * weight /
+    sqrt(mean(x * x) + eps)`` in fp32.
+
+    q_weight, k_weight: [D] of the cache's type, or both fp32 (None: ones);
+    all else as for ``kda_kv_append``.
+    """
+    lib = load_library()
+    if _quick_more is not None:
+        done = _quick_more.norm_append(lib.norm_append_address, q, k, v, key_cache, value_cache,
+                                       cu_seqlens, block_table, num_computed, inv_freq,
+                                       interleaved, q_out, request_indices, error_word, q_weight,
+                                       k_weight, eps)
+        if done is not None:
+            return done[0] if done.__class__ is tuple else _failed("kda_kv_norm_append", done)
+    dtype, dim = key_cache.dtype, key_cache.shape[-1]
+    weight_dtype = next((w.dtype for w in (q_weight, k_weight) if w is not None), torch.float32)
+    if weight_dtype not in (dtype, torch.float32):
+        raise TypeError(f"the weights must be {dtype} or float32, got {weight_dtype}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _req(w, weight_dtype, name, key_cache.device)
+            if tuple(w.shape) != (dim,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous with {dim} entries")
+    dev, q_out, args = _append_arguments(q, k, v, key_cache, value_cache, cu_seqlens, block_table,
+                                         num_computed, inv_freq, interleaved, q_out,
+                                         request_indices, error_word)
+    status = _on(dev, lib.kda_kv_norm_append_packed, args + _NORM_ARGS(
+        _address(q_weight), _address(k_weight), DTYPES[weight_dtype], eps))
+    if status:
+        raise KDAError("kda_kv_norm_append", status)
+    return q_out
+
+
+def _append_arguments(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_computed,
+                      inv_freq, interleaved, q_out, request_indices, error_word):
+    """The device, the output and the argument structure of an append, checked."""
     dev, dtype, i32 = key_cache.get_device(), key_cache.dtype, torch.int32
     code = DTYPES.get(dtype, 2)
     if code > 1:
@@ -898,16 +972,13 @@ def kda_kv_append(q, k, v, key_cache, value_cache, cu_seqlens, block_table, num_
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous with rotary_dim / 2 entries")
         rotary_dim, freq_ptr = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    status = _on(dev, lib.kda_kv_append_packed, _APPEND_ARGS(
+    return dev, q_out, _APPEND_ARGS(
         q_heads, kv_heads, dim, code, blocks, 1, 0, rotary_dim, 1 if interleaved else 0, 1.0,
         strides[0], strides[1], strides[2], stride_q, stride_k, stride_v, block_table.data_ptr(),
         table_stride, width, block_size, requests, 0, num_computed.data_ptr(),
         _address(request_indices), q_ptr, k.data_ptr(), v.data_ptr(), out_ptr,
         key_cache.data_ptr(), value_cache.data_ptr(), freq_ptr, cu_seqlens.data_ptr(), B, T,
-        _address(error_word), _raw_stream(dev)))
-    if status:
-        raise KDAError("kda_kv_append", status)
-    return q_out
+        _address(error_word), _raw_stream(dev))
 
 
 @functools.lru_cache(maxsize=256)
@@ -1080,3 +1151,99 @@ def kda_token_logprobs(logits, tokens, *, num_top: int = 0, out: TokenLogprobs |
     if status:
         raise KDAError("kda_token_logprobs", status)
     return out
+
+
+# ------------------------------------------ prompts and plain decoding of KDA --
+
+def _delta_call(name, lib, q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens,
+                state_indices, lower_bound, scale, initial_indices, out, error_word):
+    address = lib.prefill_address if cu_seqlens is not None else lib.decode_address
+    if _quick_more is not None:
+        done = _quick_more.delta(address, q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool,
+                                 cu_seqlens, state_indices, lower_bound, scale, initial_indices,
+                                 out, error_word)
+        if done is not None:
+            return done[0] if done.__class__ is tuple else _failed(name, done)
+    dev, bf, f32, i32 = state_pool.device, torch.bfloat16, torch.float32, torch.int32
+    for label, t in (("q", q), ("k", k), ("v", v), ("g_raw", g_raw), ("beta_raw", beta_raw)):
+        _req(t, bf, label, dev)
+    for label, t in (("A_log", A_log), ("g_bias", g_bias), ("state_pool", state_pool)):
+        _req(t, f32, label, dev)
+    _req(state_indices, i32, "state_indices", dev)
+    _opt(cu_seqlens, i32, "cu_seqlens", dev)
+    _opt(initial_indices, i32, "initial_indices", dev)
+    _opt(out, bf, "out", dev)
+    _opt(error_word, i32, "error_word", dev)
+    S, H, D = _check_pool(state_pool)
+    _check_gate(A_log, g_bias, H, D)
+    if state_indices.dim() != 1 or not state_indices.is_contiguous():
+        raise ValueError("state_indices must be contiguous with one entry per row")
+    B = state_indices.shape[0]
+    if initial_indices is not None and (tuple(initial_indices.shape) != (B,)
+                                        or not initial_indices.is_contiguous()):
+        raise ValueError("initial_indices must be contiguous with one entry per row")
+    if cu_seqlens is not None and (tuple(cu_seqlens.shape) != (B + 1,)
+                                   or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens must be contiguous with B + 1 entries")
+    T, heads, _ = _heads_tokens(q, "q", D)
+    if heads != H:
+        raise ValueError(f"q must be [T, {H}, {D}], got {tuple(q.shape)}")
+    strides = []
+    for label, t in (("q", q), ("k", k), ("v", v), ("g_raw", g_raw)):
+        tokens, heads, stride = _heads_tokens(t, label, D)
+        if tokens != T or heads != H:
+            raise ValueError(f"{label} must be shaped like q, got {tuple(t.shape)}")
+        strides.append(stride)
+    if tuple(beta_raw.shape) != (T, H) or (beta_raw.stride(1) != 1 and H > 1):
+        raise ValueError("beta_raw must be [T, H] with contiguous heads inside a token")
+    strides.append(beta_raw.stride(0) if T > 1 else H)
+    if cu_seqlens is None and T != B:
+        raise ValueError("q must have one token per row")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous and shaped like q")
+    _at_least(error_word, 1, "error_word")
+    if T == 0 or B == 0:  # an empty tensor has no address to pass on
+        return out
+    fn = lib.kda_prefill_packed if cu_seqlens is not None else lib.kda_decode_packed
+    status = _on(dev.index, fn, _DELTA_ARGS(
+        H, D, 1, S, 0, 0 if lower_bound is None else 1,
+        0.0 if lower_bound is None else lower_bound, D ** -0.5 if scale is None else scale,
+        *strides, 0, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), g_raw.data_ptr(),
+        beta_raw.data_ptr(), A_log.data_ptr(), g_bias.data_ptr(), state_pool.data_ptr(),
+        state_indices.data_ptr(), _address(initial_indices), out.data_ptr(), _address(error_word),
+        _raw_stream(state_pool.get_device()), B, T, _address(cu_seqlens)))
+    if status:
+        raise KDAError(name, status)
+    return out
+
+
+def kda_prefill(q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens, state_indices, *,
+                lower_bound=None, scale=None, initial_indices=None, out=None, error_word=None):
+    """``kda_prefill``: the gated delta rule over rows of any length, prompts
+    or pieces of them, with ``kda_verify``'s norms, gates and recurrence.
+
+    q, k, v, g_raw: bf16 [T, H, 128] (token stride free, [H, D] packed);
+    beta_raw: bf16 [T, H]; A_log fp32 [H]; g_bias fp32 [H * 128]; state_pool
+    fp32 [S, H, 128, 128]; cu_seqlens int32 [B + 1]; state_indices int32 [B]:
+    the slot that takes the state behind the row's last token (<= 0: the row
+    is skipped); initial_indices int32 [B]: the slot that the row starts from
+    (<= 0: zeros; None: state_indices).  No row may write a slot that another
+    reads or writes.  Returns ``out``, bf16 [T, H, 128]; rows that are skipped
+    leave theirs untouched, and rows without tokens write no state."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    return _delta_call("kda_prefill", load_library(), q, k, v, g_raw, beta_raw, A_log, g_bias,
+                       state_pool, cu_seqlens, state_indices, lower_bound, scale, initial_indices,
+                       out, error_word)
+
+
+def kda_decode(q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, state_indices, *,
+               lower_bound=None, scale=None, initial_indices=None, out=None, error_word=None):
+    """``kda_decode``: one token of each row through the gated delta rule, the
+    state read and written once.  q, k, v, g_raw: bf16 [B, H, 128]; all else as
+    for ``kda_prefill``."""
+    return _delta_call("kda_decode", load_library(), q, k, v, g_raw, beta_raw, A_log, g_bias,
+                       state_pool, None, state_indices, lower_bound, scale, initial_indices, out,
+                       error_word)

@@ -23,13 +23,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("kda_kernels.cu", "kda_conv.cu", "kda_blocks.cu", "kda_append.cu",
-                     "kda_attend.cu", "kda_logprobs.cu")]
+                     "kda_attend.cu", "kda_logprobs.cu", "kda_decode.cu")]
 DEPENDS = SOURCES + [
     os.path.join(CSRC, "kda_device.cuh"),
     os.path.join(CSRC, "kda_async.cuh"),
     os.path.join(CSRC, "kda_align.cuh"),
     os.path.join(CSRC, "kda_tc.cuh"),
     os.path.join(CSRC, "kda_cache.cuh"),
+    os.path.join(CSRC, "kda_delta.cuh"),
     os.path.join(ROOT, "include", "kda.h"),
 ]
 LIBRARY = os.path.join(PKG, "libkda.so")

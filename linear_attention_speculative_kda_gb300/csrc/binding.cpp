@@ -1,5 +1,5 @@
-// The calls of the attention layers and the acceptance for Python without its
-// cost: of the 8 to 11 us that api.py spends around a library call, most are
+// The short calls (those of the attention layers, the acceptance, and the delta
+// rule's prompts and single tokens) for Python without its cost: of the 8 to 11 us that api.py spends around a library call, most are
 // some fifty queries of tensors from Python and the allocations.  Back to back
 // on a GB300's host an append takes 4.8 us so and 11.9 without, an attention
 // 8.6 and 18.2, log probabilities 6.3 and 15.6.
@@ -173,70 +173,193 @@ PyObject *guarded(Body body) {
     }
 }
 
-// address, q, k, v, key_cache, value_cache, cu_seqlens, block_table,
-// num_computed, inv_freq, interleaved, q_out, request_indices, error_word
+// The arguments from o[1] on: q, k, v, key_cache, value_cache, cu_seqlens,
+// block_table, num_computed, inv_freq, interleaved, q_out, request_indices,
+// error_word.  Answers the output that was allocated, if one was.
+Tensor set_append(kda_append_args &a, PyObject *const *o) {
+    const Tensor &keys = tensor(o[4]);
+    const c10::Device device = keys.device();
+    need_current(device);
+    const at::ScalarType type = keys.scalar_type();
+    const Tensor &k = tensor(o[2], type, device), &v = tensor(o[3], type, device);
+    const Tensor &values = tensor(o[5], type, device);
+    const Tensor &cu = tensor(o[6], at::kInt, device), &table = tensor(o[7], at::kInt, device);
+    const Tensor &computed = tensor(o[8], at::kInt, device);
+    kda_cache_config &c = a.config;
+    int32_t block_size;
+    set_cache(c, block_size, keys, values);
+    a.B = set_rows(a.align, block_size, cu, table, computed, o[12], device);
+    c.stride_k_t = token_stride(k, c.head_dim);
+    c.stride_v_t = token_stride(v, c.head_dim);
+    need(k.size(1) == c.kv_heads && v.size(1) == c.kv_heads && v.size(0) == k.size(0));
+    a.num_tokens = narrow(k.size(0));
+    c.q_heads = c.kv_heads;
+    c.window = 1;
+    c.scale = 1.0f;
+    c.stride_q_t = 8;
+    Tensor rotated;
+    if (o[1] != Py_None) {
+        const Tensor &q = tensor(o[1], type, device);
+        c.stride_q_t = token_stride(q, c.head_dim);
+        c.q_heads = narrow(q.size(1));
+        need(q.size(0) == k.size(0) && c.kv_heads > 0 && c.q_heads > 0 &&
+             c.q_heads % c.kv_heads == 0);
+        rotated = output(o[11], q.sizes(), type, device);
+        a.q = q.const_data_ptr();
+        a.q_out = rotated.data_ptr();
+    } else {
+        need(o[11] == Py_None);
+    }
+    if (o[9] != Py_None) {
+        const Tensor &f = tensor(o[9], at::kDouble, device);
+        need(f.dim() == 1 && f.is_contiguous());
+        c.rotary_dim = narrow(2 * f.numel());
+        a.inv_freq = f.const_data_ptr<double>();
+    }
+    const int interleaved = PyObject_IsTrue(o[10]);
+    need(interleaved >= 0);  // no truth value: it raises again in api.py
+    c.interleaved = interleaved;
+    a.k = k.const_data_ptr();
+    a.v = v.const_data_ptr();
+    a.key_cache = keys.data_ptr();
+    a.value_cache = values.data_ptr();
+    a.cu_seqlens = cu.const_data_ptr<int32_t>();
+    a.error_word = error_address(o[13], device);
+    a.stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    return rotated;
+}
+
+// One output: the one that was given, or the one that was allocated, or None.
+PyObject *one_output(PyObject *given, const Tensor &made) {
+    PyObject *result = PyTuple_New(1);
+    if (result == nullptr) return nullptr;
+    PyTuple_SET_ITEM(result, 0,
+                     given != Py_None || !made.defined() ? Py_NewRef(given) : THPVariable_Wrap(made));
+    return result;
+}
+
+// address, then set_append's
 PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         need(n == 14);
-        const Tensor &keys = tensor(o[4]);
-        const c10::Device device = keys.device();
-        need_current(device);
-        const at::ScalarType type = keys.scalar_type();
-        const Tensor &k = tensor(o[2], type, device), &v = tensor(o[3], type, device);
-        const Tensor &values = tensor(o[5], type, device);
-        const Tensor &cu = tensor(o[6], at::kInt, device), &table = tensor(o[7], at::kInt, device);
-        const Tensor &computed = tensor(o[8], at::kInt, device);
         kda_append_args a{};
-        kda_cache_config &c = a.config;
-        int32_t block_size;
-        set_cache(c, block_size, keys, values);
-        a.B = set_rows(a.align, block_size, cu, table, computed, o[12], device);
-        c.stride_k_t = token_stride(k, c.head_dim);
-        c.stride_v_t = token_stride(v, c.head_dim);
-        need(k.size(1) == c.kv_heads && v.size(1) == c.kv_heads && v.size(0) == k.size(0));
-        a.num_tokens = narrow(k.size(0));
-        c.q_heads = c.kv_heads;
+        const Tensor rotated = set_append(a, o);
+        if (const int status = call(o[0], a)) return PyLong_FromLong(status);
+        return one_output(o[11], rotated);
+    });
+}
+
+// A norm's weight, and its type where it has one.
+const void *weight_address(PyObject *o, int64_t dim, int32_t &dtype, c10::Device device) {
+    if (o == Py_None) return nullptr;
+    const Tensor &w = tensor(o);
+    need(w.device() == device && w.dim() == 1 && w.numel() == dim && w.is_contiguous() &&
+         w.layout() == at::kStrided);
+    dtype = dtype_code(w.scalar_type());
+    return w.const_data_ptr();
+}
+
+// address, set_append's, q_weight, k_weight, eps
+PyObject *norm_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 17);
+        kda_norm_append_args a{};
+        const Tensor rotated = set_append(a.append, o);
+        const c10::Device device = tensor(o[4]).device();
+        int32_t types[2] = {-1, -1};
+        a.q_weight = weight_address(o[14], a.append.config.head_dim, types[0], device);
+        a.k_weight = weight_address(o[15], a.append.config.head_dim, types[1], device);
+        need(types[0] < 0 || types[1] < 0 || types[0] == types[1]);
+        a.weight_dtype = std::max(types[0], types[1]);
+        if (a.weight_dtype < 0) a.weight_dtype = KDA_DTYPE_FP32;
+        need(a.weight_dtype == KDA_DTYPE_FP32 || a.weight_dtype == a.append.config.dtype);
+        need(PyFloat_CheckExact(o[16]));
+        a.eps = (float)PyFloat_AS_DOUBLE(o[16]);
+        if (const int status = call(o[0], a)) return PyLong_FromLong(status);
+        return one_output(o[11], rotated);
+    });
+}
+
+// A [T, H, 128] activation, heads and channels packed: its token stride.
+int64_t delta_stride(const Tensor &t, int64_t tokens, int64_t heads) {
+    need(t.dim() == 3 && t.size(0) == tokens && t.size(1) == heads);
+    return token_stride(t, KDA_HEAD_DIM);
+}
+
+// address, q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens
+// (None: one token a row), state_indices, lower_bound, scale,
+// initial_indices, out, error_word
+PyObject *delta(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        need(n == 16);
+        const Tensor &pool = tensor(o[8]);
+        const c10::Device device = pool.device();
+        need_current(device);
+        need(pool.scalar_type() == at::kFloat && pool.dim() == 4 && pool.is_contiguous() &&
+             pool.size(2) == KDA_HEAD_DIM && pool.size(3) == KDA_HEAD_DIM);
+        const int64_t heads = pool.size(1);
+        const Tensor &q = tensor(o[1], at::kBFloat16, device);
+        const Tensor &k = tensor(o[2], at::kBFloat16, device);
+        const Tensor &v = tensor(o[3], at::kBFloat16, device);
+        const Tensor &g = tensor(o[4], at::kBFloat16, device);
+        const Tensor &beta = tensor(o[5], at::kBFloat16, device);
+        const Tensor &a_log = tensor(o[6], at::kFloat, device);
+        const Tensor &bias = tensor(o[7], at::kFloat, device);
+        const Tensor &slots = tensor(o[10], at::kInt, device);
+        need(a_log.is_contiguous() && a_log.numel() >= heads && bias.is_contiguous() &&
+             bias.numel() >= heads * KDA_HEAD_DIM && slots.dim() == 1 && slots.is_contiguous());
+        need(q.dim() == 3 && q.size(0) > 0 && heads > 0);
+        kda_delta_args a{};
+        kda_config &c = a.config;
+        const int64_t tokens = q.size(0);
+        c.num_heads = narrow(heads);
+        c.head_dim = KDA_HEAD_DIM;
         c.window = 1;
-        c.scale = 1.0f;
-        c.stride_q_t = 8;
-        Tensor rotated;
-        if (o[1] != Py_None) {
-            const Tensor &q = tensor(o[1], type, device);
-            c.stride_q_t = token_stride(q, c.head_dim);
-            c.q_heads = narrow(q.size(1));
-            need(q.size(0) == k.size(0) && c.kv_heads > 0 && c.q_heads > 0 &&
-                 c.q_heads % c.kv_heads == 0);
-            rotated = output(o[11], q.sizes(), type, device);
-            a.q = q.const_data_ptr();
-            a.q_out = rotated.data_ptr();
-        } else {
-            need(o[11] == Py_None);
-        }
+        c.num_slots = narrow(pool.size(0));
+        c.stride_q_t = delta_stride(q, tokens, heads);
+        c.stride_k_t = delta_stride(k, tokens, heads);
+        c.stride_v_t = delta_stride(v, tokens, heads);
+        c.stride_g_t = delta_stride(g, tokens, heads);
+        need(beta.dim() == 2 && beta.size(0) == tokens && beta.size(1) == heads &&
+             (beta.stride(1) == 1 || heads == 1));
+        c.stride_beta_t = tokens > 1 ? beta.stride(0) : heads;
+        a.B = narrow(slots.size(0));
+        a.num_tokens = narrow(tokens);
         if (o[9] != Py_None) {
-            const Tensor &f = tensor(o[9], at::kDouble, device);
-            need(f.dim() == 1 && f.is_contiguous());
-            c.rotary_dim = narrow(2 * f.numel());
-            a.inv_freq = f.const_data_ptr<double>();
+            const Tensor &cu = tensor(o[9], at::kInt, device);
+            need(cu.dim() == 1 && cu.is_contiguous() && cu.numel() == (int64_t)a.B + 1);
+            a.cu_seqlens = cu.const_data_ptr<int32_t>();
+        } else {
+            need(tokens == a.B);
         }
-        const int interleaved = PyObject_IsTrue(o[10]);
-        need(interleaved >= 0);  // no truth value: it raises again in api.py
-        c.interleaved = interleaved;
+        if (o[11] != Py_None) {
+            need(PyFloat_CheckExact(o[11]));
+            c.use_lower_bound = 1;
+            c.lower_bound = (float)PyFloat_AS_DOUBLE(o[11]);
+        }
+        need(o[12] == Py_None || PyFloat_CheckExact(o[12]));
+        c.scale = (float)(o[12] == Py_None ? 1.0 / std::sqrt((double)KDA_HEAD_DIM)
+                                           : PyFloat_AS_DOUBLE(o[12]));
+        if (o[13] != Py_None) {
+            const Tensor &from = tensor(o[13], at::kInt, device);
+            need(from.dim() == 1 && from.is_contiguous() && from.numel() == a.B);
+            a.initial_indices = from.const_data_ptr<int32_t>();
+        }
+        const Tensor out = output(o[14], q.sizes(), at::kBFloat16, device);
+        a.q = q.const_data_ptr();
         a.k = k.const_data_ptr();
         a.v = v.const_data_ptr();
-        a.key_cache = keys.data_ptr();
-        a.value_cache = values.data_ptr();
-        a.cu_seqlens = cu.const_data_ptr<int32_t>();
-        a.error_word = error_address(o[13], device);
+        a.g_raw = g.const_data_ptr();
+        a.beta_raw = beta.const_data_ptr();
+        a.A_log = a_log.const_data_ptr<float>();
+        a.g_bias = bias.const_data_ptr<float>();
+        a.state_pool = pool.data_ptr<float>();
+        a.state_indices = slots.const_data_ptr<int32_t>();
+        a.out = out.data_ptr();
+        a.error_word = error_address(o[15], device);
         a.stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
         if (const int status = call(o[0], a)) return PyLong_FromLong(status);
-        PyObject *result = PyTuple_New(1);
-        if (result == nullptr) return nullptr;
-        if (o[1] == Py_None)
-            PyTuple_SET_ITEM(result, 0, Py_NewRef(Py_None));
-        else
-            PyTuple_SET_ITEM(result, 0,
-                             o[11] != Py_None ? Py_NewRef(o[11]) : THPVariable_Wrap(rotated));
-        return result;
+        return one_output(o[14], out);
     });
 }
 
@@ -342,7 +465,8 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {method<append>("append"), method<attend>("attend"),
-                         method<logprobs>("logprobs"), {nullptr, nullptr, 0, nullptr}};
+                         method<logprobs>("logprobs"), method<norm_append>("norm_append"),
+                         method<delta>("delta"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
@@ -357,7 +481,11 @@ PyMODINIT_FUNC PyInit__binding() {
     PyObject *sizes = Py_BuildValue("(nnn)", (Py_ssize_t)sizeof(kda_append_args),
                                     (Py_ssize_t)sizeof(kda_attention_args),
                                     (Py_ssize_t)sizeof(kda_logprobs_args));
-    if (sizes == nullptr || PyModule_AddObject(m, "argument_sizes", sizes) != 0 ||
+    PyObject *more = Py_BuildValue("(nn)", (Py_ssize_t)sizeof(kda_norm_append_args),
+                                   (Py_ssize_t)sizeof(kda_delta_args));
+    if (sizes == nullptr || more == nullptr ||
+        PyModule_AddObject(m, "argument_sizes", sizes) != 0 ||
+        PyModule_AddObject(m, "more_argument_sizes", more) != 0 ||
         PyModule_AddStringConstant(m, "torch_version", KDA_TORCH_VERSION) != 0) {
         Py_XDECREF(m);
         return nullptr;

@@ -1,6 +1,6 @@
 // kda_kv_append: rotate the new tokens' queries and keys by position and
-// write keys and values to the paged cache (sm_103a).  Contract in
-// include/kda.h.
+// write keys and values to the paged cache (sm_103a), and kda_kv_norm_append,
+// which norms each head's queries and keys first.  Contracts in include/kda.h.
 //
 // Mathematics.  Pair i of a head at position p turns by the angle p * f_i.
 // Only the angle modulo a full turn counts, so the phase is kept in turns:
@@ -34,7 +34,8 @@ constexpr int kMaxPairs = 64;
 // (us, 4 | 5 CTAs an SM): 256 tokens 4.2 | 4.9 and 13.7k tokens 45 | 48 with
 // 128 channels (16k interleaved ones 53 | 51), 10k tokens 7.4 | 6.8 and 56k
 // tokens 22 | 20 with 64.
-constexpr int ctas_per_sm(int dim) { return dim == 128 ? 4 : 5; }
+// The norm needs more than 48.
+constexpr int ctas_per_sm(int dim, bool norm) { return dim == 128 || norm ? 4 : 5; }
 
 struct Params {
     Rows rows;
@@ -49,6 +50,9 @@ struct Params {
     int parts;        // warps that share a token
     int rounds;       // rounds of 32 units (one a lane) each of them takes
     int token_blocks; // CTAs that take tokens; those behind them check the rows
+    const void *q_weight, *k_weight;   // of the norms (nullptr: ones)
+    int weight_dtype;
+    float eps;
 };
 
 // The row that owns token t (the last one that starts at or before t), found
@@ -83,6 +87,22 @@ __device__ __forceinline__ unsigned long long turns_per_position(double f) {
     return (bits >> 63) != 0 ? 0 - u : u;
 }
 
+// Two pairs of one head: p and r hold them as halves (p.x with r.x) or side by
+// side (p.x with p.y), i = 0..3 of a unit's chunks.
+__device__ __forceinline__ void rotate_pairs(float2 &p, float2 &r, const float2 *turn, int i,
+                                             bool interleaved) {
+    if (interleaved) {
+        const float2 s = turn[i], t = turn[4 + i];
+        p = make_float2(p.x * s.x - p.y * s.y, p.x * s.y + p.y * s.x);
+        r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
+    } else {
+        const float2 s = turn[2 * i], t = turn[2 * i + 1];
+        const float2 u = p;
+        p = make_float2(u.x * s.x - r.x * s.y, u.y * t.x - r.y * t.y);
+        r = make_float2(u.x * s.y + r.x * s.x, u.y * t.y + r.y * t.x);
+    }
+}
+
 // 8 pairs of one head: chunk a and chunk b hold them as halves (a[e], b[e])
 // or side by side (a[2e], a[2e+1], then b).
 template <typename T>
@@ -91,21 +111,52 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, b
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float2 p = unpack(x[i], T()), r = unpack(y[i], T());
-        if (interleaved) {
-            const float2 s = turn[i], t = turn[4 + i];
-            p = make_float2(p.x * s.x - p.y * s.y, p.x * s.y + p.y * s.x);
-            r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
-        } else {
-            const float2 s = turn[2 * i], t = turn[2 * i + 1];
-            const float2 u = p;
-            p = make_float2(u.x * s.x - r.x * s.y, u.y * t.x - r.y * t.y);
-            r = make_float2(u.x * s.y + r.x * s.x, u.y * t.y + r.y * t.x);
-        }
+        rotate_pairs(p, r, turn, i, interleaved);
         x[i] = pack(p.x, p.y, T());
         y[i] = pack(r.x, r.y, T());
     }
     a = make_uint4(x[0], x[1], x[2], x[3]);
     b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// The same behind the norm of the head: wa and wb are the chunks' weights,
+// kUnits lanes beside each other hold the head (all of them get here).
+template <typename T, int kUnits>
+__device__ __forceinline__ void norm_rotate(uint4 &a, uint4 &b, const float *wa, const float *wb,
+                                            float eps, const float2 *turn, bool turned,
+                                            bool interleaved, int lane) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack(x[i], T()), r = unpack(y[i], T());
+        sum = fmaf(p.x, p.x, fmaf(p.y, p.y, fmaf(r.x, r.x, fmaf(r.y, r.y, sum))));
+    }
+    const unsigned group = ((1u << kUnits) - 1) << (lane & ~(kUnits - 1));
+#pragma unroll
+    for (int o = kUnits / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
+    const float f = rsqrtf(fmaf(sum, 1.0f / (16 * kUnits), eps));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 p = unpack(x[i], T()), r = unpack(y[i], T());
+        const float2 u = *reinterpret_cast<const float2 *>(wa + 2 * i);
+        const float2 v = *reinterpret_cast<const float2 *>(wb + 2 * i);
+        p = make_float2(p.x * f * u.x, p.y * f * u.y);
+        r = make_float2(r.x * f * v.x, r.y * f * v.y);
+        if (turned) rotate_pairs(p, r, turn, i, interleaved);
+        x[i] = pack(p.x, p.y, T());
+        y[i] = pack(r.x, r.y, T());
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// Element i of a weight as fp32.
+__device__ __forceinline__ float weight_at(const void *w, int dtype, int i) {
+    if (w == nullptr) return 1.0f;
+    if (dtype == KDA_DTYPE_FP32) return static_cast<const float *>(w)[i];
+    return dtype == KDA_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i])
+                                   : __half2float(static_cast<const __half *>(w)[i]);
 }
 
 // Where the two chunks of a head's unit j start: the same pairs in both
@@ -115,10 +166,12 @@ __device__ __forceinline__ int2 chunks_of(const Params &p, bool turned, int j) {
                                     : make_int2(j * 16, j * 16 + 8);
 }
 
-template <typename T, int kDim>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(const Params p) {
+template <typename T, int kDim, bool kNorm>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
+    append_kernel(const Params p) {
     constexpr int kUnits = kDim / 16;  // units of a head
     __shared__ float2 turns[kWarps][kMaxPairs];
+    __shared__ float weights[kNorm ? 2 : 1][kNorm ? kDim : 1];   // of queries, of keys
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
@@ -131,13 +184,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
     }
     const long long item = (long long)blockIdx.x * kWarps + warp;
     const int t = (int)(item / p.parts), part = (int)(item % p.parts);
-    if (t >= p.num_tokens) return;
     const int first_k = p.q_heads, first_v = p.q_heads + p.kv_heads;
     const int begin = part * p.rounds * 32;
     const int end = min((first_v + p.kv_heads) * kUnits, begin + p.rounds * 32);
 
     auto load = [&](int u, uint4 &x, uint4 &y) {
-        if (u >= end) return;
+        if (u >= end || t >= p.num_tokens) return;
         const int head = u / kUnits, j = u % kUnits;
         const T *src;
         if (head < first_k)
@@ -154,6 +206,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
     };
     uint4 x[2], y[2];
     load(begin + lane, x[0], y[0]);
+    if constexpr (kNorm) {  // while the first units are on their way
+        for (int i = threadIdx.x; i < 2 * kDim; i += kThreads)
+            weights[i / kDim][i % kDim] =
+                weight_at(i < kDim ? p.q_weight : p.k_weight, p.weight_dtype, i % kDim);
+        __syncthreads();
+    }
+    if (t >= p.num_tokens) return;
 
     const int b = find_row(p.rows.cu_seqlens, p.rows.B, t, lane);
     if (b < 0) return;
@@ -192,7 +251,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
             dst = reinterpret_cast<T *>(p.value_cache) + slot + (head - first_v) * p.stride_head;
         const bool turned = head < first_v && j * 8 < p.pairs;
         const int2 at = chunks_of(p, turned, j);
-        if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
+        if constexpr (kNorm) {
+            const float *w = weights[head < first_k ? 0 : 1];
+            if (head < first_v)
+                norm_rotate<T, kUnits>(x, y, w + at.x, w + at.y, p.eps, &turns[warp][j * 8], turned,
+                                       p.interleaved != 0, lane);
+        } else {
+            if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
+        }
         if (head < first_k || block > 0) {
             __stcs(reinterpret_cast<uint4 *>(dst + at.x), x);
             __stcs(reinterpret_cast<uint4 *>(dst + at.y), y);
@@ -206,13 +272,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim)) append_kernel(con
     }
 }
 
+template <bool kNorm>
+void (*kernel_for(bool bf16, bool small))(const Params) {
+    if (bf16)
+        return small ? append_kernel<__nv_bfloat16, 64, kNorm> : append_kernel<__nv_bfloat16, 128, kNorm>;
+    return small ? append_kernel<__half, 64, kNorm> : append_kernel<__half, 128, kNorm>;
+}
+
 }  // namespace
 
-extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void *k,
-                                    const void *v, void *q_out, void *key_cache,
-                                    void *value_cache, const double *inv_freq,
-                                    const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
-                                    const kda_align *align, int32_t *error_word, void *stream) {
+namespace {
+
+// The norm of a call: none, or its weights and eps.
+struct Norm {
+    const void *q_weight, *k_weight;
+    int dtype;
+    float eps;
+};
+
+kda_status append(const kda_cache_config *cfg, const void *q, const void *k, const void *v,
+                  void *q_out, void *key_cache, void *value_cache, const double *inv_freq,
+                  const int32_t *cu_seqlens, int32_t B, int32_t num_tokens, const kda_align *align,
+                  int32_t *error_word, void *stream, const Norm *norm) {
     using kda_cache::aligned;
     using kda_cache::stride_ok;
     kda_status st = kda_cache::check_config(cfg);
@@ -221,8 +302,13 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     if (cfg->rotary_dim < 0 || cfg->rotary_dim > cfg->head_dim || (cfg->rotary_dim & 15) != 0 ||
         (cfg->interleaved != 0 && cfg->interleaved != 1))
         return KDA_ERR_INVALID_ARG;
+    if (norm != nullptr) {
+        // 0 is a choice too; a sum of squares that it leaves at 0 gives 0 / 0
+        if (!(norm->eps >= 0.0f && isfinite(norm->eps))) return KDA_ERR_INVALID_ARG;
+        if (norm->dtype != cfg->dtype && norm->dtype != KDA_DTYPE_FP32) return KDA_ERR_INVALID_ARG;
+    }
     if (B == 0 || num_tokens == 0) return KDA_OK;  // nothing to do; no pointer is inspected
-    Params p;
+    Params p{};
     st = kda_cache::set_rows(cfg, align, cu_seqlens, B, num_tokens, error_word, p.rows);
     if (st != KDA_OK) return st;
     if (!k || !v || !key_cache || !value_cache || (q != nullptr && !q_out) ||
@@ -235,6 +321,15 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     if ((q != nullptr && !stride_ok(cfg->stride_q_t)) || !stride_ok(cfg->stride_k_t) ||
         !stride_ok(cfg->stride_v_t))
         return KDA_ERR_INVALID_ARG;
+    if (norm != nullptr) {
+        const uintptr_t size = norm->dtype == KDA_DTYPE_FP32 ? 4 : 2;
+        if (!aligned(norm->q_weight, size) || !aligned(norm->k_weight, size))
+            return KDA_ERR_INVALID_ARG;
+        p.q_weight = norm->q_weight;
+        p.k_weight = norm->k_weight;
+        p.weight_dtype = norm->dtype;
+        p.eps = norm->eps;
+    }
     p.q = static_cast<const char *>(q);
     p.k = static_cast<const char *>(k);
     p.v = static_cast<const char *>(v);
@@ -261,7 +356,7 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     // 4.2 | 7.1, 16k tokens 75 | 53.  So rounds grow once two full sets of
     // resident warps have one each.
     const long long most =
-        (long long)kda_cache::sm_count() * ctas_per_sm(cfg->head_dim) * kWarps * 2;
+        (long long)kda_cache::sm_count() * ctas_per_sm(cfg->head_dim, norm != nullptr) * kWarps * 2;
     if (most <= 0) return KDA_ERR_CUDA;
     const long long wanted = (long long)num_tokens * rounds / most;
     p.rounds = wanted < 1 ? 1 : wanted > rounds ? rounds : (int)wanted;
@@ -276,11 +371,41 @@ extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, 
     if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     p.token_blocks = (int)token_blocks;
     void (*kernel)(const Params) =
-        cfg->dtype == KDA_DTYPE_BF16
-            ? (cfg->head_dim == 64 ? append_kernel<__nv_bfloat16, 64>
-                                   : append_kernel<__nv_bfloat16, 128>)
-            : (cfg->head_dim == 64 ? append_kernel<__half, 64> : append_kernel<__half, 128>);
+        norm != nullptr ? kernel_for<true>(cfg->dtype == KDA_DTYPE_BF16, cfg->head_dim == 64)
+                        : kernel_for<false>(cfg->dtype == KDA_DTYPE_BF16, cfg->head_dim == 64);
     return kda_cache::launch(kernel, dim3((unsigned)grid), dim3(kThreads), 0, 1, stream, p);
+}
+
+}  // namespace
+
+extern "C" kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void *k,
+                                    const void *v, void *q_out, void *key_cache,
+                                    void *value_cache, const double *inv_freq,
+                                    const int32_t *cu_seqlens, int32_t B, int32_t num_tokens,
+                                    const kda_align *align, int32_t *error_word, void *stream) {
+    return append(cfg, q, k, v, q_out, key_cache, value_cache, inv_freq, cu_seqlens, B, num_tokens,
+                  align, error_word, stream, nullptr);
+}
+
+extern "C" kda_status kda_kv_norm_append(const kda_cache_config *cfg, const void *q, const void *k,
+                                         const void *v, const void *q_weight, const void *k_weight,
+                                         int32_t weight_dtype, float eps, void *q_out,
+                                         void *key_cache, void *value_cache,
+                                         const double *inv_freq, const int32_t *cu_seqlens,
+                                         int32_t B, int32_t num_tokens, const kda_align *align,
+                                         int32_t *error_word, void *stream) {
+    const Norm norm{q_weight, k_weight, weight_dtype, eps};
+    return append(cfg, q, k, v, q_out, key_cache, value_cache, inv_freq, cu_seqlens, B, num_tokens,
+                  align, error_word, stream, &norm);
+}
+
+extern "C" kda_status kda_kv_norm_append_packed(const kda_norm_append_args *n) {
+    if (n == nullptr) return KDA_ERR_INVALID_ARG;
+    const kda_append_args *a = &n->append;
+    return kda_kv_norm_append(&a->config, a->q, a->k, a->v, n->q_weight, n->k_weight,
+                              n->weight_dtype, n->eps, a->q_out, a->key_cache, a->value_cache,
+                              a->inv_freq, a->cu_seqlens, a->B, a->num_tokens, &a->align,
+                              a->error_word, a->stream);
 }
 
 extern "C" kda_status kda_kv_append_packed(const kda_append_args *a) {
