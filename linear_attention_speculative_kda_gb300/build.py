@@ -23,7 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("kda_kernels.cu", "kda_conv.cu", "kda_blocks.cu", "kda_append.cu",
-                     "kda_attend.cu", "kda_logprobs.cu", "kda_decode.cu")]
+                     "kda_attend.cu", "kda_logprobs.cu", "kda_decode.cu",
+                     "kda_prefill.cu")]
 DEPENDS = SOURCES + [
     os.path.join(CSRC, "kda_device.cuh"),
     os.path.join(CSRC, "kda_async.cuh"),

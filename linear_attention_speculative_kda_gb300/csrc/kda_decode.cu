@@ -151,35 +151,9 @@ extern "C" kda_status kda_decode(const kda_config *cfg, const void *q, const voi
     return st != KDA_OK ? st : launch(p, stream);
 }
 
-extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const void *k,
-                                  const void *v, const void *g_raw, const void *beta_raw,
-                                  const float *A_log, const float *g_bias, float *state_pool,
-                                  const int32_t *cu_seqlens, const int32_t *state_indices,
-                                  const int32_t *initial_indices, int32_t B, int32_t num_tokens,
-                                  void *out, int32_t *error_word, void *stream) {
-    kda_status st = kda_delta::check_config(cfg);
-    if (st != KDA_OK) return st;
-    if (B < 0 || num_tokens < 0) return KDA_ERR_INVALID_ARG;
-    if (B == 0 || num_tokens == 0) return KDA_OK;  // nothing to do; no pointer is inspected
-    if (!cu_seqlens || !kda_cache::aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
-    Params p{};
-    st = kda_delta::set_params(cfg, q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool,
-                               state_indices, initial_indices, B, num_tokens, out, error_word, p);
-    if (st != KDA_OK) return st;
-    p.cu_seqlens = cu_seqlens;
-    return launch(p, stream);
-}
-
 extern "C" kda_status kda_decode_packed(const kda_delta_args *a) {
     if (a == nullptr) return KDA_ERR_INVALID_ARG;
     return kda_decode(&a->config, a->q, a->k, a->v, a->g_raw, a->beta_raw, a->A_log, a->g_bias,
                       a->state_pool, a->state_indices, a->initial_indices, a->B, a->out,
                       a->error_word, a->stream);
-}
-
-extern "C" kda_status kda_prefill_packed(const kda_delta_args *a) {
-    if (a == nullptr) return KDA_ERR_INVALID_ARG;
-    return kda_prefill(&a->config, a->q, a->k, a->v, a->g_raw, a->beta_raw, a->A_log, a->g_bias,
-                       a->state_pool, a->cu_seqlens, a->state_indices, a->initial_indices, a->B,
-                       a->num_tokens, a->out, a->error_word, a->stream);
 }
