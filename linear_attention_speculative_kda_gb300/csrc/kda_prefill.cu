@@ -80,7 +80,7 @@ constexpr int kQueryStep = 512 + 64;
 struct __align__(128) Stage {
     unsigned char key[8 * kKeyStep];      // [k step][n tile][lane]: hi b0 b1, lo b0 b1
     unsigned char query[8 * kQueryStep];  // [k step][lane]: n tile 0 b0 b1, 1 b0 b1
-    uint4 update[16][32];                 // [n tile][slot]: b0 hi lo, b1 hi lo
+    uint4 update[16][32];                 // [n tile][slot]: hi b0 b1, lo b0 b1
     uint4 t[2][32];                       // [n tile][lane]: hi b0 b1, lo b0 b1
     uint4 b[32];                          // [lane]: n tile 0 b0 b1, 1 b0 b1
     float decay[kD];                      // P_C
@@ -130,6 +130,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The same for k steps of 8 in tf32.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -159,7 +168,10 @@ __device__ __forceinline__ uint32_t half_pair(float x, float y) {
 __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = half_pair(x, y);
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    lo = half_pair(x - h.x, y - h.y);
+    u64 rest;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(rest) : "l"(pair(x, y)), "l"(pair(h.x, h.y)));
+    const float2 r = both(rest);
+    lo = half_pair(r.x, r.y);
 }
 
 // Bounded wait of a warp: it gives up, as a whole, after the budget, or when
@@ -513,8 +525,11 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
                     split(u & 1 ? y.y : y.x, u & 1 ? z.y : z.x, x.x, x.y);
                     // channel 16 m + 4 j + u; tokens (g, g + 8) are b0 for g < 4, else b1
                     const int tile = 2 * m + (u >> 1), spot = (u & 1) * 4 + (g & 3);
-                    reinterpret_cast<uint2 *>(
-                        &st.update[tile][8 * j + (spot ^ ((j & 1) << 2))])[g >> 2] = x;
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(
+                                        &st.update[tile][8 * j + (spot ^ ((j & 1) << 2))]) +
+                                    (g >> 2);
+                    dst[0] = x.x;
+                    dst[2] = x.y;
                 }
             }
         }
@@ -676,7 +691,7 @@ __device__ __forceinline__ void consume(const Params &p, const Stage &st, unsign
     h.most[0] += 16.0f * vmax0 * down0;
     h.most[1] += 16.0f * vmax1 * down1;
     // U = S (K P)^T and O = S (Q P)^T; S takes its decay on the way
-    float u[2][4] = {}, o[2][4] = {};
+    float u[2][4], o[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         no_further_ahead();
@@ -688,10 +703,17 @@ __device__ __forceinline__ void consume(const Params &p, const Stage &st, unsign
         const uint4 k0 = *reinterpret_cast<const uint4 *>(st.key + i * kKeyStep + lane * 16);
         const uint4 k1 = *reinterpret_cast<const uint4 *>(st.key + i * kKeyStep + 512 + lane * 16);
         const uint4 q = *reinterpret_cast<const uint4 *>(st.query + i * kQueryStep + lane * 16);
-        mma(u[0], hi, k0.x, k0.y);
-        mma(u[1], hi, k1.x, k1.y);
-        mma(o[0], hi, q.x, q.y);
-        mma(o[1], hi, q.z, q.w);
+        if (i == 0) {
+            mma_first(u[0], hi, k0.x, k0.y);
+            mma_first(u[1], hi, k1.x, k1.y);
+            mma_first(o[0], hi, q.x, q.y);
+            mma_first(o[1], hi, q.z, q.w);
+        } else {
+            mma(u[0], hi, k0.x, k0.y);
+            mma(u[1], hi, k1.x, k1.y);
+            mma(o[0], hi, q.x, q.y);
+            mma(o[1], hi, q.z, q.w);
+        }
         mma(u[0], hi, k0.z, k0.w);
         mma(u[1], hi, k1.z, k1.w);
         mma(u[0], lo, k0.x, k0.y);
@@ -715,19 +737,19 @@ __device__ __forceinline__ void consume(const Params &p, const Stage &st, unsign
         split(x[0], x[1], hi[2 * n], lo[2 * n]);
         split(x[2], x[3], hi[2 * n + 1], lo[2 * n + 1]);
     }
-    float d[2][4] = {}, d2[2][4] = {};
+    float d[2][4];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const uint4 t = st.t[n][lane];
-        mma(d[n], hi, t.x, t.y);
-        mma(d2[n], hi, t.z, t.w);
-        mma(d2[n], lo, t.x, t.y);
+        mma_first(d[n], hi, t.x, t.y);
+        mma(d[n], hi, t.z, t.w);
+        mma(d[n], lo, t.x, t.y);
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         constexpr float f = 1.0f / (kTScale * kUpdateScale);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) d[n][c] = (d[n][c] + d2[n][c]) * f;
+        for (int c = 0; c < 4; ++c) d[n][c] *= f;
         split(d[n][0], d[n][1], hi[2 * n], lo[2 * n]);
         split(d[n][2], d[n][3], hi[2 * n + 1], lo[2 * n + 1]);
     }
@@ -739,9 +761,9 @@ __device__ __forceinline__ void consume(const Params &p, const Stage &st, unsign
     for (int n = 0; n < 16; ++n) {
         if ((n & 1) == 0) no_further_ahead();
         const uint4 k = st.update[n][lane ^ (((lane >> 3) & 1) << 2)];
-        mma(h.s[n], hi, k.x, k.z);
-        mma(h.s[n], hi, k.y, k.w);
-        mma(h.s[n], lo, k.x, k.z);
+        mma(h.s[n], hi, k.x, k.y);
+        mma(h.s[n], hi, k.z, k.w);
+        mma(h.s[n], lo, k.x, k.y);
     }
     // the outputs, [token][16 channels] in shared memory first
     const float up0 = power_of_two(-h.ex[0]) * (p.scale / kKeyScale);
