@@ -11,23 +11,20 @@
 // All factors are products of decays behind one another, never quotients, so
 // none is above 1 and strong decays underflow to what they are.
 //
-// Every product with S and V' runs on mma.sync m16n8k16 in fp16 with fp32
-// sums.  An fp32 operand x is two fp16 numbers, hi = fp16(x) and lo =
-// fp16(x - hi), 22 bits, and a product is hi hi + hi lo + lo hi: what is left
-// out is below 2^-22 of it.  Only O takes hi alone: it is rounded to bf16,
-// 2^-9, anyway.  Decayed keys and queries are at most 1 and scaled by powers of
-// two; the rows of S and V, whose sizes are the caller's, are held times a
-// power of two of their own that puts the larger of the two near 2^7, as
-// fp16's range needs it.
+// Every product with S and V' runs on tcgen05.mma in fp16 with fp32 sums, the
+// rows of S (values' channels) as its 128 rows.  An fp32 operand x is two fp16
+// numbers, hi = fp16(x) and lo = fp16(x - hi), 22 bits, and a product is hi hi
+// + hi lo + lo hi: what is left out is below 2^-22 of it.  Only O takes hi
+// alone: it is rounded to bf16, 2^-9, anyway.  Decayed keys and queries are at
+// most 1 and scaled by powers of two; rows of S, of V - U and of V' have
+// powers of two of their own, from their own sizes, as fp16's range needs it.
 //
-// Layout.  Rows of S (values' channels) never meet each other, so a consumer
-// warp owns 16 of them and all 128 columns as the fp32 accumulators of 16
-// n-tiles, for the whole row: no exchange between warps, and an accumulator
-// pair is an operand pair of the next product.  The operands that all rows
-// share (K P, Q P, K P_C / P_t, T, B, P_C) are made by producer warps, a chunk
-// each, in fragment order in a ring of stages.  Tokens of a chunk are numbered
-// for the products in the order 0 8 1 9 2 10 3 11, 4 12 ... 7 15: the pairs of
-// tokens that a producer's lane has are then the pairs of the fragments.
+// Layout.  A CTA has one row and head at a time.  Eight consumer warps hold S
+// in registers, a thread half a row of it: it adds what the chunk brought,
+// splits it and stores it to tensor memory, where it is the A operand of the
+// next chunk's products; four of them make V - U and split V' on the way, the
+// other four write the outputs.  The operands that all rows share (K P, Q P,
+// K P_C / P_t, T, B, P_C) are made by eight producer warps in a ring of stages.
 //
 // A and B.  Two producer warps make a chunk's operands, the first the tokens'
 // vectors, the second the products between tokens.  Four tokens t at a time
@@ -58,8 +55,8 @@ constexpr int kC = 16;           // tokens of a chunk
 constexpr int kPairs = 4;        // pairs of producer warps, a chunk each
 constexpr int kProducers = 2 * kPairs;
 constexpr int kStages = 5;
-constexpr int kMaxConsumers = 8; // warps of 16 rows of S
-constexpr int kMaxThreads = 32 * (kProducers + kMaxConsumers);
+constexpr int kConsumers = 8;    // warps: two groups of four, a half of S's columns each
+constexpr int kThreads = 32 * (kProducers + kConsumers);
 
 #ifdef KDA_TEST_PREFILL_WAIT_BUDGET  // a test build: a wait that runs out, soon
 constexpr long long kWaitBudget = KDA_TEST_PREFILL_WAIT_BUDGET;
@@ -67,25 +64,29 @@ constexpr long long kWaitBudget = KDA_TEST_PREFILL_WAIT_BUDGET;
 constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
 #endif
 
-// Powers of two on the operands: products of S with keys and queries carry
-// kKeyScale, V' and the keys that update S carry inverse ones.
+// Powers of two on the operands.
 constexpr float kKeyScale = 1024.0f;      // K P, Q P
 constexpr float kTScale = 1024.0f;        // T
-constexpr float kUpdateScale = 32.0f;     // K P_C / P_t; V' carries 1 / 32
-constexpr float kBScale = 32768.0f;       // B: kKeyScale * 32
+constexpr float kUpdateScale = 1024.0f;   // K P_C / P_t
+constexpr float kBScale = 1024.0f;        // B
 
-// One chunk's operands, in fragment order (16 bytes a lane).
-constexpr int kKeyStep = 1024 + 64;       // bytes of a k step of K P, padded against bank conflicts
-constexpr int kQueryStep = 512 + 64;
-struct __align__(128) Stage {
-    unsigned char key[8 * kKeyStep];      // [k step][n tile][lane]: hi b0 b1, lo b0 b1
-    unsigned char query[8 * kQueryStep];  // [k step][lane]: n tile 0 b0 b1, 1 b0 b1
-    uint4 update[16][32];                 // [n tile][slot]: hi b0 b1, lo b0 b1
-    uint4 t[2][32];                       // [n tile][lane]: hi b0 b1, lo b0 b1
-    uint4 b[32];                          // [lane]: n tile 0 b0 b1, 1 b0 b1
+// One chunk's operands: fp16 matrices of rows of 128 bytes with the 128-byte
+// swizzle (16-byte unit u of row r at u ^ (r & 7)), two blocks of 64 channels.
+constexpr int kTall = 3 * kC;             // rows: K P hi, Q P, K P lo
+struct __align__(1024) Stage {
+    unsigned char reach[2][kTall * 128];  // [64 channels][row]: channels along K
+    unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token]
+    unsigned char inner[kC * 128];        // [token t]: T_t hi, T_t lo, B_t; 16 tokens s each
     float decay[kD];                      // P_C
-    uint4 v[kC][16];                      // bf16 [token][channel], 16-byte units swizzled
+    __nv_bfloat16 v[kC][kD];
+    unsigned char pad[512];
 };
+static_assert(sizeof(Stage) % 1024 == 0, "swizzle atoms start on 1024 bytes");
+
+// Byte offset of channel c (even, of 64) of row r.
+__device__ __forceinline__ int place(int r, int c) {
+    return r * 128 + ((((c >> 3) ^ r) & 7) << 4) + (c & 7) * 2;
+}
 
 // What the first warp of a pair hands to the second, four tokens at a time.
 // Their decays are products from the first of them, R_u = prod_{0<i<=u} e_i.
@@ -107,39 +108,28 @@ struct __align__(16) Scratch {            // of a pair of producer warps
 struct Shared {
     Stage stage[kStages];
     Scratch scratch[kPairs];
-    unsigned char out[kMaxConsumers][kC * 48];
+    float4 info[kD];                      // of a row: see Factors
+    float most[2][kD];                    // largest of each half of a row of S
     float zeros[kD];
     uint64_t full[kStages], empty[kStages];
+    uint64_t u_done, v_done, s_done;      // products of a chunk
+    uint64_t drained;
     int gave_up;
+    uint32_t tmem;
 };
 
-// The place of token t in the products' order, and the token at a place.
-__host__ __device__ constexpr int place_of(int t) {
-    return ((t & 4) << 1) + 2 * (t & 3) + (t >> 3);
-}
-__device__ __forceinline__ int token_at(int n) {
-    return ((n & 8) >> 1) + ((n & 7) >> 1) + ((n & 1) << 3);
-}
+// Columns of tensor memory.
+constexpr uint32_t kColS = 0;             // S: 64 of hi, 64 of lo, two channels each
+constexpr uint32_t kColUpdate = 128;      // V'^T (K P_C / P_t), 128
+constexpr uint32_t kColReach = 256;       // S (K P | Q P | K P lo)^T, 48, of even and odd chunks
+constexpr uint32_t kColInner = 352;       // B V', 16, of even and odd chunks
+constexpr uint32_t kColX = 384;           // V - U: 8 of hi, 8 of lo
+constexpr uint32_t kColDelta = 400;       // V', 16
+constexpr uint32_t kColY = 416;           // V': 8 of hi, 8 of lo
+constexpr uint32_t kColLow = 432;         // lo of S with hi of K P, 16
+constexpr uint32_t kTmemColumns = 512;
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The first product of a sum.
-__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// The same for k steps of 8 in tf32.
+// D += A B for k steps of 8 in tf32.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -192,35 +182,21 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity,
     return __all_sync(kFull, done);
 }
 
-struct Work {   // one row and head's share of a CTA
+struct Work {   // one row and head
     Row row;
-    int head, part;
+    int head;
 };
 
-// parts: 2^part_bits CTAs share a row and head.
-__device__ __forceinline__ Work work_at(const Params &p, unsigned item, int part_bits, int &bits) {
+__device__ __forceinline__ Work work_at(const Params &p, unsigned item, int &bits) {
     Work w;
-    w.part = (int)(item & ((1u << part_bits) - 1));
-    const unsigned tile = item >> part_bits, b = tile / (unsigned)p.H;
-    w.head = (int)(tile - b * (unsigned)p.H);
+    const unsigned b = item / (unsigned)p.H;
+    w.head = (int)(item - b * (unsigned)p.H);
     w.row = kda_delta::read_row(p, (int)b, bits);
     return w;
 }
 
 // Keeps the compiler from fetching operands so far ahead that registers run out.
 __device__ __forceinline__ void no_further_ahead() { asm volatile("" ::: "memory"); }
-
-// Registers a thread from here on, of all four warps of a warpgroup.  The
-// shares of the launch's 128 a thread: 4 warps of 96, 4 of 128 and 8 of 144
-// are 16 times 128 (with 4 consumers 12 times 123).
-template <int kRegisters>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
-}
-template <int kRegisters>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
-}
 
 // x, in a way that keeps addresses made from it from being held in registers
 // for longer than the caller's turn of a loop: beside the states there is no
@@ -321,12 +297,10 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
         const __nv_bfloat16 *src = p.v + first * p.stride_v + at;
 #pragma unroll 4
         for (int t = 0; t < kC; ++t, src += p.stride_v) {
-            unsigned char *dst =
-                reinterpret_cast<unsigned char *>(&st.v[t][(lane >> 1) ^ (t & 7)]) + (lane & 1) * 8;
             if (t < valid)
-                kda::cp_async8(dst, src);
+                kda::cp_async8(&st.v[t][4 * lane], src);
             else
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(0u, 0u);
+                *reinterpret_cast<uint2 *>(&st.v[t][4 * lane]) = make_uint2(0u, 0u);
         }
     }
     kda::cp_async_commit();
@@ -335,8 +309,7 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     u64 reach[2] = {pair(kKeyScale, kKeyScale), pair(kKeyScale, kKeyScale)};   // P_t
     u64 total[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};                       // log2 P_t
     u64 r[2] = {pair(1.0f, 1.0f), pair(1.0f, 1.0f)};                            // R
-    unsigned char *key = st.key + (lane >> 2) * kKeyStep + (lane & 3) * 16;
-    unsigned char *query = st.query + (lane >> 2) * kQueryStep + (lane & 3) * 16;
+    unsigned char *reached = st.reach[lane >> 4];
     // two tokens a turn, the next two on their way
 #pragma unroll 1
     for (int t0 = 0; t0 < kC; t0 += 2) {
@@ -409,20 +382,19 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
             const float2 r0 = both(r[0]), r1 = both(r[1]);
             put(&out.back[t & 3][4 * lane], mul_pair(k[0], pair(reciprocal(r0.x), reciprocal(r0.y))),
                 mul_pair(k[1], pair(reciprocal(r1.x), reciprocal(r1.y))));
-            // K P and Q P: channels 4 lane .. + 3 are b0 and b1 of k step lane / 4
-            const int place = place_of(t), slot = (place & 7) * 4, tile = place >> 3;
-            uint4 f;
+            const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
+            uint2 hi, lo;
             float2 x = both(mul_pair(k[0], reach[0]));
-            split(x.x, x.y, f.x, f.z);
+            split(x.x, x.y, hi.x, lo.x);
             x = both(mul_pair(k[1], reach[1]));
-            split(x.x, x.y, f.y, f.w);
-            *reinterpret_cast<uint4 *>(key + (tile * 32 + slot) * 16) = f;
-            uint2 h;
+            split(x.x, x.y, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(reached + to) = hi;
+            *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
             x = both(mul_pair(q[0], reach[0]));
-            h.x = half_pair(x.x, x.y);
+            hi.x = half_pair(x.x, x.y);
             x = both(mul_pair(q[1], reach[1]));
-            h.y = half_pair(x.x, x.y);
-            *reinterpret_cast<uint2 *>(query + slot * 16 + tile * 8) = h;
+            hi.y = half_pair(x.x, x.y);
+            *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
         }
         if ((t0 & 2) != 0) {
             put(&out.end[4 * lane], r[0], r[1]);
@@ -510,26 +482,23 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
             const float x = d[0][c] + d[1][c];
             (j < 2 ? sc.a : sc.b)[4 * block + 2 * (j & 1) + (c & 1)][g + 4 * (c & 2)] = x;
         }
-        if (block == 3) {   // K P_C / P_t, in units of the update
+        if (block == 3) {   // K P_C / P_t
+            const u64 scale = pair(kUpdateScale, kUpdateScale);
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
                 no_further_ahead();
-                const float4 f = kda::ld4(&in.end[16 * m + 4 * j]);
-                const u64 scale = pair(kUpdateScale, kUpdateScale);
-                const u64 e[2] = {mul_pair(pair(f.x, f.y), scale), mul_pair(pair(f.z, f.w), scale)};
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&in.end[16 * m + 4 * j]);
+                const u64 e0 = mul_pair(f.x, scale), e1 = mul_pair(f.y, scale);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float2 y = both(mul_pair(w[0][2 * m + (u >> 1)], e[u >> 1]));
-                    const float2 z = both(mul_pair(w[1][2 * m + (u >> 1)], e[u >> 1]));
-                    uint2 x;
-                    split(u & 1 ? y.y : y.x, u & 1 ? z.y : z.x, x.x, x.y);
-                    // channel 16 m + 4 j + u; tokens (g, g + 8) are b0 for g < 4, else b1
-                    const int tile = 2 * m + (u >> 1), spot = (u & 1) * 4 + (g & 3);
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(
-                                        &st.update[tile][8 * j + (spot ^ ((j & 1) << 2))]) +
-                                    (g >> 2);
-                    dst[0] = x.x;
-                    dst[2] = x.y;
+                for (int i = 0; i < 2; ++i) {   // tokens g and g + 8
+                    const float2 y = both(mul_pair(w[i][2 * m], e0));
+                    const float2 z = both(mul_pair(w[i][2 * m + 1], e1));
+                    uint2 hi, lo;
+                    split(y.x, y.y, hi.x, lo.x);
+                    split(z.x, z.y, hi.y, lo.y);
+                    const int to = place(g, 16 * (m & 3) + 4 * j) + i * 8 * 128;
+                    *reinterpret_cast<uint2 *>(st.update[0][m >> 2] + to) = hi;
+                    *reinterpret_cast<uint2 *>(st.update[1][m >> 2] + to) = lo;
                 }
             }
         }
@@ -561,26 +530,17 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
             for (int t = 0; t < kC; ++t) sc.a[t][s] = col[t] * kTScale;
     }
     __syncwarp();
-    {
-        const int j = lane & 3, g = lane >> 2;
-        uint4 f;
+    // tokens s = 2 i and 2 i + 1 of row t, hi, lo and B 32 bytes apart
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-            const int t = token_at(8 * tile + g);
-            uint4 x;
-            split(sc.a[t][j], sc.a[t][j + 8], x.x, x.z);
-            split(sc.a[t][j + 4], sc.a[t][j + 12], x.y, x.w);
-            st.t[tile][lane] = x;
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = j + 8 * (i & 1) + 4 * (i >> 1);
-                y[i] = s <= t ? sc.b[t][s] * kBScale : 0.0f;
-            }
-            (tile ? f.z : f.x) = half_pair(y[0], y[1]);
-            (tile ? f.w : f.y) = half_pair(y[2], y[3]);
-        }
-        st.b[lane] = f;
+    for (int n = 0; n < 4; ++n) {
+        const int t = 4 * n + (lane >> 3), i = 2 * (lane & 7);
+        uint32_t hi, lo;
+        split(sc.a[t][i], sc.a[t][i + 1], hi, lo);
+        const float x = i <= t ? sc.b[t][i] * kBScale : 0.0f;
+        const float y = i < t ? sc.b[t][i + 1] * kBScale : 0.0f;
+        *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = hi;
+        *reinterpret_cast<uint32_t *>(st.inner + place(t, kC + i)) = lo;
+        *reinterpret_cast<uint32_t *>(st.inner + place(t, 2 * kC + i)) = half_pair(x, y);
     }
     __syncwarp();
     return true;
@@ -588,205 +548,159 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
 
 // ---------------------------------------------------------------- consumer --
 
-__device__ __forceinline__ void times(float &x, float &y, u64 f) {
-    const float2 r = both(mul_pair(pair(x, y), f));
-    x = r.x;
-    y = r.y;
-}
-
-__device__ __forceinline__ void scale4(float (&x)[4], float lower, float upper) {
-    x[0] *= lower;
-    x[1] *= lower;
-    x[2] *= upper;
-    x[3] *= upper;
-}
-
-// floor(log2 |x|) of x (-10000 for 0, subnormals and what is not finite).
+// floor(log2 |x|) of x, at least -110 (0 and the like), 127 for what is not
+// finite.
 __device__ __forceinline__ int exponent_of(float x) {
-    const int e = (int)((__float_as_uint(x) >> 23) & 0xff);
-    return e == 0 || e == 255 ? -10000 : e - 127;
+    const int e = (int)((__float_as_uint(x) >> 23) & 0xff) - 127;
+    return max(-110, min(127, e));
 }
 
 __device__ __forceinline__ float power_of_two(int e) {   // -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
-    return fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+// Instruction descriptor of kind::f16: fp16 operands, fp32 sums, 128 rows, A
+// along K, B along K or along N.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_along_n) {
+    return (1u << 4) | ((b_along_n ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void load_v(const Stage &st, int warp_v, int lane, uint32_t (&v)[4]) {
-    const int t = token_at((lane >> 4) * 8 + (lane & 7));
-    const uint4 *src = &st.v[t][(2 * warp_v + ((lane >> 3) & 1)) ^ (t & 7)];
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(kda::smem_u32(src)));
+// B along N with the 128-byte swizzle: 64-column blocks `block` bytes apart,
+// groups of 8 along K 1024 bytes apart.
+__device__ __forceinline__ uint64_t along_n(uint32_t addr, uint32_t block) {
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(block >> 4) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// What a consumer warp holds of a row: 16 rows of S, those of lane / 4 and
-// lane / 4 + 8, times powers of two of their own.
-struct Held {
-    float s[16][4];
-    int ex[2];          // exponents: held = value * 2^ex
-    float most[2];      // bound of the rows' norms as held
-};
-
-// Looks at the sizes of the rows of S and takes new powers of two, by them and
-// by the largest values to come: the larger of the two is held in [2^7, 2^8).
-__device__ __forceinline__ void rescale(Held &h, float vmax0, float vmax1) {
-    float m[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int n = 0; n < 16; ++n) {
-        m[0] = fmaxf(m[0], fmaxf(fabsf(h.s[n][0]), fabsf(h.s[n][1])));
-        m[1] = fmaxf(m[1], fmaxf(fabsf(h.s[n][2]), fabsf(h.s[n][3])));
-    }
-    int step[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        m[i] = quad_max(m[i]);
-        const int most = max(exponent_of(m[i]) - h.ex[i], exponent_of(i ? vmax1 : vmax0));
-        // within 2^-120 .. 2^120, so that the way back is a power that fp32 has
-        const int ex = most < -5000 ? h.ex[i] : max(-120, min(120, 7 - most));
-        step[i] = ex - h.ex[i];
-        h.ex[i] = ex;
-    }
-    // in two powers: a step may be twice as far
-    const float a0 = power_of_two(step[0] / 2), b0 = power_of_two(step[0] - step[0] / 2);
-    const float a1 = power_of_two(step[1] / 2), b1 = power_of_two(step[1] - step[1] / 2);
-    if (__any_sync(kFull, (step[0] | step[1]) != 0))
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-            scale4(h.s[n], a0, a1);
-            scale4(h.s[n], b0, b1);
-        }
-    h.most[0] = 11.4f * m[0] * a0 * b0;   // sqrt(128) of the largest
-    h.most[1] = 11.4f * m[1] * a1 * b1;
+// D [+]= A B^T of one K step of 16, A from tensor memory.
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+        : "memory");
 }
 
-__device__ __forceinline__ void consume(const Params &p, const Stage &st, unsigned char *out_tile,
-                                        Held &h, const Row &row, int head, int chunk, int warp_v,
-                                        int lane) {
-    lane = made_anew(lane);
-    const int j = lane & 3;
-    uint32_t v[4];   // [n tile][rows g, rows g + 8], two tokens each
-    load_v(st, warp_v, lane, v);
-    float vmax0 = 0.0f, vmax1 = 0.0f;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const float2 lower = kda::bf16x2_to_float2(v[2 * n]);
-        const float2 upper = kda::bf16x2_to_float2(v[2 * n + 1]);
-        vmax0 = fmaxf(vmax0, fmaxf(fabsf(lower.x), fabsf(lower.y)));
-        vmax1 = fmaxf(vmax1, fmaxf(fabsf(upper.x), fabsf(upper.y)));
-    }
-    vmax0 = quad_max(vmax0);
-    vmax1 = quad_max(vmax1);
-    // What V - U and V' can come to, as held, has to stay inside fp16: a row's
-    // norm grows by at most |v| a token.  Every fourth chunk the sizes are
-    // looked at anyway, as rows may have shrunk.
-    const bool grows = h.most[0] + 17.0f * vmax0 * power_of_two(h.ex[0]) > 60000.0f ||
-                       h.most[1] + 17.0f * vmax1 * power_of_two(h.ex[1]) > 60000.0f;
-    if ((chunk & 3) == 0 || __any_sync(kFull, grows)) rescale(h, vmax0, vmax1);
-    const float down0 = power_of_two(h.ex[0]), down1 = power_of_two(h.ex[1]);
-    h.most[0] += 16.0f * vmax0 * down0;
-    h.most[1] += 16.0f * vmax1 * down1;
-    // U = S (K P)^T and O = S (Q P)^T; S takes its decay on the way
-    float u[2][4], o[2][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        no_further_ahead();
-        uint32_t hi[4], lo[4];
-        split(h.s[2 * i][0], h.s[2 * i][1], hi[0], lo[0]);
-        split(h.s[2 * i][2], h.s[2 * i][3], hi[1], lo[1]);
-        split(h.s[2 * i + 1][0], h.s[2 * i + 1][1], hi[2], lo[2]);
-        split(h.s[2 * i + 1][2], h.s[2 * i + 1][3], hi[3], lo[3]);
-        const uint4 k0 = *reinterpret_cast<const uint4 *>(st.key + i * kKeyStep + lane * 16);
-        const uint4 k1 = *reinterpret_cast<const uint4 *>(st.key + i * kKeyStep + 512 + lane * 16);
-        const uint4 q = *reinterpret_cast<const uint4 *>(st.query + i * kQueryStep + lane * 16);
-        if (i == 0) {
-            mma_first(u[0], hi, k0.x, k0.y);
-            mma_first(u[1], hi, k1.x, k1.y);
-            mma_first(o[0], hi, q.x, q.y);
-            mma_first(o[1], hi, q.z, q.w);
-        } else {
-            mma(u[0], hi, k0.x, k0.y);
-            mma(u[1], hi, k1.x, k1.y);
-            mma(o[0], hi, q.x, q.y);
-            mma(o[1], hi, q.z, q.w);
-        }
-        mma(u[0], hi, k0.z, k0.w);
-        mma(u[1], hi, k1.z, k1.w);
-        mma(u[0], lo, k0.x, k0.y);
-        mma(u[1], lo, k1.x, k1.y);
-        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(&st.decay[16 * i + 4 * j]);
-        times(h.s[2 * i][0], h.s[2 * i][1], d.x);
-        times(h.s[2 * i][2], h.s[2 * i][3], d.x);
-        times(h.s[2 * i + 1][0], h.s[2 * i + 1][1], d.y);
-        times(h.s[2 * i + 1][2], h.s[2 * i + 1][3], d.y);
-    }
-    // V - U, then V' = T (V - U)
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const float2 lower = kda::bf16x2_to_float2(v[2 * n]);
-        const float2 upper = kda::bf16x2_to_float2(v[2 * n + 1]);
-        float x[4] = {lower.x, lower.y, upper.x, upper.y};
-        scale4(x, down0, down1);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = fmaf(u[n][c], -1.0f / kKeyScale, x[c]);
-        split(x[0], x[1], hi[2 * n], lo[2 * n]);
-        split(x[2], x[3], hi[2 * n + 1], lo[2 * n + 1]);
-    }
-    float d[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const uint4 t = st.t[n][lane];
-        mma_first(d[n], hi, t.x, t.y);
-        mma(d[n], hi, t.z, t.w);
-        mma(d[n], lo, t.x, t.y);
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        constexpr float f = 1.0f / (kTScale * kUpdateScale);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) d[n][c] *= f;
-        split(d[n][0], d[n][1], hi[2 * n], lo[2 * n]);
-        split(d[n][2], d[n][3], hi[2 * n + 1], lo[2 * n + 1]);
-    }
-    const uint4 b = st.b[lane];
-    mma(o[0], hi, b.x, b.y);
-    mma(o[1], hi, b.z, b.w);
-    // S += V'^T (K P_C / P_t)
-#pragma unroll
-    for (int n = 0; n < 16; ++n) {
-        if ((n & 1) == 0) no_further_ahead();
-        const uint4 k = st.update[n][lane ^ (((lane >> 3) & 1) << 2)];
-        mma(h.s[n], hi, k.x, k.y);
-        mma(h.s[n], hi, k.z, k.w);
-        mma(h.s[n], lo, k.x, k.y);
-    }
-    // the outputs, [token][16 channels] in shared memory first
-    const float up0 = power_of_two(-h.ex[0]) * (p.scale / kKeyScale);
-    const float up1 = power_of_two(-h.ex[1]) * (p.scale / kKeyScale);
-    uint32_t y[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        scale4(o[n], up0, up1);
-        y[2 * n] = kda_cache::pack(o[n][0], o[n][1], __nv_bfloat16());
-        y[2 * n + 1] = kda_cache::pack(o[n][2], o[n][3], __nv_bfloat16());
-    }
-    const int t = token_at((lane >> 4) * 8 + (lane & 7));
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     kda::smem_u32(out_tile + t * 48 + ((lane >> 3) & 1) * 16)),
-                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+// 16 columns of the warp's lanes; they are there behind arrived().
+__device__ __forceinline__ void arrived(uint32_t (&u)[16]) {
+    kda::tmem_wait_ld();
+    asm volatile(""
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
+                   "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]),
+                   "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
+                 :
                  : "memory");
-    __syncwarp();
-    const int token = chunk * kC + (lane >> 1);
-    if (token < row.tokens)
-        *reinterpret_cast<uint4 *>(p.out + ((long long)(row.first + token) * p.H + head) * kD +
-                                   16 * warp_v + 8 * (lane & 1)) =
-            *reinterpret_cast<const uint4 *>(out_tile + (lane >> 1) * 48 + (lane & 1) * 16);
-    __syncwarp();
+}
+
+// Named barriers of the consumers.
+template <int kId>
+__device__ __forceinline__ void meet() {
+    asm volatile("bar.sync %0, 256;" ::"n"(kId) : "memory");
+}
+template <int kId>
+__device__ __forceinline__ void pass() {   // arrives, does not wait
+    asm volatile("bar.arrive %0, 256;" ::"n"(kId) : "memory");
+}
+
+// A thread's half row of S as two fp16 numbers each, times `scale`, to the
+// tensor memory; the 16 channels from 16 i on.
+__device__ __forceinline__ void store_split(uint32_t tmem, int half, int i, const u64 *s,
+                                            float scale) {
+    uint32_t x[16];   // 8 of hi, 8 of lo
+    const u64 f = pair(scale, scale);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const float2 y = both(mul_pair(s[8 * i + c], f));
+        split(y.x, y.y, x[c], x[8 + c]);
+    }
+    const uint32_t to = tmem + kColS + 32 * half + 8 * i;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+        : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            to + 64),
+        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]),
+        "r"(x[15])
+        : "memory");
+}
+
+// 16 values times `scale` as two fp16 numbers each: 8 columns of hi, 8 of lo.
+__device__ __forceinline__ void store_split16(uint32_t to, const float (&x)[16], float scale) {
+    uint32_t u[16];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) split(x[2 * c] * scale, x[2 * c + 1] * scale, u[c], u[8 + c]);
+    kda::tmem_st16(to, u);
+}
+
+__device__ __forceinline__ float largest(const u64 (&s)[32]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        const float2 x = both(s[c]);
+        m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    return m;
+}
+
+// S is held in tensor memory near 2^12 by the bound of its row that is known
+// when it is split, V - U near 2^10: V' = T (V - U) is at most 16 times that.
+__device__ __forceinline__ int state_exponent(float most) { return 12 - exponent_of(most); }
+
+// The products of a chunk, by one thread.
+__device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem, unsigned parity) {
+    constexpr uint32_t kWide = idesc(kTall, false), kNarrow = idesc(kC, false);
+    const uint32_t d = tmem + kColReach + kTall * parity;
+    const uint32_t at = kda::smem_u32(st.reach[0]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma(d, tmem + kColS + 8 * k,
+             kda::sw128_desc(at + (k >> 2) * kTall * 128 + (k & 3) * 32), kWide, k > 0);
+    // (columns of their own: products of different shapes are not kept in order)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma(tmem + kColLow, tmem + kColS + 64 + 8 * k,
+             kda::sw128_desc(at + (k >> 2) * kTall * 128 + (k & 3) * 32), kNarrow, k > 0);
+}
+
+__device__ __forceinline__ void issue_delta(const Stage &st, uint32_t tmem) {
+    constexpr uint32_t kNarrow = idesc(kC, false);
+    const uint32_t at = kda::smem_u32(st.inner);
+    umma(tmem + kColDelta, tmem + kColX, kda::sw128_desc(at), kNarrow, false);
+    umma(tmem + kColDelta, tmem + kColX, kda::sw128_desc(at + 32), kNarrow, true);
+    umma(tmem + kColDelta, tmem + kColX + 8, kda::sw128_desc(at), kNarrow, true);
+}
+
+__device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem, unsigned parity) {
+    constexpr uint32_t kNarrow = idesc(kC, false), kAll = idesc(kD, true);
+    const uint32_t hi = kda::smem_u32(st.update[0][0]), lo = kda::smem_u32(st.update[1][0]);
+    umma(tmem + kColUpdate, tmem + kColY, along_n(hi, kC * 128), kAll, false);
+    umma(tmem + kColUpdate, tmem + kColY, along_n(lo, kC * 128), kAll, true);
+    umma(tmem + kColUpdate, tmem + kColY + 8, along_n(hi, kC * 128), kAll, true);
+    umma(tmem + kColInner + kC * parity, tmem + kColY,
+         kda::sw128_desc(kda::smem_u32(st.inner) + 64), kNarrow, false);
+}
+
+// A row's outputs of a chunk: from the state, and from the chunk itself.
+__device__ __forceinline__ void write_outputs(const Params &p, uint32_t tmem, unsigned parity,
+                                              float f_reach, float f_inner, const Row &row,
+                                              int head, int chunk, int r, bool ok) {
+    uint32_t x[16], y[16];
+    kda::tmem_ld16(tmem + kColReach + kTall * parity + kC, x);
+    kda::tmem_ld16(tmem + kColInner + kC * parity, y);
+    arrived(x);
+    arrived(y);
+    const int n = ok ? min(kC, row.tokens - chunk * kC) : 0;
+    __nv_bfloat16 *dst =
+        p.out + ((long long)(row.first + chunk * kC) * p.H + head) * kD + r;
+    const long long step = (long long)p.H * kD;
+#pragma unroll
+    for (int t = 0; t < kC; ++t, dst += step)
+        if (t < n)
+            *dst = __float2bfloat16_rn(
+                fmaf(__uint_as_float(y[t]), f_inner, __uint_as_float(x[t]) * f_reach));
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -794,15 +708,14 @@ __device__ __forceinline__ void consume(const Params &p, const Stage &st, unsign
 // A producer warp: the tokens' vectors (kTokens) or the products between them
 // of every kPairs-th chunk of the CTA's work.
 template <bool kBounded, bool kTokens>
-__device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned items, int part_bits,
-                                        int warp, int lane) {
+__device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned items, int warp,
+                                        int lane) {
     const unsigned pair_of = warp % kPairs;
     unsigned count = 0, blocks = 0;
     for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
         int bits = 0;
-        const Work w = work_at(p, item, part_bits, bits);
-        if (bits != 0 && w.head == 0 && w.part == 0 && threadIdx.x == 0)
-            kda_cache::flag(p.err, bits);
+        const Work w = work_at(p, item, bits);
+        if (bits != 0 && w.head == 0 && threadIdx.x == 0) kda_cache::flag(p.err, bits);
         const unsigned chunks = (unsigned)(w.row.tokens + kC - 1) / kC;
         for (unsigned c = (pair_of - count) % kPairs; c < chunks; c += kPairs) {
             const unsigned stage = (count + c) % kStages, turn = (count + c) / kStages;
@@ -815,98 +728,234 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
             else
                 made = produce_products(p, sh, st, sc, w.row, w.head, c, lane, blocks);
             if (!made) return;
+            kda::fence_proxy_async_smem();   // the tensor cores read it
+            __syncwarp();
             if (lane == 0) kda::mbar_arrive(&sh.full[stage]);
         }
         count += chunks;
     }
 }
 
+// The consumer warps.  A wait that runs out ends nothing by itself: from then
+// on the warp, and soon all of them, go through the same barriers without
+// waiting, issuing or writing, so that no barrier is left with too few.
+__device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned items, int me,
+                                        int lane) {
+    const int half = me >> 2, r = 32 * (me & 3) + lane;   // columns of S, and the row
+    const uint32_t tmem = sh.tmem + ((uint32_t)(32 * (me & 3)) << 16);
+    const bool issuer = me == 0 && lane == 0;
+    bool ok = true;
+    unsigned count = 0;
+    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+        int bits = 0;
+        const Work w = work_at(p, item, bits);
+        if (w.row.tokens == 0) continue;
+        const long long slot = (long long)p.H * kda_delta::kTile;
+        const long long at = (long long)w.head * kda_delta::kTile + r * kD + 64 * half;
+        u64 s[32];   // channels 64 half + 0..63 of row r
+        if (w.row.from > 0) {
+            const float *src = p.pool + w.row.from * slot + at;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(src + 4 * c);
+                s[2 * c] = x.x;
+                s[2 * c + 1] = x.y;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = 0ull;
+        }
+        float most = largest(s);
+        sh.most[half][r] = most;
+        meet<1>();
+        int ex = state_exponent(fmaxf(sh.most[0][r], sh.most[1][r]));
+        {
+            const float f = power_of_two(ex);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_split(tmem, half, i, s, f);
+        }
+        const int chunks = (w.row.tokens + kC - 1) / kC;
+        float f_reach = 0.0f, f_inner = 0.0f;   // of the chunk whose outputs are to be written
+        for (int c = 0; c < chunks; ++c, ++count) {
+            const unsigned stage = count % kStages, turn = count / kStages, parity = count & 1;
+            const Stage &st = sh.stage[stage];
+            ok &= wait(sh, &sh.full[stage], turn & 1, p.err);
+            kda::tmem_wait_st();
+            kda::tc_fence_before();
+            meet<1>();
+            if (issuer && ok) {
+                kda::tc_fence_after();
+                issue_reach(st, tmem, parity);
+                kda::umma_commit(&sh.u_done);
+            }
+            __syncwarp();
+            if (c > 0) {
+                most = largest(s);
+                sh.most[half][r] = most;
+            }
+            if (half == 0) {
+                float x[16];
+#pragma unroll
+                for (int t = 0; t < kC; ++t) x[t] = __bfloat162float(st.v[t][r]);
+                ok &= wait(sh, &sh.u_done, parity, p.err);
+                kda::tc_fence_after();
+                {
+                    uint32_t u[16], y[16], z[16];
+                    kda::tmem_ld16(tmem + kColReach + kTall * parity, u);
+                    kda::tmem_ld16(tmem + kColReach + kTall * parity + 2 * kC, y);
+                    kda::tmem_ld16(tmem + kColLow, z);
+                    arrived(u);
+                    arrived(y);
+                    arrived(z);
+                    const float f = -power_of_two(-ex) / kKeyScale;
+#pragma unroll
+                    for (int t = 0; t < kC; ++t)
+                        x[t] = fmaf(__uint_as_float(u[t]) +
+                                        (__uint_as_float(y[t]) + __uint_as_float(z[t])),
+                                    f, x[t]);
+                }
+                float m = 0.0f;
+#pragma unroll
+                for (int t = 0; t < kC; ++t) m = fmaxf(m, fabsf(x[t]));
+                const int ey = 10 - exponent_of(m);
+                store_split16(tmem + kColX, x, power_of_two(ey));
+                kda::tmem_wait_st();
+                kda::tc_fence_before();
+                meet<2>();
+                if (issuer && ok) {
+                    kda::tc_fence_after();
+                    issue_delta(st, tmem);
+                    kda::umma_commit(&sh.v_done);
+                }
+                __syncwarp();
+                most = fmaxf(sh.most[0][r], sh.most[1][r]);
+                ok &= wait(sh, &sh.v_done, parity, p.err);
+                kda::tc_fence_after();
+                {
+                    uint32_t u[16];
+                    kda::tmem_ld16(tmem + kColDelta, u);
+                    arrived(u);
+#pragma unroll
+                    for (int t = 0; t < kC; ++t) x[t] = __uint_as_float(u[t]);
+                }
+                store_split16(tmem + kColY, x, 1.0f / kTScale);
+                float sum = 0.0f;
+#pragma unroll
+                for (int t = 0; t < kC; ++t) sum += fabsf(x[t]);
+                // S is at most what it was and all that is added to it
+                const float back = power_of_two(-ey);
+                sh.info[r] = make_float4(back / kUpdateScale,
+                                         most + sum * back * (1.0f / kTScale),
+                                         power_of_two(-ex) * (p.scale / kKeyScale),
+                                         back * (p.scale / kBScale));
+                kda::tmem_wait_st();
+                kda::tc_fence_before();
+            } else {
+                pass<2>();
+                if (c > 0)
+                    write_outputs(p, tmem, parity ^ 1, f_reach, f_inner, w.row, w.head, c - 1, r,
+                                  ok);
+                kda::tc_fence_before();
+            }
+            meet<3>();
+            if (issuer && ok) {
+                kda::tc_fence_after();
+                issue_update(st, tmem, parity);
+                kda::umma_commit(&sh.s_done);
+                kda::umma_commit(&sh.empty[stage]);
+            }
+            __syncwarp();
+            const float4 info = sh.info[r];
+            f_reach = info.z;
+            f_inner = info.w;
+            ex = state_exponent(info.y);
+            const float f = power_of_two(ex);
+            const u64 added = pair(info.x, info.x);
+            ok &= wait(sh, &sh.s_done, parity, p.err);
+            kda::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t u[16];
+                kda::tmem_ld16(tmem + kColUpdate + 64 * half + 16 * i, u);
+                u64 d[8];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(
+                        &st.decay[64 * half + 16 * i + 4 * n]);
+                    d[2 * n] = x.x;
+                    d[2 * n + 1] = x.y;
+                }
+                arrived(u);
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    s[8 * i + n] = fma_pair(
+                        pair(__uint_as_float(u[2 * n]), __uint_as_float(u[2 * n + 1])), added,
+                        mul_pair(s[8 * i + n], d[n]));
+                if (c + 1 < chunks) store_split(tmem, half, i, s, f);
+            }
+            __syncwarp();
+            if (lane == 0) kda::mbar_arrive(&sh.empty[stage]);
+        }
+        if (half == 1)
+            write_outputs(p, tmem, (count - 1) & 1, f_reach, f_inner, w.row, w.head, chunks - 1, r,
+                          ok);
+        kda::tc_fence_before();
+        if (ok) {
+            float *dst = p.pool + w.row.to * slot + at;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                *reinterpret_cast<ulonglong2 *>(dst + 4 * c) =
+                    make_ulonglong2(s[2 * c], s[2 * c + 1]);
+        }
+    }
+}
+
 template <bool kBounded>
-__global__ void __launch_bounds__(kMaxThreads, 1)
-    prefill_kernel(const Params p, unsigned items, int part_bits) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, unsigned items) {
     extern __shared__ unsigned char raw_smem[];
     Shared &sh = *reinterpret_cast<Shared *>(
-        (reinterpret_cast<uintptr_t>(raw_smem) + 127) & ~(uintptr_t)127);
+        (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int consumers = kMaxConsumers >> part_bits;
     if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f;
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
         for (int i = 0; i < kStages; ++i) {
             kda::mbar_init(&sh.full[i], 2);
-            kda::mbar_init(&sh.empty[i], consumers);
+            kda::mbar_init(&sh.empty[i], kConsumers + 1);
         }
         for (int i = 0; i < 2 * kPairs; ++i) {
             kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
             kda::mbar_init(&sh.scratch[i >> 1].taken[i & 1], 1);
         }
+        kda::mbar_init(&sh.u_done, 1);
+        kda::mbar_init(&sh.v_done, 1);
+        kda::mbar_init(&sh.s_done, 1);
+        kda::mbar_init(&sh.drained, 1);
+        kda::fence_mbar_init();
+    }
+    if (warp == kProducers) {
+        kda::tmem_alloc(&sh.tmem, kTmemColumns);
+        kda::tc_fence_before();
     }
     kda_cache::grid_dependents_launch();
     __syncthreads();
+    kda::tc_fence_after();
     kda_cache::grid_dependency_wait();
-    unsigned count = 0;   // chunks so far, of all items
-    if (warp < kProducers) {
-        if (warp < kPairs) {
-            fewer_registers<96>();
-            produce<kBounded, true>(p, sh, items, part_bits, warp, lane);
-        } else {
-            produce<kBounded, false>(p, sh, items, part_bits, warp, lane);
-        }
-        return;
+    if (warp < kPairs)
+        produce<kBounded, true>(p, sh, items, warp, lane);
+    else if (warp < kProducers)
+        produce<kBounded, false>(p, sh, items, warp, lane);
+    else
+        consume(p, sh, items, warp - kProducers, lane);
+    if (threadIdx.x == 32 * kProducers) {
+        // no product may outlive the memory, whatever became of who waited for it
+        kda::umma_commit(&sh.drained);
+        kda::mbar_wait_bounded(&sh.drained, 0, kWaitBudget);
     }
-    more_registers<144>();
-    const int me = warp - kProducers;
-    if (me >= consumers) return;   // there to make up a warpgroup
-    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
-        int bits = 0;
-        const Work w = work_at(p, item, part_bits, bits);
-        if (w.row.tokens == 0) continue;
-        const int warp_v = w.part * consumers + me;   // of the 8 sixteenths of a state's rows
-        const long long tile = (long long)w.head * kda_delta::kTile +
-                               (16 * warp_v + (lane >> 2)) * kD + 4 * (lane & 3);
-        const long long slot = (long long)p.H * kda_delta::kTile;
-        Held h;
-        h.ex[0] = h.ex[1] = 0;
-        h.most[0] = h.most[1] = 0.0f;
-        if (w.row.from > 0) {
-            const float *src = p.pool + w.row.from * slot + tile;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 a = __ldcs(reinterpret_cast<const float4 *>(src + 16 * i));
-                const float4 b = __ldcs(reinterpret_cast<const float4 *>(src + 8 * kD + 16 * i));
-                h.s[2 * i][0] = a.x;
-                h.s[2 * i][1] = a.y;
-                h.s[2 * i][2] = b.x;
-                h.s[2 * i][3] = b.y;
-                h.s[2 * i + 1][0] = a.z;
-                h.s[2 * i + 1][1] = a.w;
-                h.s[2 * i + 1][2] = b.z;
-                h.s[2 * i + 1][3] = b.w;
-            }
-        } else {
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) h.s[n][c] = 0.0f;
-        }
-        const int chunks = (w.row.tokens + kC - 1) / kC;
-        for (int c = 0; c < chunks; ++c, ++count) {
-            const unsigned stage = count % kStages, turn = count / kStages;
-            if (!wait(sh, &sh.full[stage], turn & 1, p.err)) return;
-            consume(p, sh.stage[stage], sh.out[me], h, w.row, w.head, c, warp_v, lane);
-            if (lane == 0) kda::mbar_arrive(&sh.empty[stage]);
-        }
-        float *dst = p.pool + w.row.to * slot + tile;
-        const float up0 = power_of_two(-h.ex[0]), up1 = power_of_two(-h.ex[1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            __stcs(reinterpret_cast<float4 *>(dst + 16 * i),
-                   make_float4(h.s[2 * i][0] * up0, h.s[2 * i][1] * up0, h.s[2 * i + 1][0] * up0,
-                               h.s[2 * i + 1][1] * up0));
-            __stcs(reinterpret_cast<float4 *>(dst + 8 * kD + 16 * i),
-                   make_float4(h.s[2 * i][2] * up1, h.s[2 * i][3] * up1, h.s[2 * i + 1][2] * up1,
-                               h.s[2 * i + 1][3] * up1));
-        }
+    __syncthreads();
+    if (warp == kProducers) {
+        kda::tc_fence_after();
+        kda::tmem_dealloc(sh.tmem, kTmemColumns);
     }
 }
 
@@ -931,22 +980,14 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     const long long tiles = (long long)B * p.H;
     const int sms = kda_cache::sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
-    // A state's rows can go to several CTAs, each of which makes the shared
-    // operands for itself: where there are few states, that is better than
-    // idle SMs.
-    int part_bits = 0;
-    while (part_bits < 2 && (tiles << (part_bits + 1)) <= sms) ++part_bits;
-    const long long items = tiles << part_bits;
-    if (items > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
-    const int smem = (int)sizeof(Shared) + 128;
-    void (*kernel)(const Params, unsigned, int) =
-        p.bounded ? prefill_kernel<true> : prefill_kernel<false>;
+    if (tiles > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
+    const int smem = (int)sizeof(Shared) + 1024;
+    void (*kernel)(const Params, unsigned) = p.bounded ? prefill_kernel<true> : prefill_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return KDA_ERR_CUDA;
-    return kda_cache::launch(kernel, dim3((unsigned)(items < sms ? items : sms)),
-                             dim3(32 * (kProducers + (part_bits == 0 ? 8 : 4))), smem, 1, stream,
-                             p, (unsigned)items, part_bits);
+    return kda_cache::launch(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads),
+                             smem, 1, stream, p, (unsigned)tiles);
 }
 
 extern "C" kda_status kda_prefill_packed(const kda_delta_args *a) {
