@@ -19,12 +19,14 @@
 // most 1 and scaled by powers of two; rows of S, of V - U and of V' have
 // powers of two of their own, from their own sizes, as fp16's range needs it.
 //
-// Layout.  A CTA has one row and head at a time.  Eight consumer warps hold S
-// in registers, a thread half a row of it: it adds what the chunk brought,
-// splits it and stores it to tensor memory, where it is the A operand of the
-// next chunk's products; four of them make V - U and split V' on the way, the
-// other four write the outputs.  The operands that all rows share (K P, Q P,
-// K P_C / P_t, T, B, P_C) are made by eight producer warps in a ring of stages.
+// Layout.  A CTA has one row and head at a time.  S lies in tensor memory, in
+// fp32 and, split, as the A operand of the products.  Eight consumer warps
+// have half a row of it a thread: they add what the chunk brought and split
+// it; four of them make V - U and split V' on the way, the other four write
+// the outputs.  The operands that all rows share (K P, Q P, K P_C / P_t, T, B,
+// P_C) are made by eight producer warps in a ring of stages.  What runs once a
+// chunk is in short loops: straight code of all roles together (80 KB) missed
+// the instruction cache so often that it took twice the time.
 //
 // A and B.  Two producer warps make a chunk's operands, the first the tokens'
 // vectors, the second the products between tokens.  Four tokens t at a time
@@ -119,14 +121,15 @@ struct Shared {
 };
 
 // Columns of tensor memory.
-constexpr uint32_t kColS = 0;             // S: 64 of hi, 64 of lo, two channels each
-constexpr uint32_t kColUpdate = 128;      // V'^T (K P_C / P_t), 128
-constexpr uint32_t kColReach = 256;       // S (K P | Q P | K P lo)^T, 48, of even and odd chunks
-constexpr uint32_t kColInner = 352;       // B V', 16, of even and odd chunks
-constexpr uint32_t kColX = 384;           // V - U: 8 of hi, 8 of lo
-constexpr uint32_t kColDelta = 400;       // V', 16
-constexpr uint32_t kColY = 416;           // V': 8 of hi, 8 of lo
+constexpr uint32_t kColState = 0;         // S, fp32, 128
+constexpr uint32_t kColS = 128;           // S as fp16: 64 of hi, 64 of lo, two channels each
+constexpr uint32_t kColUpdate = 256;      // V'^T (K P_C / P_t), 128
+constexpr uint32_t kColReach = 384;       // S (K P | Q P | K P lo)^T, 48
 constexpr uint32_t kColLow = 432;         // lo of S with hi of K P, 16
+constexpr uint32_t kColInner = 448;       // B V', 16
+constexpr uint32_t kColX = 464;           // V - U: 8 of hi, 8 of lo
+constexpr uint32_t kColDelta = 480;       // V', 16
+constexpr uint32_t kColY = 496;           // V': 8 of hi, 8 of lo
 constexpr uint32_t kTmemColumns = 512;
 
 // D += A B for k steps of 8 in tf32.
@@ -290,9 +293,7 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     const long long at = (long long)head * kD + 4 * lane;
     Inputs in{p.q + first * p.stride_q + at, p.k + first * p.stride_k + at,
               p.g + first * p.stride_g + at};
-    Raw next[2];
-    next[0] = load_raw(p, in, true);
-    next[1] = load_raw(p, in, 1 < valid);
+    Raw next = load_raw(p, in, true), later = load_raw(p, in, 1 < valid);
     {   // the values as they are
         const __nv_bfloat16 *src = p.v + first * p.stride_v + at;
 #pragma unroll 4
@@ -310,93 +311,80 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     u64 total[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};                       // log2 P_t
     u64 r[2] = {pair(1.0f, 1.0f), pair(1.0f, 1.0f)};                            // R
     unsigned char *reached = st.reach[lane >> 4];
-    // two tokens a turn, the next two on their way
+    // a token a turn, the next two on their way
 #pragma unroll 1
-    for (int t0 = 0; t0 < kC; t0 += 2) {
-        const Raw now[2] = {next[0], next[1]};
-        next[0] = load_raw(p, in, t0 + 2 < valid);
-        next[1] = load_raw(p, in, t0 + 3 < valid);
+    for (int t = 0; t < kC; ++t) {
+        const Raw now = next;
+        next = later;
+        later = load_raw(p, in, t + 2 < valid);
         Block &out = sc.block[blocks & 1];
-        if ((t0 & 2) == 0 && !wait(sh, &sc.taken[blocks & 1], ((blocks >> 1) & 1) ^ 1, p.err)) {
+        if ((t & 3) == 0 && !wait(sh, &sc.taken[blocks & 1], ((blocks >> 1) & 1) ^ 1, p.err)) {
             kda::cp_async_wait_all();
             return false;
         }
-        // norms: lane bits 4 and 3 choose among the sums of k and q of both tokens
-        float norm;
-        {
-            u64 x, y;
-            float s[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                pairs_of(now[u].k, x, y);
-                s[2 * u] = squares(x, y);
-                pairs_of(now[u].q, x, y);
-                s[2 * u + 1] = squares(x, y);
-            }
-            const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0;
-            s[0] = (b4 ? s[2] : s[0]) + __shfl_xor_sync(kFull, b4 ? s[0] : s[2], 16);
-            s[1] = (b4 ? s[3] : s[1]) + __shfl_xor_sync(kFull, b4 ? s[1] : s[3], 16);
-            norm = (b3 ? s[1] : s[0]) + __shfl_xor_sync(kFull, b3 ? s[0] : s[1], 8);
+        u64 k[2], q[2];
+        pairs_of(now.k, k[0], k[1]);
+        pairs_of(now.q, q[0], q[1]);
+        float rk, rq;
+        {   // norms: of k in the lower lanes, of q in the upper ones
+            const float sk = squares(k[0], k[1]), sq = squares(q[0], q[1]);
+            const bool upper = (lane & 16) != 0;
+            float norm = (upper ? sq : sk) + __shfl_xor_sync(kFull, upper ? sk : sq, 16);
+            norm += __shfl_xor_sync(kFull, norm, 8);
             norm += __shfl_xor_sync(kFull, norm, 4);
             norm += __shfl_xor_sync(kFull, norm, 2);
             norm += __shfl_xor_sync(kFull, norm, 1);
             norm = kda::inv_l2(norm);
+            const float other = __shfl_xor_sync(kFull, norm, 16);
+            rk = upper ? other : norm;
+            rq = upper ? norm : other;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = t0 + u;
-            const float rk = __shfl_sync(kFull, norm, 16 * u);
-            const float rq = __shfl_sync(kFull, norm, 16 * u + 8);
-            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // behind the row's end nothing decays
-            if (t < valid) {
-                const float4 x = kda::bf16x4_to_float4(now[u].g);
-                y[0] = log2_decay<kBounded>(x.x + bias.x, gate, bound);
-                y[1] = log2_decay<kBounded>(x.y + bias.y, gate, bound);
-                y[2] = log2_decay<kBounded>(x.z + bias.z, gate, bound);
-                y[3] = log2_decay<kBounded>(x.w + bias.w, gate, bound);
-            }
-            total[0] = add_pair(total[0], pair(y[0], y[1]));
-            total[1] = add_pair(total[1], pair(y[2], y[3]));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = exp2_of(y[c]);
-            const u64 e[2] = {pair(y[0], y[1]), pair(y[2], y[3])};
-            u64 k[2], q[2];
-            pairs_of(now[u].k, k[0], k[1]);
-            pairs_of(now[u].q, q[0], q[1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                reach[i] = mul_pair(reach[i], e[i]);
-                k[i] = mul_pair(k[i], pair(rk, rk));
-                q[i] = mul_pair(q[i], pair(rq, rq));
-            }
-            if (u == 0 && (t0 & 2) == 0) {   // a block's first token
-                put(&out.since[4 * lane], mul_pair(r[0], e[0]), mul_pair(r[1], e[1]));
-                r[0] = r[1] = pair(1.0f, 1.0f);
-            } else {
-                r[0] = mul_pair(r[0], pair(fmaxf(y[0], 0x1p-40f), fmaxf(y[1], 0x1p-40f)));
-                r[1] = mul_pair(r[1], pair(fmaxf(y[2], 0x1p-40f), fmaxf(y[3], 0x1p-40f)));
-            }
-            float *ahead = &out.ahead[t & 3][4 * lane];
-            put(ahead, mul_pair(k[0], r[0]), mul_pair(k[1], r[1]));
-            put(ahead + 4 * kRow, mul_pair(q[0], r[0]), mul_pair(q[1], r[1]));
-            const float2 r0 = both(r[0]), r1 = both(r[1]);
-            put(&out.back[t & 3][4 * lane], mul_pair(k[0], pair(reciprocal(r0.x), reciprocal(r0.y))),
-                mul_pair(k[1], pair(reciprocal(r1.x), reciprocal(r1.y))));
-            const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
-            uint2 hi, lo;
-            float2 x = both(mul_pair(k[0], reach[0]));
-            split(x.x, x.y, hi.x, lo.x);
-            x = both(mul_pair(k[1], reach[1]));
-            split(x.x, x.y, hi.y, lo.y);
-            *reinterpret_cast<uint2 *>(reached + to) = hi;
-            *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
-            x = both(mul_pair(q[0], reach[0]));
-            hi.x = half_pair(x.x, x.y);
-            x = both(mul_pair(q[1], reach[1]));
-            hi.y = half_pair(x.x, x.y);
-            *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // behind the row's end nothing decays
+        if (t < valid) {
+            const float4 x = kda::bf16x4_to_float4(now.g);
+            y[0] = log2_decay<kBounded>(x.x + bias.x, gate, bound);
+            y[1] = log2_decay<kBounded>(x.y + bias.y, gate, bound);
+            y[2] = log2_decay<kBounded>(x.z + bias.z, gate, bound);
+            y[3] = log2_decay<kBounded>(x.w + bias.w, gate, bound);
         }
-        if ((t0 & 2) != 0) {
+        total[0] = add_pair(total[0], pair(y[0], y[1]));
+        total[1] = add_pair(total[1], pair(y[2], y[3]));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = exp2_of(y[c]);
+        const u64 e[2] = {pair(y[0], y[1]), pair(y[2], y[3])};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            reach[i] = mul_pair(reach[i], e[i]);
+            k[i] = mul_pair(k[i], pair(rk, rk));
+            q[i] = mul_pair(q[i], pair(rq, rq));
+        }
+        if ((t & 3) == 0) {   // a block's first token
+            put(&out.since[4 * lane], mul_pair(r[0], e[0]), mul_pair(r[1], e[1]));
+            r[0] = r[1] = pair(1.0f, 1.0f);
+        } else {
+            r[0] = mul_pair(r[0], pair(fmaxf(y[0], 0x1p-40f), fmaxf(y[1], 0x1p-40f)));
+            r[1] = mul_pair(r[1], pair(fmaxf(y[2], 0x1p-40f), fmaxf(y[3], 0x1p-40f)));
+        }
+        float *ahead = &out.ahead[t & 3][4 * lane];
+        put(ahead, mul_pair(k[0], r[0]), mul_pair(k[1], r[1]));
+        put(ahead + 4 * kRow, mul_pair(q[0], r[0]), mul_pair(q[1], r[1]));
+        const float2 r0 = both(r[0]), r1 = both(r[1]);
+        put(&out.back[t & 3][4 * lane], mul_pair(k[0], pair(reciprocal(r0.x), reciprocal(r0.y))),
+            mul_pair(k[1], pair(reciprocal(r1.x), reciprocal(r1.y))));
+        const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
+        uint2 hi, lo;
+        float2 x = both(mul_pair(k[0], reach[0]));
+        split(x.x, x.y, hi.x, lo.x);
+        x = both(mul_pair(k[1], reach[1]));
+        split(x.x, x.y, hi.y, lo.y);
+        *reinterpret_cast<uint2 *>(reached + to) = hi;
+        *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
+        x = both(mul_pair(q[0], reach[0]));
+        hi.x = half_pair(x.x, x.y);
+        x = both(mul_pair(q[1], reach[1]));
+        hi.y = half_pair(x.x, x.y);
+        *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
+        if ((t & 3) == 3) {
             put(&out.end[4 * lane], r[0], r[1]);
             __syncwarp();
             if (lane == 0) kda::mbar_arrive(&sc.ready[blocks & 1]);
@@ -582,7 +570,7 @@ __device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint64_t b, uint32_
         : "memory");
 }
 
-// 16 columns of the warp's lanes; they are there behind arrived().
+// 16 or 8 columns of the warp's lanes; they are there behind arrived().
 __device__ __forceinline__ void arrived(uint32_t (&u)[16]) {
     kda::tmem_wait_ld();
     asm volatile(""
@@ -591,6 +579,46 @@ __device__ __forceinline__ void arrived(uint32_t (&u)[16]) {
                    "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
                  :
                  : "memory");
+}
+
+__device__ __forceinline__ void arrived(uint32_t (&u)[8]) {
+    kda::tmem_wait_ld();
+    asm volatile(""
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
+                   "+r"(u[6]), "+r"(u[7])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void load8(uint32_t from, uint32_t (&u)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7])
+        : "r"(from)
+        : "memory");
+}
+
+__device__ __forceinline__ void store8(uint32_t to, const uint32_t (&u)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+        : "memory");
+}
+
+__device__ __forceinline__ void store4(uint32_t to, const uint32_t (&u)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ u64 pair_of(uint32_t x, uint32_t y) {
+    return pair(__uint_as_float(x), __uint_as_float(y));
+}
+
+__device__ __forceinline__ float larger(float m, u64 xy) {
+    const float2 x = both(xy);
+    return fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
 }
 
 // Named barriers of the consumers.
@@ -603,60 +631,51 @@ __device__ __forceinline__ void pass() {   // arrives, does not wait
     asm volatile("bar.arrive %0, 256;" ::"n"(kId) : "memory");
 }
 
-// A thread's half row of S as two fp16 numbers each, times `scale`, to the
-// tensor memory; the 16 channels from 16 i on.
-__device__ __forceinline__ void store_split(uint32_t tmem, int half, int i, const u64 *s,
+// 16 channels of a row of S, as they are and as two fp16 numbers each times
+// `scale`, to tensor memory: state and split are the columns of the first.
+__device__ __forceinline__ void store_state(uint32_t state, uint32_t split_to, const u64 (&s)[8],
                                             float scale) {
-    uint32_t x[16];   // 8 of hi, 8 of lo
+    uint32_t x[16], hi[8], lo[8];
     const u64 f = pair(scale, scale);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        const float2 y = both(mul_pair(s[8 * i + c], f));
-        split(y.x, y.y, x[c], x[8 + c]);
+        const float2 y = both(s[c]);
+        x[2 * c] = __float_as_uint(y.x);
+        x[2 * c + 1] = __float_as_uint(y.y);
+        const float2 z = both(mul_pair(s[c], f));
+        split(z.x, z.y, hi[c], lo[c]);
     }
-    const uint32_t to = tmem + kColS + 32 * half + 8 * i;
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to),
-        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-        : "memory");
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-            to + 64),
-        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]),
-        "r"(x[15])
-        : "memory");
+    kda::tmem_st16(state, x);
+    store8(split_to, hi);
+    store8(split_to + 64, lo);
 }
 
-// 16 values times `scale` as two fp16 numbers each: 8 columns of hi, 8 of lo.
-__device__ __forceinline__ void store_split16(uint32_t to, const float (&x)[16], float scale) {
-    uint32_t u[16];
+// 8 values times `scale` as two fp16 numbers each: hi to 4 columns, lo to the
+// 4 that are 8 further.
+__device__ __forceinline__ void store_split8(uint32_t to, const u64 (&x)[4], float scale) {
+    uint32_t hi[4], lo[4];
+    const u64 f = pair(scale, scale);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) split(x[2 * c] * scale, x[2 * c + 1] * scale, u[c], u[8 + c]);
-    kda::tmem_st16(to, u);
-}
-
-__device__ __forceinline__ float largest(const u64 (&s)[32]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        const float2 x = both(s[c]);
-        m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+    for (int c = 0; c < 4; ++c) {
+        const float2 y = both(mul_pair(x[c], f));
+        split(y.x, y.y, hi[c], lo[c]);
     }
-    return m;
+    store4(to, hi);
+    store4(to + 8, lo);
 }
 
-// S is held in tensor memory near 2^12 by the bound of its row that is known
-// when it is split, V - U near 2^10: V' = T (V - U) is at most 16 times that.
+// The split S is below 2^13 by the bound of its row that is known then.  V - U
+// is below 2^11 by |V| and the norm of the row, and V' = T (V - U) is at most
+// 16 times that, as an entry of T is at most 1.
 __device__ __forceinline__ int state_exponent(float most) { return 12 - exponent_of(most); }
 
 // The products of a chunk, by one thread.
-__device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem, unsigned parity) {
+__device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kWide = idesc(kTall, false), kNarrow = idesc(kC, false);
-    const uint32_t d = tmem + kColReach + kTall * parity;
     const uint32_t at = kda::smem_u32(st.reach[0]);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        umma(d, tmem + kColS + 8 * k,
+        umma(tmem + kColReach, tmem + kColS + 8 * k,
              kda::sw128_desc(at + (k >> 2) * kTall * 128 + (k & 3) * 32), kWide, k > 0);
     // (columns of their own: products of different shapes are not kept in order)
 #pragma unroll
@@ -673,34 +692,14 @@ __device__ __forceinline__ void issue_delta(const Stage &st, uint32_t tmem) {
     umma(tmem + kColDelta, tmem + kColX + 8, kda::sw128_desc(at), kNarrow, true);
 }
 
-__device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem, unsigned parity) {
+__device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kNarrow = idesc(kC, false), kAll = idesc(kD, true);
     const uint32_t hi = kda::smem_u32(st.update[0][0]), lo = kda::smem_u32(st.update[1][0]);
     umma(tmem + kColUpdate, tmem + kColY, along_n(hi, kC * 128), kAll, false);
     umma(tmem + kColUpdate, tmem + kColY, along_n(lo, kC * 128), kAll, true);
     umma(tmem + kColUpdate, tmem + kColY + 8, along_n(hi, kC * 128), kAll, true);
-    umma(tmem + kColInner + kC * parity, tmem + kColY,
+    umma(tmem + kColInner, tmem + kColY,
          kda::sw128_desc(kda::smem_u32(st.inner) + 64), kNarrow, false);
-}
-
-// A row's outputs of a chunk: from the state, and from the chunk itself.
-__device__ __forceinline__ void write_outputs(const Params &p, uint32_t tmem, unsigned parity,
-                                              float f_reach, float f_inner, const Row &row,
-                                              int head, int chunk, int r, bool ok) {
-    uint32_t x[16], y[16];
-    kda::tmem_ld16(tmem + kColReach + kTall * parity + kC, x);
-    kda::tmem_ld16(tmem + kColInner + kC * parity, y);
-    arrived(x);
-    arrived(y);
-    const int n = ok ? min(kC, row.tokens - chunk * kC) : 0;
-    __nv_bfloat16 *dst =
-        p.out + ((long long)(row.first + chunk * kC) * p.H + head) * kD + r;
-    const long long step = (long long)p.H * kD;
-#pragma unroll
-    for (int t = 0; t < kC; ++t, dst += step)
-        if (t < n)
-            *dst = __float2bfloat16_rn(
-                fmaf(__uint_as_float(y[t]), f_inner, __uint_as_float(x[t]) * f_reach));
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -743,6 +742,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                                         int lane) {
     const int half = me >> 2, r = 32 * (me & 3) + lane;   // columns of S, and the row
     const uint32_t tmem = sh.tmem + ((uint32_t)(32 * (me & 3)) << 16);
+    const uint32_t state = tmem + kColState + 64 * half, halves = tmem + kColS + 32 * half;
     const bool issuer = me == 0 && lane == 0;
     bool ok = true;
     unsigned count = 0;
@@ -752,73 +752,147 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
         const long long at = (long long)w.head * kda_delta::kTile + r * kD + 64 * half;
-        u64 s[32];   // channels 64 half + 0..63 of row r
-        if (w.row.from > 0) {
-            const float *src = p.pool + w.row.from * slot + at;
+        // the state, by way of the columns of what is added to it
+        float most = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(src + 4 * c);
-                s[2 * c] = x.x;
-                s[2 * c + 1] = x.y;
+            for (int c = 0; c < 4; ++c) {
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (w.row.from > 0)
+                    y = *reinterpret_cast<const float4 *>(p.pool + w.row.from * slot + at +
+                                                          16 * i + 4 * c);
+                most = fmaxf(fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y))),
+                             fmaxf(fabsf(y.z), fabsf(y.w)));
+                x[4 * c] = __float_as_uint(y.x);
+                x[4 * c + 1] = __float_as_uint(y.y);
+                x[4 * c + 2] = __float_as_uint(y.z);
+                x[4 * c + 3] = __float_as_uint(y.w);
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] = 0ull;
+            kda::tmem_st16(tmem + kColUpdate + 64 * half + 16 * i, x);
         }
-        float most = largest(s);
+        kda::tmem_wait_st();
         sh.most[half][r] = most;
         meet<1>();
         int ex = state_exponent(fmaxf(sh.most[0][r], sh.most[1][r]));
-        {
-            const float f = power_of_two(ex);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store_split(tmem, half, i, s, f);
-        }
         const int chunks = (w.row.tokens + kC - 1) / kC;
-        float f_reach = 0.0f, f_inner = 0.0f;   // of the chunk whose outputs are to be written
-        for (int c = 0; c < chunks; ++c, ++count) {
-            const unsigned stage = count % kStages, turn = count / kStages, parity = count & 1;
-            const Stage &st = sh.stage[stage];
-            ok &= wait(sh, &sh.full[stage], turn & 1, p.err);
-            kda::tmem_wait_st();
-            kda::tc_fence_before();
-            meet<1>();
-            if (issuer && ok) {
-                kda::tc_fence_after();
-                issue_reach(st, tmem, parity);
-                kda::umma_commit(&sh.u_done);
-            }
-            __syncwarp();
+        float f_reach = 0.0f, f_inner = 0.0f, added = 1.0f;
+        // turn c adds what chunk c - 1 brought, writes its outputs, and begins chunk c
+        for (int c = 0; c <= chunks; ++c) {
+            const unsigned before = count - 1;   // of chunk c - 1
             if (c > 0) {
-                most = largest(s);
-                sh.most[half][r] = most;
+                ok &= wait(sh, &sh.s_done, before & 1, p.err);
+                kda::tc_fence_after();
             }
-            if (half == 0) {
-                float x[16];
+            const float f = power_of_two(ex);
+            const float *decay = c > 0 ? &sh.stage[before % kStages].decay[64 * half] : sh.zeros;
+            most = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                uint32_t u[16], x[16];
+                kda::tmem_ld16(tmem + kColUpdate + 64 * half + 16 * i, u);
+                kda::tmem_ld16(state + 16 * i, x);
+                arrived(u);
+                arrived(x);
+                u64 s[8];
 #pragma unroll
-                for (int t = 0; t < kC; ++t) x[t] = __bfloat162float(st.v[t][r]);
+                for (int n = 0; n < 4; ++n) {
+                    const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(decay + 4 * n);
+                    s[2 * n] = mul_pair(pair_of(x[4 * n], x[4 * n + 1]), d.x);
+                    s[2 * n + 1] = mul_pair(pair_of(x[4 * n + 2], x[4 * n + 3]), d.y);
+                }
+                const u64 factor = pair(added, added);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    // (what lies in tensor memory before the first turn may be anything)
+                    if (c == 0) s[n] = 0ull;
+                    s[n] = fma_pair(pair_of(u[2 * n], u[2 * n + 1]), factor, s[n]);
+                    most = larger(most, s[n]);
+                }
+                store_state(state + 16 * i, halves + 8 * i, s, f);
+                decay += c > 0 ? 16 : 0;
+            }
+            kda::tmem_wait_st();
+            if (c > 0) {   // chunk c - 1 is done with its stage
+                __syncwarp();
+                if (lane == 0) kda::mbar_arrive(&sh.empty[before % kStages]);
+            }
+            uint32_t o[kC / 2];   // outputs of chunk c - 1: from the state, and from the chunk itself
+            if (half == 1 && c > 0) {
+                uint32_t x[16], y[16];
+                kda::tmem_ld16(tmem + kColReach + kC, x);
+                kda::tmem_ld16(tmem + kColInner, y);
+                arrived(x);
+                arrived(y);
+#pragma unroll
+                for (int t = 0; t < kC / 2; ++t) {
+                    const float2 z = both(fma_pair(pair_of(y[2 * t], y[2 * t + 1]),
+                                                   pair(f_inner, f_inner),
+                                                   mul_pair(pair_of(x[2 * t], x[2 * t + 1]),
+                                                            pair(f_reach, f_reach))));
+                    o[t] = kda_cache::pack(z.x, z.y, __nv_bfloat16());
+                }
+            }
+            sh.most[half][r] = most;
+            if (c < chunks) {
+                ok &= wait(sh, &sh.full[count % kStages], (count / kStages) & 1, p.err);
+                kda::tc_fence_before();
+                meet<1>();
+                if (issuer && ok) {
+                    kda::tc_fence_after();
+                    issue_reach(sh.stage[count % kStages], tmem);
+                    kda::umma_commit(&sh.u_done);
+                }
+                __syncwarp();
+                if (half == 1) pass<2>();
+            }
+            if (half == 1 && c > 0) {
+                const int n = ok ? min(kC, w.row.tokens - (c - 1) * kC) : 0;
+                uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) +
+                                ((long long)(w.row.first + (c - 1) * kC) * p.H + w.head) * kD + r;
+                const long long step = (long long)p.H * kD;
+#pragma unroll
+                for (int t = 0; t < kC; ++t, dst += step)
+                    if (t < n) *dst = (uint16_t)(t & 1 ? o[t / 2] >> 16 : o[t / 2]);
+            }
+            if (c == chunks) break;
+            const unsigned stage = count % kStages, parity = count & 1;
+            const Stage &st = sh.stage[stage];
+            if (half == 0) {
+                most = fmaxf(sh.most[0][r], sh.most[1][r]);
+                float vmax = 0.0f;
+#pragma unroll 4
+                for (int t = 0; t < kC; ++t)
+                    vmax = fmaxf(vmax, fabsf(__bfloat162float(st.v[t][r])));
+                // |U| is at most the norm of the row, 11.4 > sqrt(128) times its largest
+                const int ey = 10 - exponent_of(fmaf(11.4f, most, vmax));
+                const float fx = -power_of_two(-ex) / kKeyScale, scale = power_of_two(ey);
                 ok &= wait(sh, &sh.u_done, parity, p.err);
                 kda::tc_fence_after();
-                {
-                    uint32_t u[16], y[16], z[16];
-                    kda::tmem_ld16(tmem + kColReach + kTall * parity, u);
-                    kda::tmem_ld16(tmem + kColReach + kTall * parity + 2 * kC, y);
-                    kda::tmem_ld16(tmem + kColLow, z);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t u[8], y[8], z[8];
+                    load8(tmem + kColReach + 8 * i, u);
+                    load8(tmem + kColReach + 2 * kC + 8 * i, y);
+                    load8(tmem + kColLow + 8 * i, z);
                     arrived(u);
                     arrived(y);
                     arrived(z);
-                    const float f = -power_of_two(-ex) / kKeyScale;
+                    u64 x[4];
 #pragma unroll
-                    for (int t = 0; t < kC; ++t)
-                        x[t] = fmaf(__uint_as_float(u[t]) +
-                                        (__uint_as_float(y[t]) + __uint_as_float(z[t])),
-                                    f, x[t]);
+                    for (int n = 0; n < 4; ++n) {
+                        const int t = 8 * i + 2 * n;
+                        const u64 v = pair(__bfloat162float(st.v[t][r]),
+                                           __bfloat162float(st.v[t + 1][r]));
+                        const u64 sum =
+                            add_pair(pair_of(u[2 * n], u[2 * n + 1]),
+                                     add_pair(pair_of(y[2 * n], y[2 * n + 1]),
+                                              pair_of(z[2 * n], z[2 * n + 1])));
+                        x[n] = fma_pair(sum, pair(fx, fx), v);
+                    }
+                    store_split8(tmem + kColX + 4 * i, x, scale);
                 }
-                float m = 0.0f;
-#pragma unroll
-                for (int t = 0; t < kC; ++t) m = fmaxf(m, fabsf(x[t]));
-                const int ey = 10 - exponent_of(m);
-                store_split16(tmem + kColX, x, power_of_two(ey));
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
                 meet<2>();
@@ -828,84 +902,60 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                     kda::umma_commit(&sh.v_done);
                 }
                 __syncwarp();
-                most = fmaxf(sh.most[0][r], sh.most[1][r]);
                 ok &= wait(sh, &sh.v_done, parity, p.err);
                 kda::tc_fence_after();
-                {
-                    uint32_t u[16];
-                    kda::tmem_ld16(tmem + kColDelta, u);
-                    arrived(u);
-#pragma unroll
-                    for (int t = 0; t < kC; ++t) x[t] = __uint_as_float(u[t]);
-                }
-                store_split16(tmem + kColY, x, 1.0f / kTScale);
                 float sum = 0.0f;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t u[8];
+                    load8(tmem + kColDelta + 8 * i, u);
+                    arrived(u);
+                    u64 x[4];
 #pragma unroll
-                for (int t = 0; t < kC; ++t) sum += fabsf(x[t]);
+                    for (int n = 0; n < 4; ++n) {
+                        x[n] = pair_of(u[2 * n], u[2 * n + 1]);
+                        sum += fabsf(__uint_as_float(u[2 * n])) +
+                               fabsf(__uint_as_float(u[2 * n + 1]));
+                    }
+                    store_split8(tmem + kColY + 4 * i, x, 1.0f / kTScale);
+                }
                 // S is at most what it was and all that is added to it
                 const float back = power_of_two(-ey);
-                sh.info[r] = make_float4(back / kUpdateScale,
-                                         most + sum * back * (1.0f / kTScale),
+                sh.info[r] = make_float4(back / kUpdateScale, most + sum * (back / kTScale),
                                          power_of_two(-ex) * (p.scale / kKeyScale),
                                          back * (p.scale / kBScale));
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
+                meet<3>();
+                if (issuer && ok) {
+                    kda::tc_fence_after();
+                    issue_update(st, tmem);
+                    kda::umma_commit(&sh.s_done);
+                    kda::umma_commit(&sh.empty[stage]);
+                }
+                __syncwarp();
             } else {
-                pass<2>();
-                if (c > 0)
-                    write_outputs(p, tmem, parity ^ 1, f_reach, f_inner, w.row, w.head, c - 1, r,
-                                  ok);
-                kda::tc_fence_before();
+                meet<3>();
             }
-            meet<3>();
-            if (issuer && ok) {
-                kda::tc_fence_after();
-                issue_update(st, tmem, parity);
-                kda::umma_commit(&sh.s_done);
-                kda::umma_commit(&sh.empty[stage]);
-            }
-            __syncwarp();
             const float4 info = sh.info[r];
+            ex = state_exponent(info.y);
+            added = info.x;
             f_reach = info.z;
             f_inner = info.w;
-            ex = state_exponent(info.y);
-            const float f = power_of_two(ex);
-            const u64 added = pair(info.x, info.x);
-            ok &= wait(sh, &sh.s_done, parity, p.err);
-            kda::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t u[16];
-                kda::tmem_ld16(tmem + kColUpdate + 64 * half + 16 * i, u);
-                u64 d[8];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(
-                        &st.decay[64 * half + 16 * i + 4 * n]);
-                    d[2 * n] = x.x;
-                    d[2 * n + 1] = x.y;
-                }
-                arrived(u);
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    s[8 * i + n] = fma_pair(
-                        pair(__uint_as_float(u[2 * n]), __uint_as_float(u[2 * n + 1])), added,
-                        mul_pair(s[8 * i + n], d[n]));
-                if (c + 1 < chunks) store_split(tmem, half, i, s, f);
-            }
-            __syncwarp();
-            if (lane == 0) kda::mbar_arrive(&sh.empty[stage]);
+            ++count;
         }
-        if (half == 1)
-            write_outputs(p, tmem, (count - 1) & 1, f_reach, f_inner, w.row, w.head, chunks - 1, r,
-                          ok);
-        kda::tc_fence_before();
         if (ok) {
             float *dst = p.pool + w.row.to * slot + at;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x[16];
+                kda::tmem_ld16(state + 16 * i, x);
+                arrived(x);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                *reinterpret_cast<ulonglong2 *>(dst + 4 * c) =
-                    make_ulonglong2(s[2 * c], s[2 * c + 1]);
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(dst + 16 * i + 4 * c) =
+                        make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            }
         }
     }
 }
