@@ -21,9 +21,9 @@
 //
 // Layout.  A CTA has one row and head at a time.  S lies in tensor memory, in
 // fp32 and, split, as the A operand of the products.  Eight consumer warps
-// have half a row of it a thread: they add what the chunk brought and split
-// it; four of them make V - U and split V' on the way, the other four write
-// the outputs.  The operands that all rows share (K P, Q P, K P_C / P_t, T, B,
+// have a row of it each two threads: half of its columns, where they add what
+// the chunk brought and split it, and half of the chunk's tokens, of which
+// they make V - U, split V' and write the outputs.  The operands that all rows share (K P, Q P, K P_C / P_t, T, B,
 // P_C) are made by eight producer warps in a ring of stages.  What runs once a
 // chunk is in short loops: straight code of all roles together (80 KB) missed
 // the instruction cache so often that it took twice the time.
@@ -110,8 +110,8 @@ struct __align__(16) Scratch {            // of a pair of producer warps
 struct Shared {
     Stage stage[kStages];
     Scratch scratch[kPairs];
-    float4 info[kD];                      // of a row: see Factors
     float most[2][kD];                    // largest of each half of a row of S
+    float sum[2][kD];                     // of |V'| over half of the tokens, of a row
     float zeros[kD];
     uint64_t full[kStages], empty[kStages];
     uint64_t u_done, v_done, s_done;      // products of a chunk
@@ -626,28 +626,21 @@ template <int kId>
 __device__ __forceinline__ void meet() {
     asm volatile("bar.sync %0, 256;" ::"n"(kId) : "memory");
 }
-template <int kId>
-__device__ __forceinline__ void pass() {   // arrives, does not wait
-    asm volatile("bar.arrive %0, 256;" ::"n"(kId) : "memory");
-}
 
-// 16 channels of a row of S, as they are and as two fp16 numbers each times
-// `scale`, to tensor memory: state and split are the columns of the first.
-__device__ __forceinline__ void store_state(uint32_t state, uint32_t split_to, const u64 (&s)[8],
-                                            float scale) {
+// 16 channels of a row of S, as they are and as two fp16 numbers each, to
+// tensor memory: state and halves are the columns of the first.
+__device__ __forceinline__ void store_state(uint32_t state, uint32_t halves, const u64 (&s)[8]) {
     uint32_t x[16], hi[8], lo[8];
-    const u64 f = pair(scale, scale);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         const float2 y = both(s[c]);
         x[2 * c] = __float_as_uint(y.x);
         x[2 * c + 1] = __float_as_uint(y.y);
-        const float2 z = both(mul_pair(s[c], f));
-        split(z.x, z.y, hi[c], lo[c]);
+        split(y.x, y.y, hi[c], lo[c]);
     }
     kda::tmem_st16(state, x);
-    store8(split_to, hi);
-    store8(split_to + 64, lo);
+    store8(halves, hi);
+    store8(halves + 64, lo);
 }
 
 // 8 values times `scale` as two fp16 numbers each: hi to 4 columns, lo to the
@@ -664,42 +657,48 @@ __device__ __forceinline__ void store_split8(uint32_t to, const u64 (&x)[4], flo
     store4(to + 8, lo);
 }
 
-// The split S is below 2^13 by the bound of its row that is known then.  V - U
-// is below 2^11 by |V| and the norm of the row, and V' = T (V - U) is at most
-// 16 times that, as an entry of T is at most 1.
-__device__ __forceinline__ int state_exponent(float most) { return 12 - exponent_of(most); }
+// S is held times 2^ex, a power of its row.  As held, the bound of the row that
+// is known stays below 2^13, so fp16 has it, and above 2^6, so that its 22
+// bits mean something; else it moves to 2^9.  V - U is below 2^11 by |V| and
+// the norm of the row, and V' = T (V - U) at most 16 times that, as an entry
+// of T is at most 1.
+__device__ __forceinline__ int state_exponent(float bound, int ex) {
+    const int e = exponent_of(bound);
+    return e + ex > 12 || e + ex < 6 ? 9 - e : ex;
+}
 
 // The products of a chunk, by one thread.
 __device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kWide = idesc(kTall, false), kNarrow = idesc(kC, false);
-    const uint32_t at = kda::smem_u32(st.reach[0]);
+    const uint64_t b = kda::sw128_desc(kda::smem_u32(st.reach[0]));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         umma(tmem + kColReach, tmem + kColS + 8 * k,
-             kda::sw128_desc(at + (k >> 2) * kTall * 128 + (k & 3) * 32), kWide, k > 0);
+             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), kWide, k > 0);
     // (columns of their own: products of different shapes are not kept in order)
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         umma(tmem + kColLow, tmem + kColS + 64 + 8 * k,
-             kda::sw128_desc(at + (k >> 2) * kTall * 128 + (k & 3) * 32), kNarrow, k > 0);
+             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), kNarrow, k > 0);
 }
 
 __device__ __forceinline__ void issue_delta(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kNarrow = idesc(kC, false);
-    const uint32_t at = kda::smem_u32(st.inner);
-    umma(tmem + kColDelta, tmem + kColX, kda::sw128_desc(at), kNarrow, false);
-    umma(tmem + kColDelta, tmem + kColX, kda::sw128_desc(at + 32), kNarrow, true);
-    umma(tmem + kColDelta, tmem + kColX + 8, kda::sw128_desc(at), kNarrow, true);
+    const uint64_t b = kda::sw128_desc(kda::smem_u32(st.inner));
+    umma(tmem + kColDelta, tmem + kColX, b, kNarrow, false);
+    umma(tmem + kColDelta, tmem + kColX, b + (32 >> 4), kNarrow, true);
+    umma(tmem + kColDelta, tmem + kColX + 8, b, kNarrow, true);
 }
 
 __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kNarrow = idesc(kC, false), kAll = idesc(kD, true);
-    const uint32_t hi = kda::smem_u32(st.update[0][0]), lo = kda::smem_u32(st.update[1][0]);
-    umma(tmem + kColUpdate, tmem + kColY, along_n(hi, kC * 128), kAll, false);
-    umma(tmem + kColUpdate, tmem + kColY, along_n(lo, kC * 128), kAll, true);
-    umma(tmem + kColUpdate, tmem + kColY + 8, along_n(hi, kC * 128), kAll, true);
+    const uint64_t hi = along_n(kda::smem_u32(st.update[0][0]), kC * 128);
+    const uint64_t lo = along_n(kda::smem_u32(st.update[1][0]), kC * 128);
+    umma(tmem + kColUpdate, tmem + kColY, hi, kAll, false);
+    umma(tmem + kColUpdate, tmem + kColY, lo, kAll, true);
+    umma(tmem + kColUpdate, tmem + kColY + 8, hi, kAll, true);
     umma(tmem + kColInner, tmem + kColY,
-         kda::sw128_desc(kda::smem_u32(st.inner) + 64), kNarrow, false);
+         kda::sw128_desc(kda::smem_u32(st.inner)) + (64 >> 4), kNarrow, false);
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -752,91 +751,111 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
         const long long at = (long long)w.head * kda_delta::kTile + r * kD + 64 * half;
-        // the state, by way of the columns of what is added to it
+        // the state: its size first (it comes from L2 the second time)
+        const float *src = p.pool + max(w.row.from, 0) * slot + at;
         float most = 0.0f;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            uint32_t x[16];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (w.row.from > 0)
-                    y = *reinterpret_cast<const float4 *>(p.pool + w.row.from * slot + at +
-                                                          16 * i + 4 * c);
+        if (w.row.from > 0)
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const float4 y = *reinterpret_cast<const float4 *>(src + 4 * i);
                 most = fmaxf(fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y))),
                              fmaxf(fabsf(y.z), fabsf(y.w)));
-                x[4 * c] = __float_as_uint(y.x);
-                x[4 * c + 1] = __float_as_uint(y.y);
-                x[4 * c + 2] = __float_as_uint(y.z);
-                x[4 * c + 3] = __float_as_uint(y.w);
             }
-            kda::tmem_st16(tmem + kColUpdate + 64 * half + 16 * i, x);
-        }
-        kda::tmem_wait_st();
         sh.most[half][r] = most;
         meet<1>();
-        int ex = state_exponent(fmaxf(sh.most[0][r], sh.most[1][r]));
-        const int chunks = (w.row.tokens + kC - 1) / kC;
-        float f_reach = 0.0f, f_inner = 0.0f, added = 1.0f;
-        // turn c adds what chunk c - 1 brought, writes its outputs, and begins chunk c
-        for (int c = 0; c <= chunks; ++c) {
-            const unsigned before = count - 1;   // of chunk c - 1
-            if (c > 0) {
-                ok &= wait(sh, &sh.s_done, before & 1, p.err);
-                kda::tc_fence_after();
-            }
-            const float f = power_of_two(ex);
-            const float *decay = c > 0 ? &sh.stage[before % kStages].decay[64 * half] : sh.zeros;
-            most = 0.0f;
+        float bound = fmaxf(sh.most[0][r], sh.most[1][r]);   // of the row's values
+        int ex = 9 - exponent_of(bound);
+        {
+            const u64 f = pair(power_of_two(ex), power_of_two(ex));
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
-                uint32_t u[16], x[16];
-                kda::tmem_ld16(tmem + kColUpdate + 64 * half + 16 * i, u);
-                kda::tmem_ld16(state + 16 * i, x);
-                arrived(u);
-                arrived(x);
                 u64 s[8];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(decay + 4 * n);
-                    s[2 * n] = mul_pair(pair_of(x[4 * n], x[4 * n + 1]), d.x);
-                    s[2 * n + 1] = mul_pair(pair_of(x[4 * n + 2], x[4 * n + 3]), d.y);
+                    ulonglong2 y = make_ulonglong2(0ull, 0ull);
+                    if (w.row.from > 0)
+                        y = *reinterpret_cast<const ulonglong2 *>(src + 16 * i + 4 * n);
+                    s[2 * n] = mul_pair(y.x, f);
+                    s[2 * n + 1] = mul_pair(y.y, f);
                 }
-                const u64 factor = pair(added, added);
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    // (what lies in tensor memory before the first turn may be anything)
-                    if (c == 0) s[n] = 0ull;
-                    s[n] = fma_pair(pair_of(u[2 * n], u[2 * n + 1]), factor, s[n]);
-                    most = larger(most, s[n]);
-                }
-                store_state(state + 16 * i, halves + 8 * i, s, f);
-                decay += c > 0 ? 16 : 0;
+                store_state(state + 16 * i, halves + 8 * i, s);
             }
-            kda::tmem_wait_st();
-            if (c > 0) {   // chunk c - 1 is done with its stage
+        }
+        const int chunks = (w.row.tokens + kC - 1) / kC;
+        int step = 0;                               // of ex, due with the next addition
+        float added = 0.0f, f_reach = 0.0f, f_inner = 0.0f;
+        // turn c adds what chunk c - 1 brought, writes its outputs, and begins chunk c
+        for (int c = 0; c <= chunks; ++c) {
+            uint32_t o[4];   // outputs of chunk c - 1: from the state, and from the chunk itself
+            const bool look = (c & 3) == 0 && c > 0;
+            if (c > 0) {
+                const unsigned before = count - 1;
+                ok &= wait(sh, &sh.s_done, before & 1, p.err);
+                kda::tc_fence_after();
+                const float *decay = &sh.stage[before % kStages].decay[64 * half];
+                const u64 factor = pair(added, added);
+                const bool moved = __any_sync(kFull, step != 0);
+                most = 0.0f;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t u[2][16], x[2][16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        kda::tmem_ld16(tmem + kColUpdate + 64 * half + 32 * i + 16 * h, u[h]);
+                        kda::tmem_ld16(state + 32 * i + 16 * h, x[h]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        arrived(u[h]);
+                        arrived(x[h]);
+                        u64 s[8];
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) s[n] = pair_of(x[h][2 * n], x[h][2 * n + 1]);
+                        if (moved) {   // in two powers: a step may be twice as far as one goes
+                            const float g = power_of_two(step / 2);
+                            const float g2 = power_of_two(step - step / 2);
+#pragma unroll
+                            for (int n = 0; n < 8; ++n)
+                                s[n] = mul_pair(mul_pair(s[n], pair(g, g)), pair(g2, g2));
+                        }
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(
+                                decay + 32 * i + 16 * h + 4 * n);
+                            s[2 * n] = fma_pair(pair_of(u[h][4 * n], u[h][4 * n + 1]), factor,
+                                                mul_pair(s[2 * n], d.x));
+                            s[2 * n + 1] = fma_pair(pair_of(u[h][4 * n + 2], u[h][4 * n + 3]),
+                                                    factor, mul_pair(s[2 * n + 1], d.y));
+                        }
+                        if (look)
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) most = larger(most, s[n]);
+                        store_state(state + 32 * i + 16 * h, halves + 16 * i + 8 * h, s);
+                    }
+                }
+                {
+                    uint32_t x[8], y[8];
+                    load8(tmem + kColReach + kC + 8 * half, x);
+                    load8(tmem + kColInner + 8 * half, y);
+                    arrived(x);
+                    arrived(y);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const float2 z = both(fma_pair(pair_of(y[2 * t], y[2 * t + 1]),
+                                                       pair(f_inner, f_inner),
+                                                       mul_pair(pair_of(x[2 * t], x[2 * t + 1]),
+                                                                pair(f_reach, f_reach))));
+                        o[t] = kda_cache::pack(z.x, z.y, __nv_bfloat16());
+                    }
+                }
+                // chunk c - 1 is done with its stage
                 __syncwarp();
                 if (lane == 0) kda::mbar_arrive(&sh.empty[before % kStages]);
             }
-            uint32_t o[kC / 2];   // outputs of chunk c - 1: from the state, and from the chunk itself
-            if (half == 1 && c > 0) {
-                uint32_t x[16], y[16];
-                kda::tmem_ld16(tmem + kColReach + kC, x);
-                kda::tmem_ld16(tmem + kColInner, y);
-                arrived(x);
-                arrived(y);
-#pragma unroll
-                for (int t = 0; t < kC / 2; ++t) {
-                    const float2 z = both(fma_pair(pair_of(y[2 * t], y[2 * t + 1]),
-                                                   pair(f_inner, f_inner),
-                                                   mul_pair(pair_of(x[2 * t], x[2 * t + 1]),
-                                                            pair(f_reach, f_reach))));
-                    o[t] = kda_cache::pack(z.x, z.y, __nv_bfloat16());
-                }
-            }
-            sh.most[half][r] = most;
             if (c < chunks) {
+                if (look) sh.most[half][r] = most * power_of_two(-ex);
                 ok &= wait(sh, &sh.full[count % kStages], (count / kStages) & 1, p.err);
+                kda::tmem_wait_st();
                 kda::tc_fence_before();
                 meet<1>();
                 if (issuer && ok) {
@@ -845,107 +864,101 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
-                if (half == 1) pass<2>();
             }
-            if (half == 1 && c > 0) {
-                const int n = ok ? min(kC, w.row.tokens - (c - 1) * kC) : 0;
+            if (c > 0) {
+                const int n = ok ? w.row.tokens - (c - 1) * kC - 8 * half : 0;
                 uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) +
-                                ((long long)(w.row.first + (c - 1) * kC) * p.H + w.head) * kD + r;
-                const long long step = (long long)p.H * kD;
+                                ((long long)(w.row.first + (c - 1) * kC + 8 * half) * p.H +
+                                 w.head) * kD + r;
+                const long long next = (long long)p.H * kD;
 #pragma unroll
-                for (int t = 0; t < kC; ++t, dst += step)
+                for (int t = 0; t < 8; ++t, dst += next)
                     if (t < n) *dst = (uint16_t)(t & 1 ? o[t / 2] >> 16 : o[t / 2]);
             }
             if (c == chunks) break;
             const unsigned stage = count % kStages, parity = count & 1;
             const Stage &st = sh.stage[stage];
-            if (half == 0) {
-                most = fmaxf(sh.most[0][r], sh.most[1][r]);
-                float vmax = 0.0f;
-#pragma unroll 4
-                for (int t = 0; t < kC; ++t)
-                    vmax = fmaxf(vmax, fabsf(__bfloat162float(st.v[t][r])));
-                // |U| is at most the norm of the row, 11.4 > sqrt(128) times its largest
-                const int ey = 10 - exponent_of(fmaf(11.4f, most, vmax));
-                const float fx = -power_of_two(-ex) / kKeyScale, scale = power_of_two(ey);
-                ok &= wait(sh, &sh.u_done, parity, p.err);
-                kda::tc_fence_after();
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t u[8], y[8], z[8];
-                    load8(tmem + kColReach + 8 * i, u);
-                    load8(tmem + kColReach + 2 * kC + 8 * i, y);
-                    load8(tmem + kColLow + 8 * i, z);
-                    arrived(u);
-                    arrived(y);
-                    arrived(z);
-                    u64 x[4];
+            if (look) bound = fmaxf(sh.most[0][r], sh.most[1][r]);
+            float vmax = 0.0f;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const int t = 8 * i + 2 * n;
-                        const u64 v = pair(__bfloat162float(st.v[t][r]),
-                                           __bfloat162float(st.v[t + 1][r]));
-                        const u64 sum =
-                            add_pair(pair_of(u[2 * n], u[2 * n + 1]),
-                                     add_pair(pair_of(y[2 * n], y[2 * n + 1]),
-                                              pair_of(z[2 * n], z[2 * n + 1])));
-                        x[n] = fma_pair(sum, pair(fx, fx), v);
-                    }
-                    store_split8(tmem + kColX + 4 * i, x, scale);
-                }
-                kda::tmem_wait_st();
-                kda::tc_fence_before();
-                meet<2>();
-                if (issuer && ok) {
-                    kda::tc_fence_after();
-                    issue_delta(st, tmem);
-                    kda::umma_commit(&sh.v_done);
-                }
-                __syncwarp();
-                ok &= wait(sh, &sh.v_done, parity, p.err);
-                kda::tc_fence_after();
-                float sum = 0.0f;
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t u[8];
-                    load8(tmem + kColDelta + 8 * i, u);
-                    arrived(u);
-                    u64 x[4];
+            for (int t = 0; t < kC; ++t) vmax = fmaxf(vmax, fabsf(__bfloat162float(st.v[t][r])));
+            // |U| is at most the norm of the row, 11.4 > sqrt(128) times its largest
+            const int ey = 10 - exponent_of(fmaf(11.4f, bound, vmax));
+            ok &= wait(sh, &sh.u_done, parity, p.err);
+            kda::tc_fence_after();
+            {
+                uint32_t u[8], y[8], z[8];
+                load8(tmem + kColReach + 8 * half, u);
+                load8(tmem + kColReach + 2 * kC + 8 * half, y);
+                load8(tmem + kColLow + 8 * half, z);
+                const float f = -power_of_two(-ex) / kKeyScale;
+                u64 x[4];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        x[n] = pair_of(u[2 * n], u[2 * n + 1]);
-                        sum += fabsf(__uint_as_float(u[2 * n])) +
-                               fabsf(__uint_as_float(u[2 * n + 1]));
-                    }
-                    store_split8(tmem + kColY + 4 * i, x, 1.0f / kTScale);
+                for (int n = 0; n < 4; ++n) {
+                    const int t = 8 * half + 2 * n;
+                    x[n] = pair(__bfloat162float(st.v[t][r]), __bfloat162float(st.v[t + 1][r]));
                 }
-                // S is at most what it was and all that is added to it
-                const float back = power_of_two(-ey);
-                sh.info[r] = make_float4(back / kUpdateScale, most + sum * (back / kTScale),
-                                         power_of_two(-ex) * (p.scale / kKeyScale),
-                                         back * (p.scale / kBScale));
-                kda::tmem_wait_st();
-                kda::tc_fence_before();
-                meet<3>();
-                if (issuer && ok) {
-                    kda::tc_fence_after();
-                    issue_update(st, tmem);
-                    kda::umma_commit(&sh.s_done);
-                    kda::umma_commit(&sh.empty[stage]);
-                }
-                __syncwarp();
-            } else {
-                meet<3>();
+                arrived(u);
+                arrived(y);
+                arrived(z);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    x[n] = fma_pair(add_pair(pair_of(u[2 * n], u[2 * n + 1]),
+                                             add_pair(pair_of(y[2 * n], y[2 * n + 1]),
+                                                      pair_of(z[2 * n], z[2 * n + 1]))),
+                                    pair(f, f), x[n]);
+                store_split8(tmem + kColX + 4 * half, x, power_of_two(ey));
             }
-            const float4 info = sh.info[r];
-            ex = state_exponent(info.y);
-            added = info.x;
-            f_reach = info.z;
-            f_inner = info.w;
+            kda::tmem_wait_st();
+            kda::tc_fence_before();
+            meet<2>();
+            if (issuer && ok) {
+                kda::tc_fence_after();
+                issue_delta(st, tmem);
+                kda::umma_commit(&sh.v_done);
+            }
+            __syncwarp();
+            const float back = power_of_two(-ey);
+            f_reach = power_of_two(-ex) * (p.scale / kKeyScale);
+            f_inner = back * (p.scale / kBScale);
+            ok &= wait(sh, &sh.v_done, parity, p.err);
+            kda::tc_fence_after();
+            {
+                uint32_t u[8];
+                load8(tmem + kColDelta + 8 * half, u);
+                arrived(u);
+                float sum = 0.0f;
+                u64 x[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    x[n] = pair_of(u[2 * n], u[2 * n + 1]);
+                    sum += fabsf(__uint_as_float(u[2 * n])) + fabsf(__uint_as_float(u[2 * n + 1]));
+                }
+                store_split8(tmem + kColY + 4 * half, x, 1.0f / kTScale);
+                sh.sum[half][r] = sum;
+            }
+            kda::tmem_wait_st();
+            kda::tc_fence_before();
+            meet<3>();
+            if (issuer && ok) {
+                kda::tc_fence_after();
+                issue_update(st, tmem);
+                kda::umma_commit(&sh.s_done);
+                kda::umma_commit(&sh.empty[stage]);
+            }
+            __syncwarp();
+            // S is at most what it was and all that is added to it
+            bound = fmaf(sh.sum[0][r] + sh.sum[1][r], back / kTScale, bound);
+            const int moved = state_exponent(bound, ex);
+            step = moved - ex;
+            ex = moved;
+            added = back * power_of_two(ex) / kUpdateScale;
             ++count;
         }
+        kda::tmem_wait_st();
         if (ok) {
             float *dst = p.pool + w.row.to * slot + at;
+            const u64 f = pair(power_of_two(-ex), power_of_two(-ex));
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 uint32_t x[16];
@@ -953,10 +966,12 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                 arrived(x);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4 *>(dst + 16 * i + 4 * c) =
-                        make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                    *reinterpret_cast<ulonglong2 *>(dst + 16 * i + 4 * c) =
+                        make_ulonglong2(mul_pair(pair_of(x[4 * c], x[4 * c + 1]), f),
+                                        mul_pair(pair_of(x[4 * c + 2], x[4 * c + 3]), f));
             }
         }
+        __syncwarp();
     }
 }
 
