@@ -102,7 +102,7 @@ struct __align__(16) Block {
 
 struct __align__(16) Scratch {            // of a pair of producer warps
     Block block[2];
-    float a[kC][kC + 4], b[kC][kC + 4];
+    float a[kC][kC + 4], b[kC][kC + 4], t[kC][kC];
     float beta[kC];
     uint64_t ready[2], taken[2];
 };
@@ -167,22 +167,26 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     lo = half_pair(r.x, r.y);
 }
 
-// Bounded wait of a warp: it gives up, as a whole, after the budget, or when
-// another warp has.
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
-    bool done = kda::mbar_try_wait(bar, parity);
-    if (!done) {
-        const long long t0 = clock64();
-        while (!(done = kda::mbar_try_wait(bar, parity))) {
-            if (*reinterpret_cast<volatile int *>(&sh.gave_up) != 0) break;
-            if (clock64() - t0 > kWaitBudget) {
-                *reinterpret_cast<volatile int *>(&sh.gave_up) = 1;
-                kda_cache::flag(err, KDA_ERR_WAIT_TIMEOUT);
-                break;
-            }
+// The rest of a wait that is not over at once.
+__device__ __noinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+    bool done = false;
+    const long long t0 = clock64();
+    while (!(done = kda::mbar_try_wait(bar, parity))) {
+        if (*reinterpret_cast<volatile int *>(&sh.gave_up) != 0) break;
+        if (clock64() - t0 > kWaitBudget) {
+            *reinterpret_cast<volatile int *>(&sh.gave_up) = 1;
+            kda_cache::flag(err, KDA_ERR_WAIT_TIMEOUT);
+            break;
         }
     }
     return __all_sync(kFull, done);
+}
+
+// Bounded wait of a warp: it gives up, as a whole, after the budget, or when
+// another warp has.
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+    if (__all_sync(kFull, kda::mbar_try_wait(bar, parity))) return true;
+    return wait_on(sh, bar, parity, err);
 }
 
 struct Work {   // one row and head
@@ -256,6 +260,13 @@ __device__ __forceinline__ float squares(u64 a, u64 b) {
     return s.x + s.y;
 }
 
+// 1 / sqrt(sum + 1e-6), as kda::inv_l2 (the sum is never subnormal).
+__device__ __forceinline__ float inverse_norm(float sum) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(sum + 1e-6f));
+    return y;
+}
+
 __device__ __forceinline__ float reciprocal(float x) {   // within 1 ulp
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -296,7 +307,7 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     Raw next = load_raw(p, in, true), later = load_raw(p, in, 1 < valid);
     {   // the values as they are
         const __nv_bfloat16 *src = p.v + first * p.stride_v + at;
-#pragma unroll 4
+#pragma unroll 1
         for (int t = 0; t < kC; ++t, src += p.stride_v) {
             if (t < valid)
                 kda::cp_async8(&st.v[t][4 * lane], src);
@@ -334,7 +345,7 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
             norm += __shfl_xor_sync(kFull, norm, 4);
             norm += __shfl_xor_sync(kFull, norm, 2);
             norm += __shfl_xor_sync(kFull, norm, 1);
-            norm = kda::inv_l2(norm);
+            norm = inverse_norm(norm);
             const float other = __shfl_xor_sync(kFull, norm, 16);
             rk = upper ? other : norm;
             rq = upper ? norm : other;
@@ -493,37 +504,50 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
         __syncwarp();
         if (lane == 0) kda::mbar_arrive(&sc.taken[blocks & 1]);
     }
-    // T, column lane & 15 in a lane: T_t = beta_t (1_t - sum_{j<t} A_tj T_j)
+    // T, column lane & 15 in a lane, four rows at a time over A's in place:
+    // T_t = beta_t (1_t - sum_{j<t} A_tj T_j)
     {
         lane = made_anew(lane);
         const int s = lane & 15;
-        float col[kC];
+#pragma unroll 1
+        for (int t = 0; t < kC; t += 4) {
+            float x[4];
 #pragma unroll
-        for (int t = 0; t < kC; ++t) {
-            float x = t == s ? 1.0f : 0.0f, y = 0.0f;
-            if ((t & 3) == 0) no_further_ahead();
-#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = t + u == s ? 1.0f : 0.0f;
+#pragma unroll 1
             for (int i = 0; i < t; i += 4) {
-                const float4 n = kda::ld4(&sc.a[t][i]);
-                x = fmaf(-n.x, col[i], x);
-                if (i + 1 < t) y = fmaf(-n.y, col[i + 1], y);
-                if (i + 2 < t) x = fmaf(-n.z, col[i + 2], x);
-                if (i + 3 < t) y = fmaf(-n.w, col[i + 3], y);
-            }
-            col[t] = sc.beta[t] * (x + y);
-        }
-        __syncwarp();
-        if (lane < 16)
+                float y[4];
 #pragma unroll
-            for (int t = 0; t < kC; ++t) sc.a[t][s] = col[t] * kTScale;
+                for (int u = 0; u < 4; ++u) y[u] = sc.t[i + u][s];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 n = kda::ld4(&sc.a[t + u][i]);
+                    x[u] = fmaf(-n.x, y[0], x[u]);
+                    x[u] = fmaf(-n.y, y[1], x[u]);
+                    x[u] = fmaf(-n.z, y[2], x[u]);
+                    x[u] = fmaf(-n.w, y[3], x[u]);
+                }
+            }
+            const float4 b = kda::ld4(&sc.beta[t]);
+            const float4 n1 = kda::ld4(&sc.a[t + 1][t]), n2 = kda::ld4(&sc.a[t + 2][t]);
+            const float4 n3 = kda::ld4(&sc.a[t + 3][t]);
+            x[0] *= b.x;
+            x[1] = b.y * fmaf(-n1.x, x[0], x[1]);
+            x[2] = b.z * fmaf(-n2.y, x[1], fmaf(-n2.x, x[0], x[2]));
+            x[3] = b.w * fmaf(-n3.z, x[2], fmaf(-n3.y, x[1], fmaf(-n3.x, x[0], x[3])));
+            // (both half warps have the same)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sc.t[t + u][s] = x[u];
+            __syncwarp();
+        }
     }
     __syncwarp();
     // tokens s = 2 i and 2 i + 1 of row t, hi, lo and B 32 bytes apart
-#pragma unroll
+#pragma unroll 1
     for (int n = 0; n < 4; ++n) {
         const int t = 4 * n + (lane >> 3), i = 2 * (lane & 7);
         uint32_t hi, lo;
-        split(sc.a[t][i], sc.a[t][i + 1], hi, lo);
+        split(sc.t[t][i] * kTScale, sc.t[t][i + 1] * kTScale, hi, lo);
         const float x = i <= t ? sc.b[t][i] * kBScale : 0.0f;
         const float y = i < t ? sc.b[t][i + 1] * kBScale : 0.0f;
         *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = hi;
@@ -561,13 +585,22 @@ __device__ __forceinline__ uint64_t along_n(uint32_t addr, uint32_t block) {
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// D [+]= A B^T of one K step of 16, A from tensor memory.
+// D [+]= A B^T of one K step of 16, A from tensor memory; by one lane.
 __device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
         : "memory");
+}
+
+// One lane of the warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // 16 or 8 columns of the warp's lanes; they are there behind arrived().
@@ -667,19 +700,22 @@ __device__ __forceinline__ int state_exponent(float bound, int ex) {
     return e + ex > 12 || e + ex < 6 ? 9 - e : ex;
 }
 
-// The products of a chunk, by one thread.
+// The products of a chunk, by one warp each.
 __device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem) {
-    constexpr uint32_t kWide = idesc(kTall, false), kNarrow = idesc(kC, false);
     const uint64_t b = kda::sw128_desc(kda::smem_u32(st.reach[0]));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         umma(tmem + kColReach, tmem + kColS + 8 * k,
-             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), kWide, k > 0);
-    // (columns of their own: products of different shapes are not kept in order)
+             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), idesc(kTall, false), k > 0);
+}
+
+// (columns of their own: products of different shapes are not kept in order)
+__device__ __forceinline__ void issue_low(const Stage &st, uint32_t tmem) {
+    const uint64_t b = kda::sw128_desc(kda::smem_u32(st.reach[0]));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         umma(tmem + kColLow, tmem + kColS + 64 + 8 * k,
-             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), kNarrow, k > 0);
+             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), idesc(kC, false), k > 0);
 }
 
 __device__ __forceinline__ void issue_delta(const Stage &st, uint32_t tmem) {
@@ -703,9 +739,9 @@ __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
 
 // ------------------------------------------------------------------ kernel --
 
-// A producer warp: the tokens' vectors (kTokens) or the products between them
-// of every kPairs-th chunk of the CTA's work.
-template <bool kBounded, bool kTokens>
+// A producer warp: the tokens' vectors (the first kPairs) or the products
+// between them of every kPairs-th chunk of the CTA's work.
+template <bool kBounded>
 __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned items, int warp,
                                         int lane) {
     const unsigned pair_of = warp % kPairs;
@@ -721,7 +757,7 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
             Stage &st = sh.stage[stage];
             Scratch &sc = sh.scratch[pair_of];
             bool made;
-            if constexpr (kTokens)
+            if (warp < kPairs)
                 made = produce_tokens<kBounded>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
             else
                 made = produce_products(p, sh, st, sc, w.row, w.head, c, lane, blocks);
@@ -742,7 +778,6 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
     const int half = me >> 2, r = 32 * (me & 3) + lane;   // columns of S, and the row
     const uint32_t tmem = sh.tmem + ((uint32_t)(32 * (me & 3)) << 16);
     const uint32_t state = tmem + kColState + 64 * half, halves = tmem + kColS + 32 * half;
-    const bool issuer = me == 0 && lane == 0;
     bool ok = true;
     unsigned count = 0;
     for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
@@ -858,9 +893,15 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
                 meet<1>();
-                if (issuer && ok) {
+                if (ok && me == 0 && elected()) {
                     kda::tc_fence_after();
-                    issue_reach(sh.stage[count % kStages], tmem);
+                    issue_reach(sh.stage[count % kStages], sh.tmem);
+                    kda::umma_commit(&sh.u_done);
+                }
+                __syncwarp();
+                if (ok && me == 4 && elected()) {
+                    kda::tc_fence_after();
+                    issue_low(sh.stage[count % kStages], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
@@ -912,9 +953,9 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             kda::tmem_wait_st();
             kda::tc_fence_before();
             meet<2>();
-            if (issuer && ok) {
+            if (ok && me == 0 && elected()) {
                 kda::tc_fence_after();
-                issue_delta(st, tmem);
+                issue_delta(st, sh.tmem);
                 kda::umma_commit(&sh.v_done);
             }
             __syncwarp();
@@ -940,9 +981,9 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             kda::tmem_wait_st();
             kda::tc_fence_before();
             meet<3>();
-            if (issuer && ok) {
+            if (ok && me == 0 && elected()) {
                 kda::tc_fence_after();
-                issue_update(st, tmem);
+                issue_update(st, sh.tmem);
                 kda::umma_commit(&sh.s_done);
                 kda::umma_commit(&sh.empty[stage]);
             }
@@ -992,10 +1033,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
             kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
             kda::mbar_init(&sh.scratch[i >> 1].taken[i & 1], 1);
         }
-        kda::mbar_init(&sh.u_done, 1);
+        kda::mbar_init(&sh.u_done, 2);
         kda::mbar_init(&sh.v_done, 1);
         kda::mbar_init(&sh.s_done, 1);
-        kda::mbar_init(&sh.drained, 1);
+        kda::mbar_init(&sh.drained, 2);
         kda::fence_mbar_init();
     }
     if (warp == kProducers) {
@@ -1006,15 +1047,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
     __syncthreads();
     kda::tc_fence_after();
     kda_cache::grid_dependency_wait();
-    if (warp < kPairs)
-        produce<kBounded, true>(p, sh, items, warp, lane);
-    else if (warp < kProducers)
-        produce<kBounded, false>(p, sh, items, warp, lane);
+    if (warp < kProducers)
+        produce<kBounded>(p, sh, items, warp, lane);
     else
         consume(p, sh, items, warp - kProducers, lane);
-    if (threadIdx.x == 32 * kProducers) {
+    if (warp == kProducers || warp == kProducers + 4) {
         // no product may outlive the memory, whatever became of who waited for it
-        kda::umma_commit(&sh.drained);
+        if (elected()) kda::umma_commit(&sh.drained);
         kda::mbar_wait_bounded(&sh.drained, 0, kWaitBudget);
     }
     __syncthreads();
