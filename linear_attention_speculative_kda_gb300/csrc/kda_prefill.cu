@@ -68,7 +68,6 @@ constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
 
 // Powers of two on the operands.
 constexpr float kKeyScale = 1024.0f;      // K P, Q P
-constexpr float kTScale = 1024.0f;        // T
 constexpr float kUpdateScale = 1024.0f;   // K P_C / P_t
 constexpr float kBScale = 1024.0f;        // B
 
@@ -77,13 +76,26 @@ constexpr float kBScale = 1024.0f;        // B
 constexpr int kTall = 3 * kC;             // rows: K P hi, Q P, K P lo
 struct __align__(1024) Stage {
     unsigned char reach[2][kTall * 128];  // [64 channels][row]: channels along K
-    unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token]
-    unsigned char inner[kC * 128];        // [token t]: T_t hi, T_t lo, B_t; 16 tokens s each
+    unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token's place]
+    unsigned char inner[kC * 128];        // [token t]: B_t, 16 fp16; from byte 64 on T_t, 16 fp32
     float decay[kD];                      // P_C
     __nv_bfloat16 v[kC][kD];
     unsigned char pad[512];
 };
 static_assert(sizeof(Stage) % 1024 == 0, "swizzle atoms start on 1024 bytes");
+
+// The tokens along V': those of the consumers' first half, whose T have 0 3 4 7 8
+// 11 12 15 entries before the diagonal's, then those of the other, with 1 2 5
+// 6 9 10 13 14, so that both have the same to do.
+__host__ __device__ constexpr int order_of(int t) {
+    return 2 * (t >> 2) + ((t & 3) >> 1) + (((t + 1) & 2) << 2);
+}
+static_assert(order_of(0) == 0 && order_of(3) == 1 && order_of(4) == 2 && order_of(15) == 7 &&
+                  order_of(1) == 8 && order_of(2) == 9 && order_of(14) == 15,
+              "both halves have eight tokens");
+__device__ __forceinline__ int token_of(int half, int i) {   // its i-th token
+    return 4 * (i >> 1) + ((i & 1) ? 3 - half : half);
+}
 
 // Byte offset of channel c (even, of 64) of row r.
 __device__ __forceinline__ int place(int r, int c) {
@@ -114,7 +126,7 @@ struct Shared {
     float sum[2][kD];                     // of |V'| over half of the tokens, of a row
     float zeros[kD];
     uint64_t full[kStages], empty[kStages];
-    uint64_t u_done, v_done, s_done;      // products of a chunk
+    uint64_t u_done, s_done;              // products of a chunk
     uint64_t drained;
     int gave_up;
     uint32_t tmem;
@@ -127,9 +139,7 @@ constexpr uint32_t kColUpdate = 256;      // V'^T (K P_C / P_t), 128
 constexpr uint32_t kColReach = 384;       // S (K P | Q P | K P lo)^T, 48
 constexpr uint32_t kColLow = 432;         // lo of S with hi of K P, 16
 constexpr uint32_t kColInner = 448;       // B V', 16
-constexpr uint32_t kColX = 464;           // V - U: 8 of hi, 8 of lo
-constexpr uint32_t kColDelta = 480;       // V', 16
-constexpr uint32_t kColY = 496;           // V': 8 of hi, 8 of lo
+constexpr uint32_t kColY = 464;           // V': 8 of hi, 8 of lo
 constexpr uint32_t kTmemColumns = 512;
 
 // D += A B for k steps of 8 in tf32.
@@ -168,7 +178,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
 }
 
 // The rest of a wait that is not over at once.
-__device__ __noinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+__device__ __forceinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
     bool done = false;
     const long long t0 = clock64();
     while (!(done = kda::mbar_try_wait(bar, parity))) {
@@ -221,23 +231,39 @@ __device__ __forceinline__ float exp2_of(float x) { return kda_cache::exp2_fast(
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// log2 of a channel's decay, as kda::decay_factor has it.  x: the gate's input
-// with its bias; gate: -exp(A_log) log2 e; bound: lower_bound log2 e.
-template <bool kBounded>
-__device__ __forceinline__ float log2_decay(float x, float gate, float bound) {
-    if constexpr (kBounded) {
-        return __fdividef(bound, 1.0f + exp2_of(gate * x));
-    } else {
-        // softplus(x) = max(x, 0) + log1p(z), z = exp(-|x|); log1p(z) = z P(z)
-        // with the polynomial of kda::softplus
-        constexpr float c[10] = {0x1p+0f,        -0x1.ffffcp-2f,  0x1.554c9cp-2f, -0x1.ff11c2p-3f,
-                                 0x1.930202p-3f, -0x1.399642p-3f, 0x1.b2c2a2p-4f, -0x1.d3784ep-5f,
-                                 0x1.4628bp-6f,  -0x1.aad1eep-9f};
-        const float z = exp2_of(-fabsf(x) * kLog2e);
-        float r = c[9];
+// The polynomial of kda::softplus, log1p(z) = z P(z), as pairs of fp32.
+struct Poly {
+    u64 c[10];
+};
+__device__ __forceinline__ Poly softplus_poly() {
+    constexpr float c[10] = {0x1p+0f,        -0x1.ffffcp-2f,  0x1.554c9cp-2f, -0x1.ff11c2p-3f,
+                             0x1.930202p-3f, -0x1.399642p-3f, 0x1.b2c2a2p-4f, -0x1.d3784ep-5f,
+                             0x1.4628bp-6f,  -0x1.aad1eep-9f};
+    Poly p;
 #pragma unroll
-        for (int i = 8; i >= 0; --i) r = fmaf(r, z, c[i]);
-        return gate * fmaf(z, r, fmaxf(x, 0.0f));
+    for (int i = 0; i < 10; ++i) {
+        p.c[i] = pair(c[i], c[i]);
+        asm volatile("" : "+l"(p.c[i]));   // in registers, not made anew at each use
+    }
+    return p;
+}
+
+// log2 of two channels' decays, as kda::decay_factor has them.  x: the gate's
+// inputs with their bias; gate: -exp(A_log) log2 e; bound: lower_bound log2 e.
+template <bool kBounded>
+__device__ __forceinline__ u64 log2_decays(u64 x, float gate, float bound, const Poly &poly) {
+    if constexpr (kBounded) {
+        const float2 y = both(mul_pair(x, pair(gate, gate)));
+        return pair(__fdividef(bound, 1.0f + exp2_of(y.x)), __fdividef(bound, 1.0f + exp2_of(y.y)));
+    } else {
+        // softplus(x) = max(x, 0) + log1p(z), z = exp(-|x|)
+        const float2 v = both(x);
+        const u64 z = pair(exp2_of(-fabsf(v.x) * kLog2e), exp2_of(-fabsf(v.y) * kLog2e));
+        u64 r = poly.c[9];
+#pragma unroll
+        for (int i = 8; i >= 0; --i) r = fma_pair(r, z, poly.c[i]);
+        const u64 sp = fma_pair(z, r, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+        return mul_pair(sp, pair(gate, gate));
     }
 }
 
@@ -317,85 +343,99 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     }
     kda::cp_async_commit();
     const float gate = -__expf(p.A_log[head]) * kLog2e, bound = p.lower_bound * kLog2e;
-    const float4 bias = kda::ld4(p.g_bias + at);
+    const ulonglong2 biases = *reinterpret_cast<const ulonglong2 *>(p.g_bias + at);
+    const u64 bias[2] = {biases.x, biases.y};
+    Poly poly;
+    if constexpr (!kBounded) poly = softplus_poly();
     u64 reach[2] = {pair(kKeyScale, kKeyScale), pair(kKeyScale, kKeyScale)};   // P_t
     u64 total[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};                       // log2 P_t
     u64 r[2] = {pair(1.0f, 1.0f), pair(1.0f, 1.0f)};                            // R
     unsigned char *reached = st.reach[lane >> 4];
-    // a token a turn, the next two on their way
+    // two tokens a turn, the next two on their way
 #pragma unroll 1
-    for (int t = 0; t < kC; ++t) {
-        const Raw now = next;
-        next = later;
-        later = load_raw(p, in, t + 2 < valid);
+    for (int t0 = 0; t0 < kC; t0 += 2) {
+        const Raw now[2] = {next, later};
+        next = load_raw(p, in, t0 + 2 < valid);
+        later = load_raw(p, in, t0 + 3 < valid);
         Block &out = sc.block[blocks & 1];
-        if ((t & 3) == 0 && !wait(sh, &sc.taken[blocks & 1], ((blocks >> 1) & 1) ^ 1, p.err)) {
+        if ((t0 & 2) == 0 && !wait(sh, &sc.taken[blocks & 1], ((blocks >> 1) & 1) ^ 1, p.err)) {
             kda::cp_async_wait_all();
             return false;
         }
-        u64 k[2], q[2];
-        pairs_of(now.k, k[0], k[1]);
-        pairs_of(now.q, q[0], q[1]);
-        float rk, rq;
-        {   // norms: of k in the lower lanes, of q in the upper ones
-            const float sk = squares(k[0], k[1]), sq = squares(q[0], q[1]);
-            const bool upper = (lane & 16) != 0;
-            float norm = (upper ? sq : sk) + __shfl_xor_sync(kFull, upper ? sk : sq, 16);
-            norm += __shfl_xor_sync(kFull, norm, 8);
+        u64 k[2][2], q[2][2];
+        float norm;   // lane bits 4 and 3 choose the token, and k or q
+        {
+            float s[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                pairs_of(now[u].k, k[u][0], k[u][1]);
+                pairs_of(now[u].q, q[u][0], q[u][1]);
+                s[2 * u] = squares(k[u][0], k[u][1]);
+                s[2 * u + 1] = squares(q[u][0], q[u][1]);
+            }
+            const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0;
+            s[0] = (b4 ? s[2] : s[0]) + __shfl_xor_sync(kFull, b4 ? s[0] : s[2], 16);
+            s[1] = (b4 ? s[3] : s[1]) + __shfl_xor_sync(kFull, b4 ? s[1] : s[3], 16);
+            norm = (b3 ? s[1] : s[0]) + __shfl_xor_sync(kFull, b3 ? s[0] : s[1], 8);
             norm += __shfl_xor_sync(kFull, norm, 4);
             norm += __shfl_xor_sync(kFull, norm, 2);
             norm += __shfl_xor_sync(kFull, norm, 1);
             norm = inverse_norm(norm);
-            const float other = __shfl_xor_sync(kFull, norm, 16);
-            rk = upper ? other : norm;
-            rq = upper ? norm : other;
         }
-        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // behind the row's end nothing decays
-        if (t < valid) {
-            const float4 x = kda::bf16x4_to_float4(now.g);
-            y[0] = log2_decay<kBounded>(x.x + bias.x, gate, bound);
-            y[1] = log2_decay<kBounded>(x.y + bias.y, gate, bound);
-            y[2] = log2_decay<kBounded>(x.z + bias.z, gate, bound);
-            y[3] = log2_decay<kBounded>(x.w + bias.w, gate, bound);
-        }
-        total[0] = add_pair(total[0], pair(y[0], y[1]));
-        total[1] = add_pair(total[1], pair(y[2], y[3]));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = exp2_of(y[c]);
-        const u64 e[2] = {pair(y[0], y[1]), pair(y[2], y[3])};
+        for (int u = 0; u < 2; ++u) {
+            const int t = t0 + u;
+            u64 y[2] = {0ull, 0ull};   // behind the row's end nothing decays
+            if (t < valid) {
+                u64 x[2];
+                pairs_of(now[u].g, x[0], x[1]);
+                y[0] = log2_decays<kBounded>(add_pair(x[0], bias[0]), gate, bound, poly);
+                y[1] = log2_decays<kBounded>(add_pair(x[1], bias[1]), gate, bound, poly);
+            }
+            total[0] = add_pair(total[0], y[0]);
+            total[1] = add_pair(total[1], y[1]);
+            const float2 e0 = both(y[0]), e1 = both(y[1]);
+            const float e[4] = {exp2_of(e0.x), exp2_of(e0.y), exp2_of(e1.x), exp2_of(e1.y)};
+            reach[0] = mul_pair(reach[0], pair(e[0], e[1]));
+            reach[1] = mul_pair(reach[1], pair(e[2], e[3]));
+            const float nk = __shfl_sync(kFull, norm, 16 * u);
+            const float nq = __shfl_sync(kFull, norm, 16 * u + 8);
+            const u64 rk = pair(nk, nk), rq = pair(nq, nq);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            reach[i] = mul_pair(reach[i], e[i]);
-            k[i] = mul_pair(k[i], pair(rk, rk));
-            q[i] = mul_pair(q[i], pair(rq, rq));
+            for (int i = 0; i < 2; ++i) {
+                k[u][i] = mul_pair(k[u][i], rk);
+                q[u][i] = mul_pair(q[u][i], rq);
+            }
+            if (u == 0 && (t0 & 2) == 0) {   // a block's first token
+                put(&out.since[4 * lane], mul_pair(r[0], pair(e[0], e[1])),
+                    mul_pair(r[1], pair(e[2], e[3])));
+                r[0] = r[1] = pair(1.0f, 1.0f);
+            } else {
+                r[0] = mul_pair(r[0], pair(fmaxf(e[0], 0x1p-40f), fmaxf(e[1], 0x1p-40f)));
+                r[1] = mul_pair(r[1], pair(fmaxf(e[2], 0x1p-40f), fmaxf(e[3], 0x1p-40f)));
+            }
+            float *ahead = &out.ahead[t & 3][4 * lane];
+            put(ahead, mul_pair(k[u][0], r[0]), mul_pair(k[u][1], r[1]));
+            put(ahead + 4 * kRow, mul_pair(q[u][0], r[0]), mul_pair(q[u][1], r[1]));
+            const float2 r0 = both(r[0]), r1 = both(r[1]);
+            put(&out.back[t & 3][4 * lane],
+                mul_pair(k[u][0], pair(reciprocal(r0.x), reciprocal(r0.y))),
+                mul_pair(k[u][1], pair(reciprocal(r1.x), reciprocal(r1.y))));
+            const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
+            uint2 hi, lo;
+            float2 x = both(mul_pair(k[u][0], reach[0]));
+            split(x.x, x.y, hi.x, lo.x);
+            x = both(mul_pair(k[u][1], reach[1]));
+            split(x.x, x.y, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(reached + to) = hi;
+            *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
+            x = both(mul_pair(q[u][0], reach[0]));
+            hi.x = half_pair(x.x, x.y);
+            x = both(mul_pair(q[u][1], reach[1]));
+            hi.y = half_pair(x.x, x.y);
+            *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
         }
-        if ((t & 3) == 0) {   // a block's first token
-            put(&out.since[4 * lane], mul_pair(r[0], e[0]), mul_pair(r[1], e[1]));
-            r[0] = r[1] = pair(1.0f, 1.0f);
-        } else {
-            r[0] = mul_pair(r[0], pair(fmaxf(y[0], 0x1p-40f), fmaxf(y[1], 0x1p-40f)));
-            r[1] = mul_pair(r[1], pair(fmaxf(y[2], 0x1p-40f), fmaxf(y[3], 0x1p-40f)));
-        }
-        float *ahead = &out.ahead[t & 3][4 * lane];
-        put(ahead, mul_pair(k[0], r[0]), mul_pair(k[1], r[1]));
-        put(ahead + 4 * kRow, mul_pair(q[0], r[0]), mul_pair(q[1], r[1]));
-        const float2 r0 = both(r[0]), r1 = both(r[1]);
-        put(&out.back[t & 3][4 * lane], mul_pair(k[0], pair(reciprocal(r0.x), reciprocal(r0.y))),
-            mul_pair(k[1], pair(reciprocal(r1.x), reciprocal(r1.y))));
-        const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
-        uint2 hi, lo;
-        float2 x = both(mul_pair(k[0], reach[0]));
-        split(x.x, x.y, hi.x, lo.x);
-        x = both(mul_pair(k[1], reach[1]));
-        split(x.x, x.y, hi.y, lo.y);
-        *reinterpret_cast<uint2 *>(reached + to) = hi;
-        *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
-        x = both(mul_pair(q[0], reach[0]));
-        hi.x = half_pair(x.x, x.y);
-        x = both(mul_pair(q[1], reach[1]));
-        hi.y = half_pair(x.x, x.y);
-        *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
-        if ((t & 3) == 3) {
+        if ((t0 & 2) != 0) {
             put(&out.end[4 * lane], r[0], r[1]);
             __syncwarp();
             if (lane == 0) kda::mbar_arrive(&sc.ready[blocks & 1]);
@@ -495,7 +535,7 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
                     uint2 hi, lo;
                     split(y.x, y.y, hi.x, lo.x);
                     split(z.x, z.y, hi.y, lo.y);
-                    const int to = place(g, 16 * (m & 3) + 4 * j) + i * 8 * 128;
+                    const int to = place(order_of(g + 8 * i), 16 * (m & 3) + 4 * j);
                     *reinterpret_cast<uint2 *>(st.update[0][m >> 2] + to) = hi;
                     *reinterpret_cast<uint2 *>(st.update[1][m >> 2] + to) = lo;
                 }
@@ -504,7 +544,7 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
         __syncwarp();
         if (lane == 0) kda::mbar_arrive(&sc.taken[blocks & 1]);
     }
-    // T, column lane & 15 in a lane, four rows at a time over A's in place:
+    // T, column lane & 15 in a lane, four rows at a time:
     // T_t = beta_t (1_t - sum_{j<t} A_tj T_j)
     {
         lane = made_anew(lane);
@@ -542,17 +582,16 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
         }
     }
     __syncwarp();
-    // tokens s = 2 i and 2 i + 1 of row t, hi, lo and B 32 bytes apart
+    // T as it is, B where V' has its tokens
 #pragma unroll 1
     for (int n = 0; n < 4; ++n) {
         const int t = 4 * n + (lane >> 3), i = 2 * (lane & 7);
-        uint32_t hi, lo;
-        split(sc.t[t][i] * kTScale, sc.t[t][i + 1] * kTScale, hi, lo);
-        const float x = i <= t ? sc.b[t][i] * kBScale : 0.0f;
-        const float y = i < t ? sc.b[t][i + 1] * kBScale : 0.0f;
-        *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = hi;
-        *reinterpret_cast<uint32_t *>(st.inner + place(t, kC + i)) = lo;
-        *reinterpret_cast<uint32_t *>(st.inner + place(t, 2 * kC + i)) = half_pair(x, y);
+        *reinterpret_cast<float2 *>(st.inner + place(t, 32 + 2 * i)) =
+            *reinterpret_cast<const float2 *>(&sc.t[t][i]);
+        const int s0 = token_of(i >> 3, i & 7), s1 = token_of(i >> 3, (i & 7) + 1);
+        const float x = s0 <= t ? sc.b[t][s0] * kBScale : 0.0f;
+        const float y = s1 <= t ? sc.b[t][s1] * kBScale : 0.0f;
+        *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = half_pair(x, y);
     }
     __syncwarp();
     return true;
@@ -692,9 +731,8 @@ __device__ __forceinline__ void store_split8(uint32_t to, const u64 (&x)[4], flo
 
 // S is held times 2^ex, a power of its row.  As held, the bound of the row that
 // is known stays below 2^13, so fp16 has it, and above 2^6, so that its 22
-// bits mean something; else it moves to 2^9.  V - U is below 2^11 by |V| and
-// the norm of the row, and V' = T (V - U) at most 16 times that, as an entry
-// of T is at most 1.
+// bits mean something; else it moves to 2^9.  An entry of V' is at most |v| and
+// the norm of the row of S before its token, which grows by at most |v| a token.
 __device__ __forceinline__ int state_exponent(float bound, int ex) {
     const int e = exponent_of(bound);
     return e + ex > 12 || e + ex < 6 ? 9 - e : ex;
@@ -718,14 +756,6 @@ __device__ __forceinline__ void issue_low(const Stage &st, uint32_t tmem) {
              b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), idesc(kC, false), k > 0);
 }
 
-__device__ __forceinline__ void issue_delta(const Stage &st, uint32_t tmem) {
-    constexpr uint32_t kNarrow = idesc(kC, false);
-    const uint64_t b = kda::sw128_desc(kda::smem_u32(st.inner));
-    umma(tmem + kColDelta, tmem + kColX, b, kNarrow, false);
-    umma(tmem + kColDelta, tmem + kColX, b + (32 >> 4), kNarrow, true);
-    umma(tmem + kColDelta, tmem + kColX + 8, b, kNarrow, true);
-}
-
 __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
     constexpr uint32_t kNarrow = idesc(kC, false), kAll = idesc(kD, true);
     const uint64_t hi = along_n(kda::smem_u32(st.update[0][0]), kC * 128);
@@ -734,7 +764,7 @@ __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
     umma(tmem + kColUpdate, tmem + kColY, lo, kAll, true);
     umma(tmem + kColUpdate, tmem + kColY + 8, hi, kAll, true);
     umma(tmem + kColInner, tmem + kColY,
-         kda::sw128_desc(kda::smem_u32(st.inner)) + (64 >> 4), kNarrow, false);
+         kda::sw128_desc(kda::smem_u32(st.inner)), kNarrow, false);
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -786,34 +816,32 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
         const long long at = (long long)w.head * kda_delta::kTile + r * kD + 64 * half;
-        // the state: its size first (it comes from L2 the second time)
-        const float *src = p.pool + max(w.row.from, 0) * slot + at;
-        float most = 0.0f;
-        if (w.row.from > 0)
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const float4 y = *reinterpret_cast<const float4 *>(src + 4 * i);
-                most = fmaxf(fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y))),
-                             fmaxf(fabsf(y.z), fabsf(y.w)));
-            }
-        sh.most[half][r] = most;
-        meet<1>();
-        float bound = fmaxf(sh.most[0][r], sh.most[1][r]);   // of the row's values
-        int ex = 9 - exponent_of(bound);
+        float bound;   // of the row's values
+        int ex;
         {
-            const u64 f = pair(power_of_two(ex), power_of_two(ex));
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                u64 s[8];
+            const float *src = p.pool + max(w.row.from, 0) * slot + at;
+            u64 s[32];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    ulonglong2 y = make_ulonglong2(0ull, 0ull);
-                    if (w.row.from > 0)
-                        y = *reinterpret_cast<const ulonglong2 *>(src + 16 * i + 4 * n);
-                    s[2 * n] = mul_pair(y.x, f);
-                    s[2 * n + 1] = mul_pair(y.y, f);
-                }
-                store_state(state + 16 * i, halves + 8 * i, s);
+            for (int i = 0; i < 16; ++i) {
+                ulonglong2 y = make_ulonglong2(0ull, 0ull);
+                if (w.row.from > 0) y = *reinterpret_cast<const ulonglong2 *>(src + 4 * i);
+                s[2 * i] = y.x;
+                s[2 * i + 1] = y.y;
+            }
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) most = larger(most, s[i]);
+            sh.most[half][r] = most;
+            meet<1>();
+            bound = fmaxf(sh.most[0][r], sh.most[1][r]);
+            ex = 9 - exponent_of(bound);
+            const u64 f = pair(power_of_two(ex), power_of_two(ex));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u64 y[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) y[n] = mul_pair(s[8 * i + n], f);
+                store_state(state + 16 * i, halves + 8 * i, y);
             }
         }
         const int chunks = (w.row.tokens + kC - 1) / kC;
@@ -823,6 +851,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
         for (int c = 0; c <= chunks; ++c) {
             uint32_t o[4];   // outputs of chunk c - 1: from the state, and from the chunk itself
             const bool look = (c & 3) == 0 && c > 0;
+            float most = 0.0f;
             if (c > 0) {
                 const unsigned before = count - 1;
                 ok &= wait(sh, &sh.s_done, before & 1, p.err);
@@ -830,7 +859,6 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                 const float *decay = &sh.stage[before % kStages].decay[64 * half];
                 const u64 factor = pair(added, added);
                 const bool moved = __any_sync(kFull, step != 0);
-                most = 0.0f;
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     uint32_t u[2][16], x[2][16];
@@ -920,67 +948,66 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             const unsigned stage = count % kStages, parity = count & 1;
             const Stage &st = sh.stage[stage];
             if (look) bound = fmaxf(sh.most[0][r], sh.most[1][r]);
+            u64 x[kC / 2];
             float vmax = 0.0f;
 #pragma unroll
-            for (int t = 0; t < kC; ++t) vmax = fmaxf(vmax, fabsf(__bfloat162float(st.v[t][r])));
-            // |U| is at most the norm of the row, 11.4 > sqrt(128) times its largest
-            const int ey = 10 - exponent_of(fmaf(11.4f, bound, vmax));
+            for (int n = 0; n < kC / 2; ++n) {
+                x[n] = pair(__bfloat162float(st.v[2 * n][r]), __bfloat162float(st.v[2 * n + 1][r]));
+                vmax = larger(vmax, x[n]);
+            }
+            // (11.4 > sqrt(128))
+            const int ey = 10 - exponent_of(fmaf(11.4f, bound, 16.0f * vmax));
+            const float fx = -power_of_two(-ex) / kKeyScale;
             ok &= wait(sh, &sh.u_done, parity, p.err);
             kda::tc_fence_after();
             {
-                uint32_t u[8], y[8], z[8];
-                load8(tmem + kColReach + 8 * half, u);
-                load8(tmem + kColReach + 2 * kC + 8 * half, y);
-                load8(tmem + kColLow + 8 * half, z);
-                const float f = -power_of_two(-ex) / kKeyScale;
-                u64 x[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int t = 8 * half + 2 * n;
-                    x[n] = pair(__bfloat162float(st.v[t][r]), __bfloat162float(st.v[t + 1][r]));
-                }
+                uint32_t u[16], y[16], z[16];
+                kda::tmem_ld16(tmem + kColReach, u);
+                kda::tmem_ld16(tmem + kColReach + 2 * kC, y);
+                kda::tmem_ld16(tmem + kColLow, z);
                 arrived(u);
                 arrived(y);
                 arrived(z);
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < kC / 2; ++n)
                     x[n] = fma_pair(add_pair(pair_of(u[2 * n], u[2 * n + 1]),
                                              add_pair(pair_of(y[2 * n], y[2 * n + 1]),
                                                       pair_of(z[2 * n], z[2 * n + 1]))),
-                                    pair(f, f), x[n]);
-                store_split8(tmem + kColX + 4 * half, x, power_of_two(ey));
+                                    pair(fx, fx), x[n]);
             }
-            kda::tmem_wait_st();
-            kda::tc_fence_before();
-            meet<2>();
-            if (ok && me == 0 && elected()) {
-                kda::tc_fence_after();
-                issue_delta(st, sh.tmem);
-                kda::umma_commit(&sh.v_done);
+            {
+                float d[8];   // V' of this half's tokens
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned char *t = st.inner + token_of(half, i) * 128;
+                    const int turn = token_of(half, i) & 7;
+                    u64 sum = 0ull;
+#pragma unroll
+                    for (int n = 0; n <= i >> 1; ++n) {   // four entries each
+                        const ulonglong2 f =
+                            *reinterpret_cast<const ulonglong2 *>(t + (((4 + n) ^ turn) << 4));
+                        sum = n == 0 ? mul_pair(f.x, x[0]) : fma_pair(f.x, x[2 * n], sum);
+                        sum = fma_pair(f.y, x[2 * n + 1], sum);
+                    }
+                    const float2 y = both(sum);
+                    d[i] = y.x + y.y;
+                }
+                float sum = 0.0f;
+                u64 y[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    sum += fabsf(d[2 * n]) + fabsf(d[2 * n + 1]);
+                    y[n] = pair(d[2 * n], d[2 * n + 1]);
+                }
+                store_split8(tmem + kColY + 4 * half, y, power_of_two(ey));
+                sh.sum[half][r] = sum;
             }
-            __syncwarp();
             const float back = power_of_two(-ey);
             f_reach = power_of_two(-ex) * (p.scale / kKeyScale);
             f_inner = back * (p.scale / kBScale);
-            ok &= wait(sh, &sh.v_done, parity, p.err);
-            kda::tc_fence_after();
-            {
-                uint32_t u[8];
-                load8(tmem + kColDelta + 8 * half, u);
-                arrived(u);
-                float sum = 0.0f;
-                u64 x[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    x[n] = pair_of(u[2 * n], u[2 * n + 1]);
-                    sum += fabsf(__uint_as_float(u[2 * n])) + fabsf(__uint_as_float(u[2 * n + 1]));
-                }
-                store_split8(tmem + kColY + 4 * half, x, 1.0f / kTScale);
-                sh.sum[half][r] = sum;
-            }
             kda::tmem_wait_st();
             kda::tc_fence_before();
-            meet<3>();
+            meet<2>();
             if (ok && me == 0 && elected()) {
                 kda::tc_fence_after();
                 issue_update(st, sh.tmem);
@@ -989,7 +1016,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             }
             __syncwarp();
             // S is at most what it was and all that is added to it
-            bound = fmaf(sh.sum[0][r] + sh.sum[1][r], back / kTScale, bound);
+            bound += sh.sum[0][r] + sh.sum[1][r];
             const int moved = state_exponent(bound, ex);
             step = moved - ex;
             ex = moved;
@@ -1034,7 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
             kda::mbar_init(&sh.scratch[i >> 1].taken[i & 1], 1);
         }
         kda::mbar_init(&sh.u_done, 2);
-        kda::mbar_init(&sh.v_done, 1);
         kda::mbar_init(&sh.s_done, 1);
         kda::mbar_init(&sh.drained, 2);
         kda::fence_mbar_init();
