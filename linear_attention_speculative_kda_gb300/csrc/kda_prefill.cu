@@ -178,7 +178,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
 }
 
 // The rest of a wait that is not over at once.
-__device__ __forceinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+__device__ __noinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
     bool done = false;
     const long long t0 = clock64();
     while (!(done = kda::mbar_try_wait(bar, parity))) {
@@ -1045,9 +1045,8 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
 
 template <bool kBounded>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, unsigned items) {
-    extern __shared__ unsigned char raw_smem[];
-    Shared &sh = *reinterpret_cast<Shared *>(
-        (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f;
     if (threadIdx.x == 0) {
@@ -1111,7 +1110,7 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     const int sms = kda_cache::sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     if (tiles > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
-    const int smem = (int)sizeof(Shared) + 1024;
+    const int smem = (int)sizeof(Shared);
     void (*kernel)(const Params, unsigned) = p.bounded ? prefill_kernel<true> : prefill_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
