@@ -497,21 +497,26 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
             no_further_ahead();
             const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&in.since[c]);
             const ulonglong2 k0 = *reinterpret_cast<const ulonglong2 *>(&back0[c]);
-            const ulonglong2 k1 = *reinterpret_cast<const ulonglong2 *>(&back1[c]);
             const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(&in.ahead[g][c]);
             w[0][2 * m] = fma_pair(w[0][2 * m], f.x, k0.x);
             w[0][2 * m + 1] = fma_pair(w[0][2 * m + 1], f.y, k0.y);
-            w[1][2 * m] = fma_pair(w[1][2 * m], f.x, k1.x);
-            w[1][2 * m + 1] = fma_pair(w[1][2 * m + 1], f.y, k1.y);
+            uint32_t hi[2][4] = {}, lo[2][4] = {};
+            if (block >= 2) {   // tokens 8..15 come in here
+                const ulonglong2 k1 = *reinterpret_cast<const ulonglong2 *>(&back1[c]);
+                w[1][2 * m] = fma_pair(w[1][2 * m], f.x, k1.x);
+                w[1][2 * m + 1] = fma_pair(w[1][2 * m + 1], f.y, k1.y);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    split_tf32(w[1][2 * m + h], hi[h][1], hi[h][3], lo[h][1], lo[h][3]);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t hi[4], lo[4], b[2], bl[2];
+                uint32_t b[2], bl[2];
                 split_tf32(h ? n.y : n.x, b[0], b[1], bl[0], bl[1]);
-                split_tf32(w[0][2 * m + h], hi[0], hi[2], lo[0], lo[2]);
-                split_tf32(w[1][2 * m + h], hi[1], hi[3], lo[1], lo[3]);
-                mma_tf32(d[0], hi, b[0], b[1]);
-                mma_tf32(d[1], hi, bl[0], bl[1]);
-                mma_tf32(d[1], lo, b[0], b[1]);
+                split_tf32(w[0][2 * m + h], hi[h][0], hi[h][2], lo[h][0], lo[h][2]);
+                mma_tf32(d[0], hi[h], b[0], b[1]);
+                mma_tf32(d[1], hi[h], bl[0], bl[1]);
+                mma_tf32(d[1], lo[h], b[0], b[1]);
             }
         }
 #pragma unroll
@@ -780,6 +785,12 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
         int bits = 0;
         const Work w = work_at(p, item, bits);
         if (bits != 0 && w.head == 0 && threadIdx.x == 0) kda_cache::flag(p.err, bits);
+        if (warp == 0 && lane == 0 && w.row.tokens > 0 && w.row.from > 0)
+            // the state is on its way to L2 before a consumer asks for it
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             p.pool + ((long long)w.row.from * p.H + w.head) * kda_delta::kTile),
+                         "r"(kda_delta::kTile * 4)
+                         : "memory");
         const unsigned chunks = (unsigned)(w.row.tokens + kC - 1) / kC;
         for (unsigned c = (pair_of - count) % kPairs; c < chunks; c += kPairs) {
             const unsigned stage = (count + c) % kStages, turn = (count + c) / kStages;
@@ -1012,7 +1023,6 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                 kda::tc_fence_after();
                 issue_update(st, sh.tmem);
                 kda::umma_commit(&sh.s_done);
-                kda::umma_commit(&sh.empty[stage]);
             }
             __syncwarp();
             // S is at most what it was and all that is added to it
@@ -1053,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
         sh.gave_up = 0;
         for (int i = 0; i < kStages; ++i) {
             kda::mbar_init(&sh.full[i], 2);
-            kda::mbar_init(&sh.empty[i], kConsumers + 1);
+            kda::mbar_init(&sh.empty[i], kConsumers);
         }
         for (int i = 0; i < 2 * kPairs; ++i) {
             kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
