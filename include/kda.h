@@ -514,8 +514,8 @@ kda_status kda_kv_append(const kda_cache_config *cfg, const void *q, const void 
  * keys: every query and key head x of D channels becomes
  *   y = x * weight / sqrt(sum x^2 / D + eps)
  * in fp32 before its rotation, and is rounded once, behind it.  q_weight and
- * k_weight: [D] of the cache's type or fp32 (weight_dtype), or NULL (ones);
- * eps >= 0.  A model that stores weight - 1 adds the 1 before the call.  The
+ * k_weight: [D] of the cache's type or fp32 (weight_dtype), 16-byte aligned, or
+ * NULL (ones); eps >= 0.  A model that stores weight - 1 adds the 1 before the call.  The
  * sum of squares is fp32: it overflows for elements above some 1e18, whose
  * head is then 0.  All else as for kda_kv_append.
  */

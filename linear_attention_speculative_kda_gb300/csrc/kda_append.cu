@@ -119,10 +119,28 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *turn, b
     b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// The same behind the norm of the head: wa and wb are the chunks' weights,
-// kUnits lanes beside each other hold the head (all of them get here).
+// Element i of a weight as fp32.
+__device__ __forceinline__ float weight_at(const void *w, int dtype, int i) {
+    if (w == nullptr) return 1.0f;
+    if (dtype == KDA_DTYPE_FP32) return static_cast<const float *>(w)[i];
+    return dtype == KDA_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i])
+                                   : __half2float(static_cast<const __half *>(w)[i]);
+}
+
+// Eight weights of a chunk, the halves kUnits units apart.
+template <int kUnits>
+__device__ __forceinline__ void weights_at(const float4 *w, float2 (&out)[4]) {
+    const float4 x = w[0], y = w[kUnits];
+    out[0] = make_float2(x.x, x.y);
+    out[1] = make_float2(x.z, x.w);
+    out[2] = make_float2(y.x, y.y);
+    out[3] = make_float2(y.z, y.w);
+}
+
+// The same behind the norm of the head, which kUnits lanes beside each other
+// hold (all of them get here).  weight: the unit's, four fourths kUnits apart.
 template <typename T, int kUnits>
-__device__ __forceinline__ void norm_rotate(uint4 &a, uint4 &b, const float *wa, const float *wb,
+__device__ __forceinline__ void norm_rotate(uint4 &a, uint4 &b, const float4 *weight,
                                             float eps, const float2 *turn, bool turned,
                                             bool interleaved, int lane) {
     uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -136,27 +154,20 @@ __device__ __forceinline__ void norm_rotate(uint4 &a, uint4 &b, const float *wa,
 #pragma unroll
     for (int o = kUnits / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
     const float f = rsqrtf(fmaf(sum, 1.0f / (16 * kUnits), eps));
+    float2 u[4], v[4];
+    weights_at<kUnits>(weight, u);
+    weights_at<kUnits>(weight + 2 * kUnits, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float2 p = unpack(x[i], T()), r = unpack(y[i], T());
-        const float2 u = *reinterpret_cast<const float2 *>(wa + 2 * i);
-        const float2 v = *reinterpret_cast<const float2 *>(wb + 2 * i);
-        p = make_float2(p.x * f * u.x, p.y * f * u.y);
-        r = make_float2(r.x * f * v.x, r.y * f * v.y);
+        p = make_float2(p.x * f * u[i].x, p.y * f * u[i].y);
+        r = make_float2(r.x * f * v[i].x, r.y * f * v[i].y);
         if (turned) rotate_pairs(p, r, turn, i, interleaved);
         x[i] = pack(p.x, p.y, T());
         y[i] = pack(r.x, r.y, T());
     }
     a = make_uint4(x[0], x[1], x[2], x[3]);
     b = make_uint4(y[0], y[1], y[2], y[3]);
-}
-
-// Element i of a weight as fp32.
-__device__ __forceinline__ float weight_at(const void *w, int dtype, int i) {
-    if (w == nullptr) return 1.0f;
-    if (dtype == KDA_DTYPE_FP32) return static_cast<const float *>(w)[i];
-    return dtype == KDA_DTYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i])
-                                   : __half2float(static_cast<const __half *>(w)[i]);
 }
 
 // Where the two chunks of a head's unit j start: the same pairs in both
@@ -171,7 +182,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
     append_kernel(const Params p) {
     constexpr int kUnits = kDim / 16;  // units of a head
     __shared__ float2 turns[kWarps][kMaxPairs];
-    __shared__ float weights[kNorm ? 2 : 1][kNorm ? kDim : 1];   // of queries, of keys
+    // of q and of k: fourths of a unit's weights, so that the units that read one
+    // lie side by side
+    __shared__ float4 weights[kNorm ? 2 : 1][kNorm ? 4 * kUnits : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
@@ -207,13 +220,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
     uint4 x[2], y[2];
     load(begin + lane, x[0], y[0]);
     if constexpr (kNorm) {  // while the first units are on their way
-        for (int i = threadIdx.x; i < 2 * kDim; i += kThreads)
-            weights[i / kDim][i % kDim] =
-                weight_at(i < kDim ? p.q_weight : p.k_weight, p.weight_dtype, i % kDim);
+        for (int i = threadIdx.x; i < 2 * kDim; i += kThreads) {
+            const int which = i / kDim, quarter = i / (4 * kUnits) & 3, j = i / 4 % kUnits;
+            const int2 at = chunks_of(p, j * 8 < p.pairs, j);
+            reinterpret_cast<float *>(weights)[i] =
+                weight_at(which == 0 ? p.q_weight : p.k_weight, p.weight_dtype,
+                          (quarter < 2 ? at.x : at.y) + (quarter & 1) * 4 + (i & 3));
+        }
         __syncthreads();
     }
     if (t >= p.num_tokens) return;
-
     const int b = find_row(p.rows.cu_seqlens, p.rows.B, t, lane);
     if (b < 0) return;
     int bits = 0;  // flagged where the rows are checked
@@ -252,10 +268,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
         const bool turned = head < first_v && j * 8 < p.pairs;
         const int2 at = chunks_of(p, turned, j);
         if constexpr (kNorm) {
-            const float *w = weights[head < first_k ? 0 : 1];
             if (head < first_v)
-                norm_rotate<T, kUnits>(x, y, w + at.x, w + at.y, p.eps, &turns[warp][j * 8], turned,
-                                       p.interleaved != 0, lane);
+                norm_rotate<T, kUnits>(x, y, &weights[head < first_k ? 0 : 1][j], p.eps,
+                                       &turns[warp][j * 8], turned, p.interleaved != 0, lane);
         } else {
             if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
         }
@@ -322,8 +337,7 @@ kda_status append(const kda_cache_config *cfg, const void *q, const void *k, con
         !stride_ok(cfg->stride_v_t))
         return KDA_ERR_INVALID_ARG;
     if (norm != nullptr) {
-        const uintptr_t size = norm->dtype == KDA_DTYPE_FP32 ? 4 : 2;
-        if (!aligned(norm->q_weight, size) || !aligned(norm->k_weight, size))
+        if (!aligned(norm->q_weight, 16) || !aligned(norm->k_weight, 16))
             return KDA_ERR_INVALID_ARG;
         p.q_weight = norm->q_weight;
         p.k_weight = norm->k_weight;

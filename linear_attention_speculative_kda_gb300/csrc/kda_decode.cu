@@ -1,5 +1,5 @@
-// kda_decode: the gated delta rule for one token a row, and kda_prefill for
-// rows of any length, token by token (sm_103a).  Contract in include/kda.h.
+// kda_decode: the gated delta rule for one token a row, and kda_prefill's rows
+// of a few tokens, token by token (sm_103a).  Contracts in include/kda.h.
 //
 // Mathematics, a head's state S [V, K] and a token:
 //   S' = S diag(e),  u = S' k^,  v' = beta (v - u),  S <- S' + v' k^T,  o = S q^.
@@ -127,14 +127,14 @@ __global__ void __launch_bounds__(kThreads, 2) recurrent_kernel(const Params p) 
             __stcs(reinterpret_cast<float4 *>(dst + i * kD + 32 * m), s[i][m]);
 }
 
-kda_status launch(const Params &p, void *stream) {
+}  // namespace
+
+kda_status kda_delta::launch_recurrent(const Params &p, void *stream) {
     const long long tiles = (long long)p.B * p.H;
     if (tiles > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     return kda_cache::launch(recurrent_kernel, dim3((unsigned)tiles), dim3(kThreads), 0, 1, stream,
                              p);
 }
-
-}  // namespace
 
 extern "C" kda_status kda_decode(const kda_config *cfg, const void *q, const void *k,
                                  const void *v, const void *g_raw, const void *beta_raw,
@@ -148,7 +148,7 @@ extern "C" kda_status kda_decode(const kda_config *cfg, const void *q, const voi
     Params p{};
     st = kda_delta::set_params(cfg, q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool,
                                state_indices, initial_indices, B, B, out, error_word, p);
-    return st != KDA_OK ? st : launch(p, stream);
+    return st != KDA_OK ? st : kda_delta::launch_recurrent(p, stream);
 }
 
 extern "C" kda_status kda_decode_packed(const kda_delta_args *a) {

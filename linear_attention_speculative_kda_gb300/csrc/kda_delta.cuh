@@ -24,6 +24,7 @@ struct Params {
     int H, S, B, num_tokens;
     int bounded;
     float lower_bound, scale;
+    int least, most;   // token counts of the rows that the kernel takes
 };
 
 struct Row {
@@ -48,12 +49,15 @@ __device__ __forceinline__ Row read_row(const Params &p, int b, int &bits) {
         bits |= KDA_ROW_BAD_LENGTH;
     else if (to >= p.S || from >= p.S)
         bits |= KDA_ROW_BAD_SLOT;
-    else
+    else if (n >= p.least && n <= p.most)
         row.tokens = (int)n;
     return row;
 }
 
 // ------------------------------------------------------------------- host --
+
+// The rows of p.least to p.most tokens, token by token (kda_decode.cu).
+kda_status launch_recurrent(const Params &p, void *stream);
 
 inline kda_status set_params(const kda_config *c, const void *q, const void *k, const void *v,
                              const void *g_raw, const void *beta_raw, const float *A_log,
@@ -96,6 +100,8 @@ inline kda_status set_params(const kda_config *c, const void *q, const void *k, 
     p.bounded = c->use_lower_bound;
     p.lower_bound = c->lower_bound;
     p.scale = c->scale;
+    p.least = 1;
+    p.most = 0x7fffffff;
     return KDA_OK;
 }
 

@@ -1125,6 +1125,18 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return KDA_ERR_CUDA;
+    // Rows of up to kShort tokens go token by token where most rows can be such
+    // (512 rows x 16 heads: 219 us with 1 token, 359 with 4, 577 with 8, and 505
+    // as chunks).  Elsewhere the second launch costs more than it gives: 256 rows
+    // of 1 to 45 tokens x 32 heads took 680 us, not 645.
+    constexpr int kShort = 6;
+    if (num_tokens <= (long long)kShort * B) {
+        p.most = kShort;
+        st = kda_delta::launch_recurrent(p, stream);
+        if (st != KDA_OK || num_tokens <= kShort) return st;
+        p.least = kShort + 1;
+        p.most = 0x7fffffff;
+    }
     return kda_cache::launch(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads),
                              smem, 1, stream, p, (unsigned)tiles);
 }
