@@ -8,34 +8,47 @@
 //   T    = (1 + diag(beta) A)^-1 diag(beta)                      [C, C]
 //   V'   = T (V - (K P) S^T),   O = (Q P) S^T + B V'
 //   S   <- S diag(P_C) + V'^T (K P_C / P_t)
-// All factors are products of decays behind one another, never quotients, so
-// none is above 1 and strong decays underflow to what they are.
 //
-// Every product with S and V' runs on tcgen05.mma in fp16 with fp32 sums, the
-// rows of S (values' channels) as its 128 rows.  An fp32 operand x is two fp16
-// numbers, hi = fp16(x) and lo = fp16(x - hi), 22 bits, and a product is hi hi
-// + hi lo + lo hi: what is left out is below 2^-22 of it.  Only O takes hi
-// alone: it is rounded to bf16, 2^-9, anyway.  Decayed keys and queries are at
-// most 1 and scaled by powers of two; rows of S, of V - U and of V' have
-// powers of two of their own, from their own sizes, as fp16's range needs it.
+// Precision.  States are fp32 and the products with them have to be: every
+// product with S and V' runs on tcgen05.mma in fp16 with fp32 sums, an fp32
+// operand x as two fp16 numbers, hi = fp16(x) and lo = fp16(x - hi), 22 bits,
+// and a product as hi hi + hi lo + lo hi; what is left out is below 2^-22 of
+// it.  Only O takes hi alone: it is rounded to bf16, 2^-9, anyway.  Decayed
+// keys and queries are at most 1 and scaled by powers of two; rows of S and of
+// V' have powers of two of their own, from bounds of their sizes, as fp16's
+// range needs it.  V' itself is 136 fp32 products a row, made where V - U lies:
+// less than the way to the tensor cores and back.
 //
-// Layout.  A CTA has one row and head at a time.  S lies in tensor memory, in
-// fp32 and, split, as the A operand of the products.  Eight consumer warps
-// have a row of it each two threads: half of its columns, where they add what
-// the chunk brought and split it, and half of the chunk's tokens, of which
-// they make V - U, split V' and write the outputs.  The operands that all rows share (K P, Q P, K P_C / P_t, T, B,
-// P_C) are made by eight producer warps in a ring of stages.  What runs once a
-// chunk is in short loops: straight code of all roles together (80 KB) missed
-// the instruction cache so often that it took twice the time.
+// A and B.  Four tokens t at a time meet all s before and among them: k_s
+// decayed to the block's first token times k_t, q_t decayed from it, all of
+// them products of decays, which strong decays may take to 0.  Among the four
+// that is k_s / R_s, R_s the decays from the first.  There, and in K P_C / P_t,
+// a decay below 2^-40 counts as 2^-40, so that three of them fit fp32: what
+// that adds is 2^-40 beside factors of 1.  The operands keep fp32's range:
+// mma.sync in tf32, hi and lo as above (5% of the tensor pipe's time).
 //
-// A and B.  Two producer warps make a chunk's operands, the first the tokens'
-// vectors, the second the products between tokens.  Four tokens t at a time
-// meet all s before and among them: k_s decayed to the block's first token
-// times k_t, q_t decayed from it.  Among the four that is k_s / R_s, R_s the
-// decays from the first, a quotient.  There, and in K P_C / P_t, a decay below
-// 2^-40 counts as 2^-40, so that three of them fit fp32: what that adds is
-// 2^-40 beside factors of 1.  The operands keep fp32's range: tf32, hi and lo
-// as above.
+// Layout.  A CTA has one row and head at a time: the chunks of a row follow
+// one another, so rows and heads are what runs side by side.  S lies in tensor
+// memory, in fp32 and, split, as the A operand of the products.  Of the
+// eight consumer warps two threads have a row of it, each half of its columns,
+// where they add what the chunk brought and split it, and half of the chunk's
+// tokens, of which they make V', split it and write the outputs.  The operands
+// that all rows share (K P, Q P, K P_C / P_t, T, B, P_C) are made by eight
+// producer warps, a pair a chunk, in a ring of stages: the first warp of a pair
+// makes the tokens' vectors, the second the products between them.
+//
+// What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
+// 32 heads, 2.6 ms) nor the tensor cores (11%), but issue: some 13,000 warp
+// instructions a chunk, 55% of the issue slots, a consumer's turn of 6,000
+// clocks (S 1,800, the products with S 1,100, V' 1,000, the update 800, the
+// barriers 700).  On the way here, the same 64 rows: token by token in fp32
+// 13.3 ms (the decay, two dot products and the update are 8 fp32 operations an
+// element of S: 3.2 ms at the least); consumers on mma.sync with S in their
+// registers 3.8; straight code of all roles (80 KB) missed the instruction
+// cache, 60 KB in short loops took 4.6 to 3.1; both halves of a row on V'
+// and the outputs, and shared memory addressed as such, 2.7.  CTAs that take
+// over others' rows as they finish (cluster launch control) were slower than
+// rows dealt out in turn: 256 rows of 1 to 45 tokens x 32 heads 713, not 656 us.
 #include <cuda_fp16.h>
 
 #include "kda_delta.cuh"
@@ -474,8 +487,8 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
             lane < valid ? kda::sigmoidf_rn(__bfloat162float(
                                p.beta[(first + lane) * p.stride_beta + head]))
                          : 0.0f;
-    // lane 4 g + j: tokens s = g and g + 8, channels 16 m + 4 j + 0..3: k_s decayed to where the
-    // block in work needs it
+    // lane 4 g + j: tokens s = g and g + 8, channels 16 m + 4 j + 0..3: k_s decayed
+    // to where the block in work needs it
     u64 w[2][16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) w[0][c] = w[1][c] = pair(0.0f, 0.0f);
@@ -805,6 +818,9 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
             if (!made) return;
             kda::fence_proxy_async_smem();   // the tensor cores read it
             __syncwarp();
+#ifdef KDA_TEST_PREFILL_WAIT_BUDGET
+            if (blockIdx.x == 0) continue;   // CTA 0's operands are never handed over
+#endif
             if (lane == 0) kda::mbar_arrive(&sh.full[stage]);
         }
         count += chunks;
