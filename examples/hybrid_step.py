@@ -89,6 +89,11 @@ class HybridModel:
                                        device=d)
         self.error_word = torch.zeros(1, dtype=I32, device=d)
 
+    def append(self, q, k, v, cu_seqlens, block_table, num_computed):
+        """Rotated queries; rotated keys and values are in the cache."""
+        return api.kda_kv_append(q, k, v, self.key_cache, self.value_cache, cu_seqlens, block_table,
+                                 num_computed, inv_freq=self.inv_freq, error_word=self.error_word)
+
     def verify(self, tokens: torch.Tensor) -> api.TokenLogprobs:
         """The target's view of a window of tokens int32 [requests, window]:
         at every position the log probability of the token that follows in
@@ -110,8 +115,7 @@ class HybridModel:
         q = merged[:, :s.q_heads]
         k, v = merged[:, s.q_heads:].split(s.kv_heads, dim=1)
         where = (self.cu_seqlens, self.block_table, self.num_computed)
-        q = api.kda_kv_append(q, k, v, self.key_cache, self.value_cache, *where,
-                              inv_freq=self.inv_freq, error_word=self.error_word)
+        q = self.append(q, k, v, *where)
         y, _ = api.kda_window_attention(q, self.key_cache, self.value_cache, *where,
                                         self.workspace, **rows)
         x = x + y.flatten(1) @ self.w_out
