@@ -29,6 +29,9 @@ using kda_cache::unpack;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 64;
+// Pair 8 j + i of a token (unit j's i-th) is kept at kTurn i + j: the lanes that
+// read the i-th side by side find it side by side.
+constexpr int kTurn = 8;
 
 // With 64 registers a thread for heads of 128 channels and 48 for 64.  Measured
 // (us, 4 | 5 CTAs an SM): 256 tokens 4.2 | 4.9 and 13.7k tokens 45 | 48 with
@@ -92,11 +95,11 @@ __device__ __forceinline__ unsigned long long turns_per_position(double f) {
 __device__ __forceinline__ void rotate_pairs(float2 &p, float2 &r, const float2 *turn, int i,
                                              bool interleaved) {
     if (interleaved) {
-        const float2 s = turn[i], t = turn[4 + i];
+        const float2 s = turn[kTurn * i], t = turn[kTurn * (4 + i)];
         p = make_float2(p.x * s.x - p.y * s.y, p.x * s.y + p.y * s.x);
         r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
     } else {
-        const float2 s = turn[2 * i], t = turn[2 * i + 1];
+        const float2 s = turn[kTurn * 2 * i], t = turn[kTurn * (2 * i + 1)];
         const float2 u = p;
         p = make_float2(u.x * s.x - r.x * s.y, u.y * t.x - r.y * t.y);
         r = make_float2(u.x * s.y + r.x * s.x, u.y * t.y + r.y * t.x);
@@ -127,16 +130,6 @@ __device__ __forceinline__ float weight_at(const void *w, int dtype, int i) {
                                    : __half2float(static_cast<const __half *>(w)[i]);
 }
 
-// Eight weights of a chunk, the halves kUnits units apart.
-template <int kUnits>
-__device__ __forceinline__ void weights_at(const float4 *w, float2 (&out)[4]) {
-    const float4 x = w[0], y = w[kUnits];
-    out[0] = make_float2(x.x, x.y);
-    out[1] = make_float2(x.z, x.w);
-    out[2] = make_float2(y.x, y.y);
-    out[3] = make_float2(y.z, y.w);
-}
-
 // The same behind the norm of the head, which kUnits lanes beside each other
 // hold (all of them get here).  weight: the unit's, four fourths kUnits apart.
 template <typename T, int kUnits>
@@ -144,27 +137,33 @@ __device__ __forceinline__ void norm_rotate(uint4 &a, uint4 &b, const float4 *we
                                             float eps, const float2 *turn, bool turned,
                                             bool interleaved, int lane) {
     uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float sum = 0.0f;
+    unsigned long long p[4], r[4], squares = kda_cache::pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack(x[i], T()), r = unpack(y[i], T());
-        sum = fmaf(p.x, p.x, fmaf(p.y, p.y, fmaf(r.x, r.x, fmaf(r.y, r.y, sum))));
+        const float2 u = unpack(x[i], T()), v = unpack(y[i], T());
+        p[i] = kda_cache::pair(u.x, u.y);
+        r[i] = kda_cache::pair(v.x, v.y);
+        squares = kda_cache::fma_pair(p[i], p[i], kda_cache::fma_pair(r[i], r[i], squares));
     }
+    const float2 both = kda_cache::both(squares);
+    float sum = both.x + both.y;
     const unsigned group = ((1u << kUnits) - 1) << (lane & ~(kUnits - 1));
 #pragma unroll
     for (int o = kUnits / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
-    const float f = rsqrtf(fmaf(sum, 1.0f / (16 * kUnits), eps));
-    float2 u[4], v[4];
-    weights_at<kUnits>(weight, u);
-    weights_at<kUnits>(weight + 2 * kUnits, v);
+    const float root = rsqrtf(fmaf(sum, 1.0f / (16 * kUnits), eps));
+    const unsigned long long f = kda_cache::pair(root, root);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 p = unpack(x[i], T()), r = unpack(y[i], T());
-        p = make_float2(p.x * f * u[i].x, p.y * f * u[i].y);
-        r = make_float2(r.x * f * v[i].x, r.y * f * v[i].y);
-        if (turned) rotate_pairs(p, r, turn, i, interleaved);
-        x[i] = pack(p.x, p.y, T());
-        y[i] = pack(r.x, r.y, T());
+        // (two weights are a half of a fourth)
+        const ulonglong2 *w = reinterpret_cast<const ulonglong2 *>(weight + (i >> 1) * kUnits);
+        const ulonglong2 *z = reinterpret_cast<const ulonglong2 *>(weight + (2 + (i >> 1)) * kUnits);
+        float2 u = kda_cache::both(
+            kda_cache::mul_pair(kda_cache::mul_pair(p[i], f), (i & 1) ? w->y : w->x));
+        float2 v = kda_cache::both(
+            kda_cache::mul_pair(kda_cache::mul_pair(r[i], f), (i & 1) ? z->y : z->x));
+        if (turned) rotate_pairs(u, v, turn, i, interleaved);
+        x[i] = pack(u.x, u.y, T());
+        y[i] = pack(v.x, v.y, T());
     }
     a = make_uint4(x[0], x[1], x[2], x[3]);
     b = make_uint4(y[0], y[1], y[2], y[3]);
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
         sincospif((float)phase * 0x1p-31f, &cs.y, &cs.x);
         if ((__double2hiint(f) & 0x7ff00000) == 0x7ff00000)  // infinite or a NaN: no angle
             cs = make_float2(NAN, NAN);
-        turns[warp][i] = cs;
+        turns[warp][kTurn * (i & 7) + (i >> 3)] = cs;
     }
     __syncwarp();
     const long long slot = (long long)max(block, 0) * p.stride_block +
@@ -270,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kDim, kNorm))
         if constexpr (kNorm) {
             if (head < first_v)
                 norm_rotate<T, kUnits>(x, y, &weights[head < first_k ? 0 : 1][j], p.eps,
-                                       &turns[warp][j * 8], turned, p.interleaved != 0, lane);
+                                       &turns[warp][j], turned, p.interleaved != 0, lane);
         } else {
-            if (turned) rotate<T>(x, y, &turns[warp][j * 8], p.interleaved != 0);
+            if (turned) rotate<T>(x, y, &turns[warp][j], p.interleaved != 0);
         }
         if (head < first_k || block > 0) {
             __stcs(reinterpret_cast<uint4 *>(dst + at.x), x);

@@ -6,12 +6,16 @@
 // With z = S' q^ the output is o = z + v' (k^ . q^), so both products of a
 // token read S' and one round of sums serves them.
 //
-// A CTA has one head of one row.  Its 64 KiB of state lie in registers: lane
-// 8 g + j of warp w has the rows 16 w + 4 g + i and of each the columns
-// 32 m + 4 j + c (i, m, c = 0..3), so a load or store of a warp moves whole
-// 128-byte lines and a row's sums stay in 8 lanes.  All its loads are issued
-// before the token's vectors are made, and two CTAs of an SM keep 128 KiB on
-// the way: HBM bounds the call (the state once each way).
+// HBM bounds the call: the state once each way.  Rows of S (values' channels)
+// do not meet, so a CTA has half of the rows of one head of one row, 32 KiB in
+// registers: lane 8 g + j of warp w has the rows 16 w + 4 g + i and of each the
+// columns 32 m + 4 j + c (i, m, c = 0..3), so a load or store of a warp moves
+// whole 128-byte lines and a row's sums stay in 8 lanes.  All its loads are
+// issued before the token's vectors are made, and the four CTAs of an SM start
+// and end at different times: 1024 rows x 16 heads take 325 us (99% of the
+// measured copy rate), 357 with a whole head a CTA and two of them an SM, 332
+// with a quarter.  Loads that are not marked to leave the caches first took 318
+// there, but 45 us for 64 rows x 32 heads and not 44.
 #include "kda_delta.cuh"
 
 namespace {
@@ -20,7 +24,7 @@ using kda_delta::kD;
 using kda_delta::kFull;
 using kda_delta::Params;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
 struct Token {
@@ -33,17 +37,18 @@ __device__ __forceinline__ float sum8(float x) {  // over the 8 lanes of a row
     return x + __shfl_xor_sync(kFull, x, 1);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) recurrent_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) recurrent_kernel(const Params p) {
     __shared__ __align__(16) Token token;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int half = blockIdx.x & 1, tile = blockIdx.x >> 1;
+    const int b = tile / p.H, h = tile % p.H;
     kda_cache::grid_dependents_launch();
     kda_cache::grid_dependency_wait();
     int bits = 0;
     const kda_delta::Row row = kda_delta::read_row(p, b, bits);
-    if (bits != 0 && h == 0 && tid == 0) kda_cache::flag(p.err, bits);
+    if (bits != 0 && h == 0 && half == 0 && tid == 0) kda_cache::flag(p.err, bits);
     if (row.tokens == 0) return;
-    const int r0 = 16 * warp + 4 * (lane >> 3), c0 = 4 * (lane & 7);
+    const int r0 = 64 * half + 16 * warp + 4 * (lane >> 3), c0 = 4 * (lane & 7);
     float4 s[4][4];
     if (row.from > 0) {
         const float *src =
@@ -63,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrent_kernel(const Params p) 
     for (int n = 0; n < row.tokens; ++n) {
         const long long t = row.first + n;
         // a warp each: q and k normalised, the decays, v; four channels a lane
-        if (warp < 4) {
+        {
             const __nv_bfloat16 *src = warp == 0   ? p.q + t * p.stride_q
                                        : warp == 1 ? p.k + t * p.stride_k
                                        : warp == 2 ? p.g + t * p.stride_g
@@ -131,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrent_kernel(const Params p) 
 
 kda_status kda_delta::launch_recurrent(const Params &p, void *stream) {
     const long long tiles = (long long)p.B * p.H;
-    if (tiles > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-    return kda_cache::launch(recurrent_kernel, dim3((unsigned)tiles), dim3(kThreads), 0, 1, stream,
-                             p);
+    if (tiles > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
+    return kda_cache::launch(recurrent_kernel, dim3((unsigned)(2 * tiles)), dim3(kThreads), 0, 1,
+                             stream, p);
 }
 
 extern "C" kda_status kda_decode(const kda_config *cfg, const void *q, const void *k,

@@ -1142,9 +1142,9 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
         cudaSuccess)
         return KDA_ERR_CUDA;
     // Rows of up to kShort tokens go token by token where most rows can be such
-    // (512 rows x 16 heads: 219 us with 1 token, 359 with 4, 577 with 8, and 505
-    // as chunks).  Elsewhere the second launch costs more than it gives: 256 rows
-    // of 1 to 45 tokens x 32 heads took 680 us, not 645.
+    // (512 rows x 16 heads: 203 us with 1 token, 332 with 4, 424 with 6, and 505
+    // as a chunk each).  Elsewhere the second launch costs more than it gives: 256
+    // rows of 1 to 45 tokens x 32 heads took 680 us, not 649.
     constexpr int kShort = 6;
     if (num_tokens <= (long long)kShort * B) {
         p.most = kShort;
