@@ -36,6 +36,10 @@
 // that all rows share (K P, Q P, K P_C / P_t, T, B, P_C) are made by eight
 // producer warps, a pair a chunk, in a ring of stages: the first warp of a pair
 // makes the tokens' vectors, the second the products between them.
+//   Where fewer rows and heads than SMs have many tokens, a cluster of two CTAs
+// shares one (kSplit): all warps of the second produce, eight pairs, and write
+// their operands into the first's stages (mapa), all warps of the first
+// consume, four threads a row of S.
 //
 // What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
 // 32 heads, 2.6 ms) nor the tensor cores (11%), but issue: some 13,000 warp
@@ -49,6 +53,9 @@
 // and the outputs, and shared memory addressed as such, 2.7.  CTAs that take
 // over others' rows as they finish (cluster launch control) were slower than
 // rows dealt out in turn: 256 rows of 1 to 45 tokens x 32 heads 713, not 656 us.
+//   A single long row is a chain: a turn a chunk, 2.3 us where two CTAs share it
+// (16 heads x 16384 tokens 2.38 ms), 2.8 in one; with four pairs of producers in
+// the second CTA the consumers waited for them, 2.6.
 #include <cuda_fp16.h>
 
 #include "kda_delta.cuh"
@@ -67,11 +74,17 @@ using kda_delta::Row;
 typedef unsigned long long u64;
 
 constexpr int kC = 16;           // tokens of a chunk
-constexpr int kPairs = 4;        // pairs of producer warps, a chunk each
-constexpr int kProducers = 2 * kPairs;
-constexpr int kStages = 5;
-constexpr int kConsumers = 8;    // warps: two groups of four, a half of S's columns each
-constexpr int kThreads = 32 * (kProducers + kConsumers);
+constexpr int kThreads = 512;
+// Pairs of producer warps, a chunk each, and stages of their ring, with 8
+// consumer warps beside them, or 16 in another CTA (kSplit).
+template <bool kSplit>
+constexpr int kPairs = kSplit ? 8 : 4;
+template <bool kSplit>
+constexpr int kStages = kSplit ? 8 : 5;
+// A pair waits for a stage to be empty by the parity of its turn: all that was
+// taken from a stage before that is done when the pair's last chunk was begun.
+static_assert(kPairs<true> <= kStages<true> && kPairs<false> <= kStages<false>,
+              "a wait for a stage is never two turns ahead");
 
 #ifdef KDA_TEST_PREFILL_WAIT_BUDGET  // a test build: a wait that runs out, soon
 constexpr long long kWaitBudget = KDA_TEST_PREFILL_WAIT_BUDGET;
@@ -93,21 +106,31 @@ struct __align__(1024) Stage {
     unsigned char inner[kC * 128];        // [token t]: B_t, 16 fp16; from byte 64 on T_t, 16 fp32
     float decay[kD];                      // P_C
     __nv_bfloat16 v[kC][kD];
-    unsigned char pad[512];
 };
 static_assert(sizeof(Stage) % 1024 == 0, "swizzle atoms start on 1024 bytes");
 
-// The tokens along V': those of the consumers' first half, whose T have 0 3 4 7 8
-// 11 12 15 entries before the diagonal's, then those of the other, with 1 2 5
-// 6 9 10 13 14, so that both have the same to do.
-__host__ __device__ constexpr int order_of(int t) {
-    return 2 * (t >> 2) + ((t & 3) >> 1) + (((t + 1) & 2) << 2);
+// Consumer threads that share a row of S: each has its part of the columns and
+// of the tokens.
+template <bool kSplit>
+constexpr int kParts = kSplit ? 4 : 2;
+
+// A part's i-th token, in order along V'.  All parts have the same to do: the T
+// of their tokens have as many entries up to the diagonal's group of four (0 3
+// 4 7 8 11 12 15 and 1 2 5 6 9 10 13 14 of two parts; 0 7 8 15, 1 6 9 14 ... of
+// four).
+template <bool kSplit>
+__device__ __forceinline__ int token_of(int part, int i) {
+    const int group = kSplit ? i : i >> 1;
+    return 4 * group + ((i & 1) ? 3 - part : part);
 }
-static_assert(order_of(0) == 0 && order_of(3) == 1 && order_of(4) == 2 && order_of(15) == 7 &&
-                  order_of(1) == 8 && order_of(2) == 9 && order_of(14) == 15,
-              "both halves have eight tokens");
-__device__ __forceinline__ int token_of(int half, int i) {   // its i-th token
-    return 4 * (i >> 1) + ((i & 1) ? 3 - half : half);
+
+// The place along V' of token t.
+template <bool kSplit>
+__device__ __forceinline__ int order_of(int t) {
+    const int group = t >> 2, off = t & 3;
+    if (kSplit) return 4 * ((group & 1) ? 3 - off : off) + group;
+    const int part = off == 0 || off == 3 ? 0 : 1;
+    return 8 * part + 2 * group + (off >> 1);
 }
 
 // Byte offset of channel c (even, of 64) of row r.
@@ -132,13 +155,25 @@ struct __align__(16) Scratch {            // of a pair of producer warps
     uint64_t ready[2], taken[2];
 };
 
-struct Shared {
-    Stage stage[kStages];
-    Scratch scratch[kPairs];
-    float most[2][kD];                    // largest of each half of a row of S
-    float sum[2][kD];                     // of |V'| over half of the tokens, of a row
+template <bool kSplit>
+struct Work_space {
+    Stage stage[kStages<false>];
+    Scratch scratch[kPairs<false>];
+};
+template <>
+struct Work_space<true> {
+    union {
+        Stage stage[kStages<true>];       // of the CTA that consumes
+        Scratch scratch[kPairs<true>];    // of the other
+    };
+};
+
+template <bool kSplit>
+struct Shared : Work_space<kSplit> {
+    float most[4][kD];                    // largest of each part of a row of S
+    float sum[4][kD];                     // of |V'| over each part's tokens, of a row
     float zeros[kD];
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages<kSplit>], empty[kStages<kSplit>];
     uint64_t u_done, s_done;              // products of a chunk
     uint64_t drained;
     int gave_up;
@@ -190,14 +225,61 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     lo = half_pair(r.x, r.y);
 }
 
+// Where two CTAs share a row and head (kSplit), the first consumes and the
+// second produces: its operands and its arrivals go to the first's shared
+// memory, as the consumers' arrivals come to it.
+__device__ __forceinline__ uint32_t rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ T &at_rank(T &x, uint32_t r) {
+    uint64_t y;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(y) : "l"(reinterpret_cast<uint64_t>(&x)), "r"(r));
+    return *reinterpret_cast<T *>(y);
+}
+
+__device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t r) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(
+            kda::smem_u32(bar)),
+        "r"(r)
+        : "memory");
+}
+
+__device__ __forceinline__ void meet_cluster() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
+}
+
+// Whether the phase is over; across CTAs, with what was written before it.
+template <bool kAcross>
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+    if constexpr (!kAcross) return kda::mbar_try_wait(bar, parity);
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(kda::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // The rest of a wait that is not over at once.
-__device__ __noinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+template <bool kAcross>
+__device__ __noinline__ bool wait_on(int &gave_up, uint64_t *bar, uint32_t parity, int *err) {
     bool done = false;
     const long long t0 = clock64();
-    while (!(done = kda::mbar_try_wait(bar, parity))) {
-        if (*reinterpret_cast<volatile int *>(&sh.gave_up) != 0) break;
+    while (!(done = try_wait<kAcross>(bar, parity))) {
+        if (*reinterpret_cast<volatile int *>(&gave_up) != 0) break;
         if (clock64() - t0 > kWaitBudget) {
-            *reinterpret_cast<volatile int *>(&sh.gave_up) = 1;
+            *reinterpret_cast<volatile int *>(&gave_up) = 1;
             kda_cache::flag(err, KDA_ERR_WAIT_TIMEOUT);
             break;
         }
@@ -207,9 +289,10 @@ __device__ __noinline__ bool wait_on(Shared &sh, uint64_t *bar, uint32_t parity,
 
 // Bounded wait of a warp: it gives up, as a whole, after the budget, or when
 // another warp has.
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
-    if (__all_sync(kFull, kda::mbar_try_wait(bar, parity))) return true;
-    return wait_on(sh, bar, parity, err);
+template <bool kAcross = false, typename S>
+__device__ __forceinline__ bool wait(S &sh, uint64_t *bar, uint32_t parity, int *err) {
+    if (__all_sync(kFull, try_wait<kAcross>(bar, parity))) return true;
+    return wait_on<kAcross>(sh.gave_up, bar, parity, err);
 }
 
 struct Work {   // one row and head
@@ -333,8 +416,8 @@ __device__ __forceinline__ Raw load_raw(const Params &p, Inputs &in, bool valid)
 
 // The tokens' vectors of a chunk, by the first warp of a pair.  blocks: how
 // many blocks of four tokens the pair has had.
-template <bool kBounded>
-__device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stage &st, Scratch &sc,
+template <bool kBounded, bool kSplit>
+__device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &sh, Stage &st, Scratch &sc,
                                                const Row &row, int head, int chunk, int lane,
                                                unsigned &blocks) {
     lane = made_anew(lane);
@@ -346,12 +429,13 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
     Raw next = load_raw(p, in, true), later = load_raw(p, in, 1 < valid);
     {   // the values as they are
         const __nv_bfloat16 *src = p.v + first * p.stride_v + at;
-#pragma unroll 1
+#pragma unroll kSplit ? 8 : 1
         for (int t = 0; t < kC; ++t, src += p.stride_v) {
-            if (t < valid)
+            if (!kSplit && t < valid)
                 kda::cp_async8(&st.v[t][4 * lane], src);
             else
-                *reinterpret_cast<uint2 *>(&st.v[t][4 * lane]) = make_uint2(0u, 0u);
+                *reinterpret_cast<uint2 *>(&st.v[t][4 * lane]) =
+                    t < valid ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0u, 0u);
         }
     }
     kda::cp_async_commit();
@@ -476,7 +560,8 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared &sh, Stag
 }
 
 // The products between tokens, by the second warp of a pair.
-__device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, Stage &st,
+template <bool kSplit>
+__device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit> &sh, Stage &st,
                                                  Scratch &sc, const Row &row, int head, int chunk,
                                                  int lane, unsigned &blocks) {
     lane = made_anew(lane);
@@ -553,7 +638,7 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
                     uint2 hi, lo;
                     split(y.x, y.y, hi.x, lo.x);
                     split(z.x, z.y, hi.y, lo.y);
-                    const int to = place(order_of(g + 8 * i), 16 * (m & 3) + 4 * j);
+                    const int to = place(order_of<kSplit>(g + 8 * i), 16 * (m & 3) + 4 * j);
                     *reinterpret_cast<uint2 *>(st.update[0][m >> 2] + to) = hi;
                     *reinterpret_cast<uint2 *>(st.update[1][m >> 2] + to) = lo;
                 }
@@ -606,7 +691,9 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared &sh, St
         const int t = 4 * n + (lane >> 3), i = 2 * (lane & 7);
         *reinterpret_cast<float2 *>(st.inner + place(t, 32 + 2 * i)) =
             *reinterpret_cast<const float2 *>(&sc.t[t][i]);
-        const int s0 = token_of(i >> 3, i & 7), s1 = token_of(i >> 3, (i & 7) + 1);
+        constexpr int kTokens = kC / kParts<kSplit>;
+        const int s0 = token_of<kSplit>(i / kTokens, i % kTokens);
+        const int s1 = token_of<kSplit>(i / kTokens, i % kTokens + 1);
         const float x = s0 <= t ? sc.b[t][s0] * kBScale : 0.0f;
         const float y = s1 <= t ? sc.b[t][s1] * kBScale : 0.0f;
         *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = half_pair(x, y);
@@ -680,7 +767,19 @@ __device__ __forceinline__ void arrived(uint32_t (&u)[8]) {
                  : "memory");
 }
 
-__device__ __forceinline__ void load8(uint32_t from, uint32_t (&u)[8]) {
+__device__ __forceinline__ void arrived(uint32_t (&u)[4]) {
+    kda::tmem_wait_ld();
+    asm volatile("" : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]) : : "memory");
+}
+
+__device__ __forceinline__ void load(uint32_t from, uint32_t (&u)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"(from)
+                 : "memory");
+}
+
+__device__ __forceinline__ void load(uint32_t from, uint32_t (&u)[8]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
@@ -696,9 +795,15 @@ __device__ __forceinline__ void store8(uint32_t to, const uint32_t (&u)[8]) {
         : "memory");
 }
 
-__device__ __forceinline__ void store4(uint32_t to, const uint32_t (&u)[4]) {
+__device__ __forceinline__ void store(uint32_t to, const uint32_t (&u)[4]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to),
                  "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void store(uint32_t to, const uint32_t (&u)[2]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(to), "r"(u[0]),
+                 "r"(u[1])
                  : "memory");
 }
 
@@ -712,9 +817,9 @@ __device__ __forceinline__ float larger(float m, u64 xy) {
 }
 
 // Named barriers of the consumers.
-template <int kId>
+template <int kId, int kMembers>
 __device__ __forceinline__ void meet() {
-    asm volatile("bar.sync %0, 256;" ::"n"(kId) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kMembers) : "memory");
 }
 
 // 16 channels of a row of S, as they are and as two fp16 numbers each, to
@@ -733,18 +838,19 @@ __device__ __forceinline__ void store_state(uint32_t state, uint32_t halves, con
     store8(halves + 64, lo);
 }
 
-// 8 values times `scale` as two fp16 numbers each: hi to 4 columns, lo to the
-// 4 that are 8 further.
-__device__ __forceinline__ void store_split8(uint32_t to, const u64 (&x)[4], float scale) {
-    uint32_t hi[4], lo[4];
+// 2 kPairsOf values times `scale` as two fp16 numbers each: hi to as many
+// columns, lo to those that are 8 further.
+template <int kPairsOf>
+__device__ __forceinline__ void store_split(uint32_t to, const u64 (&x)[kPairsOf], float scale) {
+    uint32_t hi[kPairsOf], lo[kPairsOf];
     const u64 f = pair(scale, scale);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kPairsOf; ++c) {
         const float2 y = both(mul_pair(x[c], f));
         split(y.x, y.y, hi[c], lo[c]);
     }
-    store4(to, hi);
-    store4(to + 8, lo);
+    store(to, hi);
+    store(to + 8, lo);
 }
 
 // S is held times 2^ex, a power of its row.  As held, the bound of the row that
@@ -787,14 +893,24 @@ __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
 
 // ------------------------------------------------------------------ kernel --
 
+// A CTA's rows and heads, or a pair's: dealt out in turn.
+template <bool kSplit>
+__device__ __forceinline__ unsigned first_item() {
+    return kSplit ? blockIdx.x >> 1 : blockIdx.x;
+}
+template <bool kSplit>
+__device__ __forceinline__ unsigned item_step() {
+    return kSplit ? gridDim.x >> 1 : gridDim.x;
+}
+
 // A producer warp: the tokens' vectors (the first kPairs) or the products
 // between them of every kPairs-th chunk of the CTA's work.
-template <bool kBounded>
-__device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned items, int warp,
+template <bool kBounded, bool kSplit>
+__device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, unsigned items, int warp,
                                         int lane) {
-    const unsigned pair_of = warp % kPairs;
+    const unsigned pair_of = warp % kPairs<kSplit>;
     unsigned count = 0, blocks = 0;
-    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+    for (unsigned item = first_item<kSplit>(); item < items; item += item_step<kSplit>()) {
         int bits = 0;
         const Work w = work_at(p, item, bits);
         if (bits != 0 && w.head == 0 && threadIdx.x == 0) kda_cache::flag(p.err, bits);
@@ -805,23 +921,32 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
                          "r"(kda_delta::kTile * 4)
                          : "memory");
         const unsigned chunks = (unsigned)(w.row.tokens + kC - 1) / kC;
-        for (unsigned c = (pair_of - count) % kPairs; c < chunks; c += kPairs) {
-            const unsigned stage = (count + c) % kStages, turn = (count + c) / kStages;
-            if (!wait(sh, &sh.empty[stage], (turn & 1) ^ 1, p.err)) return;
-            Stage &st = sh.stage[stage];
+        for (unsigned c = (pair_of - count) % kPairs<kSplit>; c < chunks; c += kPairs<kSplit>) {
+            const unsigned stage = (count + c) % kStages<kSplit>, turn = (count + c) / kStages<kSplit>;
+            if (!wait<kSplit>(sh, &sh.empty[stage], (turn & 1) ^ 1, p.err)) return;
+            Stage &st = kSplit ? at_rank(sh.stage[stage], 0) : sh.stage[stage];
             Scratch &sc = sh.scratch[pair_of];
             bool made;
-            if (warp < kPairs)
-                made = produce_tokens<kBounded>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
+            if (warp < kPairs<kSplit>)
+                made = produce_tokens<kBounded, kSplit>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
             else
-                made = produce_products(p, sh, st, sc, w.row, w.head, c, lane, blocks);
+                made = produce_products<kSplit>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
             if (!made) return;
-            kda::fence_proxy_async_smem();   // the tensor cores read it
+            // the tensor cores read it
+            if (kSplit)
+                asm volatile("fence.proxy.async;" ::: "memory");
+            else
+                kda::fence_proxy_async_smem();
             __syncwarp();
 #ifdef KDA_TEST_PREFILL_WAIT_BUDGET
-            if (blockIdx.x == 0) continue;   // CTA 0's operands are never handed over
+            if (item == 0) continue;   // the first row and head's operands are never handed over
 #endif
-            if (lane == 0) kda::mbar_arrive(&sh.full[stage]);
+            if (lane == 0) {
+                if (kSplit)
+                    arrive_at(&sh.full[stage], 0);
+                else
+                    kda::mbar_arrive(&sh.full[stage]);
+            }
         }
         count += chunks;
     }
@@ -830,26 +955,36 @@ __device__ __forceinline__ void produce(const Params &p, Shared &sh, unsigned it
 // The consumer warps.  A wait that runs out ends nothing by itself: from then
 // on the warp, and soon all of them, go through the same barriers without
 // waiting, issuing or writing, so that no barrier is left with too few.
-__device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned items, int me,
+template <int kOf>
+__device__ __forceinline__ float largest_of(const float (&x)[4][kD], int r) {
+    float m = fmaxf(x[0][r], x[1][r]);
+    if (kOf > 2) m = fmaxf(m, fmaxf(x[2][r], x[3][r]));
+    return m;
+}
+
+template <bool kSplit>
+__device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, unsigned items, int me,
                                         int lane) {
-    const int half = me >> 2, r = 32 * (me & 3) + lane;   // columns of S, and the row
+    constexpr int kOf = kParts<kSplit>, kCols = kD / kOf, kTokens = kC / kOf;
+    const int part = me >> 2, r = 32 * (me & 3) + lane;   // columns of S, and the row
     const uint32_t tmem = sh.tmem + ((uint32_t)(32 * (me & 3)) << 16);
-    const uint32_t state = tmem + kColState + 64 * half, halves = tmem + kColS + 32 * half;
+    const uint32_t state = tmem + kColState + kCols * part;
+    const uint32_t halves = tmem + kColS + kCols / 2 * part;
     bool ok = true;
     unsigned count = 0;
-    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+    for (unsigned item = first_item<kSplit>(); item < items; item += item_step<kSplit>()) {
         int bits = 0;
         const Work w = work_at(p, item, bits);
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
-        const long long at = (long long)w.head * kda_delta::kTile + r * kD + 64 * half;
+        const long long at = (long long)w.head * kda_delta::kTile + r * kD + kCols * part;
         float bound;   // of the row's values
         int ex;
         {
             const float *src = p.pool + max(w.row.from, 0) * slot + at;
-            u64 s[32];
+            u64 s[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kCols / 4; ++i) {
                 ulonglong2 y = make_ulonglong2(0ull, 0ull);
                 if (w.row.from > 0) y = *reinterpret_cast<const ulonglong2 *>(src + 4 * i);
                 s[2 * i] = y.x;
@@ -857,14 +992,14 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             }
             float most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) most = larger(most, s[i]);
-            sh.most[half][r] = most;
-            meet<1>();
-            bound = fmaxf(sh.most[0][r], sh.most[1][r]);
+            for (int i = 0; i < kCols / 2; ++i) most = larger(most, s[i]);
+            sh.most[part][r] = most;
+            meet<1, 128 * kOf>();
+            bound = largest_of<kOf>(sh.most, r);
             ex = 9 - exponent_of(bound);
             const u64 f = pair(power_of_two(ex), power_of_two(ex));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kCols / 16; ++i) {
                 u64 y[8];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) y[n] = mul_pair(s[8 * i + n], f);
@@ -876,22 +1011,22 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
         float added = 0.0f, f_reach = 0.0f, f_inner = 0.0f;
         // turn c adds what chunk c - 1 brought, writes its outputs, and begins chunk c
         for (int c = 0; c <= chunks; ++c) {
-            uint32_t o[4];   // outputs of chunk c - 1: from the state, and from the chunk itself
+            uint32_t o[kTokens / 2];   // outputs of chunk c - 1: from the state, and from the chunk itself
             const bool look = (c & 3) == 0 && c > 0;
             float most = 0.0f;
             if (c > 0) {
                 const unsigned before = count - 1;
                 ok &= wait(sh, &sh.s_done, before & 1, p.err);
                 kda::tc_fence_after();
-                const float *decay = &sh.stage[before % kStages].decay[64 * half];
+                const float *decay = &sh.stage[before % kStages<kSplit>].decay[kCols * part];
                 const u64 factor = pair(added, added);
                 const bool moved = __any_sync(kFull, step != 0);
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kCols / 32; ++i) {
                     uint32_t u[2][16], x[2][16];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        kda::tmem_ld16(tmem + kColUpdate + 64 * half + 32 * i + 16 * h, u[h]);
+                        kda::tmem_ld16(tmem + kColUpdate + kCols * part + 32 * i + 16 * h, u[h]);
                         kda::tmem_ld16(state + 32 * i + 16 * h, x[h]);
                     }
 #pragma unroll
@@ -924,13 +1059,13 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                     }
                 }
                 {
-                    uint32_t x[8], y[8];
-                    load8(tmem + kColReach + kC + 8 * half, x);
-                    load8(tmem + kColInner + 8 * half, y);
+                    uint32_t x[kTokens], y[kTokens];
+                    load(tmem + kColReach + kC + kTokens * part, x);
+                    load(tmem + kColInner + kTokens * part, y);
                     arrived(x);
                     arrived(y);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
+                    for (int t = 0; t < kTokens / 2; ++t) {
                         const float2 z = both(fma_pair(pair_of(y[2 * t], y[2 * t + 1]),
                                                        pair(f_inner, f_inner),
                                                        mul_pair(pair_of(x[2 * t], x[2 * t + 1]),
@@ -940,41 +1075,47 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                 }
                 // chunk c - 1 is done with its stage
                 __syncwarp();
-                if (lane == 0) kda::mbar_arrive(&sh.empty[before % kStages]);
+                if (lane == 0) {
+                    if (kSplit)
+                        arrive_at(&sh.empty[before % kStages<kSplit>], 1);
+                    else
+                        kda::mbar_arrive(&sh.empty[before % kStages<kSplit>]);
+                }
             }
             if (c < chunks) {
-                if (look) sh.most[half][r] = most * power_of_two(-ex);
-                ok &= wait(sh, &sh.full[count % kStages], (count / kStages) & 1, p.err);
+                if (look) sh.most[part][r] = most * power_of_two(-ex);
+                ok &= wait<kSplit>(sh, &sh.full[count % kStages<kSplit>], (count / kStages<kSplit>) & 1, p.err);
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
-                meet<1>();
+                meet<1, 128 * kOf>();
+                if (kSplit) asm volatile("fence.proxy.async;" ::: "memory");
                 if (ok && me == 0 && elected()) {
                     kda::tc_fence_after();
-                    issue_reach(sh.stage[count % kStages], sh.tmem);
+                    issue_reach(sh.stage[count % kStages<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
                 if (ok && me == 4 && elected()) {
                     kda::tc_fence_after();
-                    issue_low(sh.stage[count % kStages], sh.tmem);
+                    issue_low(sh.stage[count % kStages<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
             }
             if (c > 0) {
-                const int n = ok ? w.row.tokens - (c - 1) * kC - 8 * half : 0;
+                const int n = ok ? w.row.tokens - (c - 1) * kC - kTokens * part : 0;
                 uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) +
-                                ((long long)(w.row.first + (c - 1) * kC + 8 * half) * p.H +
+                                ((long long)(w.row.first + (c - 1) * kC + kTokens * part) * p.H +
                                  w.head) * kD + r;
                 const long long next = (long long)p.H * kD;
 #pragma unroll
-                for (int t = 0; t < 8; ++t, dst += next)
+                for (int t = 0; t < kTokens; ++t, dst += next)
                     if (t < n) *dst = (uint16_t)(t & 1 ? o[t / 2] >> 16 : o[t / 2]);
             }
             if (c == chunks) break;
-            const unsigned stage = count % kStages, parity = count & 1;
+            const unsigned stage = count % kStages<kSplit>, parity = count & 1;
             const Stage &st = sh.stage[stage];
-            if (look) bound = fmaxf(sh.most[0][r], sh.most[1][r]);
+            if (look) bound = largest_of<kOf>(sh.most, r);
             u64 x[kC / 2];
             float vmax = 0.0f;
 #pragma unroll
@@ -1003,14 +1144,14 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                                     pair(fx, fx), x[n]);
             }
             {
-                float d[8];   // V' of this half's tokens
+                float d[kTokens];   // V' of the part's tokens
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const unsigned char *t = st.inner + token_of(half, i) * 128;
-                    const int turn = token_of(half, i) & 7;
+                for (int i = 0; i < kTokens; ++i) {
+                    const unsigned char *t = st.inner + token_of<kSplit>(part, i) * 128;
+                    const int turn = token_of<kSplit>(part, i) & 7;
                     u64 sum = 0ull;
 #pragma unroll
-                    for (int n = 0; n <= i >> 1; ++n) {   // four entries each
+                    for (int n = 0; n <= (kSplit ? i : i >> 1); ++n) {   // four entries each
                         const ulonglong2 f =
                             *reinterpret_cast<const ulonglong2 *>(t + (((4 + n) ^ turn) << 4));
                         sum = n == 0 ? mul_pair(f.x, x[0]) : fma_pair(f.x, x[2 * n], sum);
@@ -1020,21 +1161,21 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
                     d[i] = y.x + y.y;
                 }
                 float sum = 0.0f;
-                u64 y[4];
+                u64 y[kTokens / 2];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < kTokens / 2; ++n) {
                     sum += fabsf(d[2 * n]) + fabsf(d[2 * n + 1]);
                     y[n] = pair(d[2 * n], d[2 * n + 1]);
                 }
-                store_split8(tmem + kColY + 4 * half, y, power_of_two(ey));
-                sh.sum[half][r] = sum;
+                store_split(tmem + kColY + kTokens / 2 * part, y, power_of_two(ey));
+                sh.sum[part][r] = sum;
             }
             const float back = power_of_two(-ey);
             f_reach = power_of_two(-ex) * (p.scale / kKeyScale);
             f_inner = back * (p.scale / kBScale);
             kda::tmem_wait_st();
             kda::tc_fence_before();
-            meet<2>();
+            meet<2, 128 * kOf>();
             if (ok && me == 0 && elected()) {
                 kda::tc_fence_after();
                 issue_update(st, sh.tmem);
@@ -1042,7 +1183,8 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             }
             __syncwarp();
             // S is at most what it was and all that is added to it
-            bound += sh.sum[0][r] + sh.sum[1][r];
+#pragma unroll
+            for (int i = 0; i < kOf; ++i) bound += sh.sum[i][r];
             const int moved = state_exponent(bound, ex);
             step = moved - ex;
             ex = moved;
@@ -1054,7 +1196,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
             float *dst = p.pool + w.row.to * slot + at;
             const u64 f = pair(power_of_two(-ex), power_of_two(-ex));
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kCols / 16; ++i) {
                 uint32_t x[16];
                 kda::tmem_ld16(state + 16 * i, x);
                 arrived(x);
@@ -1069,46 +1211,51 @@ __device__ __forceinline__ void consume(const Params &p, Shared &sh, unsigned it
     }
 }
 
-template <bool kBounded>
+template <bool kBounded, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, unsigned items) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    Shared &sh = *reinterpret_cast<Shared *>(smem);
+    Shared<kSplit> &sh = *reinterpret_cast<Shared<kSplit> *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f;
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kStages<kSplit>; ++i) {
             kda::mbar_init(&sh.full[i], 2);
-            kda::mbar_init(&sh.empty[i], kConsumers);
+            kda::mbar_init(&sh.empty[i], 4 * kParts<kSplit>);
         }
-        for (int i = 0; i < 2 * kPairs; ++i) {
-            kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
-            kda::mbar_init(&sh.scratch[i >> 1].taken[i & 1], 1);
-        }
+        if (!kSplit || rank() == 1)
+            for (int i = 0; i < 2 * kPairs<kSplit>; ++i) {
+                kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
+                kda::mbar_init(&sh.scratch[i >> 1].taken[i & 1], 1);
+            }
         kda::mbar_init(&sh.u_done, 2);
         kda::mbar_init(&sh.s_done, 1);
         kda::mbar_init(&sh.drained, 2);
         kda::fence_mbar_init();
     }
-    if (warp == kProducers) {
+    const bool consumes = !kSplit || rank() == 0, produces = !kSplit || rank() == 1;
+    constexpr int kFirst = kSplit ? 0 : 2 * kPairs<kSplit>;   // of the consumers
+    if (consumes && warp == kFirst) {
         kda::tmem_alloc(&sh.tmem, kTmemColumns);
         kda::tc_fence_before();
     }
     kda_cache::grid_dependents_launch();
     __syncthreads();
+    if (kSplit) meet_cluster();   // the barriers of both are there
     kda::tc_fence_after();
     kda_cache::grid_dependency_wait();
-    if (warp < kProducers)
-        produce<kBounded>(p, sh, items, warp, lane);
-    else
-        consume(p, sh, items, warp - kProducers, lane);
-    if (warp == kProducers || warp == kProducers + 4) {
+    if (consumes && warp >= kFirst)
+        consume<kSplit>(p, sh, items, warp - kFirst, lane);
+    else if (produces && warp < 2 * kPairs<kSplit>)
+        produce<kBounded, kSplit>(p, sh, items, warp, lane);
+    if (consumes && (warp == kFirst || warp == kFirst + 4)) {
         // no product may outlive the memory, whatever became of who waited for it
         if (elected()) kda::umma_commit(&sh.drained);
         kda::mbar_wait_bounded(&sh.drained, 0, kWaitBudget);
     }
     __syncthreads();
-    if (warp == kProducers) {
+    if (kSplit) meet_cluster();   // neither's memory goes while the other may still use it
+    if (consumes && warp == kFirst) {
         kda::tc_fence_after();
         kda::tmem_dealloc(sh.tmem, kTmemColumns);
     }
@@ -1136,8 +1283,17 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     const int sms = kda_cache::sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     if (tiles > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
-    const int smem = (int)sizeof(Shared);
-    void (*kernel)(const Params, unsigned) = p.bounded ? prefill_kernel<true> : prefill_kernel<false>;
+    // Where SMs would be idle and rows are long, two SMs share a row and head, one
+    // that produces and one that consumes: a row of 16384 tokens x 16 heads takes
+    // 2.38 ms, not 2.87, one of 512 98 us, not 104, but one of 256 60, not 59, and
+    // of 64 27, not 22 (it starts later).  (Pairs of SMs: not every SM has another
+    // beside it, so no more than a third of them.)
+    constexpr int kLong = 512;
+    const bool split = 3 * tiles <= sms && num_tokens >= (long long)kLong * B;
+    void (*kernel)(const Params, unsigned) =
+        split ? (p.bounded ? prefill_kernel<true, true> : prefill_kernel<false, true>)
+              : (p.bounded ? prefill_kernel<true, false> : prefill_kernel<false, false>);
+    const int smem = (int)(split ? sizeof(Shared<true>) : sizeof(Shared<false>));
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return KDA_ERR_CUDA;
@@ -1153,8 +1309,9 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
         p.least = kShort + 1;
         p.most = 0x7fffffff;
     }
-    return kda_cache::launch(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads),
-                             smem, 1, stream, p, (unsigned)tiles);
+    const long long grid = split ? 2 * tiles : tiles < sms ? tiles : sms;
+    return kda_cache::launch(kernel, dim3((unsigned)grid), dim3(kThreads), smem, split ? 2 : 1,
+                             stream, p, (unsigned)tiles);
 }
 
 extern "C" kda_status kda_prefill_packed(const kda_delta_args *a) {

@@ -38,6 +38,35 @@ def test_long_row():
     check(Case([1500, 700], 1, seed=9))
 
 
+@pytest.mark.parametrize("lower_bound", [None, -5.0])
+@pytest.mark.parametrize("memory", ["long", "short"])
+@pytest.mark.parametrize("lens,heads", [([1500, 0, 17, 1, 1200], 3),   # two CTAs a row and head
+                                        ([1025], 16), ([520, 500, 520], 16),
+                                        ([520, 510], 26)])             # one, many of them
+def test_long_rows(lens, heads, memory, lower_bound):
+    c = Case(lens, heads, lower_bound, seed=24, memory=memory)
+    check(c)
+    mixed = c.sources.clone()
+    mixed[1::2] = 0
+    check(c, initial=mixed)
+    c.slots[-1] = 0
+    check(c)
+
+
+def test_long_rows_are_the_short_ones_rows():
+    """A row alone and among many short ones: the same states and outputs, to
+    the order of the sums over the values' tokens."""
+    c = Case([700] + [1] * 60, 2, seed=25)
+    want = run(c)
+    d = Case([700] + [1] * 60, 2, seed=25)
+    got = api.kda_prefill(*(x[:700] for x in d.inputs()[:5]), d.A_log, d.bias, d.pool,
+                          d.cu[:2], d.slots[:1])
+    slot = int(c.slots[0])
+    top = c.pool[slot].abs().amax(dim=(-1, -2), keepdim=True)
+    assert ((d.pool[slot] - c.pool[slot]).abs() <= 2e-5 * top).all()
+    assert (got.float() - want[:700].float()).norm() <= 2.0 ** -7 * got.float().norm()
+
+
 def test_many_rows():
     rng = np.random.default_rng(0)
     check(Case(rng.integers(0, 40, 170).tolist(), 2, -5.0, seed=10))
@@ -148,17 +177,18 @@ def test_rows_that_are_skipped():
     check(c, want_err=api.ROW_BAD_LENGTH)
 
 
-def test_what_is_not_a_number_stays_in_its_row_and_behind_its_token():
-    c = Case([40, 40], 2, seed=21)
+@pytest.mark.parametrize("tokens", [40, 616])
+def test_what_is_not_a_number_stays_in_its_row_and_behind_its_token(tokens):
+    c = Case([tokens, 600], 2, seed=21)
     clean = run(c).clone()
     for name in ("q", "k", "v", "g", "beta"):
-        d = Case([40, 40], 2, seed=21)
+        d = Case([tokens, 600], 2, seed=21)
         x = getattr(d, name).clone()
         x[37, 0] = float("nan")
         setattr(d, name, x)
         got = run(d)
         # head 0 of the first row, from the piece of 16 tokens on that holds it
-        assert torch.equal(got[:32], clean[:32]) and torch.equal(got[40:], clean[40:])
+        assert torch.equal(got[:32], clean[:32]) and torch.equal(got[tokens:], clean[tokens:])
         assert torch.equal(got[:, 1], clean[:, 1])
         assert got[37, 0].isnan().any()
 
@@ -174,8 +204,9 @@ def test_empty_calls():
     assert out.shape == (0, 1, 128)
 
 
-def test_runs_are_alike_and_captured():
-    c = Case([70, 3, 33], 4, -5.0, seed=23)
+@pytest.mark.parametrize("lens", [[70, 3, 33], [1200, 100, 530]])
+def test_runs_are_alike_and_captured(lens):
+    c = Case(lens, 4, -5.0, seed=23)
     first = run(c, initial=c.sources).clone()
     after = c.pool.clone()
     out = torch.zeros_like(first)

@@ -25,14 +25,22 @@ def starved_lib():
     return api.bind_library(path)
 
 
-@pytest.mark.parametrize("lens", [[20, 100], [200, 30, 33]])
-def test_a_starved_cta_gives_up_and_the_context_stays_usable(starved_lib, monkeypatch, lens):
-    c = Case(lens, 1, seed=3)
+@pytest.mark.parametrize("lens,heads", [([600, 700], 1), ([1300, 230, 333], 2),  # two CTAs
+                                        ([20, 100], 1), ([40, 100], 76)])         # a head; one
+def test_a_starved_cta_gives_up_and_the_context_stays_usable(starved_lib, monkeypatch, lens, heads):
+    if len(lens) * heads > torch.cuda.get_device_properties(0).multi_processor_count:
+        pytest.skip("a CTA would have more than one row and head")
+    c = Case(lens, heads, seed=3)
     out = torch.zeros_like(c.q, memory_format=torch.contiguous_format)
     start = c.pool.clone()
     want = run(c, initial=c.sources).clone()
     after = c.pool.clone()
     assert int(c.err.item()) == 0
+    # the first CTA has the first row's first head, of which nothing is written
+    want_out, want_pool = want.clone(), after.clone()
+    want_out[:lens[0], 0] = 7.0
+    slot = int(c.slots[0])
+    want_pool[slot, 0] = start[slot, 0]
     for _ in range(2):
         c.pool.copy_(start)
         out.fill_(7.0)
@@ -41,13 +49,7 @@ def test_a_starved_cta_gives_up_and_the_context_stays_usable(starved_lib, monkey
             run(c, initial=c.sources, out=out)
         torch.cuda.synchronize()
         assert int(c.err.item()) == api.ERR_WAIT_TIMEOUT
-        # the first CTA has the first row, of which nothing is written
-        first = int(c.cu[1])
-        assert torch.equal(out[first:], want[first:]) and (out[:first] == 7.0).all()
-        slot = int(c.slots[0])
-        assert torch.equal(c.pool[slot], start[slot])
-        others = [i for i in range(len(start)) if i != slot]
-        assert torch.equal(c.pool[others], after[others])
+        assert torch.equal(out, want_out) and torch.equal(c.pool, want_pool)
         c.err.zero_()
     c.pool.copy_(start)
     assert torch.equal(run(c, initial=c.sources), want) and torch.equal(c.pool, after)
