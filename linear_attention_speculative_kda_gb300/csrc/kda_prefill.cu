@@ -54,7 +54,7 @@
 // over others' rows as they finish (cluster launch control) were slower than
 // rows dealt out in turn: 256 rows of 1 to 45 tokens x 32 heads 713, not 656 us.
 //   A single long row is a chain: a turn a chunk, 2.3 us where two CTAs share it
-// (16 heads x 16384 tokens 2.38 ms), 2.8 in one; with four pairs of producers in
+// (32 heads x 16001 tokens 2.38 ms), 2.8 in one; with four pairs of producers in
 // the second CTA the consumers waited for them, 2.6.
 #include <cuda_fp16.h>
 
@@ -1284,8 +1284,8 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     if (sms <= 0) return KDA_ERR_CUDA;
     if (tiles > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
     // Where SMs would be idle and rows are long, two SMs share a row and head, one
-    // that produces and one that consumes: a row of 16384 tokens x 16 heads takes
-    // 2.38 ms, not 2.87, one of 512 98 us, not 104, but one of 256 60, not 59, and
+    // that produces and one that consumes: a row of 16001 tokens x 32 heads takes
+    // 2.38 ms, not 2.87, one of 512 x 16 98 us, not 104, but one of 256 60, not 59, and
     // of 64 27, not 22 (it starts later).  (Pairs of SMs: not every SM has another
     // beside it, so no more than a third of them.)
     constexpr int kLong = 512;
