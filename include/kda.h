@@ -386,6 +386,7 @@ kda_status kda_record_state_blocks(const kda_align *align,
  * So a row may go on in its slot, start from nothing, or start from a cached
  * block and leave it as it is (several rows may start from one block).  A slot
  * that one row writes must not be one that another reads or writes.
+ * out must not overlap an input.
  *
  * Per token and head the recurrence is kda_verify's (same norms, gates and
  * scale).  Rows without tokens are skipped and write nothing.  Outputs of

@@ -1230,8 +1230,9 @@ def kda_prefill(q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens,
     the slot that takes the state behind the row's last token (<= 0: the row
     is skipped); initial_indices int32 [B]: the slot that the row starts from
     (<= 0: zeros; None: state_indices).  No row may write a slot that another
-    reads or writes.  Returns ``out``, bf16 [T, H, 128]; rows that are skipped
-    leave theirs untouched, and rows without tokens write no state."""
+    reads or writes.  Returns ``out``, bf16 [T, H, 128], which overlaps no input;
+    rows that are skipped leave theirs untouched, and rows without tokens write
+    no state."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _delta_call("kda_prefill", load_library(), q, k, v, g_raw, beta_raw, A_log, g_bias,

@@ -36,13 +36,15 @@
 // that all rows share (K P, Q P, K P_C / P_t, T, B, P_C) are made by eight
 // producer warps, a pair a chunk, in a ring of stages: the first warp of a pair
 // makes the tokens' vectors, the second the products between them.
+//   Rows and heads are dealt out to the CTAs by their lengths, or in turn where each
+// CTA has many (make_plan, and the rule at the launch).
 //   Where fewer rows and heads than SMs have many tokens, a cluster of two CTAs
 // shares one (kSplit): all warps of the second produce, eight pairs, and write
 // their operands into the first's stages (mapa), all warps of the first
 // consume, four threads a row of S.
 //
 // What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
-// 32 heads, 2.6 ms) nor the tensor cores (11%), but issue: some 13,000 warp
+// 32 heads, 2.7 ms) nor the tensor cores (11%), but issue: some 13,000 warp
 // instructions a chunk, 55% of the issue slots, a consumer's turn of 6,000
 // clocks (S 1,800, the products with S 1,100, V' 1,000, the update 800, the
 // barriers 700).  On the way here, the same 64 rows: token by token in fp32
@@ -168,11 +170,25 @@ struct Work_space<true> {
     };
 };
 
+// The rows and heads of a CTA: one, and more of those that are left (make_plan;
+// dealt out in turn where it makes none).
+constexpr unsigned kNone = 0xffffffffu;
+constexpr int kPlanRows = kThreads;
+struct Plan {
+    unsigned long long start[kPlanRows + 2];   // of a row's cost for a head, falling
+    unsigned short row[kPlanRows];
+    unsigned rest, end;                        // places of the CTA's items
+    unsigned down, across;                     // items of a column, columns
+    int planned;                               // 0: dealt out in turn
+};
+
 template <bool kSplit>
 struct Shared : Work_space<kSplit> {
-    float most[4][kD];                    // largest of each part of a row of S
-    float sum[4][kD];                     // of |V'| over each part's tokens, of a row
-    float zeros[kD];
+    Plan plan;
+    // (what is read 16 bytes at a time)
+    __align__(16) float most[4][kD];      // largest of each part of a row of S
+    __align__(16) float sum[4][kD];       // of |V'| over each part's tokens, of a row
+    __align__(16) float zeros[kD];
     uint64_t full[kStages<kSplit>], empty[kStages<kSplit>];
     uint64_t u_done, s_done;              // products of a chunk
     uint64_t drained;
@@ -300,11 +316,13 @@ struct Work {   // one row and head
     int head;
 };
 
-__device__ __forceinline__ Work work_at(const Params &p, unsigned item, int &bits) {
+template <bool kPlanned>
+__device__ __forceinline__ Work work_at(const Params &p, const Plan &plan, unsigned item,
+                                        int &bits) {
+    const unsigned at = item / (unsigned)p.H;
     Work w;
-    const unsigned b = item / (unsigned)p.H;
-    w.head = (int)(item - b * (unsigned)p.H);
-    w.row = kda_delta::read_row(p, (int)b, bits);
+    w.head = (int)(item - at * (unsigned)p.H);
+    w.row = kda_delta::read_row(p, kPlanned && plan.planned ? plan.row[at] : (int)at, bits);
     return w;
 }
 
@@ -417,7 +435,8 @@ __device__ __forceinline__ Raw load_raw(const Params &p, Inputs &in, bool valid)
 // The tokens' vectors of a chunk, by the first warp of a pair.  blocks: how
 // many blocks of four tokens the pair has had.
 template <bool kBounded, bool kSplit>
-__device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &sh, Stage &st, Scratch &sc,
+__device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &sh, Stage &st,
+                                               Scratch &sc,
                                                const Row &row, int head, int chunk, int lane,
                                                unsigned &blocks) {
     lane = made_anew(lane);
@@ -893,26 +912,159 @@ __device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
 
 // ------------------------------------------------------------------ kernel --
 
-// A CTA's rows and heads, or a pair's: dealt out in turn.
+// The sum over the CTA's threads up to this one.
+__device__ __forceinline__ u64 sum_up_to(u64 *sums, u64 sum) {
+    const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+        const u64 x = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += x;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+#pragma unroll 1
+    for (unsigned i = 0; i < warp; ++i) sum += sums[i];
+    return sum;
+}
+
+// A CTA's rows and heads by cost: a chunk is 2, a state 5 (its way in and out
+// takes as long as some 2.5 chunks).  In the order of falling cost each CTA takes
+// one of the first.  What is left goes to the CTAs whose first is below the level
+// that this fills them up to, D of them: dealt out to as many columns in turn, the
+// columns lie one behind the other on a line, and the CTAs take of it, in turn, as
+// much as their firsts leave room for.  An item is the CTA's that its middle falls
+// to, so a CTA is over the level by half an item at most, or by its first one.
+// All CTAs come to the same.
+__device__ __forceinline__ void make_plan(const Params &p, Shared<false> &sh, unsigned items) {
+    Plan &plan = sh.plan;
+    unsigned *key = reinterpret_cast<unsigned *>(sh.stage[0].reach);   // not in use yet
+    unsigned *cost = key + kPlanRows;
+    u64 *sums = reinterpret_cast<u64 *>(cost + kPlanRows);
+    u64 *column = sums + kThreads / 32;   // where it starts
+    const unsigned tid = threadIdx.x, B = (unsigned)p.B, H = (unsigned)p.H, G = gridDim.x;
+    unsigned mine = 0;
+    if (tid < B) {
+        int bits = 0;   // flagged where the row's turn comes
+        const unsigned n = (unsigned)kda_delta::read_row(p, (int)tid, bits).tokens;
+        mine = n == 0 ? 1 : min(2 * ((n + kC - 1) / kC) + 5, (1u << 23) - 1);
+    }
+    u64 sum = sum_up_to(sums, mine);
+    if (tid == kThreads - 1) column[0] = sum;
+    __syncthreads();
+    // Where no row is long beside a CTA's share, dealing out in turn does as well or
+    // better (256 rows of 1 to 45 tokens x 32 heads: 663 us in turn, 704 planned).
+    if (__syncthreads_or((u64)mine * G * 8 > column[0] * H) == 0) {
+        if (tid == 0) plan.planned = 0;
+        return;
+    }
+    const unsigned my_key = mine * kPlanRows + (kPlanRows - 1 - tid);
+    key[tid] = my_key;   // (those behind the last row are below all others)
+    cost[tid] = 0;
+    __syncthreads();
+    unsigned place = 0;
+#pragma unroll 1
+    for (unsigned r = 0; r < B; r += 4) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(key + r);
+        place += (unsigned)(c.x > my_key) + (unsigned)(c.y > my_key) + (unsigned)(c.z > my_key) +
+                 (unsigned)(c.w > my_key);
+    }
+    if (tid < B) {
+        plan.row[place] = (unsigned short)tid;
+        cost[place] = mine;
+    }
+    __syncthreads();
+    sum = sum_up_to(sums, cost[tid]);
+    plan.start[tid + 1] = sum;
+    if (tid == 0) plan.start[0] = 0;
+    if (tid == kThreads - 1) plan.start[kPlanRows + 1] = sum;
+    __syncthreads();
+    auto cost_of = [&](unsigned n) { return plan.start[n / H + 1] - plan.start[n / H]; };
+    auto start_of = [&](unsigned n) { return plan.start[n / H] * H + n % H * cost_of(n); };
+    const u64 total = start_of(items);
+    // The CTAs whose first item alone is over the level of it and those behind it.
+    const unsigned full = (unsigned)__syncthreads_count(
+        tid < G && cost_of(tid) * (G - tid) > total - start_of(tid));
+    const unsigned share = G - full, left = items - G;
+    const unsigned across = min(share, left), down = (left + across - 1) / across;
+    const unsigned row_step = across / H, head_step = across % H;
+    // Down column x from the top: whether `stop` at an item of cost c behind a sum.
+    auto walk = [&](unsigned x, u64 &sum, auto stop) {
+        unsigned n = G + x, y = 0, k = n / H, h = n % H;
+#pragma unroll 1
+        for (; n < items; n += across, ++y) {
+            const unsigned c = cost[k];
+            if (stop(sum, c)) return y;
+            sum += c;
+            k += row_step;
+            h += head_step;
+            if (h >= H) h -= H, ++k;
+        }
+        return down;
+    };
+    sum = 0;
+    if (tid < across) walk(tid, sum, [](u64, unsigned) { return false; });
+    sum = sum_up_to(sums, sum);
+    column[tid + 1] = sum;
+    if (tid == 0) column[0] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (unsigned i = 0; i < 2; ++i) {   // where this CTA's part of the line starts and ends
+        const unsigned j = blockIdx.x + i;
+        // (times D)
+        const u64 edge = j <= full ? 0 : (total - start_of(full)) * (j - full) -
+                                             share * (start_of(j) - start_of(full));
+        const unsigned x =
+            (unsigned)__syncthreads_count(tid < across && column[tid] * share <= edge) - 1;
+        if (tid == 0) {
+            sum = column[x];
+            (i == 0 ? plan.rest : plan.end) =   // the first item with its middle behind it
+                x * down + walk(x, sum, [&](u64 at, unsigned c) {
+                    return (2 * at + c) * share >= 2 * edge;
+                });
+        }
+    }
+    if (tid == 0) {
+        plan.down = down;
+        plan.across = across;
+        plan.planned = 1;
+    }
+}
+
 template <bool kSplit>
 __device__ __forceinline__ unsigned first_item() {
     return kSplit ? blockIdx.x >> 1 : blockIdx.x;
 }
-template <bool kSplit>
-__device__ __forceinline__ unsigned item_step() {
-    return kSplit ? gridDim.x >> 1 : gridDim.x;
+
+// The CTA's item behind this one; in a plan the one at place i, or the next one behind
+// it.
+template <bool kPlanned, bool kSplit>
+__device__ __forceinline__ unsigned next_item(const Plan &plan, unsigned item, unsigned &i,
+                                              unsigned items) {
+    const unsigned in_turn = item + (kSplit ? gridDim.x >> 1 : gridDim.x);
+    if constexpr (kPlanned) {
+        if (!plan.planned) return in_turn;
+        while (i < plan.end) {
+            const unsigned x = i / plan.down, n = gridDim.x + (i - x * plan.down) * plan.across + x;
+            ++i;
+            if (n < items) return n;
+        }
+        return kNone;
+    }
+    return in_turn;
 }
 
 // A producer warp: the tokens' vectors (the first kPairs) or the products
 // between them of every kPairs-th chunk of the CTA's work.
-template <bool kBounded, bool kSplit>
-__device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, unsigned items, int warp,
-                                        int lane) {
+template <bool kBounded, bool kSplit, bool kPlanned>
+__device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, unsigned items,
+                                        int warp, int lane) {
     const unsigned pair_of = warp % kPairs<kSplit>;
     unsigned count = 0, blocks = 0;
-    for (unsigned item = first_item<kSplit>(); item < items; item += item_step<kSplit>()) {
+    for (unsigned next = kPlanned ? sh.plan.rest : 0, item = first_item<kSplit>(); item < items;
+         item = next_item<kPlanned, kSplit>(sh.plan, item, next, items)) {
         int bits = 0;
-        const Work w = work_at(p, item, bits);
+        const Work w = work_at<kPlanned>(p, sh.plan, item, bits);
         if (bits != 0 && w.head == 0 && threadIdx.x == 0) kda_cache::flag(p.err, bits);
         if (warp == 0 && lane == 0 && w.row.tokens > 0 && w.row.from > 0)
             // the state is on its way to L2 before a consumer asks for it
@@ -922,13 +1074,15 @@ __device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, uns
                          : "memory");
         const unsigned chunks = (unsigned)(w.row.tokens + kC - 1) / kC;
         for (unsigned c = (pair_of - count) % kPairs<kSplit>; c < chunks; c += kPairs<kSplit>) {
-            const unsigned stage = (count + c) % kStages<kSplit>, turn = (count + c) / kStages<kSplit>;
+            const unsigned stage = (count + c) % kStages<kSplit>;
+            const unsigned turn = (count + c) / kStages<kSplit>;
             if (!wait<kSplit>(sh, &sh.empty[stage], (turn & 1) ^ 1, p.err)) return;
             Stage &st = kSplit ? at_rank(sh.stage[stage], 0) : sh.stage[stage];
             Scratch &sc = sh.scratch[pair_of];
             bool made;
             if (warp < kPairs<kSplit>)
-                made = produce_tokens<kBounded, kSplit>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
+                made = produce_tokens<kBounded, kSplit>(p, sh, st, sc, w.row, w.head, c, lane,
+                                                        blocks);
             else
                 made = produce_products<kSplit>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
             if (!made) return;
@@ -962,7 +1116,7 @@ __device__ __forceinline__ float largest_of(const float (&x)[4][kD], int r) {
     return m;
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kPlanned>
 __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, unsigned items, int me,
                                         int lane) {
     constexpr int kOf = kParts<kSplit>, kCols = kD / kOf, kTokens = kC / kOf;
@@ -972,9 +1126,10 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
     const uint32_t halves = tmem + kColS + kCols / 2 * part;
     bool ok = true;
     unsigned count = 0;
-    for (unsigned item = first_item<kSplit>(); item < items; item += item_step<kSplit>()) {
+    for (unsigned next = kPlanned ? sh.plan.rest : 0, item = first_item<kSplit>(); item < items;
+         item = next_item<kPlanned, kSplit>(sh.plan, item, next, items)) {
         int bits = 0;
-        const Work w = work_at(p, item, bits);
+        const Work w = work_at<kPlanned>(p, sh.plan, item, bits);
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
         const long long at = (long long)w.head * kda_delta::kTile + r * kD + kCols * part;
@@ -1211,7 +1366,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
     }
 }
 
-template <bool kBounded, bool kSplit>
+template <bool kBounded, bool kSplit, bool kPlanned>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, unsigned items) {
     extern __shared__ __align__(1024) unsigned char smem[];
     Shared<kSplit> &sh = *reinterpret_cast<Shared<kSplit> *>(smem);
@@ -1244,10 +1399,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
     if (kSplit) meet_cluster();   // the barriers of both are there
     kda::tc_fence_after();
     kda_cache::grid_dependency_wait();
+    if constexpr (kPlanned) {
+        make_plan(p, sh, items);
+        __syncthreads();
+    }
     if (consumes && warp >= kFirst)
-        consume<kSplit>(p, sh, items, warp - kFirst, lane);
+        consume<kSplit, kPlanned>(p, sh, items, warp - kFirst, lane);
     else if (produces && warp < 2 * kPairs<kSplit>)
-        produce<kBounded, kSplit>(p, sh, items, warp, lane);
+        produce<kBounded, kSplit, kPlanned>(p, sh, items, warp, lane);
     if (consumes && (warp == kFirst || warp == kFirst + 4)) {
         // no product may outlive the memory, whatever became of who waited for it
         if (elected()) kda::umma_commit(&sh.drained);
@@ -1290,9 +1449,19 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     // beside it, so no more than a third of them.)
     constexpr int kLong = 512;
     const bool split = 3 * tiles <= sms && num_tokens >= (long long)kLong * B;
+    // A plan costs some us, and little is gained where each CTA has many rows and
+    // heads: 256 rows of 1 to 45 tokens x 32 heads (54 each) take 647 us, 663 in a
+    // kernel that could plan.  200 rows, some of up to 1501 tokens, x 16 heads (21
+    // each) take 415 planned and 472 in turn, 13 rows of 1 to 2501 x 16 heads 432 and
+    // 637; where all are alike a plan costs 1 to 4% (64 rows of 1024 x 32 heads 2.70
+    // ms, not 2.66), and only the device knows.  With up to 20 tokens for an SM it
+    // costs as much as it gives (25 us), with 70 to 150 it takes off a third.
+    const bool planned = !split && tiles > sms && tiles <= 32LL * sms && B <= kPlanRows &&
+                         sms <= kThreads && (long long)num_tokens * p.H >= 64LL * sms;
     void (*kernel)(const Params, unsigned) =
-        split ? (p.bounded ? prefill_kernel<true, true> : prefill_kernel<false, true>)
-              : (p.bounded ? prefill_kernel<true, false> : prefill_kernel<false, false>);
+        split     ? (p.bounded ? prefill_kernel<true, true, false> : prefill_kernel<false, true, false>)
+        : planned ? (p.bounded ? prefill_kernel<true, false, true> : prefill_kernel<false, false, true>)
+                  : (p.bounded ? prefill_kernel<true, false, false> : prefill_kernel<false, false, false>);
     const int smem = (int)(split ? sizeof(Shared<true>) : sizeof(Shared<false>));
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)

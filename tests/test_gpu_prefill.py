@@ -72,6 +72,53 @@ def test_many_rows():
     check(Case(rng.integers(0, 40, 170).tolist(), 2, -5.0, seed=10))
 
 
+def uneven(rows, most, long, seed):
+    """Rows of 0 to most tokens, and long ones among them."""
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, most + 1, rows)
+    lens[rng.choice(rows, len(long), replace=False)] = long
+    return lens.tolist()
+
+
+@pytest.mark.parametrize("lens,heads", [
+    (uneven(40, 60, [1500], 0), 5), (uneven(300, 12, [900, 700, 17], 1), 3),
+    (uneven(512, 20, [1, 2000, 2900], 2), 1), (uneven(513, 20, [1, 2000, 2900], 2), 1),
+    (uneven(13, 250, [], 3), 16), ([700] + [9] * 160, 7), ([9] * 160 + [700], 7), ([40] * 62, 5),
+    (uneven(460, 12, [], 4), 3), ([8, 9, 10, 11, 12] * 92, 3)])
+def test_uneven_rows(lens, heads):
+    """More rows and heads than SMs, dealt out by their lengths."""
+    c = Case(lens, heads, seed=26)
+    c.slots[3::7] = 0
+    check(c, initial=c.sources)
+    c = Case(lens, heads, -5.0, seed=27, pad_tokens=5)
+    c.slots[5] = c.pool.shape[0]
+    check(c, want_err=api.ROW_BAD_SLOT)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    lens = uneven(60, 60, [1400], 5)
+    c = Case(lens, 4, seed=28)
+    start, order = c.pool.clone(), np.random.default_rng(6).permutation(60)
+    out = torch.zeros(c.q.shape, dtype=BF, device="cuda")
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        run(c, out=out)
+        with torch.cuda.graph(graph, stream=stream):
+            run(c, out=out)
+    stream.synchronize()
+    for some in (np.array(lens)[order], np.array(lens)):
+        c.cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(some)])))
+        c.pool.copy_(start)
+        want = run(c).clone()
+        after = c.pool.clone()
+        c.pool.copy_(start)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(c.pool, after)
+
+
 @pytest.mark.parametrize("heads", [1, 5, 40])
 def test_heads(heads):
     check(Case([50, 18], heads, seed=heads))
