@@ -44,8 +44,8 @@
 // consume, four threads a row of S.
 //
 // What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
-// 32 heads, 2.7 ms) nor the tensor cores (11%), but issue: some 13,000 warp
-// instructions a chunk, 55% of the issue slots, a consumer's turn of 6,000
+// 32 heads, 2.7 ms) nor the tensor cores (13%), but issue: some 13,700 warp
+// instructions a chunk, 54% of the issue slots, a consumer's turn of 6,000
 // clocks (S 1,800, the products with S 1,100, V' 1,000, the update 800, the
 // barriers 700).  On the way here, the same 64 rows: token by token in fp32
 // 13.3 ms (the decay, two dot products and the update are 8 fp32 operations an
