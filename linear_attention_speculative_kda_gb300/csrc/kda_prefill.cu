@@ -6,18 +6,20 @@
 //   A_ts = sum_c k_t k_s prod_{s<i<=t} e_i   (s < t)
 //   B_ts = sum_c q_t k_s prod_{s<i<=t} e_i   (s <= t)
 //   T    = (1 + diag(beta) A)^-1 diag(beta)                      [C, C]
-//   V'   = T (V - (K P) S^T),   O = (Q P) S^T + B V'
+//   X    = V - (K P) S^T,  V' = T X,  O = (Q P) S^T + B V' = (Q P) S^T + (B T) X
 //   S   <- S diag(P_C) + V'^T (K P_C / P_t)
 //
 // Precision.  States are fp32 and the products with them have to be: every
-// product with S and V' runs on tcgen05.mma in fp16 with fp32 sums, an fp32
-// operand x as two fp16 numbers, hi = fp16(x) and lo = fp16(x - hi), 22 bits,
-// and a product as hi hi + hi lo + lo hi; what is left out is below 2^-22 of
-// it.  Only O takes hi alone: it is rounded to bf16, 2^-9, anyway.  Decayed
-// keys and queries are at most 1 and scaled by powers of two; rows of S and of
-// V' have powers of two of their own, from bounds of their sizes, as fp16's
-// range needs it.  V' itself is 136 fp32 products a row, made where V - U lies:
-// less than the way to the tensor cores and back.
+// product with S, and of V' into S, runs on tcgen05.mma in fp16 with fp32 sums,
+// an fp32 operand x as two fp16 numbers, hi = fp16(x) and lo = fp16(x - hi), 22
+// bits, and a product as hi hi + hi lo + lo hi; what is left out is below 2^-22
+// of it.  Decayed keys and queries are at most 1 and scaled by powers of two;
+// rows of S and of V' have powers of two of their own, from bounds of their
+// sizes, as fp16's range needs it.  V' = T X and (B T) X are 136 fp32 products a
+// row each, made where X lies: less than the way to the tensor cores and back.
+// O is rounded once, to bf16 (with hi alone in its products, 11 bits, 64 rows of
+// 1024 tokens x 32 heads took 2.71 ms, not 2.88, and 1 output in 20 was another
+// bf16 number than the exact one's).
 //
 // A and B.  Four tokens t at a time meet all s before and among them: k_s
 // decayed to the block's first token times k_t, q_t decayed from it, all of
@@ -33,14 +35,14 @@
 // eight consumer warps two threads have a row of it, each half of its columns,
 // where they add what the chunk brought and split it, and half of the chunk's
 // tokens, of which they make V', split it and write the outputs.  The operands
-// that all rows share (K P, Q P, K P_C / P_t, T, B, P_C) are made by eight
-// producer warps, a pair a chunk, in a ring of stages: the first warp of a pair
-// makes the tokens' vectors, the second the products between them.
+// that all rows share (K P, Q P, K P_C / P_t, T, B T, P_C) are made by eight
+// producer warps, a pair a chunk, in two rings: the first warp of a pair makes
+// the tokens' vectors, the second the products between them.
 //   Rows and heads are dealt out to the CTAs by their lengths, or in turn where each
 // CTA has many (make_plan, and the rule at the launch).
 //   Where fewer rows and heads than SMs have many tokens, a cluster of two CTAs
-// shares one (kSplit): all warps of the second produce, eight pairs, and write
-// their operands into the first's stages (mapa), all warps of the first
+// shares one (kSplit): the warps of the second produce, seven pairs, and write
+// their operands into the first's rings (mapa), all warps of the first
 // consume, four threads a row of S.
 //
 // What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
@@ -77,16 +79,22 @@ typedef unsigned long long u64;
 
 constexpr int kC = 16;           // tokens of a chunk
 constexpr int kThreads = 512;
-// Pairs of producer warps, a chunk each, and stages of their ring, with 8
-// consumer warps beside them, or 16 in another CTA (kSplit).
+// Pairs of producer warps, a chunk each, and places of their rings, with 8
+// consumer warps beside them, or 16 in another CTA (kSplit).  A chunk's operands
+// lie in two rings: what the products with the state read is written from the
+// chunk's first token on and done with in the middle of the consumers' turn, the
+// rest is written at the end and done with a turn later.
 template <bool kSplit>
-constexpr int kPairs = kSplit ? 8 : 4;
+constexpr int kPairs = kSplit ? 7 : 4;
 template <bool kSplit>
-constexpr int kStages = kSplit ? 8 : 5;
-// A pair waits for a stage to be empty by the parity of its turn: all that was
-// taken from a stage before that is done when the pair's last chunk was begun.
-static_assert(kPairs<true> <= kStages<true> && kPairs<false> <= kStages<false>,
-              "a wait for a stage is never two turns ahead");
+constexpr int kReaches = kSplit ? 7 : 5;
+template <bool kSplit>
+constexpr int kUpdates = kSplit ? 7 : 4;
+// A pair waits for a place to be empty by the parity of its turn: all that was
+// taken from it before that is done when the pair's last chunk was begun.
+static_assert(kPairs<true> <= kReaches<true> && kPairs<false> <= kReaches<false> &&
+                  kPairs<true> <= kUpdates<true> && kPairs<false> <= kUpdates<false>,
+              "a wait for a place is never two turns ahead");
 
 #ifdef KDA_TEST_PREFILL_WAIT_BUDGET  // a test build: a wait that runs out, soon
 constexpr long long kWaitBudget = KDA_TEST_PREFILL_WAIT_BUDGET;
@@ -97,19 +105,20 @@ constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
 // Powers of two on the operands.
 constexpr float kKeyScale = 1024.0f;      // K P, Q P
 constexpr float kUpdateScale = 1024.0f;   // K P_C / P_t
-constexpr float kBScale = 1024.0f;        // B
 
 // One chunk's operands: fp16 matrices of rows of 128 bytes with the 128-byte
 // swizzle (16-byte unit u of row r at u ^ (r & 7)), two blocks of 64 channels.
-constexpr int kTall = 3 * kC;             // rows: K P hi, Q P, K P lo
-struct __align__(1024) Stage {
-    unsigned char reach[2][kTall * 128];  // [64 channels][row]: channels along K
-    unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token's place]
-    unsigned char inner[kC * 128];        // [token t]: B_t, 16 fp16; from byte 64 on T_t, 16 fp32
-    float decay[kD];                      // P_C
+constexpr int kTall = 4 * kC;             // rows: K P hi, Q P hi, K P lo, Q P lo
+struct __align__(1024) Reach {
+    // [64 channels][row]: channels along K, the tokens of Q P in the order of V'
+    unsigned char reach[2][kTall * 128];
     __nv_bfloat16 v[kC][kD];
 };
-static_assert(sizeof(Stage) % 1024 == 0, "swizzle atoms start on 1024 bytes");
+struct __align__(1024) Update {
+    unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token's place]
+    float inner[kC][2 * kC];              // [token t]: (B T)_t, then T_t
+    float decay[kD];                      // P_C
+};
 
 // Consumer threads that share a row of S: each has its part of the columns and
 // of the tokens.
@@ -159,13 +168,17 @@ struct __align__(16) Scratch {            // of a pair of producer warps
 
 template <bool kSplit>
 struct Work_space {
-    Stage stage[kStages<false>];
+    Reach reach[kReaches<false>];
+    Update update[kUpdates<false>];
     Scratch scratch[kPairs<false>];
 };
 template <>
 struct Work_space<true> {
     union {
-        Stage stage[kStages<true>];       // of the CTA that consumes
+        struct {                          // of the CTA that consumes
+            Reach reach[kReaches<true>];
+            Update update[kUpdates<true>];
+        };
         Scratch scratch[kPairs<true>];    // of the other
     };
 };
@@ -175,7 +188,6 @@ struct Work_space<true> {
 constexpr unsigned kNone = 0xffffffffu;
 constexpr int kPlanRows = kThreads;
 struct Plan {
-    unsigned long long start[kPlanRows + 2];   // of a row's cost for a head, falling
     unsigned short row[kPlanRows];
     unsigned rest, end;                        // places of the CTA's items
     unsigned down, across;                     // items of a column, columns
@@ -186,24 +198,27 @@ template <bool kSplit>
 struct Shared : Work_space<kSplit> {
     Plan plan;
     // (what is read 16 bytes at a time)
-    __align__(16) float most[4][kD];      // largest of each part of a row of S
-    __align__(16) float sum[4][kD];       // of |V'| over each part's tokens, of a row
+    __align__(16) float most[kParts<kSplit>][kD];  // largest of each part of a row of S
+    __align__(16) float sum[kParts<kSplit>][kD];   // of |V'| over each part's tokens, of a row
     __align__(16) float zeros[kD];
-    uint64_t full[kStages<kSplit>], empty[kStages<kSplit>];
+    uint64_t full[kReaches<kSplit>];      // both operands
+    uint64_t reach_empty[kReaches<kSplit>], update_empty[kUpdates<kSplit>];
     uint64_t u_done, s_done;              // products of a chunk
     uint64_t drained;
     int gave_up;
     uint32_t tmem;
 };
 
+static_assert(sizeof(Shared<true>) <= 227 * 1024 && sizeof(Shared<false>) <= 227 * 1024,
+              "a CTA's shared memory");
+
 // Columns of tensor memory.
 constexpr uint32_t kColState = 0;         // S, fp32, 128
 constexpr uint32_t kColS = 128;           // S as fp16: 64 of hi, 64 of lo, two channels each
 constexpr uint32_t kColUpdate = 256;      // V'^T (K P_C / P_t), 128
-constexpr uint32_t kColReach = 384;       // S (K P | Q P | K P lo)^T, 48
-constexpr uint32_t kColLow = 432;         // lo of S with hi of K P, 16
-constexpr uint32_t kColInner = 448;       // B V', 16
-constexpr uint32_t kColY = 464;           // V': 8 of hi, 8 of lo
+constexpr uint32_t kColReach = 384;       // S (K P | Q P | K P lo | Q P lo)^T, 64
+constexpr uint32_t kColLow = 448;         // lo of S with hi of K P and of Q P, 32
+constexpr uint32_t kColY = 480;           // V': 8 of hi, 8 of lo
 constexpr uint32_t kTmemColumns = 512;
 
 // D += A B for k steps of 8 in tf32.
@@ -432,11 +447,24 @@ __device__ __forceinline__ Raw load_raw(const Params &p, Inputs &in, bool valid)
     return raw;
 }
 
+// The place of chunk n of a CTA, and the wait for it to be empty.
+template <bool kSplit>
+__device__ __forceinline__ Update &update_of(Shared<kSplit> &sh, unsigned n) {
+    Update &up = sh.update[n % kUpdates<kSplit>];
+    return kSplit ? at_rank(up, 0) : up;
+}
+
+template <bool kSplit>
+__device__ __forceinline__ bool wait_for_update(Shared<kSplit> &sh, unsigned n, int *err) {
+    return wait<kSplit>(sh, &sh.update_empty[n % kUpdates<kSplit>],
+                        ((n / kUpdates<kSplit>) & 1) ^ 1, err);
+}
+
 // The tokens' vectors of a chunk, by the first warp of a pair.  blocks: how
 // many blocks of four tokens the pair has had.
 template <bool kBounded, bool kSplit>
-__device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &sh, Stage &st,
-                                               Scratch &sc,
+__device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &sh, Reach &st,
+                                               unsigned n, Scratch &sc,
                                                const Row &row, int head, int chunk, int lane,
                                                unsigned &blocks) {
     lane = made_anew(lane);
@@ -537,7 +565,7 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             put(&out.back[t & 3][4 * lane],
                 mul_pair(k[u][0], pair(reciprocal(r0.x), reciprocal(r0.y))),
                 mul_pair(k[u][1], pair(reciprocal(r1.x), reciprocal(r1.y))));
-            const int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
+            int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
             uint2 hi, lo;
             float2 x = both(mul_pair(k[u][0], reach[0]));
             split(x.x, x.y, hi.x, lo.x);
@@ -545,11 +573,13 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             split(x.x, x.y, hi.y, lo.y);
             *reinterpret_cast<uint2 *>(reached + to) = hi;
             *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
+            to = place(kC + order_of<kSplit>(t), 4 * (lane & 15));
             x = both(mul_pair(q[u][0], reach[0]));
-            hi.x = half_pair(x.x, x.y);
+            split(x.x, x.y, hi.x, lo.x);
             x = both(mul_pair(q[u][1], reach[1]));
-            hi.y = half_pair(x.x, x.y);
-            *reinterpret_cast<uint2 *>(reached + to + kC * 128) = hi;
+            split(x.x, x.y, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(reached + to) = hi;
+            *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
         }
         if ((t0 & 2) != 0) {
             put(&out.end[4 * lane], r[0], r[1]);
@@ -571,16 +601,17 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             f[2] = f[3];
             f[3] = 1.0f + expm1f(v * 0.693147180559945309f);
         }
-        *reinterpret_cast<float4 *>(&st.decay[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+        kda::cp_async_wait_all();
+        if (!wait_for_update(sh, n, p.err)) return false;
+        *reinterpret_cast<float4 *>(&update_of(sh, n).decay[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
     }
-    kda::cp_async_wait_all();
     __syncwarp();
     return true;
 }
 
 // The products between tokens, by the second warp of a pair.
 template <bool kSplit>
-__device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit> &sh, Stage &st,
+__device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit> &sh, unsigned n,
                                                  Scratch &sc, const Row &row, int head, int chunk,
                                                  int lane, unsigned &blocks) {
     lane = made_anew(lane);
@@ -644,6 +675,8 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit>
             (j < 2 ? sc.a : sc.b)[4 * block + 2 * (j & 1) + (c & 1)][g + 4 * (c & 2)] = x;
         }
         if (block == 3) {   // K P_C / P_t
+            if (!wait_for_update(sh, n, p.err)) return false;
+            Update &up = update_of(sh, n);
             const u64 scale = pair(kUpdateScale, kUpdateScale);
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
@@ -658,24 +691,25 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit>
                     split(y.x, y.y, hi.x, lo.x);
                     split(z.x, z.y, hi.y, lo.y);
                     const int to = place(order_of<kSplit>(g + 8 * i), 16 * (m & 3) + 4 * j);
-                    *reinterpret_cast<uint2 *>(st.update[0][m >> 2] + to) = hi;
-                    *reinterpret_cast<uint2 *>(st.update[1][m >> 2] + to) = lo;
+                    *reinterpret_cast<uint2 *>(up.update[0][m >> 2] + to) = hi;
+                    *reinterpret_cast<uint2 *>(up.update[1][m >> 2] + to) = lo;
                 }
             }
         }
         __syncwarp();
         if (lane == 0) kda::mbar_arrive(&sc.taken[blocks & 1]);
     }
-    // T, column lane & 15 in a lane, four rows at a time:
-    // T_t = beta_t (1_t - sum_{j<t} A_tj T_j)
+    // T and B T, column s in a lane of each half of the warp, four rows at a time:
+    // T_t = beta_t (1_t - sum_{j<t} A_tj T_j),  (B T)_t = sum_{j<=t} B_tj T_j
     {
         lane = made_anew(lane);
         const int s = lane & 15;
+        const bool second = lane >= 16;   // B T
+        Update &up = update_of(sh, n);
+        const float(*const m)[kC + 4] = second ? sc.b : sc.a;
 #pragma unroll 1
         for (int t = 0; t < kC; t += 4) {
-            float x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = t + u == s ? 1.0f : 0.0f;
+            float x[4] = {};
 #pragma unroll 1
             for (int i = 0; i < t; i += 4) {
                 float y[4];
@@ -683,41 +717,41 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit>
                 for (int u = 0; u < 4; ++u) y[u] = sc.t[i + u][s];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float4 n = kda::ld4(&sc.a[t + u][i]);
-                    x[u] = fmaf(-n.x, y[0], x[u]);
-                    x[u] = fmaf(-n.y, y[1], x[u]);
-                    x[u] = fmaf(-n.z, y[2], x[u]);
-                    x[u] = fmaf(-n.w, y[3], x[u]);
+                    const float4 n = kda::ld4(&m[t + u][i]);
+                    x[u] = fmaf(n.x, y[0], x[u]);
+                    x[u] = fmaf(n.y, y[1], x[u]);
+                    x[u] = fmaf(n.z, y[2], x[u]);
+                    x[u] = fmaf(n.w, y[3], x[u]);
                 }
             }
-            const float4 b = kda::ld4(&sc.beta[t]);
-            const float4 n1 = kda::ld4(&sc.a[t + 1][t]), n2 = kda::ld4(&sc.a[t + 2][t]);
-            const float4 n3 = kda::ld4(&sc.a[t + 3][t]);
-            x[0] *= b.x;
-            x[1] = b.y * fmaf(-n1.x, x[0], x[1]);
-            x[2] = b.z * fmaf(-n2.y, x[1], fmaf(-n2.x, x[0], x[2]));
-            x[3] = b.w * fmaf(-n3.z, x[2], fmaf(-n3.y, x[1], fmaf(-n3.x, x[0], x[3])));
-            // (both half warps have the same)
+            float y[4];   // T
+            {
+                const float4 b = kda::ld4(&sc.beta[t]);
+                const float4 n1 = kda::ld4(&sc.a[t + 1][t]), n2 = kda::ld4(&sc.a[t + 2][t]);
+                const float4 n3 = kda::ld4(&sc.a[t + 3][t]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sc.t[t + u][s] = x[u];
+                for (int u = 0; u < 4; ++u) y[u] = (t + u == s ? 1.0f : 0.0f) - x[u];
+                y[0] *= b.x;
+                y[1] = b.y * fmaf(-n1.x, y[0], y[1]);
+                y[2] = b.z * fmaf(-n2.y, y[1], fmaf(-n2.x, y[0], y[2]));
+                y[3] = b.w * fmaf(-n3.z, y[2], fmaf(-n3.y, y[1], fmaf(-n3.x, y[0], y[3])));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = __shfl_sync(kFull, y[u], s);
+            // (what lies above the diagonal of B is not looked at)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 n = kda::ld4(&sc.b[t + u][t]);
+                float z = fmaf(n.x, y[0], x[u]);
+                if (u > 0) z = fmaf(n.y, y[1], z);
+                if (u > 1) z = fmaf(n.z, y[2], z);
+                if (u > 2) z = fmaf(n.w, y[3], z);
+                if (!second) sc.t[t + u][s] = z = y[u];
+                up.inner[t + u][second ? s : kC + s] = z;
+            }
             __syncwarp();
         }
     }
-    __syncwarp();
-    // T as it is, B where V' has its tokens
-#pragma unroll 1
-    for (int n = 0; n < 4; ++n) {
-        const int t = 4 * n + (lane >> 3), i = 2 * (lane & 7);
-        *reinterpret_cast<float2 *>(st.inner + place(t, 32 + 2 * i)) =
-            *reinterpret_cast<const float2 *>(&sc.t[t][i]);
-        constexpr int kTokens = kC / kParts<kSplit>;
-        const int s0 = token_of<kSplit>(i / kTokens, i % kTokens);
-        const int s1 = token_of<kSplit>(i / kTokens, i % kTokens + 1);
-        const float x = s0 <= t ? sc.b[t][s0] * kBScale : 0.0f;
-        const float y = s1 <= t ? sc.b[t][s1] * kBScale : 0.0f;
-        *reinterpret_cast<uint32_t *>(st.inner + place(t, i)) = half_pair(x, y);
-    }
-    __syncwarp();
     return true;
 }
 
@@ -835,6 +869,21 @@ __device__ __forceinline__ float larger(float m, u64 xy) {
     return fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
 }
 
+// The product of x, all tokens' of a chunk, with the row of a triangular matrix
+// that is the part's i-th token's.
+template <bool kSplit>
+__device__ __forceinline__ float dot_row(const float *row, int i, const u64 (&x)[kC / 2]) {
+    u64 sum = 0ull;
+#pragma unroll
+    for (int n = 0; n <= (kSplit ? i : i >> 1); ++n) {   // four entries each, up to the diagonal
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(row + 4 * n);
+        sum = n == 0 ? mul_pair(f.x, x[0]) : fma_pair(f.x, x[2 * n], sum);
+        sum = fma_pair(f.y, x[2 * n + 1], sum);
+    }
+    const float2 y = both(sum);
+    return y.x + y.y;
+}
+
 // Named barriers of the consumers.
 template <int kId, int kMembers>
 __device__ __forceinline__ void meet() {
@@ -882,7 +931,7 @@ __device__ __forceinline__ int state_exponent(float bound, int ex) {
 }
 
 // The products of a chunk, by one warp each.
-__device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem) {
+__device__ __forceinline__ void issue_reach(const Reach &st, uint32_t tmem) {
     const uint64_t b = kda::sw128_desc(kda::smem_u32(st.reach[0]));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -891,23 +940,21 @@ __device__ __forceinline__ void issue_reach(const Stage &st, uint32_t tmem) {
 }
 
 // (columns of their own: products of different shapes are not kept in order)
-__device__ __forceinline__ void issue_low(const Stage &st, uint32_t tmem) {
+__device__ __forceinline__ void issue_low(const Reach &st, uint32_t tmem) {
     const uint64_t b = kda::sw128_desc(kda::smem_u32(st.reach[0]));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         umma(tmem + kColLow, tmem + kColS + 64 + 8 * k,
-             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), idesc(kC, false), k > 0);
+             b + (((k >> 2) * kTall * 128 + (k & 3) * 32) >> 4), idesc(2 * kC, false), k > 0);
 }
 
-__device__ __forceinline__ void issue_update(const Stage &st, uint32_t tmem) {
-    constexpr uint32_t kNarrow = idesc(kC, false), kAll = idesc(kD, true);
+__device__ __forceinline__ void issue_update(const Update &st, uint32_t tmem) {
+    constexpr uint32_t kAll = idesc(kD, true);
     const uint64_t hi = along_n(kda::smem_u32(st.update[0][0]), kC * 128);
     const uint64_t lo = along_n(kda::smem_u32(st.update[1][0]), kC * 128);
     umma(tmem + kColUpdate, tmem + kColY, hi, kAll, false);
     umma(tmem + kColUpdate, tmem + kColY, lo, kAll, true);
     umma(tmem + kColUpdate, tmem + kColY + 8, hi, kAll, true);
-    umma(tmem + kColInner, tmem + kColY,
-         kda::sw128_desc(kda::smem_u32(st.inner)), kNarrow, false);
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -938,10 +985,14 @@ __device__ __forceinline__ u64 sum_up_to(u64 *sums, u64 sum) {
 // All CTAs come to the same.
 __device__ __forceinline__ void make_plan(const Params &p, Shared<false> &sh, unsigned items) {
     Plan &plan = sh.plan;
-    unsigned *key = reinterpret_cast<unsigned *>(sh.stage[0].reach);   // not in use yet
+    unsigned *key = reinterpret_cast<unsigned *>(sh.reach[0].reach);   // not in use yet
     unsigned *cost = key + kPlanRows;
     u64 *sums = reinterpret_cast<u64 *>(cost + kPlanRows);
     u64 *column = sums + kThreads / 32;   // where it starts
+    u64 *start = column + kThreads + 1;   // of a row's cost for a head, falling
+    static_assert(2 * 4 * kPlanRows + 8 * (kThreads / 32 + kThreads + 1 + kPlanRows + 2) <=
+                      sizeof(Reach::reach),
+                  "what the plan is made of");
     const unsigned tid = threadIdx.x, B = (unsigned)p.B, H = (unsigned)p.H, G = gridDim.x;
     unsigned mine = 0;
     if (tid < B) {
@@ -975,12 +1026,12 @@ __device__ __forceinline__ void make_plan(const Params &p, Shared<false> &sh, un
     }
     __syncthreads();
     sum = sum_up_to(sums, cost[tid]);
-    plan.start[tid + 1] = sum;
-    if (tid == 0) plan.start[0] = 0;
-    if (tid == kThreads - 1) plan.start[kPlanRows + 1] = sum;
+    start[tid + 1] = sum;
+    if (tid == 0) start[0] = 0;
+    if (tid == kThreads - 1) start[kPlanRows + 1] = sum;
     __syncthreads();
-    auto cost_of = [&](unsigned n) { return plan.start[n / H + 1] - plan.start[n / H]; };
-    auto start_of = [&](unsigned n) { return plan.start[n / H] * H + n % H * cost_of(n); };
+    auto cost_of = [&](unsigned n) { return start[n / H + 1] - start[n / H]; };
+    auto start_of = [&](unsigned n) { return start[n / H] * H + n % H * cost_of(n); };
     const u64 total = start_of(items);
     // The CTAs whose first item alone is over the level of it and those behind it.
     const unsigned full = (unsigned)__syncthreads_count(
@@ -1073,18 +1124,20 @@ __device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, uns
                          "r"(kda_delta::kTile * 4)
                          : "memory");
         const unsigned chunks = (unsigned)(w.row.tokens + kC - 1) / kC;
-        for (unsigned c = (pair_of - count) % kPairs<kSplit>; c < chunks; c += kPairs<kSplit>) {
-            const unsigned stage = (count + c) % kStages<kSplit>;
-            const unsigned turn = (count + c) / kStages<kSplit>;
-            if (!wait<kSplit>(sh, &sh.empty[stage], (turn & 1) ^ 1, p.err)) return;
-            Stage &st = kSplit ? at_rank(sh.stage[stage], 0) : sh.stage[stage];
+        for (unsigned c = (pair_of + kPairs<kSplit> - count % kPairs<kSplit>) % kPairs<kSplit>;
+             c < chunks; c += kPairs<kSplit>) {
+            const unsigned n = count + c;
+            Reach &reach = kSplit ? at_rank(sh.reach[n % kReaches<kSplit>], 0)
+                                  : sh.reach[n % kReaches<kSplit>];
             Scratch &sc = sh.scratch[pair_of];
             bool made;
             if (warp < kPairs<kSplit>)
-                made = produce_tokens<kBounded, kSplit>(p, sh, st, sc, w.row, w.head, c, lane,
-                                                        blocks);
+                made = (kSplit ? wait_for_update(sh, n, p.err)
+                               : wait<kSplit>(sh, &sh.reach_empty[n % kReaches<kSplit>],
+                                              ((n / kReaches<kSplit>) & 1) ^ 1, p.err)) &&
+                       produce_tokens<kBounded, kSplit>(p, sh, reach, n, sc, w.row, w.head, c, lane, blocks);
             else
-                made = produce_products<kSplit>(p, sh, st, sc, w.row, w.head, c, lane, blocks);
+                made = produce_products<kSplit>(p, sh, n, sc, w.row, w.head, c, lane, blocks);
             if (!made) return;
             // the tensor cores read it
             if (kSplit)
@@ -1097,25 +1150,37 @@ __device__ __forceinline__ void produce(const Params &p, Shared<kSplit> &sh, uns
 #endif
             if (lane == 0) {
                 if (kSplit)
-                    arrive_at(&sh.full[stage], 0);
+                    arrive_at(&sh.full[n % kReaches<kSplit>], 0);
                 else
-                    kda::mbar_arrive(&sh.full[stage]);
+                    kda::mbar_arrive(&sh.full[n % kReaches<kSplit>]);
             }
         }
         count += chunks;
     }
 }
 
-// The consumer warps.  A wait that runs out ends nothing by itself: from then
-// on the warp, and soon all of them, go through the same barriers without
-// waiting, issuing or writing, so that no barrier is left with too few.
+// The largest of a row's parts.
 template <int kOf>
-__device__ __forceinline__ float largest_of(const float (&x)[4][kD], int r) {
+__device__ __forceinline__ float largest_of(const float (&x)[kOf][kD], int r) {
     float m = fmaxf(x[0][r], x[1][r]);
-    if (kOf > 2) m = fmaxf(m, fmaxf(x[2][r], x[3][r]));
+    if constexpr (kOf > 2) m = fmaxf(m, fmaxf(x[2][r], x[3][r]));
     return m;
 }
 
+// The warp is done with a place of a ring.
+template <bool kSplit>
+__device__ __forceinline__ void hand_back(uint64_t *empty, int lane) {
+    __syncwarp();
+    if (lane != 0) return;
+    if (kSplit)
+        arrive_at(empty, 1);
+    else
+        kda::mbar_arrive(empty);
+}
+
+// The consumer warps.  A wait that runs out ends nothing by itself: from then
+// on the warp, and soon all of them, go through the same barriers without
+// waiting, issuing or writing, so that no barrier is left with too few.
 template <bool kSplit, bool kPlanned>
 __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, unsigned items, int me,
                                         int lane) {
@@ -1163,17 +1228,16 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
         }
         const int chunks = (w.row.tokens + kC - 1) / kC;
         int step = 0;                               // of ex, due with the next addition
-        float added = 0.0f, f_reach = 0.0f, f_inner = 0.0f;
-        // turn c adds what chunk c - 1 brought, writes its outputs, and begins chunk c
+        float added = 0.0f;
+        // turn c adds what chunk c - 1 brought, makes chunk c's V' and writes its outputs
         for (int c = 0; c <= chunks; ++c) {
-            uint32_t o[kTokens / 2];   // outputs of chunk c - 1: from the state, and from the chunk itself
             const bool look = (c & 3) == 0 && c > 0;
             float most = 0.0f;
             if (c > 0) {
                 const unsigned before = count - 1;
                 ok &= wait(sh, &sh.s_done, before & 1, p.err);
                 kda::tc_fence_after();
-                const float *decay = &sh.stage[before % kStages<kSplit>].decay[kCols * part];
+                const float *decay = &sh.update[before % kUpdates<kSplit>].decay[kCols * part];
                 const u64 factor = pair(added, added);
                 const bool moved = __any_sync(kFull, step != 0);
 #pragma unroll 1
@@ -1213,63 +1277,33 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                         store_state(state + 32 * i + 16 * h, halves + 16 * i + 8 * h, s);
                     }
                 }
-                {
-                    uint32_t x[kTokens], y[kTokens];
-                    load(tmem + kColReach + kC + kTokens * part, x);
-                    load(tmem + kColInner + kTokens * part, y);
-                    arrived(x);
-                    arrived(y);
-#pragma unroll
-                    for (int t = 0; t < kTokens / 2; ++t) {
-                        const float2 z = both(fma_pair(pair_of(y[2 * t], y[2 * t + 1]),
-                                                       pair(f_inner, f_inner),
-                                                       mul_pair(pair_of(x[2 * t], x[2 * t + 1]),
-                                                                pair(f_reach, f_reach))));
-                        o[t] = kda_cache::pack(z.x, z.y, __nv_bfloat16());
-                    }
-                }
-                // chunk c - 1 is done with its stage
-                __syncwarp();
-                if (lane == 0) {
-                    if (kSplit)
-                        arrive_at(&sh.empty[before % kStages<kSplit>], 1);
-                    else
-                        kda::mbar_arrive(&sh.empty[before % kStages<kSplit>]);
-                }
             }
             if (c < chunks) {
                 if (look) sh.most[part][r] = most * power_of_two(-ex);
-                ok &= wait<kSplit>(sh, &sh.full[count % kStages<kSplit>], (count / kStages<kSplit>) & 1, p.err);
+                ok &= wait<kSplit>(sh, &sh.full[count % kReaches<kSplit>],
+                                   (count / kReaches<kSplit>) & 1, p.err);
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
                 meet<1, 128 * kOf>();
                 if (kSplit) asm volatile("fence.proxy.async;" ::: "memory");
                 if (ok && me == 0 && elected()) {
                     kda::tc_fence_after();
-                    issue_reach(sh.stage[count % kStages<kSplit>], sh.tmem);
+                    issue_reach(sh.reach[count % kReaches<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
                 if (ok && me == 4 && elected()) {
                     kda::tc_fence_after();
-                    issue_low(sh.stage[count % kStages<kSplit>], sh.tmem);
+                    issue_low(sh.reach[count % kReaches<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
             }
-            if (c > 0) {
-                const int n = ok ? w.row.tokens - (c - 1) * kC - kTokens * part : 0;
-                uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) +
-                                ((long long)(w.row.first + (c - 1) * kC + kTokens * part) * p.H +
-                                 w.head) * kD + r;
-                const long long next = (long long)p.H * kD;
-#pragma unroll
-                for (int t = 0; t < kTokens; ++t, dst += next)
-                    if (t < n) *dst = (uint16_t)(t & 1 ? o[t / 2] >> 16 : o[t / 2]);
-            }
+            if (c > 0) hand_back<kSplit>(&sh.update_empty[(count - 1) % kUpdates<kSplit>], lane);
             if (c == chunks) break;
-            const unsigned stage = count % kStages<kSplit>, parity = count & 1;
-            const Stage &st = sh.stage[stage];
+            const unsigned parity = count & 1;
+            const Reach &st = sh.reach[count % kReaches<kSplit>];
+            const Update &up = sh.update[count % kUpdates<kSplit>];
             if (look) bound = largest_of<kOf>(sh.most, r);
             u64 x[kC / 2];
             float vmax = 0.0f;
@@ -1298,22 +1332,12 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                                                       pair_of(z[2 * n], z[2 * n + 1]))),
                                     pair(fx, fx), x[n]);
             }
+            if (!kSplit) hand_back<kSplit>(&sh.reach_empty[count % kReaches<kSplit>], lane);
             {
                 float d[kTokens];   // V' of the part's tokens
 #pragma unroll
                 for (int i = 0; i < kTokens; ++i) {
-                    const unsigned char *t = st.inner + token_of<kSplit>(part, i) * 128;
-                    const int turn = token_of<kSplit>(part, i) & 7;
-                    u64 sum = 0ull;
-#pragma unroll
-                    for (int n = 0; n <= (kSplit ? i : i >> 1); ++n) {   // four entries each
-                        const ulonglong2 f =
-                            *reinterpret_cast<const ulonglong2 *>(t + (((4 + n) ^ turn) << 4));
-                        sum = n == 0 ? mul_pair(f.x, x[0]) : fma_pair(f.x, x[2 * n], sum);
-                        sum = fma_pair(f.y, x[2 * n + 1], sum);
-                    }
-                    const float2 y = both(sum);
-                    d[i] = y.x + y.y;
+                    d[i] = dot_row<kSplit>(up.inner[token_of<kSplit>(part, i)] + kC, i, x);
                 }
                 float sum = 0.0f;
                 u64 y[kTokens / 2];
@@ -1326,17 +1350,46 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                 sh.sum[part][r] = sum;
             }
             const float back = power_of_two(-ey);
-            f_reach = power_of_two(-ex) * (p.scale / kKeyScale);
-            f_inner = back * (p.scale / kBScale);
             kda::tmem_wait_st();
             kda::tc_fence_before();
             meet<2, 128 * kOf>();
             if (ok && me == 0 && elected()) {
                 kda::tc_fence_after();
-                issue_update(st, sh.tmem);
+                issue_update(up, sh.tmem);
                 kda::umma_commit(&sh.s_done);
             }
             __syncwarp();
+            {   // outputs, from the state and from the chunk itself, while S is updated
+                u64 o[kTokens / 2];
+                {
+                    uint32_t hi[kTokens], lo[kTokens], low[kTokens];
+                    load(tmem + kColReach + kC + kTokens * part, hi);
+                    load(tmem + kColReach + 3 * kC + kTokens * part, lo);
+                    load(tmem + kColLow + kC + kTokens * part, low);
+                    arrived(hi);
+                    arrived(lo);
+                    arrived(low);
+                    const float f = power_of_two(-ex) * (p.scale / kKeyScale);
+#pragma unroll
+                    for (int i = 0; i < kTokens; i += 2)
+                        o[i / 2] = mul_pair(add_pair(pair_of(hi[i], hi[i + 1]),
+                                                     add_pair(pair_of(lo[i], lo[i + 1]),
+                                                              pair_of(low[i], low[i + 1]))),
+                                            pair(f, f));
+                }
+                const int n = ok ? w.row.tokens - c * kC : 0;
+                const long long token = (long long)p.H * kD;
+                __nv_bfloat16 *dst = p.out + (w.row.first + (long long)c * kC) * token +
+                                     w.head * kD + r;
+#pragma unroll
+                for (int i = 0; i < kTokens; ++i) {
+                    const int t = token_of<kSplit>(part, i);
+                    const float y = dot_row<kSplit>(up.inner[t], i, x);
+                    const float2 z = both(o[i / 2]);
+                    if (t < n)
+                        dst[t * token] = __float2bfloat16_rn(fmaf(y, p.scale, i & 1 ? z.y : z.x));
+                }
+            }
             // S is at most what it was and all that is added to it
 #pragma unroll
             for (int i = 0; i < kOf; ++i) bound += sh.sum[i][r];
@@ -1374,10 +1427,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
     if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f;
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
-        for (int i = 0; i < kStages<kSplit>; ++i) {
+        for (int i = 0; i < kReaches<kSplit>; ++i) {
             kda::mbar_init(&sh.full[i], 2);
-            kda::mbar_init(&sh.empty[i], 4 * kParts<kSplit>);
+            kda::mbar_init(&sh.reach_empty[i], 4 * kParts<kSplit>);
         }
+        for (int i = 0; i < kUpdates<kSplit>; ++i)
+            kda::mbar_init(&sh.update_empty[i], 4 * kParts<kSplit>);
         if (!kSplit || rank() == 1)
             for (int i = 0; i < 2 * kPairs<kSplit>; ++i) {
                 kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);

@@ -20,23 +20,30 @@ def log_decay(x, a_log, lower_bound=None):
     return -a * (np.maximum(x, 0.0) + np.log1p(np.exp(-np.abs(x))))
 
 
-def row(state, q, k, v, g_raw, beta_raw, a_log, g_bias, lower_bound=None, scale=None):
-    """One row from state [H, V, K]: (outputs [T, H, V], the state behind it,
-    sizes [T, H, V]).  A size bounds what an output's sums are made of: the
-    largest norm of its row of the state and the deltas that were added to it,
-    over the 16 tokens up to it."""
+def tokens(state, q, k, v, g_raw, beta_raw, a_log, g_bias, lower_bound=None, scale=None):
+    """One row from state [H, V, K], token by token: (output [H, V], the state
+    behind the token, its delta [H, V])."""
     s = np.array(state, dtype=np.float64)
     n, h, d = q.shape
     scale = d ** -0.5 if scale is None else scale
-    out, sizes = np.zeros((n, h, d)), np.zeros((n, h, d))
-    norms, deltas = [np.sqrt((s * s).sum(-1))], []
     for t in range(n):
         s = s * np.exp(log_decay(g_raw[t] + g_bias.reshape(h, d), a_log, lower_bound))[:, None, :]
         unit_k = k[t] / np.sqrt((k[t] ** 2).sum(-1, keepdims=True) + 1e-6)
         unit_q = q[t] / np.sqrt((q[t] ** 2).sum(-1, keepdims=True) + 1e-6)
         delta = _sigmoid(beta_raw[t])[:, None] * (v[t] - np.einsum("hvk,hk->hv", s, unit_k))
         s = s + delta[:, :, None] * unit_k[:, None, :]
-        out[t] = scale * np.einsum("hvk,hk->hv", s, unit_q)
+        yield scale * np.einsum("hvk,hk->hv", s, unit_q), s, delta
+
+
+def row(state, q, *args):
+    """One row, with the arguments of tokens(): (outputs [T, H, V], the state
+    behind it, sizes [T, H, V]).  A size bounds what an output's sums are made
+    of: the largest norm of its row of the state and the deltas that were added
+    to it, over the 16 tokens up to it."""
+    s = np.array(state, dtype=np.float64)
+    out, sizes = np.zeros(q.shape), np.zeros(q.shape)
+    norms, deltas = [np.sqrt((s * s).sum(-1))], []
+    for t, (out[t], s, delta) in enumerate(tokens(state, q, *args)):
         norms.append(np.sqrt((s * s).sum(-1)))
         deltas.append(np.abs(delta))
         first = max(0, t - 15)

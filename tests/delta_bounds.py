@@ -1,0 +1,44 @@
+"""Checks of kda_prefill and kda_decode beside what each token leaves, and gates
+of known strength.
+
+Bounds.  States: 1e-5 of the tile's largest value, the library's stated
+tolerance.  An output is a product of such a state with a query of norm 1, so
+1e-5 sqrt(128) of the largest value of the tile behind its token, times the
+scale, and one rounding to bf16, 2^-8 of the value."""
+
+from __future__ import annotations
+
+import numpy as np
+import torch
+
+from oracle import delta_oracle as D
+from tests.attention_helpers import f64
+from tests.delta_helpers import run
+
+
+def hold(c, initial=None, outputs=True):
+    """Runs the case and holds the rows' states, and their outputs, to the
+    oracle."""
+    start, inputs = f64(c.pool), [f64(x) for x in c.inputs()]
+    got = f64(run(c, initial))
+    assert int(c.err.item()) == 0
+    state, cu = f64(c.pool), c.cu.tolist()
+    scale = 128 ** -0.5 if c.scale is None else c.scale
+    sources = c.slots if initial is None else initial
+    for slot, source, first, end in zip(c.slots.tolist(), sources.tolist(), cu, cu[1:]):
+        s = start[source] if source > 0 else np.zeros(start.shape[1:])
+        for t, (out, s, _) in enumerate(D.tokens(
+                s, *(x[first:end] for x in inputs[:5]), *inputs[5:], c.lower_bound, scale), first):
+            more = 1e-5 * 128 ** 0.5 * abs(scale) * np.abs(s).max((1, 2))[:, None]
+            off = np.abs(got[t] - out) / (2.0 ** -8 * (np.abs(out) + more) + more + 1e-38)
+            assert not outputs or off.max() <= 1.0, (t - first, end - first, off.max())
+        off = np.abs(state[slot] - s).max((1, 2)) / (1e-5 * np.abs(s).max((1, 2)) + 1e-38)
+        assert off.max() <= 1.0, (end - first, off.max())
+
+
+def decays_of(c, each):
+    """Each token takes exp(-each) of the state, of all channels or of each."""
+    c.g = torch.zeros_like(c.g)
+    c.A_log = torch.zeros_like(c.A_log)
+    each = torch.as_tensor(each, dtype=torch.float64).expand(len(c.bias))
+    c.bias = (each + torch.log(-torch.expm1(-each))).float().to(c.bias.device)   # softplus^-1
