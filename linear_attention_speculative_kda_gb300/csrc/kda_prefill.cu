@@ -104,7 +104,7 @@ constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
 
 // Powers of two on the operands.
 constexpr float kKeyScale = 1024.0f;      // K P, Q P
-constexpr float kUpdateScale = 1024.0f;   // K P_C / P_t
+constexpr int kUpdateExponent = 13;       // of a token's largest K P_C / P_t
 
 // One chunk's operands: fp16 matrices of rows of 128 bytes with the 128-byte
 // swizzle (16-byte unit u of row r at u ^ (r & 7)), two blocks of 64 channels.
@@ -118,6 +118,7 @@ struct __align__(1024) Update {
     unsigned char update[2][2][kC * 128]; // K P_C / P_t, [hi, lo][64 channels][token's place]
     float inner[kC][2 * kC];              // [token t]: (B T)_t, then T_t
     float decay[kD];                      // P_C
+    float given[kC];                      // [token's place]: about its largest K P_C / P_t
 };
 
 // Consumer threads that share a row of S: each has its part of the columns and
@@ -199,7 +200,7 @@ struct Shared : Work_space<kSplit> {
     Plan plan;
     // (what is read 16 bytes at a time)
     __align__(16) float most[kParts<kSplit>][kD];  // largest of each part of a row of S
-    __align__(16) float sum[kParts<kSplit>][kD];   // of |V'| over each part's tokens, of a row
+    __align__(16) float sum[kParts<kSplit>][kD];   // of |V'| as given, of each part's tokens
     __align__(16) float zeros[kD];
     uint64_t full[kReaches<kSplit>];      // both operands
     uint64_t reach_empty[kReaches<kSplit>], update_empty[kUpdates<kSplit>];
@@ -254,6 +255,22 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(rest) : "l"(pair(x, y)), "l"(pair(h.x, h.y)));
     const float2 r = both(rest);
     lo = half_pair(r.x, r.y);
+}
+
+// floor(log2 |x|) of x, at least -110 (0 and the like), 127 for what is not
+// finite.
+__device__ __forceinline__ int exponent_of(float x) {
+    const int e = (int)((__float_as_uint(x) >> 23) & 0xff) - 127;
+    return max(-110, min(127, e));
+}
+
+__device__ __forceinline__ float power_of_two(int e) {   // -126 <= e <= 127
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ float larger(float m, u64 xy) {
+    const float2 x = both(xy);
+    return fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
 }
 
 // Where two CTAs share a row and head (kSplit), the first consumes and the
@@ -678,20 +695,36 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit>
         if (block == 3) {   // K P_C / P_t
             if (!wait_for_update(sh, n, p.err)) return false;
             Update &up = update_of(sh, n);
-            const u64 scale = pair(kUpdateScale, kUpdateScale);
+            float most[2] = {};
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
                 no_further_ahead();
                 const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&in.end[16 * m + 4 * j]);
-                const u64 e0 = mul_pair(f.x, scale), e1 = mul_pair(f.y, scale);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {   // tokens g and g + 8
-                    const float2 y = both(mul_pair(w[i][2 * m], e0));
-                    const float2 z = both(mul_pair(w[i][2 * m + 1], e1));
+                    w[i][2 * m] = mul_pair(w[i][2 * m], f.x);
+                    w[i][2 * m + 1] = mul_pair(w[i][2 * m + 1], f.y);
+                    most[i] = larger(larger(most[i], w[i][2 * m]), w[i][2 * m + 1]);
+                }
+            }
+            // A token's are held beside their own largest, whose power of two V' takes:
+            // what the chunk's decays leave of a token is as exact as what they leave of
+            // the others, however large its value was.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                most[i] = fmaxf(most[i], __shfl_xor_sync(kFull, most[i], 1));
+                most[i] = fmaxf(most[i], __shfl_xor_sync(kFull, most[i], 2));
+                const int e = exponent_of(most[i]), row = order_of<kSplit>(g + 8 * i);
+                const float f = power_of_two(kUpdateExponent - e);
+                if (j == 0) up.given[row] = power_of_two(e);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const float2 y = both(mul_pair(w[i][2 * m], pair(f, f)));
+                    const float2 z = both(mul_pair(w[i][2 * m + 1], pair(f, f)));
                     uint2 hi, lo;
                     split(y.x, y.y, hi.x, lo.x);
                     split(z.x, z.y, hi.y, lo.y);
-                    const int to = place(order_of<kSplit>(g + 8 * i), 16 * (m & 3) + 4 * j);
+                    const int to = place(row, 16 * (m & 3) + 4 * j);
                     *reinterpret_cast<uint2 *>(up.update[0][m >> 2] + to) = hi;
                     *reinterpret_cast<uint2 *>(up.update[1][m >> 2] + to) = lo;
                 }
@@ -757,17 +790,6 @@ __device__ __forceinline__ bool produce_products(const Params &p, Shared<kSplit>
 }
 
 // ---------------------------------------------------------------- consumer --
-
-// floor(log2 |x|) of x, at least -110 (0 and the like), 127 for what is not
-// finite.
-__device__ __forceinline__ int exponent_of(float x) {
-    const int e = (int)((__float_as_uint(x) >> 23) & 0xff) - 127;
-    return max(-110, min(127, e));
-}
-
-__device__ __forceinline__ float power_of_two(int e) {   // -126 <= e <= 127
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
 
 // Instruction descriptor of kind::f16: fp16 operands, fp32 sums, 128 rows, A
 // along K, B along K or along N.
@@ -865,11 +887,6 @@ __device__ __forceinline__ u64 pair_of(uint32_t x, uint32_t y) {
     return pair(__uint_as_float(x), __uint_as_float(y));
 }
 
-__device__ __forceinline__ float larger(float m, u64 xy) {
-    const float2 x = both(xy);
-    return fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
-}
-
 // The product of x, all tokens' of a chunk, with the row of a triangular matrix
 // that is the part's i-th token's.
 template <bool kSplit>
@@ -889,6 +906,12 @@ __device__ __forceinline__ float dot_row(const float *row, int i, const u64 (&x)
 template <int kId, int kMembers>
 __device__ __forceinline__ void meet() {
     asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kMembers) : "memory");
+}
+
+// Those that share 32 rows of S.
+template <int kOf>
+__device__ __forceinline__ void meet_row(int me) {
+    asm volatile("bar.sync %0, %1;" ::"r"(3 + (me & 3)), "n"(32 * kOf) : "memory");
 }
 
 // 16 channels of a row of S, as they are and as two fp16 numbers each, to
@@ -924,8 +947,7 @@ __device__ __forceinline__ void store_split(uint32_t to, const u64 (&x)[kPairsOf
 
 // S is held times 2^ex, a power of its row.  As held, the bound of the row that
 // is known stays below 2^13, so fp16 has it, and above 2^6, so that its 22
-// bits mean something; else it moves to 2^9.  An entry of V' is at most |v| and
-// the norm of the row of S before its token, which grows by at most |v| a token.
+// bits mean something; else it moves to 2^9.
 __device__ __forceinline__ int state_exponent(float bound, int ex) {
     const int e = exponent_of(bound);
     return e + ex > 12 || e + ex < 6 ? 9 - e : ex;
@@ -1307,14 +1329,9 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
             const Update &up = sh.update[count % kUpdates<kSplit>];
             if (look) bound = largest_of<kOf>(sh.most, r);
             u64 x[kC / 2];
-            float vmax = 0.0f;
 #pragma unroll
-            for (int n = 0; n < kC / 2; ++n) {
+            for (int n = 0; n < kC / 2; ++n)
                 x[n] = pair(__bfloat162float(st.v[2 * n][r]), __bfloat162float(st.v[2 * n + 1][r]));
-                vmax = larger(vmax, x[n]);
-            }
-            // (11.4 > sqrt(128))
-            const int ey = 10 - exponent_of(fmaf(11.4f, bound, 16.0f * vmax));
             const float fx = -power_of_two(-ex) / kKeyScale;
             ok &= wait(sh, &sh.u_done, parity, p.err);
             kda::tc_fence_after();
@@ -1334,23 +1351,30 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                                     pair(fx, fx), x[n]);
             }
             if (!kSplit) hand_back<kSplit>(&sh.reach_empty[count % kReaches<kSplit>], lane);
+            float sum = 0.0f, back;   // of |V'| as given, of the row's tokens
             {
-                float d[kTokens];   // V' of the part's tokens
+                u64 y[kTokens / 2];   // V' of the part's tokens, times what is given of them
 #pragma unroll
-                for (int i = 0; i < kTokens; ++i) {
-                    d[i] = dot_row<kSplit>(up.inner[token_of<kSplit>(part, i)] + kC, i, x);
+                for (int i = 0; i < kTokens; i += 2) {
+                    const float *f = up.inner[token_of<kSplit>(part, i)] + kC;
+                    const float *f1 = up.inner[token_of<kSplit>(part, i + 1)] + kC;
+                    y[i / 2] = mul_pair(
+                        pair(dot_row<kSplit>(f, i, x), dot_row<kSplit>(f1, i + 1, x)),
+                        *reinterpret_cast<const u64 *>(&up.given[kTokens * part + i]));
+                    const float2 z = both(y[i / 2]);
+                    sum += fabsf(z.x) + fabsf(z.y);
                 }
-                float sum = 0.0f;
-                u64 y[kTokens / 2];
-#pragma unroll
-                for (int n = 0; n < kTokens / 2; ++n) {
-                    sum += fabsf(d[2 * n]) + fabsf(d[2 * n + 1]);
-                    y[n] = pair(d[2 * n], d[2 * n + 1]);
-                }
-                store_split(tmem + kColY + kTokens / 2 * part, y, power_of_two(ey));
+                // the power of two is from V' itself, so that weakly written tokens keep
+                // their bits (a bound by the values and the state does not know beta)
                 sh.sum[part][r] = sum;
+                meet_row<kOf>(me);
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kOf; ++i) sum += sh.sum[i][r];
+                const int ey = 13 - exponent_of(sum);
+                store_split(tmem + kColY + kTokens / 2 * part, y, power_of_two(ey));
+                back = power_of_two(-ey);
             }
-            const float back = power_of_two(-ey);
             kda::tmem_wait_st();
             kda::tc_fence_before();
             meet<2, 128 * kOf>();
@@ -1392,12 +1416,11 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                 }
             }
             // S is at most what it was and all that is added to it
-#pragma unroll
-            for (int i = 0; i < kOf; ++i) bound += sh.sum[i][r];
+            bound += 2.0f * sum;
             const int moved = state_exponent(bound, ex);
             step = moved - ex;
             ex = moved;
-            added = back * power_of_two(ex) / kUpdateScale;
+            added = back / (float)(1 << kUpdateExponent) * power_of_two(ex);
             ++count;
         }
         kda::tmem_wait_st();

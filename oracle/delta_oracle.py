@@ -9,7 +9,8 @@ import numpy as np
 
 
 def _sigmoid(x):
-    return 0.5 * (1.0 + np.tanh(0.5 * x))
+    z = np.exp(-np.abs(x))   # (as exact beside itself far below 0)
+    return np.where(x < 0.0, z, 1.0) / (1.0 + z)
 
 
 def log_decay(x, a_log, lower_bound=None):
