@@ -201,7 +201,7 @@ struct Shared : Work_space<kSplit> {
     // (what is read 16 bytes at a time)
     __align__(16) float most[kParts<kSplit>][kD];  // largest of each part of a row of S
     __align__(16) float sum[kParts<kSplit>][kD];   // of |V'| as given, of each part's tokens
-    __align__(16) float zeros[kD];
+    __align__(16) float zeros[kD], ones[kD];
     uint64_t full[kReaches<kSplit>];      // both operands
     uint64_t reach_empty[kReaches<kSplit>], update_empty[kUpdates<kSplit>];
     uint64_t u_done, s_done;              // products of a chunk
@@ -268,9 +268,10 @@ __device__ __forceinline__ float power_of_two(int e) {   // -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float larger(float m, u64 xy) {
-    const float2 x = both(xy);
-    return fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+__device__ __forceinline__ float larger(float m, u64 xy) {   // of m >= 0, |x| and |y|
+    const float2 v = both(xy);
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v.x), "f"(v.y));
+    return m;
 }
 
 // Where two CTAs share a row and head (kSplit), the first consumes and the
@@ -945,12 +946,16 @@ __device__ __forceinline__ void store_split(uint32_t to, const u64 (&x)[kPairsOf
     store(to + 8, lo);
 }
 
-// S is held times 2^ex, a power of its row.  As held, the bound of the row that
-// is known stays below 2^13, so fp16 has it, and above 2^6, so that its 22
-// bits mean something; else it moves to 2^9.
+// S is held times 2^ex, a power of its row.  As held, a bound of the row's largest
+// stays below 2^15, so that fp16 has it, and the largest above 2^-2, so that what
+// is left out of two fp16 numbers, 2^-25, is below 2^-23 of it; else the row moves
+// to 2^8.  (Rows gain and lose some powers of two from chunk to chunk where strong
+// decays leave the last tokens' values alone: moving costs a twentieth of a turn.)
+constexpr int kHeld = 8, kLeast = -2, kMost = 14, kMostExponent = 119;
+
 __device__ __forceinline__ int state_exponent(float bound, int ex) {
     const int e = exponent_of(bound);
-    return e + ex > 12 || e + ex < 6 ? 9 - e : ex;
+    return e + ex > kMost || e + ex < kLeast ? min(kHeld - e, kMostExponent) : ex;
 }
 
 // The products of a chunk, by one warp each.
@@ -1221,7 +1226,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
         if (w.row.tokens == 0) continue;
         const long long slot = (long long)p.H * kda_delta::kTile;
         const long long at = (long long)w.head * kda_delta::kTile + r * kD + kCols * part;
-        float bound;   // of the row's values
+        float bound;   // the largest of the row's values, or above it
         int ex;
         {
             const float *src = p.pool + max(w.row.from, 0) * slot + at;
@@ -1237,9 +1242,9 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) most = larger(most, s[i]);
             sh.most[part][r] = most;
-            meet<1, 128 * kOf>();
+            meet_row<kOf>(me);
             bound = largest_of<kOf>(sh.most, r);
-            ex = 9 - exponent_of(bound);
+            ex = min(kHeld - exponent_of(bound), kMostExponent);
             const u64 f = pair(power_of_two(ex), power_of_two(ex));
 #pragma unroll
             for (int i = 0; i < kCols / 16; ++i) {
@@ -1254,55 +1259,74 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
         float added = 0.0f;
         // turn c adds what chunk c - 1 brought, makes chunk c's V' and writes its outputs
         for (int c = 0; c <= chunks; ++c) {
-            const bool look = (c & 3) == 0 && c > 0;
-            float most = 0.0f;
             if (c > 0) {
                 const unsigned before = count - 1;
                 ok &= wait(sh, &sh.s_done, before & 1, p.err);
                 kda::tc_fence_after();
                 const float *decay = &sh.update[before % kUpdates<kSplit>].decay[kCols * part];
-                const u64 factor = pair(added, added);
-                const bool moved = __any_sync(kFull, step != 0);
+                bool all = (c & 3) == 0;   // look at all columns, not at some
+                for (;;) {
+                    float most = 0.0f;
+                    const u64 factor = pair(added, added);
+                    const bool moved = __any_sync(kFull, step != 0);
 #pragma unroll 1
-                for (int i = 0; i < kCols / 32; ++i) {
-                    uint32_t u[2][16], x[2][16];
+                    for (int i = 0; i < kCols / 32; ++i) {
+                        uint32_t u[2][16], x[2][16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        kda::tmem_ld16(tmem + kColUpdate + kCols * part + 32 * i + 16 * h, u[h]);
-                        kda::tmem_ld16(state + 32 * i + 16 * h, x[h]);
-                    }
+                        for (int h = 0; h < 2; ++h) {
+                            kda::tmem_ld16(tmem + kColUpdate + kCols * part + 32 * i + 16 * h, u[h]);
+                            kda::tmem_ld16(state + 32 * i + 16 * h, x[h]);
+                        }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        arrived(u[h]);
-                        arrived(x[h]);
-                        u64 s[8];
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) s[n] = pair_of(x[h][2 * n], x[h][2 * n + 1]);
-                        if (moved) {   // in two powers: a step may be twice as far as one goes
-                            const float g = power_of_two(step / 2);
-                            const float g2 = power_of_two(step - step / 2);
+                        for (int h = 0; h < 2; ++h) {
+                            arrived(u[h]);
+                            arrived(x[h]);
+                            u64 s[8];
 #pragma unroll
                             for (int n = 0; n < 8; ++n)
-                                s[n] = mul_pair(mul_pair(s[n], pair(g, g)), pair(g2, g2));
-                        }
+                                s[n] = pair_of(x[h][2 * n], x[h][2 * n + 1]);
+                            if (moved) {   // in two powers: a step may be twice as far as one goes
+                                const float g = power_of_two(step / 2);
+                                const float g2 = power_of_two(step - step / 2);
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(
-                                decay + 32 * i + 16 * h + 4 * n);
-                            s[2 * n] = fma_pair(pair_of(u[h][4 * n], u[h][4 * n + 1]), factor,
-                                                mul_pair(s[2 * n], d.x));
-                            s[2 * n + 1] = fma_pair(pair_of(u[h][4 * n + 2], u[h][4 * n + 3]),
-                                                    factor, mul_pair(s[2 * n + 1], d.y));
-                        }
-                        if (look)
+                                for (int n = 0; n < 8; ++n)
+                                    s[n] = mul_pair(mul_pair(s[n], pair(g, g)), pair(g2, g2));
+                            }
 #pragma unroll
-                            for (int n = 0; n < 8; ++n) most = larger(most, s[n]);
-                        store_state(state + 32 * i + 16 * h, halves + 16 * i + 8 * h, s);
+                            for (int n = 0; n < 4; ++n) {
+                                const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(
+                                    decay + 32 * i + 16 * h + 4 * n);
+                                s[2 * n] = fma_pair(pair_of(u[h][4 * n], u[h][4 * n + 1]), factor,
+                                                    mul_pair(s[2 * n], d.x));
+                                s[2 * n + 1] = fma_pair(pair_of(u[h][4 * n + 2], u[h][4 * n + 3]),
+                                                        factor, mul_pair(s[2 * n + 1], d.y));
+                            }
+                            most = larger(larger(most, s[0]), s[1]);
+                            if (all)
+#pragma unroll
+                                for (int n = 2; n < 8; ++n) most = larger(most, s[n]);
+                            store_state(state + 32 * i + 16 * h, halves + 16 * i + 8 * h, s);
+                        }
                     }
+                    if (c == chunks) break;
+                    // The bound knows of no decay.  Where the row is far below it, the columns
+                    // that were looked at are: then all are, and the row moves.
+                    sh.most[part][r] = most;
+                    meet_row<kOf>(me);
+                    most = largest_of<kOf>(sh.most, r);
+                    if (all) bound = most * power_of_two(-ex);
+                    const bool low = bound > 0.0f && exponent_of(most) < kLeast;
+                    step = low && all ? min(kHeld - exponent_of(most), kMostExponent - ex) : 0;
+                    ex += step;
+                    if (!__any_sync(kFull, low && !(all && step == 0))) break;
+                    all = true;
+                    added = 0.0f;   // (it is there)
+                    decay = sh.ones;
+                    kda::tmem_wait_st();
+                    meet_row<kOf>(me);   // before `most` is written again
                 }
             }
             if (c < chunks) {
-                if (look) sh.most[part][r] = most * power_of_two(-ex);
                 ok &= wait<kSplit>(sh, &sh.full[count % kReaches<kSplit>],
                                    (count / kReaches<kSplit>) & 1, p.err);
                 kda::tmem_wait_st();
@@ -1327,7 +1351,6 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
             const unsigned parity = count & 1;
             const Reach &st = sh.reach[count % kReaches<kSplit>];
             const Update &up = sh.update[count % kUpdates<kSplit>];
-            if (look) bound = largest_of<kOf>(sh.most, r);
             u64 x[kC / 2];
 #pragma unroll
             for (int n = 0; n < kC / 2; ++n)
@@ -1448,7 +1471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
     extern __shared__ __align__(1024) unsigned char smem[];
     Shared<kSplit> &sh = *reinterpret_cast<Shared<kSplit> *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f;
+    if (threadIdx.x < kD) sh.zeros[threadIdx.x] = 0.0f, sh.ones[threadIdx.x] = 1.0f;
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
         for (int i = 0; i < kReaches<kSplit>; ++i) {

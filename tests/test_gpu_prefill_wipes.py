@@ -1,0 +1,44 @@
+"""GPU: states of kda_prefill behind decays that take most of them away are as
+exact beside what is left (bounds in delta_bounds)."""
+
+import pytest
+import torch
+
+from tests.delta_bounds import decays_of, hold
+from tests.delta_helpers import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("each", [0.7, 2.0, 5.0, 20.0])
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8])
+@pytest.mark.parametrize("lens,heads", [([18, 60, 130], 2), ([600], 2), ([40, 50] * 40, 2)])
+def test_a_large_state_that_decays_away(lens, heads, size, each):
+    c = Case(lens, heads, seed=8, size=size)
+    decays_of(c, each)
+    hold(c, outputs=False)
+
+
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e10])
+def test_strong_gates_take_a_large_state_away(size):
+    c = Case([60, 130], 2, seed=10, memory="short", size=size)
+    c.bias += 6.0
+    c.A_log += 3.0
+    hold(c, outputs=False)
+
+
+@pytest.mark.parametrize("at", [3, 18, 31])
+@pytest.mark.parametrize("tokens", [35, 90, 530])
+@pytest.mark.parametrize("size", [1e4, 1e8])
+def test_a_large_value_that_decays_away(tokens, at, size):
+    c = Case([tokens], 2, seed=11)
+    c.v = c.v.clone()
+    c.v[at] *= size
+    decays_of(c, 20.0)
+    hold(c, outputs=False)
+    c = Case([tokens], 2, seed=12)     # taken by one token's gate
+    c.v, c.g = c.v.clone(), c.g.clone()
+    c.v[at] *= size
+    c.bias[:], c.A_log[:] = -4.0, 0.0
+    c.g[at + 2] = 32.0
+    hold(c, outputs=False)
