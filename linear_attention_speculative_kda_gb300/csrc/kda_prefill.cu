@@ -103,7 +103,8 @@ constexpr long long kWaitBudget = 4000000000LL;   // clock cycles (about 2 s)
 #endif
 
 // Powers of two on the operands.
-constexpr float kKeyScale = 1024.0f;      // K P, Q P
+constexpr int kKeyExponent = 14;          // K P, Q P: of the largest P
+constexpr float kKeyLeast = 0x1p10f;      // below which it is moved there again
 constexpr int kUpdateExponent = 13;       // of a token's largest K P_C / P_t
 
 // One chunk's operands: fp16 matrices of rows of 128 bytes with the 128-byte
@@ -119,6 +120,7 @@ struct __align__(1024) Update {
     float inner[kC][2 * kC];              // [token t]: (B T)_t, then T_t
     float decay[kD];                      // P_C
     float given[kC];                      // [token's place]: about its largest K P_C / P_t
+    float undo[2][kC];                    // K P and Q P are held times 1 / undo: [token], [place]
 };
 
 // Consumer threads that share a row of S: each has its part of the columns and
@@ -509,7 +511,9 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
     const u64 bias[2] = {biases.x, biases.y};
     Poly poly;
     if constexpr (!kBounded) poly = softplus_poly();
-    u64 reach[2] = {pair(kKeyScale, kKeyScale), pair(kKeyScale, kKeyScale)};   // P_t
+    const float start = power_of_two(kKeyExponent);
+    u64 reach[2] = {pair(start, start), pair(start, start)};                   // P_t
+    float undo = 1.0f, mine = 1.0f;   // of P_t, and of token `lane`'s
     u64 total[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};                       // log2 P_t
     u64 r[2] = {pair(1.0f, 1.0f), pair(1.0f, 1.0f)};                            // R
     unsigned char *reached = st.reach[lane >> 4];
@@ -560,6 +564,16 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             const float e[4] = {exp2_of(e0.x), exp2_of(e0.y), exp2_of(e1.x), exp2_of(e1.y)};
             reach[0] = mul_pair(reach[0], pair(e[0], e[1]));
             reach[1] = mul_pair(reach[1], pair(e[2], e[3]));
+            const float most = larger(larger(0.0f, reach[0]), reach[1]);
+            if (!__any_sync(kFull, most >= kKeyLeast)) {   // no channel has much left
+                const int up = kKeyExponent - exponent_of(__uint_as_float(
+                                   __reduce_max_sync(kFull, __float_as_uint(most))));
+                const float f = power_of_two(min(up, 120));
+                reach[0] = mul_pair(reach[0], pair(f, f));
+                reach[1] = mul_pair(reach[1], pair(f, f));
+                undo *= power_of_two(-min(up, 120));
+            }
+            if (lane == t) mine = undo;
             const float nk = __shfl_sync(kFull, norm, 16 * u);
             const float nq = __shfl_sync(kFull, norm, 16 * u + 8);
             const u64 rk = pair(nk, nk), rq = pair(nq, nq);
@@ -622,7 +636,9 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
         }
         kda::cp_async_wait_all();
         if (!wait_for_update(sh, n, p.err)) return false;
-        *reinterpret_cast<float4 *>(&update_of(sh, n).decay[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+        Update &up = update_of(sh, n);
+        *reinterpret_cast<float4 *>(&up.decay[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+        if (lane < kC) up.undo[0][lane] = up.undo[1][order_of<kSplit>(lane)] = mine;
     }
     __syncwarp();
     return true;
@@ -907,6 +923,17 @@ __device__ __forceinline__ float dot_row(const float *row, int i, const u64 (&x)
 template <int kId, int kMembers>
 __device__ __forceinline__ void meet() {
     asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kMembers) : "memory");
+}
+
+template <int kN>
+__device__ __forceinline__ void undo_pairs(u64 (&x)[kN], const float *undo) {
+    asm volatile("" ::: "memory");   // (a branch, not predicated loads)
+#pragma unroll
+    for (int n = 0; n < kN; n += 2) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(undo + 2 * n);
+        x[n] = mul_pair(x[n], f.x);
+        x[n + 1] = mul_pair(x[n + 1], f.y);
+    }
 }
 
 // Those that share 32 rows of S.
@@ -1355,11 +1382,13 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
 #pragma unroll
             for (int n = 0; n < kC / 2; ++n)
                 x[n] = pair(__bfloat162float(st.v[2 * n][r]), __bfloat162float(st.v[2 * n + 1][r]));
-            const float fx = -power_of_two(-ex) / kKeyScale;
+            const float fx = -power_of_two(-ex) / (float)(1 << kKeyExponent);
+            const bool undo = up.undo[0][kC - 1] != 1.0f;   // (of some token, then of the last)
             ok &= wait(sh, &sh.u_done, parity, p.err);
             kda::tc_fence_after();
             {
                 uint32_t u[16], y[16], z[16];
+                u64 s[kC / 2];
                 kda::tmem_ld16(tmem + kColReach, u);
                 kda::tmem_ld16(tmem + kColReach + 2 * kC, y);
                 kda::tmem_ld16(tmem + kColLow, z);
@@ -1368,10 +1397,12 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                 arrived(z);
 #pragma unroll
                 for (int n = 0; n < kC / 2; ++n)
-                    x[n] = fma_pair(add_pair(pair_of(u[2 * n], u[2 * n + 1]),
-                                             add_pair(pair_of(y[2 * n], y[2 * n + 1]),
-                                                      pair_of(z[2 * n], z[2 * n + 1]))),
-                                    pair(fx, fx), x[n]);
+                    s[n] = add_pair(pair_of(u[2 * n], u[2 * n + 1]),
+                                    add_pair(pair_of(y[2 * n], y[2 * n + 1]),
+                                             pair_of(z[2 * n], z[2 * n + 1])));
+                if (undo) undo_pairs(s, up.undo[0]);
+#pragma unroll
+                for (int n = 0; n < kC / 2; ++n) x[n] = fma_pair(s[n], pair(fx, fx), x[n]);
             }
             if (!kSplit) hand_back<kSplit>(&sh.reach_empty[count % kReaches<kSplit>], lane);
             float sum = 0.0f, back;   // of |V'| as given, of the row's tokens
@@ -1417,13 +1448,14 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                     arrived(hi);
                     arrived(lo);
                     arrived(low);
-                    const float f = power_of_two(-ex) * (p.scale / kKeyScale);
+                    const float f = power_of_two(-ex) * (p.scale / (float)(1 << kKeyExponent));
 #pragma unroll
                     for (int i = 0; i < kTokens; i += 2)
                         o[i / 2] = mul_pair(add_pair(pair_of(hi[i], hi[i + 1]),
                                                      add_pair(pair_of(lo[i], lo[i + 1]),
                                                               pair_of(low[i], low[i + 1]))),
                                             pair(f, f));
+                    if (undo) undo_pairs(o, &up.undo[1][kTokens * part]);
                 }
                 const int n = ok ? w.row.tokens - c * kC : 0;
                 const long long token = (long long)p.H * kD;

@@ -42,3 +42,50 @@ def test_a_large_value_that_decays_away(tokens, at, size):
     c.bias[:], c.A_log[:] = -4.0, 0.0
     c.g[at + 2] = 32.0
     hold(c, outputs=False)
+
+
+# The tokens' own products with a state that decays away, and their outputs.
+
+@pytest.mark.parametrize("each", [0.3, 0.7, 2.0, 5.0, 20.0])
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8, 1e12])
+@pytest.mark.parametrize("lens,heads", [([7], 2), ([18, 60, 130], 2), ([600], 2),
+                                        ([10, 50] * 40, 2)])
+def test_tokens_see_what_is_left_of_a_large_state(lens, heads, size, each):
+    c = Case(lens, heads, seed=15, size=size)
+    decays_of(c, each)
+    hold(c)
+
+
+@pytest.mark.parametrize("lens", [[9, 60], [530]])
+def test_tokens_behind_strong_gates(lens):
+    c = Case(lens, 2, seed=16, size=1e8)
+    decays_of(c, 0.01)
+    c.g = c.g.clone()
+    c.g[3::11] = 30.0
+    hold(c)
+
+
+@pytest.mark.parametrize("size", [1e4, 1e6])
+@pytest.mark.parametrize("lens", [[7, 90], [520]])
+def test_a_large_state_that_decays_away_unevenly(lens, size):
+    c = Case(lens, 2, seed=9, size=size)
+    gen = torch.Generator().manual_seed(1)
+    decays_of(c, 0.3 * 100.0 ** torch.rand(len(c.bias), generator=gen, dtype=torch.float64))
+    hold(c)
+
+
+@pytest.mark.parametrize("at", [3, 18, 31])
+@pytest.mark.parametrize("tokens", [35, 90, 530])
+@pytest.mark.parametrize("size", [1e4, 1e8])
+def test_tokens_behind_a_large_value_that_decays_away(tokens, at, size):
+    c = Case([tokens], 2, seed=11)
+    c.v = c.v.clone()
+    c.v[at] *= size
+    decays_of(c, 20.0)
+    hold(c)
+    c = Case([tokens], 2, seed=12)
+    c.v, c.g = c.v.clone(), c.g.clone()
+    c.v[at] *= size
+    c.bias[:], c.A_log[:] = -4.0, 0.0
+    c.g[at + 2] = 32.0
+    hold(c)
