@@ -905,16 +905,27 @@ __device__ __forceinline__ u64 pair_of(uint32_t x, uint32_t y) {
 }
 
 // The product of x, all tokens' of a chunk, with the row of a triangular matrix
-// that is the part's i-th token's.
+// that is the part's i-th token's.  Behind the diagonal x counts as 0, whatever it
+// is: 0 in the matrix would not do where it is not finite.
 template <bool kSplit>
-__device__ __forceinline__ float dot_row(const float *row, int i, const u64 (&x)[kC / 2]) {
+__device__ __forceinline__ float dot_row(const float *row, int i, int part,
+                                         const u64 (&x)[kC / 2]) {
+    const int last = kSplit ? i : i >> 1, off = (i & 1) ? 3 - part : part;   // token_of
     u64 sum = 0ull;
 #pragma unroll
-    for (int n = 0; n <= (kSplit ? i : i >> 1); ++n) {   // four entries each, up to the diagonal
+    for (int n = 0; n < last; ++n) {   // four entries each
         const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(row + 4 * n);
         sum = n == 0 ? mul_pair(f.x, x[0]) : fma_pair(f.x, x[2 * n], sum);
         sum = fma_pair(f.y, x[2 * n + 1], sum);
     }
+    const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(row + 4 * last);
+    const float2 u = both(x[2 * last]), v = both(x[2 * last + 1]);
+    const u64 w = kSplit || !(i & 1) ? pair(u.x, off > 0 ? u.y : 0.0f) : x[2 * last];
+    sum = last == 0 ? mul_pair(f.x, w) : fma_pair(f.x, w, sum);
+    if (kSplit)
+        sum = fma_pair(f.y, pair(off > 1 ? v.x : 0.0f, off > 2 ? v.y : 0.0f), sum);
+    else if (i & 1)
+        sum = fma_pair(f.y, pair(v.x, off > 2 ? v.y : 0.0f), sum);
     const float2 y = both(sum);
     return y.x + y.y;
 }
@@ -1413,7 +1424,8 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                     const float *f = up.inner[token_of<kSplit>(part, i)] + kC;
                     const float *f1 = up.inner[token_of<kSplit>(part, i + 1)] + kC;
                     y[i / 2] = mul_pair(
-                        pair(dot_row<kSplit>(f, i, x), dot_row<kSplit>(f1, i + 1, x)),
+                        pair(dot_row<kSplit>(f, i, part, x),
+                             dot_row<kSplit>(f1, i + 1, part, x)),
                         *reinterpret_cast<const u64 *>(&up.given[kTokens * part + i]));
                     const float2 z = both(y[i / 2]);
                     sum += fabsf(z.x) + fabsf(z.y);
@@ -1464,7 +1476,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
 #pragma unroll
                 for (int i = 0; i < kTokens; ++i) {
                     const int t = token_of<kSplit>(part, i);
-                    const float y = dot_row<kSplit>(up.inner[t], i, x);
+                    const float y = dot_row<kSplit>(up.inner[t], i, part, x);
                     const float2 z = both(o[i / 2]);
                     if (t < n)
                         dst[t * token] = __float2bfloat16_rn(fmaf(y, p.scale, i & 1 ? z.y : z.x));

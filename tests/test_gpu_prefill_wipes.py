@@ -89,3 +89,15 @@ def test_tokens_behind_a_large_value_that_decays_away(tokens, at, size):
     c.bias[:], c.A_log[:] = -4.0, 0.0
     c.g[at + 2] = 32.0
     hold(c)
+
+
+@pytest.mark.parametrize("each", [30.0, 41.0])
+@pytest.mark.parametrize("at", [0, 1, 2, 6])
+@pytest.mark.parametrize("lens", [[8, 16], [10] * 90, [520]])
+def test_a_huge_value_that_one_token_takes_away(lens, at, each):
+    """e^-30 is 2^-43 and e^-41 2^-59: below what is told apart from nothing."""
+    c = Case(lens, 2, seed=17)
+    c.v = c.v.clone()
+    c.v[at::23] *= 1e12
+    decays_of(c, each)
+    hold(c, largest=float(c.v.float().abs().max()))
