@@ -548,13 +548,15 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             norm += __shfl_xor_sync(kFull, norm, 1);
             norm = inverse_norm(norm);
         }
-#pragma unroll
+        // one copy of the code for both where other warps' code lies beside it
+        uint2 gates = now[0].g;
+#pragma unroll kSplit ? 2 : 1
         for (int u = 0; u < 2; ++u) {
             const int t = t0 + u;
             u64 y[2] = {0ull, 0ull};   // behind the row's end nothing decays
             if (t < valid) {
                 u64 x[2];
-                pairs_of(now[u].g, x[0], x[1]);
+                pairs_of(gates, x[0], x[1]);
                 y[0] = log2_decays<kBounded>(add_pair(x[0], bias[0]), gate, bound, poly);
                 y[1] = log2_decays<kBounded>(add_pair(x[1], bias[1]), gate, bound, poly);
             }
@@ -579,8 +581,8 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
             const u64 rk = pair(nk, nk), rq = pair(nq, nq);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                k[u][i] = mul_pair(k[u][i], rk);
-                q[u][i] = mul_pair(q[u][i], rq);
+                k[0][i] = mul_pair(k[0][i], rk);
+                q[0][i] = mul_pair(q[0][i], rq);
             }
             if (u == 0 && (t0 & 2) == 0) {   // a block's first token
                 put(&out.since[4 * lane], mul_pair(r[0], pair(e[0], e[1])),
@@ -591,27 +593,30 @@ __device__ __forceinline__ bool produce_tokens(const Params &p, Shared<kSplit> &
                 r[1] = mul_pair(r[1], pair(fmaxf(e[2], 0x1p-40f), fmaxf(e[3], 0x1p-40f)));
             }
             float *ahead = &out.ahead[t & 3][4 * lane];
-            put(ahead, mul_pair(k[u][0], r[0]), mul_pair(k[u][1], r[1]));
-            put(ahead + 4 * kRow, mul_pair(q[u][0], r[0]), mul_pair(q[u][1], r[1]));
+            put(ahead, mul_pair(k[0][0], r[0]), mul_pair(k[0][1], r[1]));
+            put(ahead + 4 * kRow, mul_pair(q[0][0], r[0]), mul_pair(q[0][1], r[1]));
             const float2 r0 = both(r[0]), r1 = both(r[1]);
             put(&out.back[t & 3][4 * lane],
-                mul_pair(k[u][0], pair(reciprocal(r0.x), reciprocal(r0.y))),
-                mul_pair(k[u][1], pair(reciprocal(r1.x), reciprocal(r1.y))));
+                mul_pair(k[0][0], pair(reciprocal(r0.x), reciprocal(r0.y))),
+                mul_pair(k[0][1], pair(reciprocal(r1.x), reciprocal(r1.y))));
             int to = place(t, 4 * (lane & 15));   // (rows 16 and 32 further swizzle alike)
             uint2 hi, lo;
-            float2 x = both(mul_pair(k[u][0], reach[0]));
+            float2 x = both(mul_pair(k[0][0], reach[0]));
             split(x.x, x.y, hi.x, lo.x);
-            x = both(mul_pair(k[u][1], reach[1]));
+            x = both(mul_pair(k[0][1], reach[1]));
             split(x.x, x.y, hi.y, lo.y);
             *reinterpret_cast<uint2 *>(reached + to) = hi;
             *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
             to = place(kC + order_of<kSplit>(t), 4 * (lane & 15));
-            x = both(mul_pair(q[u][0], reach[0]));
+            x = both(mul_pair(q[0][0], reach[0]));
             split(x.x, x.y, hi.x, lo.x);
-            x = both(mul_pair(q[u][1], reach[1]));
+            x = both(mul_pair(q[0][1], reach[1]));
             split(x.x, x.y, hi.y, lo.y);
             *reinterpret_cast<uint2 *>(reached + to) = hi;
             *reinterpret_cast<uint2 *>(reached + to + 2 * kC * 128) = lo;
+            gates = now[1].g;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) k[0][i] = k[1][i], q[0][i] = q[1][i];
         }
         if ((t0 & 2) != 0) {
             put(&out.end[4 * lane], r[0], r[1]);
@@ -1234,14 +1239,9 @@ __device__ __forceinline__ float largest_of(const float (&x)[kOf][kD], int r) {
 }
 
 // The warp is done with a place of a ring.
-template <bool kSplit>
 __device__ __forceinline__ void hand_back(uint64_t *empty, int lane) {
     __syncwarp();
-    if (lane != 0) return;
-    if (kSplit)
-        arrive_at(empty, 1);
-    else
-        kda::mbar_arrive(empty);
+    if (lane == 0) kda::mbar_arrive(empty);
 }
 
 // The consumer warps.  A wait that runs out ends nothing by itself: from then
@@ -1280,21 +1280,40 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) most = larger(most, s[i]);
             sh.most[part][r] = most;
+#pragma unroll
+            for (int i = 0; i < kCols / 16; ++i) {
+                uint32_t y[16];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float2 z = both(s[8 * i + n]);
+                    y[2 * n] = __float_as_uint(z.x);
+                    y[2 * n + 1] = __float_as_uint(z.y);
+                }
+                kda::tmem_st16(state + 16 * i, y);
+            }
+            kda::tmem_wait_st();
             meet_row<kOf>(me);
             bound = largest_of<kOf>(sh.most, r);
             ex = min(kHeld - exponent_of(bound), kMostExponent);
             const u64 f = pair(power_of_two(ex), power_of_two(ex));
-#pragma unroll
-            for (int i = 0; i < kCols / 16; ++i) {
+#pragma unroll 1
+            for (int i = 0; i < kCols / 16; ++i) {   // (one copy of the code)
+                uint32_t x[16];
+                kda::tmem_ld16(state + 16 * i, x);
+                arrived(x);
                 u64 y[8];
 #pragma unroll
-                for (int n = 0; n < 8; ++n) y[n] = mul_pair(s[8 * i + n], f);
+                for (int n = 0; n < 8; ++n) y[n] = mul_pair(pair_of(x[2 * n], x[2 * n + 1]), f);
                 store_state(state + 16 * i, halves + 8 * i, y);
             }
         }
         const int chunks = (w.row.tokens + kC - 1) / kC;
         int step = 0;                               // of ex, due with the next addition
         float added = 0.0f;
+        const int token = p.H * kD;
+        uint16_t *const out = reinterpret_cast<uint16_t *>(p.out) +
+                              (long long)w.row.first * token + w.head * kD + r;
+        uint32_t result[kTokens / 2] = {};   // outputs of the last chunk
         // turn c adds what chunk c - 1 brought, makes chunk c's V' and writes its outputs
         for (int c = 0; c <= chunks; ++c) {
             if (c > 0) {
@@ -1307,44 +1326,38 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                     float most = 0.0f;
                     const u64 factor = pair(added, added);
                     const bool moved = __any_sync(kFull, step != 0);
+                    // (16 columns at a time: code of 32 took longer, see the kernel's size)
 #pragma unroll 1
-                    for (int i = 0; i < kCols / 32; ++i) {
-                        uint32_t u[2][16], x[2][16];
+                    for (int i = 0; i < kCols / 16; ++i) {
+                        uint32_t u[16], x[16];
+                        kda::tmem_ld16(tmem + kColUpdate + kCols * part + 16 * i, u);
+                        kda::tmem_ld16(state + 16 * i, x);
+                        arrived(u);
+                        arrived(x);
+                        u64 s[8];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            kda::tmem_ld16(tmem + kColUpdate + kCols * part + 32 * i + 16 * h, u[h]);
-                            kda::tmem_ld16(state + 32 * i + 16 * h, x[h]);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            arrived(u[h]);
-                            arrived(x[h]);
-                            u64 s[8];
+                        for (int n = 0; n < 8; ++n) s[n] = pair_of(x[2 * n], x[2 * n + 1]);
+                        if (moved) {   // in two powers: a step may be twice as far as one goes
+                            const float g = power_of_two(step / 2);
+                            const float g2 = power_of_two(step - step / 2);
 #pragma unroll
                             for (int n = 0; n < 8; ++n)
-                                s[n] = pair_of(x[h][2 * n], x[h][2 * n + 1]);
-                            if (moved) {   // in two powers: a step may be twice as far as one goes
-                                const float g = power_of_two(step / 2);
-                                const float g2 = power_of_two(step - step / 2);
-#pragma unroll
-                                for (int n = 0; n < 8; ++n)
-                                    s[n] = mul_pair(mul_pair(s[n], pair(g, g)), pair(g2, g2));
-                            }
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(
-                                    decay + 32 * i + 16 * h + 4 * n);
-                                s[2 * n] = fma_pair(pair_of(u[h][4 * n], u[h][4 * n + 1]), factor,
-                                                    mul_pair(s[2 * n], d.x));
-                                s[2 * n + 1] = fma_pair(pair_of(u[h][4 * n + 2], u[h][4 * n + 3]),
-                                                        factor, mul_pair(s[2 * n + 1], d.y));
-                            }
-                            most = larger(larger(most, s[0]), s[1]);
-                            if (all)
-#pragma unroll
-                                for (int n = 2; n < 8; ++n) most = larger(most, s[n]);
-                            store_state(state + 32 * i + 16 * h, halves + 16 * i + 8 * h, s);
+                                s[n] = mul_pair(mul_pair(s[n], pair(g, g)), pair(g2, g2));
                         }
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const ulonglong2 d =
+                                *reinterpret_cast<const ulonglong2 *>(decay + 16 * i + 4 * n);
+                            s[2 * n] = fma_pair(pair_of(u[4 * n], u[4 * n + 1]), factor,
+                                                mul_pair(s[2 * n], d.x));
+                            s[2 * n + 1] = fma_pair(pair_of(u[4 * n + 2], u[4 * n + 3]), factor,
+                                                    mul_pair(s[2 * n + 1], d.y));
+                        }
+                        most = larger(larger(most, s[0]), s[1]);
+                        if (all)
+#pragma unroll
+                            for (int n = 2; n < 8; ++n) most = larger(most, s[n]);
+                        store_state(state + 16 * i, halves + 8 * i, s);
                     }
                     if (c == chunks) break;
                     // The bound knows of no decay.  Where the row is far below it, the columns
@@ -1370,21 +1383,43 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                 kda::tmem_wait_st();
                 kda::tc_fence_before();
                 meet<1, 128 * kOf>();
-                if (kSplit) asm volatile("fence.proxy.async;" ::: "memory");
                 if (ok && me == 0 && elected()) {
                     kda::tc_fence_after();
+                    if (kSplit) kda::fence_proxy_async_smem();
                     issue_reach(sh.reach[count % kReaches<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
                 if (ok && me == 4 && elected()) {
                     kda::tc_fence_after();
+                    if (kSplit) kda::fence_proxy_async_smem();
                     issue_low(sh.reach[count % kReaches<kSplit>], sh.tmem);
                     kda::umma_commit(&sh.u_done);
                 }
                 __syncwarp();
             }
-            if (c > 0) hand_back<kSplit>(&sh.update_empty[(count - 1) % kUpdates<kSplit>], lane);
+            if (c > 0) {
+                uint64_t *empty = &sh.update_empty[(count - 1) % kUpdates<kSplit>];
+                if constexpr (kSplit) {
+                    // (one for all, who have met: its release takes some 1000 clocks)
+                    if (c == chunks) meet<1, 128 * kOf>();
+                    if (me == 4 * kOf - 1 && lane == 0) arrive_at(empty, 1);
+                    __syncwarp();
+                } else {
+                    hand_back(empty, lane);
+                }
+                // (behind that, which would wait for what was written before it)
+                const int n = ok ? w.row.tokens - (c - 1) * kC : 0;
+                uint16_t *to = out + (long long)(c - 1) * kC * token;
+                uint16_t *even = to + part * token, *odd = to + (3 - part) * token;   // token_of
+                const int step = 4 * token, evens = n - part, odds = n - (3 - part);
+#pragma unroll
+                for (int i = 0; i < kTokens; i += 2) {
+                    const int g = kSplit ? i : i >> 1, h = kSplit ? i + 1 : g;   // fours of tokens
+                    if (4 * g < evens) even[g * step] = (uint16_t)result[i / 2];
+                    if (4 * h < odds) odd[h * step] = (uint16_t)(result[i / 2] >> 16);
+                }
+            }
             if (c == chunks) break;
             const unsigned parity = count & 1;
             const Reach &st = sh.reach[count % kReaches<kSplit>];
@@ -1415,7 +1450,7 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
 #pragma unroll
                 for (int n = 0; n < kC / 2; ++n) x[n] = fma_pair(s[n], pair(fx, fx), x[n]);
             }
-            if (!kSplit) hand_back<kSplit>(&sh.reach_empty[count % kReaches<kSplit>], lane);
+            if (!kSplit) hand_back(&sh.reach_empty[count % kReaches<kSplit>], lane);
             float sum = 0.0f, back;   // of |V'| as given, of the row's tokens
             {
                 u64 y[kTokens / 2];   // V' of the part's tokens, times what is given of them
@@ -1469,17 +1504,18 @@ __device__ __forceinline__ void consume(const Params &p, Shared<kSplit> &sh, uns
                                             pair(f, f));
                     if (undo) undo_pairs(o, &up.undo[1][kTokens * part]);
                 }
-                const int n = ok ? w.row.tokens - c * kC : 0;
-                const long long token = (long long)p.H * kD;
-                __nv_bfloat16 *dst = p.out + (w.row.first + (long long)c * kC) * token +
-                                     w.head * kD + r;
+                const u64 f = pair(p.scale, p.scale);
 #pragma unroll
-                for (int i = 0; i < kTokens; ++i) {
-                    const int t = token_of<kSplit>(part, i);
-                    const float y = dot_row<kSplit>(up.inner[t], i, part, x);
-                    const float2 z = both(o[i / 2]);
-                    if (t < n)
-                        dst[t * token] = __float2bfloat16_rn(fmaf(y, p.scale, i & 1 ? z.y : z.x));
+                for (int i = 0; i < kTokens; i += 2)
+                    o[i / 2] = fma_pair(
+                        pair(dot_row<kSplit>(up.inner[token_of<kSplit>(part, i)], i, part, x),
+                             dot_row<kSplit>(up.inner[token_of<kSplit>(part, i + 1)], i + 1, part,
+                                             x)),
+                        f, o[i / 2]);
+#pragma unroll
+                for (int i = 0; i < kTokens / 2; ++i) {
+                    const float2 z = both(o[i]);
+                    result[i] = kda_cache::pack(z.x, z.y, __nv_bfloat16());
                 }
             }
             // S is at most what it was and all that is added to it
@@ -1523,7 +1559,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
             kda::mbar_init(&sh.reach_empty[i], 4 * kParts<kSplit>);
         }
         for (int i = 0; i < kUpdates<kSplit>; ++i)
-            kda::mbar_init(&sh.update_empty[i], 4 * kParts<kSplit>);
+            kda::mbar_init(&sh.update_empty[i], kSplit ? 1 : 4 * kParts<kSplit>);
         if (!kSplit || rank() == 1)
             for (int i = 0; i < 2 * kPairs<kSplit>; ++i) {
                 kda::mbar_init(&sh.scratch[i >> 1].ready[i & 1], 1);
@@ -1540,7 +1576,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
         kda::tmem_alloc(&sh.tmem, kTmemColumns);
         kda::tc_fence_before();
     }
-    kda_cache::grid_dependents_launch();
+    if (!kSplit) kda_cache::grid_dependents_launch();
     __syncthreads();
     if (kSplit) meet_cluster();   // the barriers of both are there
     kda::tc_fence_after();
@@ -1553,6 +1589,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
         consume<kSplit, kPlanned>(p, sh, items, warp - kFirst, lane);
     else if (produces && warp < 2 * kPairs<kSplit>)
         produce<kBounded, kSplit, kPlanned>(p, sh, items, warp, lane);
+    if (kSplit) kda_cache::grid_dependents_launch();
     if (consumes && (warp == kFirst || warp == kFirst + 4)) {
         // no product may outlive the memory, whatever became of who waited for it
         if (elected()) kda::umma_commit(&sh.drained);
