@@ -404,7 +404,21 @@ kda_status kda_record_state_blocks(const kda_align *align,
  */
 
 /* kda_prefill -- the gated delta rule over rows of any length: row b has the
- * tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 (rows must not overlap). */
+ * tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 (rows must not overlap).
+ *
+ * The tokens are taken 16 at a time from the row's first on (in rows of up to 6
+ * they may go one by one).  States keep the library's tolerance (1e-5 of the
+ * tile's largest value) and outputs are rounded once, as token by token, but for
+ * two limits, which show only beside numbers of very different sizes:
+ *  - the 16 tokens see an entry of the state before them to within 2^-23 of the
+ *    largest entry of its row, so what a token writes there may be off by 2^-19
+ *    of an entry that the decays of its channel have taken away since;
+ *  - what decays leave below 2^-40 between two of the 16 tokens may count as
+ *    anything up to that, 0 included.
+ * What is not finite in a token's k, v (in v: in that channel), g_raw or beta_raw
+ * reaches it and the tokens behind it in its row and head, and the state; in q its
+ * own output alone.  Infinite gates and betas are their limits.
+ */
 kda_status kda_prefill(const kda_config *cfg,
                        const void *q, const void *k, const void *v,
                        const void *g_raw, const void *beta_raw,

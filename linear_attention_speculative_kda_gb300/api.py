@@ -1232,7 +1232,11 @@ def kda_prefill(q, k, v, g_raw, beta_raw, A_log, g_bias, state_pool, cu_seqlens,
     (<= 0: zeros; None: state_indices).  No row may write a slot that another
     reads or writes.  Returns ``out``, bf16 [T, H, 128], which overlaps no input;
     rows that are skipped leave theirs untouched, and rows without tokens write
-    no state."""
+    no state.
+
+    Tokens are taken 16 at a time: what the decays take away within them is told
+    from what stays to 2^-23 of a row of the state and to 2^-40 between tokens
+    (include/kda.h has the limits, and where NaN and infinities go)."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _delta_call("kda_prefill", load_library(), q, k, v, g_raw, beta_raw, A_log, g_bias,

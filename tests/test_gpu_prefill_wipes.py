@@ -101,3 +101,15 @@ def test_a_huge_value_that_one_token_takes_away(lens, at, each):
     c.v[at::23] *= 1e12
     decays_of(c, each)
     hold(c, largest=float(c.v.float().abs().max()))
+
+
+@pytest.mark.parametrize("size", [1e4, 1e8])
+@pytest.mark.parametrize("lens", [[5, 12], [40] * 80, [300]])
+def test_channels_that_decay_apart(lens, size):
+    """Large channels that are gone at once, beside small ones that stay."""
+    c = Case(lens, 2, seed=18, size=1.0)
+    c.pool[..., :64] *= size
+    each = torch.full((256,), 0.01, dtype=torch.float64)
+    each.view(2, 128)[:, :64] = 40.0
+    decays_of(c, each)
+    hold(c, taken=float(c.pool.abs().max()))
