@@ -1,8 +1,9 @@
 // The short calls (those of the attention layers, the acceptance, and the delta
-// rule's prompts and single tokens) for Python without its cost: of the 8 to 11 us that api.py spends around a library call, most are
-// some fifty queries of tensors from Python and the allocations.  Back to back
-// on a GB300's host an append takes 4.8 us so and 11.9 without, an attention
-// 8.6 and 18.2, log probabilities 6.3 and 15.6.
+// rule's prompts and single tokens) for Python without its cost: of the 8 to 11
+// us that api.py spends around a library call, most are some fifty queries of
+// tensors from Python and the allocations.  Back to back on a GB300's host an
+// append takes 4.8 us so and 11.9 without, an attention 8.6 and 18.2, log
+// probabilities 6.3 and 15.6.
 //
 // Each function takes the address of the library's packed entry point and
 // api.py's arguments in order.  It answers None, having done nothing, where

@@ -13,21 +13,26 @@
 // product with S, and of V' into S, runs on tcgen05.mma in fp16 with fp32 sums,
 // an fp32 operand x as two fp16 numbers, hi = fp16(x) and lo = fp16(x - hi), 22
 // bits, and a product as hi hi + hi lo + lo hi; what is left out is below 2^-22
-// of it.  Decayed keys and queries are at most 1 and scaled by powers of two;
-// rows of S and of V' have powers of two of their own, from bounds of their
-// sizes, as fp16's range needs it.  V' = T X and (B T) X are 136 fp32 products a
-// row each, made where X lies: less than the way to the tensor cores and back.
-// O is rounded once, to bf16 (with hi alone in its products, 11 bits, 64 rows of
-// 1024 tokens x 32 heads took 2.71 ms, not 2.88, and the outputs were 1e-3 off
-// those of fp32 products, not 5e-5).
+// of it.  fp16's range needs powers of two, and each is from what it scales, not
+// from a bound that knows no decay or no beta: a row of S has its own, moved with
+// its values; a token's K P and Q P have one of the largest P that is left, and
+// its K P_C / P_t one of their largest, which V' takes; a row of V', so taken, has
+// its own.  What decays leave, and what weak betas write, is so as exact as what
+// was there before, but for one thing: an entry of S far below its row's largest
+// has 2^-23 of that, in the chunk at whose start it is.
+//   V' = T X and (B T) X are 136 fp32 products a row each, made where X lies.  O is
+// rounded once, to bf16 (with hi alone in its products, 11 bits, the outputs were
+// 1e-3 off those of fp32 products, not 5e-5).  Behind the diagonals nothing is
+// multiplied: 0 times what is not finite would reach the tokens before it.
 //
 // A and B.  Four tokens t at a time meet all s before and among them: k_s
 // decayed to the block's first token times k_t, q_t decayed from it, all of
 // them products of decays, which strong decays may take to 0.  Among the four
 // that is k_s / R_s, R_s the decays from the first.  There, and in K P_C / P_t,
-// a decay below 2^-40 counts as 2^-40, so that three of them fit fp32: what
-// that adds is 2^-40 beside factors of 1.  The operands keep fp32's range:
-// mma.sync in tf32, hi and lo as above (5% of the tensor pipe's time).
+// a decay below 2^-40 counts as 2^-40, so that three of them fit fp32 (and a
+// product over blocks that fp32 does not have as 0): what that adds or takes is
+// 2^-40 beside factors of 1.  The operands keep fp32's range: mma.sync in tf32, hi
+// and lo as above (5% of the tensor pipe's time).
 //
 // Layout.  A CTA has one row and head at a time: the chunks of a row follow
 // one another, so rows and heads are what runs side by side.  S lies in tensor
@@ -45,21 +50,26 @@
 // their operands into the first's rings (mapa), all warps of the first
 // consume, four threads a row of S.
 //
-// What bounds it.  Neither HBM (16% of its rate over 64 rows of 1024 tokens x
-// 32 heads, 2.7 ms) nor the tensor cores (13%), but issue: some 13,700 warp
-// instructions a chunk, 54% of the issue slots, a consumer's turn of 6,000
-// clocks (S 1,800, the products with S 1,100, V' 1,000, the update 800, the
-// barriers 700).  On the way here, the same 64 rows: token by token in fp32
-// 13.3 ms (the decay, two dot products and the update are 8 fp32 operations an
-// element of S: 3.2 ms at the least); consumers on mma.sync with S in their
-// registers 3.8; straight code of all roles (80 KB) missed the instruction
-// cache, 60 KB in short loops took 4.6 to 3.1; both halves of a row on V'
-// and the outputs, and shared memory addressed as such, 2.7.  CTAs that take
-// over others' rows as they finish (cluster launch control) were slower than
-// rows dealt out in turn: 256 rows of 1 to 45 tokens x 32 heads 713, not 656 us.
-//   A single long row is a chain: a turn a chunk, 2.3 us where two CTAs share it
-// (32 heads x 16001 tokens 2.38 ms), 2.8 in one; with four pairs of producers in
-// the second CTA the consumers waited for them, 2.6.
+// What bounds it.  Neither HBM (15% of its rate over 64 rows of 1024 tokens x
+// 32 heads, 2.86 ms) nor the tensor cores (14%), but instructions: some 15,900 a
+// chunk, 57% of the issue slots.  A consumer's turn is 6,400 clocks (S 2,000, its
+// products 1,400, V' 1,000, outputs 1,300, barriers 700), of which it waits some
+// 400 for the tensor cores and 200 for operands; the producers are idle for a
+// quarter and a third of it.
+//   Code that lies in the way counts too: 2.4 KB more of it in the pass over S cost
+// 10%, so loops are short where all roles share an SM (63 KB of code: 6% of the
+// instruction fetches miss, 13% of 69 KB).
+//   On the way here, the same 64 rows: token by token in fp32 13.3 ms (the decay,
+// two dot products and the update are 8 fp32 operations an element of S: 3.2 ms at
+// the least); consumers on mma.sync with S in their registers 3.8; 80 KB of
+// straight code 4.6; both halves of a row on V' and the outputs, and shared memory
+// addressed as such, 2.7, with outputs of 11 bits and powers of two from bounds
+// that missed (see above); with neither 3.3, and with less code 2.9.  CTAs that
+// take over others' rows as they finish (cluster launch control) were 9% slower
+// over 256 rows of 1 to 45 tokens x 32 heads than rows dealt out in turn.
+//   A single long row is a chain: a turn a chunk, 2.6 us where two CTAs share it
+// (32 heads x 16001 tokens 2.58 ms), 3.1 in one.  All warps' hand-backs to the other
+// CTA, each with a release of its own, took 1,000 clocks a turn: one warp's does.
 #include <cuda_fp16.h>
 
 #include "kda_delta.cuh"
@@ -1074,8 +1084,8 @@ __device__ __forceinline__ void make_plan(const Params &p, Shared<false> &sh, un
     u64 sum = sum_up_to(sums, mine);
     if (tid == kThreads - 1) column[0] = sum;
     __syncthreads();
-    // Where no row is long beside a CTA's share, dealing out in turn does as well or
-    // better (256 rows of 1 to 45 tokens x 32 heads: 663 us in turn, 704 planned).
+    // Where no row is long beside a CTA's share, dealing out in turn does as well (256
+    // rows of 1 to 45 tokens x 32 heads: 770 us in turn, 763 planned) and needs no plan.
     if (__syncthreads_or((u64)mine * G * 8 > column[0] * H) == 0) {
         if (tid == 0) plan.planned = 0;
         return;
@@ -1576,6 +1586,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p, un
         kda::tmem_alloc(&sh.tmem, kTmemColumns);
         kda::tc_fence_before();
     }
+    // (Two CTAs a head leave SMs free: what follows would sit there, and what follows
+    // that, and the clusters of a long run of calls would end up scattered.)
     if (!kSplit) kda_cache::grid_dependents_launch();
     __syncthreads();
     if (kSplit) meet_cluster();   // the barriers of both are there
@@ -1627,18 +1639,19 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
     if (tiles > 0x7fffffffLL - sms) return KDA_ERR_UNSUPPORTED;
     // Where SMs would be idle and rows are long, two SMs share a row and head, one
     // that produces and one that consumes: a row of 16001 tokens x 32 heads takes
-    // 2.38 ms, not 2.87, one of 512 x 16 98 us, not 104, but one of 256 60, not 59, and
-    // of 64 27, not 22 (it starts later).  (Pairs of SMs: not every SM has another
-    // beside it, so no more than a third of them.)
-    constexpr int kLong = 512;
+    // 2.59 ms, not 3.12, one of 512 x 16 103 us, not 115, of 256 62, not 66, but of 64
+    // 28, not 27 (it starts later).  (Pairs of SMs: not every SM has another beside it,
+    // so no more than a third of them.)
+    constexpr int kLong = 256;
     const bool split = 3 * tiles <= sms && num_tokens >= (long long)kLong * B;
     // A plan costs some us, and little is gained where each CTA has many rows and
-    // heads: 256 rows of 1 to 45 tokens x 32 heads (54 each) take 647 us, 663 in a
-    // kernel that could plan.  200 rows, some of up to 1501 tokens, x 16 heads (21
-    // each) take 415 planned and 472 in turn, 13 rows of 1 to 2501 x 16 heads 432 and
-    // 637; where all are alike a plan costs 1 to 4% (64 rows of 1024 x 32 heads 2.70
-    // ms, not 2.66), and only the device knows.  With up to 20 tokens for an SM it
-    // costs as much as it gives (25 us), with 70 to 150 it takes off a third.
+    // heads: 256 rows of 1 to 45 tokens x 32 heads (54 each) take 770 us either way.
+    // 200 rows, 30 of them of 300 to 1501 tokens, x 16 heads (21 each) take 1035 planned
+    // and 1118 in turn, 13 rows of 1 to 2501 x 16 heads 468 and 834; where all are
+    // alike a plan costs 1% at most (19 rows of 512 x 16 heads 231 us, not 228), and
+    // only the device knows.  With up to 20 tokens for an SM it costs as much as it
+    // gives, with 70 to 150 it takes off a fifth to a third (100 rows of 1 to 150 x 2
+    // heads 57 us, not 72).
     const bool planned = !split && tiles > sms && tiles <= 32LL * sms && B <= kPlanRows &&
                          sms <= kThreads && (long long)num_tokens * p.H >= 64LL * sms;
     void (*kernel)(const Params, unsigned) =
@@ -1650,9 +1663,10 @@ extern "C" kda_status kda_prefill(const kda_config *cfg, const void *q, const vo
         cudaSuccess)
         return KDA_ERR_CUDA;
     // Rows of up to kShort tokens go token by token where most rows can be such
-    // (512 rows x 16 heads: 203 us with 1 token, 332 with 4, 424 with 6, and 505
-    // as a chunk each).  Elsewhere the second launch costs more than it gives: 256
-    // rows of 1 to 45 tokens x 32 heads took 680 us, not 649.
+    // (512 rows x 16 heads: 228 us with 1 token, 347 with 4, 441 with 6, and 550
+    // as a chunk each; states from the slots that they go to).  Elsewhere the second
+    // launch costs more than it gives: 256 rows of 1 to 45 tokens x 32 heads took 789
+    // us, not 770.
     constexpr int kShort = 6;
     if (num_tokens <= (long long)kShort * B) {
         p.most = kShort;
