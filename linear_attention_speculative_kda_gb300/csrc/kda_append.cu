@@ -37,7 +37,7 @@ constexpr int kTurn = 8;
 // (us, 4 | 5 CTAs an SM): 256 tokens 4.2 | 4.9 and 13.7k tokens 45 | 48 with
 // 128 channels (16k interleaved ones 53 | 51), 10k tokens 7.4 | 6.8 and 56k
 // tokens 22 | 20 with 64.
-// The norm needs more than 48.
+// The norm takes 62 and spills with 48: 14k tokens of 64 channels 34 us, not 39.
 constexpr int ctas_per_sm(int dim, bool norm) { return dim == 128 || norm ? 4 : 5; }
 
 struct Params {
