@@ -43,6 +43,8 @@ def hold(c, initial=None, outputs=True, total=0.0, largest=0.0, taken=0.0):
     scale = 128 ** -0.5 if c.scale is None else c.scale
     sources = c.slots if initial is None else initial
     for slot, source, first, end in zip(c.slots.tolist(), sources.tolist(), cu, cu[1:]):
+        if first == end:   # writes nothing
+            continue
         s = start[source] if source > 0 else np.zeros(start.shape[1:])
         for t, (out, s, _) in enumerate(D.tokens(
                 s, *(x[first:end] for x in inputs[:5]), *inputs[5:], c.lower_bound, scale), first):
